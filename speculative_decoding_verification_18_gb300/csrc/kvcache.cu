@@ -11,6 +11,7 @@
 #include <cmath>
 #include <cstdint>
 #include <mutex>
+#include <type_traits>
 
 namespace svkv {
 
@@ -240,6 +241,17 @@ __global__ void __launch_bounds__(kAppendThreads) kv_append_kernel(const AppendA
 }
 
 // ---------------------------------------------------------------- attention
+//
+// out_j = sum_l p_jl v_l, p_j = softmax over the visible slots l of scale * q_j . k_l.
+//
+// The query rows of one key head (new token j, group member g: row j * group + g) are the rows
+// of a matrix product with the keys, so that a key or value is read from memory once for all of
+// them.  Work is cut by bytes, not by sequences: an item is (sequence, key head, row tile), it
+// has one unit per 64 slots, and the units of all items, in order, are cut into one equal range
+// per resident CTA, whatever the lengths (they are known on the device only).  A CTA whose range
+// ends inside an item leaves its running maximum, sum and output in the workspace (at most two
+// such pieces per CTA), and the join kernel adds the pieces of an item up.  Which CTA does what
+// depends on the lengths alone, so results repeat bit for bit.
 
 struct AttentionArgs {
     Cache c;
@@ -251,91 +263,692 @@ struct AttentionArgs {
     const int32_t* parents;
     uint32_t* status;
     float scale;
-    int N, q_heads, group;
+    int B, N, q_heads, group;
+    int ctas;             // ranges
+    long long* prefix;    // workspace: [B + 1] units before each sequence
+    float* part_o;        // workspace: [2 * ctas, rows, DP]
+    float2* part_ml;      // workspace: [2 * ctas, rows] maximum (base 2) and sum
 };
 
-constexpr int kSimpleThreads = 128;
+constexpr int kUnit = 64;          // slots of a unit: 16 per warp
+constexpr int kSplitThreads = 128;
+constexpr int kMaxCtas = 304;      // two per SM
 
-// One CTA per query row, a warp per cached position in turn, each warp with its
-// own running maximum, sum and output; the four warps are joined at the end.
-template <typename T, typename CT>
-__global__ void __launch_bounds__(kSimpleThreads) kv_attention_kernel(const AttentionArgs a) {
-    __shared__ int s_par[kMaxN];
-    __shared__ float s_m[4], s_l[4], s_o[4][kMaxDim];
-    const int b = blockIdx.z, j = blockIdx.y, h = blockIdx.x;
+// One sequence's share of the work, for row tiles of `rows` rows.
+struct Share {
+    int len, n, tiles, mts;
+    bool bad;
+    __device__ long long units(int heads) const { return (long long)heads * mts * tiles; }
+};
+
+__device__ __forceinline__ Share share_of(const AttentionArgs& a, int b, int rows) {
+    Share s;
+    s.n = new_tokens(a.kv_len, a.num_new, b, a.N, a.c, &s.len);
+    s.bad = s.n < 0;
+    if (s.bad) s.n = a.N;  // one unit per item: its rows become NaN
+    s.tiles = s.bad ? 1 : (int)(((long long)s.len + s.n + kUnit - 1) / kUnit);
+    s.mts = (s.n * a.group + rows - 1) / rows;
+    return s;
+}
+
+// Ranges that W units are cut into: none of them is empty.
+__device__ __forceinline__ int ranges_of(long long W, int ctas) {
+    return (int)min((long long)ctas, max(W, 1ll));
+}
+// Range c of P equal ranges of W units starts at floor(c W / P).
+__device__ __forceinline__ long long range_start(long long W, int P, int c) {
+    return W / P * c + W % P * c / P;
+}
+__device__ __forceinline__ int range_of(long long W, int P, long long x) {
+    return (int)(((x + 1) * P - 1) / W);
+}
+
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool take) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
+                 "r"(take ? 16 : 0));
+}
+__device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t at) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(at) : "memory");
+}
+__device__ __forceinline__ void ldsm4t(uint32_t (&r)[4], uint32_t at) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(at) : "memory");
+}
+template <typename M>
+__device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
+                                    uint32_t b1) {
+    if constexpr (sizeof(M) == 2 && !std::is_same<M, __half>::value)
+        asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, "
+                     "{%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                     : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+                     : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+    else
+        asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, "
+                     "{%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                     : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+                     : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+// Two values as a pair of type M in one word (x low), rounded to nearest.
+template <typename M> __device__ __forceinline__ uint32_t pair(float x, float y) {
+    if constexpr (std::is_same<M, __half>::value) {
+        const __half2 h = __floats2half2_rn(x, y);
+        return reinterpret_cast<const uint32_t&>(h);
+    } else {
+        const __nv_bfloat162 h = __floats2bfloat162_rn(x, y);
+        return reinterpret_cast<const uint32_t&>(h);
+    }
+}
+template <typename M> __device__ __forceinline__ float2 unpair(uint32_t w) {
+    if constexpr (std::is_same<M, __half>::value)
+        return __half22float2(reinterpret_cast<const __half2&>(w));
+    else
+        return __bfloat1622float2(reinterpret_cast<const __nv_bfloat162&>(w));
+}
+// Two e4m3 bytes (the low half of w) as two halves: exact.
+__device__ __forceinline__ uint32_t widen(uint32_t w) {
+    uint32_t r;
+    asm("{ .reg .b16 lo, hi; mov.b32 {lo, hi}, %1; cvt.rn.f16x2.e4m3x2 %0, lo; }"
+        : "=r"(r) : "r"(w));
+    return r;
+}
+
+// Layout of a warp's stage: 16 keys, then 16 values, rows of DP elements whose 16-byte chunks
+// are exchanged so that neither ldmatrix (8 rows, one chunk) nor the 16-byte loads of float8
+// keys (two rows, four chunks at a time) meet in a bank.
+template <typename CT, int DP> struct Stage {
+    static constexpr int kPitch = DP * (int)sizeof(CT);
+    static constexpr int kChunks = kPitch / 16;  // 4, 8 or 16
+    static constexpr int kBytes = 2 * 16 * kPitch;
+    // as many stages as fit 96 KiB for the four warps (two CTAs per SM), six at most
+    static constexpr int kStages = 4 * kBytes * 6 <= 98304 ? 6 : 98304 / (4 * kBytes);
+    static __device__ __forceinline__ int at(int row, int chunk) {
+        const int x = kChunks == 16  ? chunk ^ (row & 7)
+                      : kChunks == 8 ? chunk ^ ((row & 1) << 2 | (row >> 1 & 3))
+                                     : chunk ^ (row >> 1 & 3);
+        return row * kPitch + x * 16;
+    }
+};
+
+template <typename CT, int DP, int MI> constexpr int split_smem() {
+    const int ring = 4 * Stage<CT, DP>::kStages * Stage<CT, DP>::kBytes;
+    const int merge = 4 * MI * 16 * (DP + 8) * 4 + 4 * MI * 16 * 8;
+    return ring > merge ? ring : merge;
+}
+
+// Whether node j's row may look at new token i of the sequence (bit i - 1 of its ancestors).
+__device__ __forceinline__ bool sees(uint64_t anc, int i) { return i == 0 || (anc >> (i - 1) & 1); }
+
+// Rows of a CTA: MI * 16.  Each of the four warps walks its own 16 slots of every unit, with its
+// own ring of stages filled by 16-byte asynchronous copies, its own running maximum, sum and
+// output; no barrier inside a piece.  The four are joined in shared memory at a piece's end.
+// Matrix products by mma.sync: with at most 32 rows the tensor pipe has time to spare (measured
+// against the memory's share of a stage), and the weights may take two products: P = hi + lo,
+// two 16-bit halves, so that rounding the weights costs nothing next to rounding the result.
+// float8 caches become halves on the way into the registers (exact), with a power of two taken
+// out of each query row so that a bfloat16 query fits a half too; their weights are single
+// halves, four bits finer than a bfloat16 result.
+template <typename T, typename CT, int DP, int MI>
+__global__ void __launch_bounds__(kSplitThreads, 2) kv_split_kernel(const AttentionArgs a) {
+    constexpr bool kF8 = sizeof(CT) == 1;
+    using M = typename std::conditional<kF8, __half, T>::type;  // type of the products
+    constexpr bool kLo = !kF8 || std::is_same<T, __half>::value;
+    using St = Stage<CT, DP>;
+    constexpr int S = St::kStages, KS = DP / 16, NT = DP / 8, ROWS = MI * 16;
+    extern __shared__ __align__(128) char smem[];
+    __shared__ long long s_scan[4];
+    __shared__ long long s_start;
+    __shared__ int s_b, s_par[kMaxN];
+    __shared__ uint64_t s_anc[kMaxN];
+    const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5, t4 = lane & 3;
+    const Cache& c = a.c;
+
+    cudaGridDependencySynchronize();
+    cudaTriggerProgrammaticLaunchCompletion();
+
+    // Units before each sequence (a scan over the batch), the total, and where this range starts.
+    long long W, x0, x1;
+    {
+        const int per = (a.B + kSplitThreads - 1) / kSplitThreads;
+        const int b0 = min(a.B, tid * per), b1 = min(a.B, b0 + per);
+        long long sum = 0;
+        for (int b = b0; b < b1; ++b) sum += share_of(a, b, ROWS).units(c.heads);
+        long long inc = sum;
+        for (int k = 1; k < 32; k <<= 1) {
+            const long long y = __shfl_up_sync(~0u, inc, k);
+            if (lane >= k) inc += y;
+        }
+        if (lane == 31) s_scan[w] = inc;
+        __syncthreads();
+        W = s_scan[0] + s_scan[1] + s_scan[2] + s_scan[3];
+        long long before = inc - sum;
+        for (int i = 0; i < w; ++i) before += s_scan[i];
+        const int P = ranges_of(W, a.ctas);
+        x0 = (int)blockIdx.x < P ? range_start(W, P, blockIdx.x) : W;
+        x1 = (int)blockIdx.x < P ? range_start(W, P, blockIdx.x + 1) : W;
+        long long at = before;
+        if (blockIdx.x == 0 || (x0 >= before && x0 < before + sum)) {
+            for (int b = b0; b < b1; ++b) {
+                const long long u = share_of(a, b, ROWS).units(c.heads);
+                if (x0 >= at && x0 < at + u) s_b = b, s_start = at;
+                if (blockIdx.x == 0) a.prefix[b] = at;
+                at += u;
+            }
+            if (blockIdx.x == 0 && tid == 0) a.prefix[a.B] = W;
+        }
+        __syncthreads();
+    }
+    if (x0 >= x1) return;
+
+    int b = s_b;
+    long long base = s_start;  // units before sequence b
+    Share sh = share_of(a, b, ROWS);
+    const uint32_t ring = (uint32_t)__cvta_generic_to_shared(smem) + w * S * St::kBytes;
+    int anc_of = -1;  // the sequence whose ancestors s_anc holds
+
+    for (long long x = x0; x < x1;) {
+        while (x >= base + sh.units(c.heads)) {
+            base += sh.units(c.heads);
+            sh = share_of(a, ++b, ROWS);
+        }
+        const long long r = x - base;
+        const int item = (int)(r / sh.tiles), t0 = (int)(r - (long long)item * sh.tiles);
+        const int h = item / sh.mts, mt = item - h * sh.mts;
+        const int t1 = (int)min((long long)sh.tiles, t0 + (x1 - x));
+        const int len = sh.len, total = len + sh.n, rows = min(ROWS, sh.n * a.group - mt * ROWS);
+        x += t1 - t0;
+        bool bad = sh.bad;
+        if (bad && tid == 0) mark(a.status, b, SV_DEV_BAD_LENGTH);
+
+        // The ancestors of every node, where this piece reaches the new tokens.
+        if (!bad && (long long)t1 * kUnit > len && anc_of != b) {
+            __syncthreads();
+            int f = 0;
+            if (a.parents)
+                for (int i = tid; i < sh.n; i += kSplitThreads) {
+                    const int p = a.parents[(long long)b * a.N + i];
+                    s_par[i] = p;
+                    f |= i > 0 && (p < 0 || p >= i);
+                }
+            f = __syncthreads_or(f);
+            if (tid < sh.n) {
+                uint64_t m = 0;
+                if (!a.parents)
+                    m = tid == 64 ? ~0ull : (1ull << tid) - 1;
+                else if (!f)
+                    for (int i = tid; i > 0; i = s_par[i]) m |= 1ull << (i - 1);
+                s_anc[tid] = m;
+            }
+            __syncthreads();
+            if (f) {
+                bad = true;
+                if (tid == 0) mark(a.status, b, SV_DEV_BAD_TREE);
+                anc_of = -1;
+            } else {
+                anc_of = b;
+            }
+        }
+
+        // Queries as the A operand: thread (row lane / 4, + 8; elements by lane % 4).
+        uint32_t qa[MI][KS][4];
+        float mul[MI][2];  // from a product to the exponent (base 2)
+        const float unit = a.scale * 1.4426950408889634f * (kF8 ? c.k_scale[h] : 1.0f);
+#pragma unroll
+        for (int mi = 0; mi < MI; ++mi) {
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+                const int row = mi * 16 + half * 8 + (lane >> 2), R = mt * ROWS + row;
+                const int j = R / a.group, g = R - j * a.group;
+                const bool live = row < rows && !bad;
+                const T* q = (const T*)a.q + (live ? b * a.qb + j * a.qt +
+                                                         (long long)(h * a.group + g) * a.qh : 0);
+                float top = 0.0f;
+#pragma unroll
+                for (int ks = 0; ks < KS; ++ks) {
+                    // float8: 16 consecutive elements of a block of 64 per thread, 4 per step
+                    const int e0 = kF8 ? (ks >> 2) * 64 + t4 * 16 + (ks & 3) * 4 : ks * 16 + t4 * 2;
+                    const int e1 = kF8 ? e0 + 2 : e0 + 8;
+                    const bool in = live && (kF8 ? e0 : ks * 16) < c.dim;
+                    const uint32_t w0 = in ? __ldg((const uint32_t*)(q + e0)) : 0u;
+                    const uint32_t w1 = in ? __ldg((const uint32_t*)(q + e1)) : 0u;
+                    qa[mi][ks][half] = w0;
+                    qa[mi][ks][half + 2] = w1;
+                    if constexpr (kF8 && !std::is_same<T, __half>::value) {
+                        const float2 f0 = unpair<T>(w0), f1 = unpair<T>(w1);
+                        top = fmaxf(fmaxf(top, fmaxf(fabsf(f0.x), fabsf(f0.y))),
+                                    fmaxf(fabsf(f1.x), fabsf(f1.y)));
+                    }
+                }
+                mul[mi][half] = unit;
+                if constexpr (kF8 && !std::is_same<T, __half>::value) {
+                    top = fmaxf(top, __shfl_xor_sync(~0u, top, 1));
+                    top = fmaxf(top, __shfl_xor_sync(~0u, top, 2));
+                    // the row's largest element becomes 2^8 .. 2^9: what then falls below the
+                    // smallest half is 2^-33 of it
+                    int e = top > 0.0f && top < INFINITY ? ilogbf(top) - 8 : 0;
+                    e = max(-100, min(100, e));
+                    const float down = exp2f((float)-e);
+                    mul[mi][half] = unit * exp2f((float)e);
+#pragma unroll
+                    for (int ks = 0; ks < KS; ++ks)
+#pragma unroll
+                        for (int k = half; k < 4; k += 2) {
+                            const float2 f = unpair<T>(qa[mi][ks][k]);
+                            qa[mi][ks][k] = pair<__half>(f.x * down, f.y * down);
+                        }
+                }
+            }
+        }
+
+        float o[MI][NT][4], l[MI][2], mr[MI][2];
+#pragma unroll
+        for (int mi = 0; mi < MI; ++mi) {
+            l[mi][0] = l[mi][1] = 0.0f;
+            mr[mi][0] = mr[mi][1] = -INFINITY;
+#pragma unroll
+            for (int k = 0; k < NT; ++k) o[mi][k][0] = o[mi][k][1] = o[mi][k][2] = o[mi][k][3] = 0.0f;
+        }
+        bool bad_page = false;
+
+        const char* kb = c.k + h * c.head_stride;
+        const char* vb = c.v + h * c.head_stride;
+        const int32_t* table = c.table + (long long)b * c.table_width;
+        const int my = w * 16 + (lane & 15);  // the slot of a unit whose page this lane looks up
+        const int dch = c.dim * (int)sizeof(CT) / 16;
+        auto page_of = [&](int t) -> int {
+            const int s = t * kUnit + my;
+            return t < t1 && s < total ? __ldg(table + (s >> c.page_shift)) : -1;
+        };
+        auto issue = [&](int t, int page) {
+            const int s = t * kUnit + my;
+            long long off = -1;
+            if (t < t1 && s < total) {
+                if ((unsigned)page < (unsigned)c.num_pages)
+                    off = page * c.page_stride + (s & ((1 << c.page_shift) - 1)) * c.slot_stride;
+                else
+                    bad_page = true;
+            }
+            if (t < t1) {
+                const uint32_t dst = ring + (t - t0) % S * St::kBytes;
+                constexpr int kRows = 32 / St::kChunks;
+#pragma unroll
+                for (int i = 0; i < 16 / kRows; ++i) {
+                    const int row = i * kRows + lane / St::kChunks, ch = lane % St::kChunks;
+                    const long long f = __shfl_sync(~0u, off, row);
+                    const bool take = f >= 0 && ch < dch;
+                    const long long at = take ? f + ch * 16 : 0;
+                    cp_async16(dst + St::at(row, ch), kb + at, take);
+                    cp_async16(dst + 16 * St::kPitch + St::at(row, ch), vb + at, take);
+                }
+            }
+            asm volatile("cp.async.commit_group;" ::: "memory");
+        };
+        int page = -1;
+        if (!bad) {
+            int first[S - 1];
+#pragma unroll
+            for (int i = 0; i < S - 1; ++i) first[i] = page_of(t0 + i);
+            page = page_of(t0 + S - 1);
+#pragma unroll
+            for (int i = 0; i < S - 1; ++i) issue(t0 + i, first[i]);
+        }
+
+        for (int t = t0; t < t1 && !bad; ++t) {
+            asm volatile("cp.async.wait_group %0;" ::"n"(S - 2) : "memory");
+            __syncwarp();
+            issue(t + S - 1, page);
+            page = page_of(t + S);
+            const int slot0 = t * kUnit + w * 16;
+            if (slot0 >= total) continue;
+            const uint32_t kt = ring + (t - t0) % S * St::kBytes, vt = kt + 16 * St::kPitch;
+
+            // Scores: 16 slots = two tiles of 8 columns.
+            float s[MI][2][4];
+#pragma unroll
+            for (int mi = 0; mi < MI; ++mi)
+#pragma unroll
+                for (int k = 0; k < 4; ++k) s[mi][0][k] = s[mi][1][k] = 0.0f;
+            if constexpr (!kF8) {
+#pragma unroll
+                for (int ks = 0; ks < KS; ++ks) {
+                    uint32_t f[4];
+                    const int row = (lane & 7) + (lane >> 4) * 8, ch = ks * 2 + (lane >> 3 & 1);
+                    ldsm4(f, kt + St::at(row, ch));
+#pragma unroll
+                    for (int mi = 0; mi < MI; ++mi) {
+                        mma<M>(s[mi][0], qa[mi][ks], f[0], f[1]);
+                        mma<M>(s[mi][1], qa[mi][ks], f[2], f[3]);
+                    }
+                }
+            } else {
+#pragma unroll
+                for (int kb4 = 0; kb4 < DP / 64; ++kb4)
+#pragma unroll
+                    for (int nt = 0; nt < 2; ++nt) {
+                        uint32_t f[4];
+                        const uint32_t at = kt + St::at(nt * 8 + (lane >> 2), kb4 * 4 + t4);
+                        asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
+                                     : "=r"(f[0]), "=r"(f[1]), "=r"(f[2]), "=r"(f[3])
+                                     : "r"(at) : "memory");
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            const uint32_t b0 = widen(f[k]), b1 = widen(f[k] >> 16);
+#pragma unroll
+                            for (int mi = 0; mi < MI; ++mi)
+                                mma<M>(s[mi][nt], qa[mi][kb4 * 4 + k], b0, b1);
+                        }
+                    }
+            }
+            const bool fresh = slot0 + 16 > len;  // new tokens or the end are among the 16
+#pragma unroll
+            for (int mi = 0; mi < MI; ++mi) {
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    s[mi][0][k] *= mul[mi][k >> 1];
+                    s[mi][1][k] *= mul[mi][k >> 1];
+                }
+                if (fresh) {
+#pragma unroll
+                    for (int half = 0; half < 2; ++half) {
+                        const int R = mt * ROWS + mi * 16 + half * 8 + (lane >> 2);
+                        const uint64_t anc = s_anc[min(R / a.group, sh.n - 1)];
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            const int i = slot0 + (k >> 1) * 8 + t4 * 2 + (k & 1) - len;
+                            if (i >= 0 && (i >= sh.n || !sees(anc, i)))
+                                s[mi][k >> 1][half * 2 + (k & 1)] = -INFINITY;
+                        }
+                    }
+                }
+                // The reference of a row follows its maximum only when that has grown by 2^8:
+                // weights stay below 2^8 and the output is rarely rescaled.
+                float mx[2];
+#pragma unroll
+                for (int half = 0; half < 2; ++half) {
+                    mx[half] = fmaxf(fmaxf(s[mi][0][half * 2], s[mi][0][half * 2 + 1]),
+                                     fmaxf(s[mi][1][half * 2], s[mi][1][half * 2 + 1]));
+                    mx[half] = fmaxf(mx[half], __shfl_xor_sync(~0u, mx[half], 1));
+                    mx[half] = fmaxf(mx[half], __shfl_xor_sync(~0u, mx[half], 2));
+                }
+                const bool grow0 = mx[0] > mr[mi][0] + 8.0f, grow1 = mx[1] > mr[mi][1] + 8.0f;
+                if (__any_sync(~0u, grow0 || grow1)) {
+                    const float f0 = grow0 ? ex2(mr[mi][0] - mx[0]) : 1.0f;
+                    const float f1 = grow1 ? ex2(mr[mi][1] - mx[1]) : 1.0f;
+                    if (grow0) mr[mi][0] = mx[0];
+                    if (grow1) mr[mi][1] = mx[1];
+                    l[mi][0] *= f0;
+                    l[mi][1] *= f1;
+#pragma unroll
+                    for (int k = 0; k < NT; ++k) {
+                        o[mi][k][0] *= f0;
+                        o[mi][k][1] *= f0;
+                        o[mi][k][2] *= f1;
+                        o[mi][k][3] *= f1;
+                    }
+                }
+#pragma unroll
+                for (int half = 0; half < 2; ++half) {
+                    const float ref = mr[mi][half] == -INFINITY ? 0.0f : mr[mi][half];
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        float& p = s[mi][k >> 1][half * 2 + (k & 1)];
+                        p = ex2(p - ref);
+                        l[mi][half] += p;
+                    }
+                }
+            }
+            if (fresh) {
+                // A masked entry may hold anything, but 0 times NaN is NaN: values that are not
+                // finite are taken out of the product and added for the rows that see them.
+                uint32_t wild = 0;
+                const int row = lane >> 1;
+                if (slot0 + row > len && slot0 + row < total) {
+                    bool f = false;
+                    for (int ch = (lane & 1); ch < dch; ch += 2) {
+                        uint32_t v[4];
+                        asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
+                                     : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3])
+                                     : "r"(vt + St::at(row, ch)) : "memory");
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            if constexpr (kF8) {
+                                for (int i = 0; i < 32; i += 8) f |= (v[k] >> i & 0x7f) == 0x7f;
+                            } else {
+                                constexpr uint32_t e = std::is_same<T, __half>::value ? 0x7c00u
+                                                                                      : 0x7f80u;
+                                f |= (v[k] & e) == e || (v[k] >> 16 & e) == e;
+                            }
+                        }
+                    }
+                    wild = f;
+                }
+                wild = __ballot_sync(~0u, wild != 0);
+                for (int rw = 0; wild != 0 && rw < 16; ++rw) {
+                    if (!(wild >> (2 * rw) & 3)) continue;
+                    const int i = slot0 + rw - len;
+                    const int from = (lane & ~3) | (rw & 7) >> 1;
+#pragma unroll
+                    for (int mi = 0; mi < MI; ++mi)
+#pragma unroll
+                        for (int half = 0; half < 2; ++half) {
+                            const float pe = rw < 8 ? s[mi][0][half * 2] : s[mi][1][half * 2];
+                            const float po = rw < 8 ? s[mi][0][half * 2 + 1] : s[mi][1][half * 2 + 1];
+                            const float p = __shfl_sync(~0u, rw & 1 ? po : pe, from);
+                            const int R = mt * ROWS + mi * 16 + half * 8 + (lane >> 2);
+                            if (sees(s_anc[min(R / a.group, sh.n - 1)], i)) {
+#pragma unroll
+                                for (int k = 0; k < NT; ++k)
+#pragma unroll
+                                    for (int e = 0; e < 2; ++e) {
+                                        const int d = kF8 ? (k >> 1) * 16 + t4 * 4 + e * 2 + (k & 1)
+                                                          : k * 8 + t4 * 2 + e;
+                                        const int by = d * (int)sizeof(CT);
+                                        const CT* v = reinterpret_cast<const CT*>(
+                                            smem + (vt + St::at(rw, by >> 4) + (by & 15) -
+                                                    (uint32_t)__cvta_generic_to_shared(smem)));
+                                        o[mi][k][half * 2 + e] += p * Conv<CT>::to(*v);
+                                    }
+                            }
+                        }
+                    __syncwarp();
+                    for (int ch = lane; ch < St::kChunks; ch += 32)
+                        asm volatile("st.shared.v4.b32 [%0], {%1,%1,%1,%1};" ::"r"(
+                                         vt + St::at(rw, ch)), "r"(0) : "memory");
+                    __syncwarp();
+                }
+            }
+            uint32_t pa[MI][4], pl[MI][4];
+#pragma unroll
+            for (int mi = 0; mi < MI; ++mi)
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const float u = s[mi][k >> 1][(k & 1) * 2], v = s[mi][k >> 1][(k & 1) * 2 + 1];
+                    pa[mi][k] = pair<M>(u, v);
+                    if constexpr (kLo) {
+                        const float2 f = unpair<M>(pa[mi][k]);
+                        pl[mi][k] = pair<M>(u - f.x, v - f.y);
+                    }
+                }
+            if constexpr (!kF8) {
+#pragma unroll
+                for (int dt = 0; dt < KS; ++dt) {
+                    uint32_t f[4];
+                    ldsm4t(f, vt + St::at(lane & 15, dt * 2 + (lane >> 4)));
+#pragma unroll
+                    for (int mi = 0; mi < MI; ++mi) {
+                        mma<M>(o[mi][2 * dt], pa[mi], f[0], f[1]);
+                        mma<M>(o[mi][2 * dt + 1], pa[mi], f[2], f[3]);
+                        mma<M>(o[mi][2 * dt], pl[mi], f[0], f[1]);
+                        mma<M>(o[mi][2 * dt + 1], pl[mi], f[2], f[3]);
+                    }
+                }
+            } else {
+                // a word: elements 2i and 2i + 1 of two slots; the even elements make one tile of
+                // 8 columns, the odd ones the next
+#pragma unroll
+                for (int dt = 0; dt < DP / 32; ++dt) {
+                    uint32_t f[4];
+                    ldsm4t(f, vt + St::at(lane & 15, dt * 2 + (lane >> 4)));
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) {
+                        const uint32_t e0 = widen(__byte_perm(f[2 * k], 0, 0x20));
+                        const uint32_t e1 = widen(__byte_perm(f[2 * k + 1], 0, 0x20));
+                        const uint32_t o0 = widen(__byte_perm(f[2 * k], 0, 0x31));
+                        const uint32_t o1 = widen(__byte_perm(f[2 * k + 1], 0, 0x31));
+#pragma unroll
+                        for (int mi = 0; mi < MI; ++mi) {
+                            mma<M>(o[mi][4 * dt + 2 * k], pa[mi], e0, e1);
+                            mma<M>(o[mi][4 * dt + 2 * k + 1], pa[mi], o0, o1);
+                            if constexpr (kLo) {
+                                mma<M>(o[mi][4 * dt + 2 * k], pl[mi], e0, e1);
+                                mma<M>(o[mi][4 * dt + 2 * k + 1], pl[mi], o0, o1);
+                            }
+                        }
+                    }
+                }
+            }
+        }
+        asm volatile("cp.async.wait_all;" ::: "memory");
+        bad_page = __syncthreads_or(bad_page);
+        if (bad_page) {
+            if (tid == 0) mark(a.status, b, SV_DEV_BAD_PAGE);
+            bad = true;
+        }
+
+        // Join the four warps.
+        float* so = reinterpret_cast<float*>(smem);
+        constexpr int kP = DP + 8;  // rows of eight banks apart
+        float2* sml = reinterpret_cast<float2*>(so + 4 * ROWS * kP);
+#pragma unroll
+        for (int mi = 0; mi < MI; ++mi)
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+                const int row = mi * 16 + half * 8 + (lane >> 2);
+                float sum = l[mi][half];
+                sum += __shfl_xor_sync(~0u, sum, 1);
+                sum += __shfl_xor_sync(~0u, sum, 2);
+                if (t4 == 0) sml[w * ROWS + row] = make_float2(mr[mi][half], sum);
+                float* dst = so + (w * ROWS + row) * kP;
+                if constexpr (!kF8) {
+#pragma unroll
+                    for (int k = 0; k < NT; ++k)
+                        *reinterpret_cast<float2*>(dst + k * 8 + t4 * 2) =
+                            make_float2(o[mi][k][half * 2], o[mi][k][half * 2 + 1]);
+                } else {
+#pragma unroll
+                    for (int k = 0; k < NT; k += 2)
+                        *reinterpret_cast<float4*>(dst + k * 8 + t4 * 4) =
+                            make_float4(o[mi][k][half * 2], o[mi][k + 1][half * 2],
+                                        o[mi][k][half * 2 + 1], o[mi][k + 1][half * 2 + 1]);
+                }
+            }
+        __syncthreads();
+        const bool whole = t0 == 0 && t1 == sh.tiles;
+        const long long part = 2 * blockIdx.x + (t0 == 0 ? 1 : 0);
+        const float vs = kF8 ? c.v_scale[h] : 1.0f;
+        for (int i = tid; i < rows * (DP / 4); i += kSplitThreads) {
+            const int row = i / (DP / 4), d = i % (DP / 4) * 4;
+            float2 ml[4];
+            float top = -INFINITY;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                ml[k] = sml[k * ROWS + row];
+                top = fmaxf(top, ml[k].x);
+            }
+            const float ref = top == -INFINITY ? 0.0f : top;
+            float L = 0.0f;
+            float4 y = make_float4(0, 0, 0, 0);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const float f = ex2(ml[k].x - ref);
+                const float4 v = *reinterpret_cast<const float4*>(so + (k * ROWS + row) * kP + d);
+                L += ml[k].y * f;
+                y.x += v.x * f, y.y += v.y * f, y.z += v.z * f, y.w += v.w * f;
+            }
+            if (bad) L = NAN;
+            if (!whole) {
+                *reinterpret_cast<float4*>(a.part_o + (part * ROWS + row) * DP + d) = y;
+                if (d == 0) a.part_ml[part * ROWS + row] = make_float2(top, L);
+            } else if (d < c.dim) {
+                const int R = mt * ROWS + row, j = R / a.group, g = R - j * a.group;
+                const float f = vs / L;
+                T* dst = (T*)a.out +
+                         (((long long)b * a.N + j) * a.q_heads + h * a.group + g) * c.dim + d;
+                *reinterpret_cast<uint2*>(dst) =
+                    make_uint2(pair<T>(y.x * f, y.y * f), pair<T>(y.z * f, y.w * f));
+            }
+        }
+        __syncthreads();
+    }
+}
+
+// Adds up the pieces of the items that more than one range holds: sum over pieces of
+// 2^(m - max) (o, l), then o / l.  A CTA of four warps per four rows of an item (a warp each), or
+// per row (the warps share its pieces) where the host expects many pieces per item.
+template <typename T, int DP>
+__global__ void __launch_bounds__(128) kv_join_kernel(const AttentionArgs a, int rows, int mts_max,
+                                                      int warps) {
+    __shared__ float4 s_o[4][DP / 4];
     const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
     const Cache& c = a.c;
-    int len;
-    const int n = new_tokens(a.kv_len, a.num_new, b, a.N, c, &len);
-    if (n >= 0 && j >= n) return;
-    uint32_t bad = n < 0 ? SV_DEV_BAD_LENGTH : 0;
-    T* out = (T*)a.out + (((long long)b * a.N + j) * a.q_heads + h) * c.dim;
-    int bad_tree = 0;
-    if (!bad && a.parents) {
-        for (int i = tid; i < n; i += kSimpleThreads) {
-            const int p = a.parents[(long long)b * a.N + i];
-            s_par[i] = p;
-            bad_tree |= i > 0 && (p < 0 || p >= i);
+    cudaGridDependencySynchronize();
+    const int mt = blockIdx.x % mts_max, bh = blockIdx.x / mts_max;
+    const int h = bh % c.heads, b = bh / c.heads;
+    const Share sh = share_of(a, b, rows);
+    if (mt >= sh.mts) return;
+    const long long W = a.prefix[a.B];
+    const long long from = a.prefix[b] + (long long)(h * sh.mts + mt) * sh.tiles;
+    const int P = ranges_of(W, a.ctas);
+    const int c0 = range_of(W, P, from), c1 = range_of(W, P, from + sh.tiles - 1);
+    if (c0 == c1) return;
+    const int row = warps == 1 ? blockIdx.y * 4 + w : blockIdx.y;
+    const int live = min(rows, sh.n * a.group - mt * rows);
+    const bool mine = row < live;
+    if (warps == 4 && !mine) return;
+    // piece i of c0 .. c1: the first starts the item (slot 1 of its CTA), the others continue it
+    auto at = [&](int i) { return (long long)(2 * i + (i == c0 ? 1 : 0)) * rows + row; };
+    float top = -INFINITY, L = 0.0f;
+    float4 y = make_float4(0, 0, 0, 0);
+    if (mine) {
+        for (int i = c0 + lane; i <= c1; i += 32) top = fmaxf(top, a.part_ml[at(i)].x);
+        for (int k = 16; k; k >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, k));
+        const float ref = top == -INFINITY ? 0.0f : top;
+        for (int i = c0 + lane; i <= c1; i += 32) {
+            const float2 ml = a.part_ml[at(i)];
+            L += ml.y * ex2(ml.x - ref);
         }
-        if (__syncthreads_or(bad_tree)) bad = SV_DEV_BAD_TREE;
-    }
-    if (!bad) {
-        int bp = 0;
-        for (int p = tid; p < (len + n + (1 << c.page_shift) - 1) >> c.page_shift; p += kSimpleThreads)
-            bp |= (unsigned)c.table[(long long)b * c.table_width + p] >= (unsigned)c.num_pages;
-        if (__syncthreads_or(bp)) bad = SV_DEV_BAD_PAGE;
-    }
-    if (bad) {
-        if (tid == 0 && j == 0 && h == 0) mark(a.status, b, bad);
-        for (int d = tid; d < c.dim; d += kSimpleThreads) out[d] = Conv<T>::from(NAN);
-        return;
-    }
-    uint64_t seen = 0;  // bit i - 1: node i is node j or an ancestor of it
-    if (!a.parents)
-        seen = j == 64 ? ~0ull : (1ull << j) - 1;
-    else
-        for (int i = j; i > 0; i = s_par[i]) seen |= 1ull << (i - 1);
-    const int kh = h / a.group, D = c.dim, per = 4;  // lane: elements 4 lane ..
-    const T* q = (const T*)a.q + b * a.qb + j * a.qt + h * a.qh;
-    float qf[4], o[4] = {0, 0, 0, 0};
-    const float ks = (c.k_scale ? c.k_scale[kh] : 1.0f) * a.scale;
-    for (int i = 0; i < per; ++i) qf[i] = lane * 4 + i < D ? Conv<T>::to(q[lane * 4 + i]) : 0.0f;
-    float m = -INFINITY, l = 0;
-    for (int s = w; s < len + n; s += 4) {
-        if (s > len && !(seen >> (s - len - 1) & 1)) continue;
-        const long long at = slot_offset(c, b, s) + kh * c.head_stride;
-        const CT* kp = (const CT*)(c.k + at);
-        const CT* vp = (const CT*)(c.v + at);
-        float x = 0, vv[4];
-        for (int i = 0; i < per; ++i) {
-            const int d = lane * 4 + i;
-            x += d < D ? qf[i] * Conv<CT>::to(kp[d]) : 0.0f;
-            vv[i] = d < D ? Conv<CT>::to(vp[d]) : 0.0f;
+        for (int k = 16; k; k >>= 1) L += __shfl_xor_sync(~0u, L, k);
+        if (lane < DP / 4) {
+            const int first = c0 + (warps == 4 ? w : 0);
+#pragma unroll 8
+            for (int i = first; i <= c1; i += warps) {
+                const float f = ex2(a.part_ml[at(i)].x - ref);
+                const float4 v = *reinterpret_cast<const float4*>(a.part_o + at(i) * DP + lane * 4);
+                y.x += v.x * f, y.y += v.y * f, y.z += v.z * f, y.w += v.w * f;
+            }
         }
-        for (int k = 16; k; k >>= 1) x += __shfl_xor_sync(~0u, x, k);
-        x *= ks;
-        const float mn = fmaxf(m, x);
-        const float base = mn == -INFINITY ? 0.0f : mn;
-        const float f = __expf(m - base), p = __expf(x - base);
-        l = l * f + p;
-        for (int i = 0; i < per; ++i) o[i] = o[i] * f + p * vv[i];
-        m = mn;
     }
-    if (lane == 0) s_m[w] = m, s_l[w] = l;
-    for (int i = 0; i < per; ++i) s_o[w][lane * 4 + i] = o[i];
-    __syncthreads();
-    float M = fmaxf(fmaxf(s_m[0], s_m[1]), fmaxf(s_m[2], s_m[3]));
-    if (M == -INFINITY) M = 0;
-    const float vs = c.v_scale ? c.v_scale[kh] : 1.0f;
-    for (int d = tid; d < D; d += kSimpleThreads) {
-        float L = 0, O = 0;
-        for (int i = 0; i < 4; ++i) {
-            const float f = s_l[i] == 0 && s_m[i] == -INFINITY ? 0.0f : __expf(s_m[i] - M);
-            L += s_l[i] * f;
-            O += f == 0 && s_l[i] == 0 ? 0.0f : s_o[i][d] * f;
-        }
-        out[d] = Conv<T>::from(O / L * vs);
+    if (warps == 4) {
+        if (lane < DP / 4) s_o[w][lane] = y;
+        __syncthreads();
+        if (w) return;
+        if (lane < DP / 4)
+            for (int k = 1; k < 4; ++k) {
+                const float4 v = s_o[k][lane];
+                y.x += v.x, y.y += v.y, y.z += v.z, y.w += v.w;
+            }
     }
+    if (!mine || lane * 4 >= c.dim) return;
+    const int R = mt * rows + row, j = R / a.group, g = R - j * a.group;
+    const float f = (c.v_scale ? c.v_scale[h] : 1.0f) / L;
+    T* dst = (T*)a.out + (((long long)b * a.N + j) * a.q_heads + h * a.group + g) * c.dim + lane * 4;
+    *reinterpret_cast<uint2*>(dst) =
+        make_uint2(pair<T>(y.x * f, y.y * f), pair<T>(y.z * f, y.w * f));
 }
 
 // ---------------------------------------------------------------- commit
@@ -420,9 +1033,48 @@ __global__ void __launch_bounds__(kCommitThreads) kv_commit_kernel(const CommitA
 
 static bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
 
-static sv_status device_ok() {
+// Calls f with the types and sizes of the split kernel that these sizes take: 16 query rows
+// of a key head per CTA, or 32 where there are more (one CTA then reads each key once for all).
+template <typename F>
+static auto with_split(sv_dtype dtype, sv_dtype cache, int dim, int rows, F f) {
+    auto sized = [&](auto t, auto ct) {
+        using T = decltype(t);
+        using CT = decltype(ct);
+        if (dim <= 64)
+            return rows <= 16 ? f(kv_split_kernel<T, CT, 64, 1>, kv_join_kernel<T, 64>,
+                                  split_smem<CT, 64, 1>())
+                              : f(kv_split_kernel<T, CT, 64, 2>, kv_join_kernel<T, 64>,
+                                  split_smem<CT, 64, 2>());
+        return rows <= 16 ? f(kv_split_kernel<T, CT, 128, 1>, kv_join_kernel<T, 128>,
+                              split_smem<CT, 128, 1>())
+                          : f(kv_split_kernel<T, CT, 128, 2>, kv_join_kernel<T, 128>,
+                              split_smem<CT, 128, 2>());
+    };
+    if (dtype == SV_BF16)
+        return cache == SV_E4M3 ? sized(__nv_bfloat16(), __nv_fp8_e4m3())
+                                : sized(__nv_bfloat16(), __nv_bfloat16());
+    return cache == SV_E4M3 ? sized(__half(), __nv_fp8_e4m3()) : sized(__half(), __half());
+}
+
+// Shared memory of every split kernel, once per device.
+static cudaError_t split_setup() {
+    cudaError_t e = cudaSuccess;
+    for (sv_dtype t : {SV_BF16, SV_F16})
+        for (bool f8 : {false, true})
+            for (int dim : {64, 128})
+                for (int rows : {16, 32})
+                    if (e == cudaSuccess)
+                        e = with_split(t, f8 ? SV_E4M3 : t, dim, rows, [](auto k, auto, int smem) {
+                            return cudaFuncSetAttribute(
+                                k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+                        });
+    return e;
+}
+
+// The current device's SM count, if it is one that these kernels run on.
+static sv_status device_ok(int* sms) {
     static std::mutex mu;
-    static int known[64];  // 0 unknown, 1 sm_103, 2 another device
+    static int known[64];  // 0 unknown, -1 another device, else the SM count
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) return SV_ERR_CUDA;
     if (dev < 0 || dev >= 64) return SV_ERR_UNSUPPORTED;
@@ -432,9 +1084,27 @@ static sv_status device_ok() {
         if (cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev) != cudaSuccess ||
             cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev) != cudaSuccess)
             return SV_ERR_CUDA;
-        known[dev] = major == 10 && minor == 3 ? 1 : 2;
+        int n = -1;
+        if (major == 10 && minor == 3 &&
+            cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+            return SV_ERR_CUDA;
+        if (n > 0 && split_setup() != cudaSuccess) return SV_ERR_CUDA;
+        known[dev] = n;
     }
-    return known[dev] == 1 ? SV_OK : SV_ERR_UNSUPPORTED;
+    if (known[dev] < 0) return SV_ERR_UNSUPPORTED;
+    *sms = known[dev];
+    return SV_OK;
+}
+
+// The workspace: units before each sequence, then two pieces of up to 32 rows per CTA.
+struct AttentionWs { size_t part_o, part_ml, bytes; };
+static AttentionWs attention_ws(int B, int dim) {
+    const size_t dp = dim <= 64 ? 64 : 128, rows = (size_t)2 * kMaxCtas * 32;
+    AttentionWs l;
+    l.part_o = ((size_t)(B + 1) * 8 + 255) / 256 * 256;
+    l.part_ml = l.part_o + rows * dp * 4;
+    l.bytes = l.part_ml + rows * 8;
+    return l;
 }
 
 static int elem_bytes(sv_dtype t) { return t == SV_E4M3 ? 1 : 2; }
@@ -556,7 +1226,8 @@ sv_status spec_kv_append(const sv_kv_cache* cache, const sv_rope* rope, const vo
         a.magnitude = rope->magnitude;
     }
     if (B == 0) return SV_OK;
-    if ((st = device_ok()) != SV_OK) return st;
+    int sms;
+    if ((st = device_ok(&sms)) != SV_OK) return st;
     a.q = (const char*)q;
     a.k = (const char*)k;
     a.v = (const char*)v;
@@ -587,7 +1258,7 @@ size_t spec_kv_attention_workspace_size(int B, int N, int q_heads, int heads, in
     if (B < 0 || B > kMaxB || N < 1 || N > kMaxN || heads < 1 || q_heads < 1 || q_heads % heads ||
         q_heads > kMaxQHeads || dim < 16 || dim > kMaxDim || dim % 16)
         return 0;
-    return 256;
+    return attention_ws(B, dim).bytes;
 }
 
 sv_status spec_kv_attention(const sv_kv_cache* cache, const void* q, const sv_strides* q_strides,
@@ -608,7 +1279,8 @@ sv_status spec_kv_attention(const sv_kv_cache* cache, const void* q, const sv_st
     if (ws_bytes < spec_kv_attention_workspace_size(B, N, q_heads, cache->heads, cache->dim))
         return SV_ERR_WORKSPACE;
     if (B == 0) return SV_OK;
-    if ((st = device_ok()) != SV_OK) return st;
+    int sms;
+    if ((st = device_ok(&sms)) != SV_OK) return st;
     a.q = (const char*)q;
     a.out = (char*)out;
     a.qb = q_strides->batch, a.qt = q_strides->token, a.qh = q_strides->head;
@@ -620,19 +1292,40 @@ sv_status spec_kv_attention(const sv_kv_cache* cache, const void* q, const sv_st
     a.N = N;
     a.q_heads = q_heads;
     a.group = q_heads / cache->heads;
-    const dim3 grid(q_heads, N, B);
-    if (dtype == SV_BF16) {
-        if (cache->dtype == SV_E4M3)
-            kv_attention_kernel<__nv_bfloat16, __nv_fp8_e4m3><<<grid, kSimpleThreads, 0, stream>>>(a);
-        else
-            kv_attention_kernel<__nv_bfloat16, __nv_bfloat16><<<grid, kSimpleThreads, 0, stream>>>(a);
-    } else {
-        if (cache->dtype == SV_E4M3)
-            kv_attention_kernel<__half, __nv_fp8_e4m3><<<grid, kSimpleThreads, 0, stream>>>(a);
-        else
-            kv_attention_kernel<__half, __half><<<grid, kSimpleThreads, 0, stream>>>(a);
-    }
-    return launched();
+    a.B = B;
+    const int rows = N * a.group, tile = rows <= 16 ? 16 : 32;
+    const int mts = (rows + tile - 1) / tile;
+    if ((long double)B * cache->heads * mts *
+            ((double)cache->table_width * cache->page_size / kUnit + 1) >= (long double)(1ll << 50))
+        return SV_ERR_UNSUPPORTED;
+    if ((long long)B * cache->heads * mts >= (1ll << 31)) return SV_ERR_UNSUPPORTED;  // grid size
+    a.ctas = 2 * sms < kMaxCtas ? 2 * sms : kMaxCtas;
+    const AttentionWs l = attention_ws(B, cache->dim);
+    a.prefix = (long long*)ws;
+    a.part_o = (float*)((char*)ws + l.part_o);
+    a.part_ml = (float2*)((char*)ws + l.part_ml);
+    // Pieces per item, if all sequences were alike: with many, the warps of a CTA share a row.
+    const int warps = a.ctas >= 8 * (long long)B * cache->heads * mts ? 4 : 1;
+    cudaLaunchAttribute pdl;
+    pdl.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    pdl.val.programmaticStreamSerializationAllowed = 1;
+    const cudaError_t e = with_split(dtype, cache->dtype, cache->dim, rows, [&](auto split, auto join,
+                                                                               int smem) {
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3(a.ctas);
+        cfg.blockDim = dim3(kSplitThreads);
+        cfg.dynamicSmemBytes = smem;
+        cfg.stream = stream;
+        cfg.attrs = &pdl;
+        cfg.numAttrs = 1;
+        cudaError_t r = cudaLaunchKernelEx(&cfg, split, a);
+        if (r != cudaSuccess) return r;
+        cfg.gridDim = dim3(B * cache->heads * mts, warps == 4 ? tile : tile / 4);
+        cfg.blockDim = dim3(128);
+        cfg.dynamicSmemBytes = 0;
+        return cudaLaunchKernelEx(&cfg, join, a, tile, mts, warps);
+    });
+    return e == cudaSuccess ? SV_OK : SV_ERR_CUDA;
 }
 
 sv_status spec_kv_commit(const sv_kv_cache* cache, int layers, int64_t layer_stride,
@@ -654,7 +1347,8 @@ sv_status spec_kv_commit(const sv_kv_cache* cache, int layers, int64_t layer_str
         return SV_ERR_INVALID_ARG;
     if (B == 0) return SV_OK;
     if (kv_len_out == kv_len) return SV_ERR_INVALID_ARG;
-    if ((st = device_ok()) != SV_OK) return st;
+    int sms;
+    if ((st = device_ok(&sms)) != SV_OK) return st;
     a.layer_stride = layers > 1 ? layer_stride * e : 0;
     a.kv_len = kv_len;
     a.out_nodes = out_nodes;

@@ -93,7 +93,7 @@ class Round:
         out = gd.empty(self.q.shape, self.dtype, fill=7.0)
         n = kv.spec_kv_attention_workspace_size(self.B, self.N, self.heads * self.group, self.heads,
                                                 self.dim)
-        ws = gd.empty((n,), torch.uint8)
+        ws = gd.empty((n,), torch.uint8, fill=255)  # NaN wherever it is read unwritten
         status = gd.empty((self.B,), torch.int32, fill=0)
         kv.spec_kv_attention(c, d(self.q), d(self.lens), out, ws, self.scale,
                              parents=d(self.parents),
