@@ -61,6 +61,7 @@ extern "C" {
 
 #define SV_DEV_BAD_PAGE 0x80u
 #define SV_DEV_BAD_LENGTH 0x100u
+#define SV_DEV_TIMEOUT 0x200u /* spec_kv_attention: a bounded wait inside the kernel gave up */
 
 /* One layer of a paged cache.  Entry (page p, slot s, head h) starts at element
  * p*page_stride + s*slot_stride + h*head_stride of k and of v, its dim elements
@@ -137,7 +138,8 @@ size_t spec_kv_attention_workspace_size(int B, int N, int q_heads, int heads, in
  *        has the same type, or SV_E4M3.
  *   out  [B, N, q_heads, dim] contiguous (written), the type of q.
  * Entries that a node does not attend to take no part, whatever they hold.  The
- * sums are fp32.  Every row of a sequence with a bad length, tree or page is
+ * sums are fp32.  Workspace as for the other calls (no initialisation; calls that
+ * share one must not overlap).  Every row of a sequence with a bad length, tree or page is
  * NaN (its first num_new rows; all N when num_new itself is bad). */
 sv_status spec_kv_attention(const sv_kv_cache* cache, const void* q, const sv_strides* q_strides,
                             sv_dtype dtype, const int32_t* kv_len, const int32_t* num_new,

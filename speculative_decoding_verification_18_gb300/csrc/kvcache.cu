@@ -281,12 +281,12 @@ struct Share {
     __device__ long long units(int heads) const { return (long long)heads * mts * tiles; }
 };
 
-__device__ __forceinline__ Share share_of(const AttentionArgs& a, int b, int rows) {
+__device__ __forceinline__ Share share_of(const AttentionArgs& a, int b, int rows, int unit) {
     Share s;
     s.n = new_tokens(a.kv_len, a.num_new, b, a.N, a.c, &s.len);
     s.bad = s.n < 0;
     if (s.bad) s.n = a.N;  // one unit per item: its rows become NaN
-    s.tiles = s.bad ? 1 : (int)(((long long)s.len + s.n + kUnit - 1) / kUnit);
+    s.tiles = s.bad ? 1 : (int)(((long long)s.len + s.n + unit - 1) / unit);
     s.mts = (s.n * a.group + rows - 1) / rows;
     return s;
 }
@@ -417,7 +417,7 @@ __global__ void __launch_bounds__(kSplitThreads, 2) kv_split_kernel(const Attent
         const int per = (a.B + kSplitThreads - 1) / kSplitThreads;
         const int b0 = min(a.B, tid * per), b1 = min(a.B, b0 + per);
         long long sum = 0;
-        for (int b = b0; b < b1; ++b) sum += share_of(a, b, ROWS).units(c.heads);
+        for (int b = b0; b < b1; ++b) sum += share_of(a, b, ROWS, kUnit).units(c.heads);
         long long inc = sum;
         for (int k = 1; k < 32; k <<= 1) {
             const long long y = __shfl_up_sync(~0u, inc, k);
@@ -434,7 +434,7 @@ __global__ void __launch_bounds__(kSplitThreads, 2) kv_split_kernel(const Attent
         long long at = before;
         if (blockIdx.x == 0 || (x0 >= before && x0 < before + sum)) {
             for (int b = b0; b < b1; ++b) {
-                const long long u = share_of(a, b, ROWS).units(c.heads);
+                const long long u = share_of(a, b, ROWS, kUnit).units(c.heads);
                 if (x0 >= at && x0 < at + u) s_b = b, s_start = at;
                 if (blockIdx.x == 0) a.prefix[b] = at;
                 at += u;
@@ -447,14 +447,14 @@ __global__ void __launch_bounds__(kSplitThreads, 2) kv_split_kernel(const Attent
 
     int b = s_b;
     long long base = s_start;  // units before sequence b
-    Share sh = share_of(a, b, ROWS);
+    Share sh = share_of(a, b, ROWS, kUnit);
     const uint32_t ring = (uint32_t)__cvta_generic_to_shared(smem) + w * S * St::kBytes;
     int anc_of = -1;  // the sequence whose ancestors s_anc holds
 
     for (long long x = x0; x < x1;) {
         while (x >= base + sh.units(c.heads)) {
             base += sh.units(c.heads);
-            sh = share_of(a, ++b, ROWS);
+            sh = share_of(a, ++b, ROWS, kUnit);
         }
         const long long r = x - base;
         const int item = (int)(r / sh.tiles), t0 = (int)(r - (long long)item * sh.tiles);
@@ -887,19 +887,784 @@ __global__ void __launch_bounds__(kSplitThreads, 2) kv_split_kernel(const Attent
     }
 }
 
+// ---------------------------------------------------------------- many rows: tcgen05
+//
+// With more query rows per key head than mma.sync keeps up with, the products run on tcgen05.mma:
+// 128 rows by 128 slots, scores, weights and outputs in tensor memory.  One CTA per SM; its warps
+// have roles: 4 load keys and values (16-byte asynchronous copies through the page table into
+// 128-byte-swizzled panels of 64 elements), one thread issues the products, 2 x 4 hold one query
+// row per thread and turn scores into weights.  Two streams of scores alternate on the tensor
+// pipe, so that one is multiplied while the other is exponentiated: two tiles of 128 rows over
+// the same slots, or, when the rows fit one tile, every other 128 slots of it (joined at the
+// end).  Work is cut into ranges and joined as for the split kernel, in units of 128 slots.
+
+constexpr int kTcThreads = 512;
+constexpr int kTcUnit = 128;  // slots
+constexpr int kTcMaxCtas = 152;
+
+template <int DP, int ROWS> struct Tc {
+    static constexpr int kTile = 128 * DP * 2;          // bytes of 128 keys, values or queries
+    static constexpr int kQ = ROWS / 128 * kTile;
+    static constexpr int kFit = (224 * 1024 - kQ) / (2 * kTile);  // the static part: below 3 KiB
+    static constexpr int kStages = kFit > 6 ? 6 : kFit;  // of keys and values each
+    static constexpr int kSmem = kQ + 2 * kStages * kTile;
+};
+
+struct TcBars {
+    uint64_t q_full, q_empty, epi_done, drain;
+    uint64_t k_full[6], k_empty[6], v_full[6], v_empty[6];
+    uint64_t s_full[2], p_full[2], pv_done[2];
+};
+
+__device__ __forceinline__ uint32_t saddr(const void* p) {
+    return (uint32_t)__cvta_generic_to_shared(p);
+}
+__device__ __forceinline__ void bar_init(uint64_t* bar, int count) {
+    asm volatile("mbarrier.init.shared.b64 [%0], %1;" ::"r"(saddr(bar)), "r"(count) : "memory");
+}
+__device__ __forceinline__ void bar_arrive(uint64_t* bar) {
+    asm volatile("mbarrier.arrive.shared.b64 _, [%0];" ::"r"(saddr(bar)) : "memory");
+}
+// Arrives when this thread's asynchronous copies so far have landed.
+__device__ __forceinline__ void bar_arrive_copies(uint64_t* bar) {
+    asm volatile("cp.async.mbarrier.arrive.noinc.shared.b64 [%0];" ::"r"(saddr(bar)) : "memory");
+}
+constexpr uint64_t kGiveUp = 2000000000;  // two seconds
+__device__ __forceinline__ uint64_t nanoseconds() {
+    uint64_t now;
+    asm volatile("mov.u64 %0, %globaltimer;" : "=l"(now));
+    return now;
+}
+// Whether a phase is complete, for a whole warp.
+__device__ __forceinline__ bool warp_test(uint64_t* bar, uint32_t parity) {
+    uint32_t done;
+    asm volatile("{ .reg .pred p; mbarrier.test_wait.parity.shared.b64 p, [%1], %2; "
+                 "selp.u32 %0, 1, 0, p; }" : "=r"(done) : "r"(saddr(bar)), "r"(parity) : "memory");
+    return __all_sync(~0u, done != 0);
+}
+// Waits for a phase of a barrier, two seconds at most, and no longer once another wait has given
+// up; false when it gave up.
+__device__ __forceinline__ bool bar_wait(uint64_t* bar, uint32_t parity, volatile int* gave_up) {
+    const uint32_t at = saddr(bar);
+    uint64_t since = 0;
+    for (int i = 1;; ++i) {
+        uint32_t done;
+        asm volatile("{ .reg .pred p; mbarrier.try_wait.parity.shared.b64 p, [%1], %2; "
+                     "selp.u32 %0, 1, 0, p; }" : "=r"(done) : "r"(at), "r"(parity) : "memory");
+        if (done) return true;
+        if (i & 31) continue;
+        const uint64_t now = nanoseconds();
+        if (!since) since = now;
+        if (*gave_up || now - since > kGiveUp) break;
+    }
+    *gave_up = 1;
+    return false;
+}
+// The same for a whole warp, with one answer.
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* gave_up) {
+    return __all_sync(~0u, bar_wait(bar, parity, gave_up));
+}
+__device__ __forceinline__ void named_sync(int id, int threads) {
+    asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
+}
+
+// Shared-memory operand descriptor, 128-byte swizzle: rows of 128 bytes, 1024 bytes from one
+// group of eight rows to the next; `panel`: bytes between panels of 64 elements, used where the
+// operand's contiguous dimension is not the summed one (values: rows are slots).
+__device__ __forceinline__ uint64_t operand(uint32_t at, uint32_t panel) {
+    return (uint64_t)(at >> 4 & 0x3fff) | (uint64_t)(panel >> 4) << 16 | (uint64_t)(1024 >> 4) << 32 |
+           (uint64_t)1 << 46 | (uint64_t)2 << 61;
+}
+// Instruction descriptor: 128 x N, fp32 sums of bf16 or fp16 products; `rows`: the second
+// operand's contiguous dimension is N.
+template <typename T> __device__ constexpr uint32_t product(int N, bool rows) {
+    const uint32_t type = std::is_same<T, __half>::value ? 0u : 1u;
+    return 1u << 4 | type << 7 | type << 10 | (rows ? 1u << 16 : 0u) | (uint32_t)(N >> 3) << 17 |
+           (128u >> 4) << 24;
+}
+__device__ __forceinline__ void tc_mma(uint32_t d, uint64_t a, uint64_t b, uint32_t desc, bool add) {
+    asm volatile("{ .reg .pred p; setp.ne.b32 p, %4, 0; "
+                 "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p; }"
+                 ::"r"(d), "l"(a), "l"(b), "r"(desc), "r"((int)add) : "memory");
+}
+__device__ __forceinline__ void tc_mma_t(uint32_t d, uint32_t a, uint64_t b, uint32_t desc,
+                                         bool add) {
+    asm volatile("{ .reg .pred p; setp.ne.b32 p, %4, 0; "
+                 "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p; }"
+                 ::"r"(d), "r"(a), "l"(b), "r"(desc), "r"((int)add) : "memory");
+}
+__device__ __forceinline__ void tc_commit(uint64_t* bar) {
+    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];"
+                 ::"r"(saddr(bar)) : "memory");
+}
+// 32 columns of this thread's lane of tensor memory, as floats.
+__device__ __forceinline__ void tc_ld32(float* r, uint32_t at) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+        : "=f"(r[0]), "=f"(r[1]), "=f"(r[2]), "=f"(r[3]), "=f"(r[4]), "=f"(r[5]),
+          "=f"(r[6]), "=f"(r[7]), "=f"(r[8]), "=f"(r[9]), "=f"(r[10]), "=f"(r[11]),
+          "=f"(r[12]), "=f"(r[13]), "=f"(r[14]), "=f"(r[15]), "=f"(r[16]), "=f"(r[17]),
+          "=f"(r[18]), "=f"(r[19]), "=f"(r[20]), "=f"(r[21]), "=f"(r[22]), "=f"(r[23]),
+          "=f"(r[24]), "=f"(r[25]), "=f"(r[26]), "=f"(r[27]), "=f"(r[28]), "=f"(r[29]),
+          "=f"(r[30]), "=f"(r[31])
+        : "r"(at) : "memory");
+}
+__device__ __forceinline__ void tc_st32(uint32_t at, const float* r) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, "
+        "%17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};"
+        ::"r"(at), "f"(r[0]), "f"(r[1]), "f"(r[2]), "f"(r[3]), "f"(r[4]), "f"(r[5]), "f"(r[6]),
+          "f"(r[7]), "f"(r[8]), "f"(r[9]), "f"(r[10]), "f"(r[11]), "f"(r[12]),
+          "f"(r[13]), "f"(r[14]), "f"(r[15]), "f"(r[16]), "f"(r[17]), "f"(r[18]),
+          "f"(r[19]), "f"(r[20]), "f"(r[21]), "f"(r[22]), "f"(r[23]), "f"(r[24]),
+          "f"(r[25]), "f"(r[26]), "f"(r[27]), "f"(r[28]), "f"(r[29]), "f"(r[30]),
+          "f"(r[31])
+        : "memory");
+}
+__device__ __forceinline__ void tc_st32(uint32_t at, const uint32_t (&r)[32]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,"
+        "%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};"
+        ::"r"(at), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]),
+          "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]),
+          "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]),
+          "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
+          "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31]) : "memory");
+}
+__device__ __forceinline__ void tc_ld16(float* r, uint32_t at) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, "
+        "%8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+        : "=f"(r[0]), "=f"(r[1]), "=f"(r[2]), "=f"(r[3]), "=f"(r[4]), "=f"(r[5]), "=f"(r[6]),
+          "=f"(r[7]), "=f"(r[8]), "=f"(r[9]), "=f"(r[10]), "=f"(r[11]), "=f"(r[12]), "=f"(r[13]),
+          "=f"(r[14]), "=f"(r[15])
+        : "r"(at) : "memory");
+}
+__device__ __forceinline__ void tc_st16(uint32_t at, const float* r) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, "
+        "%9, %10, %11, %12, %13, %14, %15, %16};"
+        ::"r"(at), "f"(r[0]), "f"(r[1]), "f"(r[2]), "f"(r[3]), "f"(r[4]), "f"(r[5]), "f"(r[6]),
+          "f"(r[7]), "f"(r[8]), "f"(r[9]), "f"(r[10]), "f"(r[11]), "f"(r[12]), "f"(r[13]),
+          "f"(r[14]), "f"(r[15]) : "memory");
+}
+__device__ __forceinline__ float tc_ld1(uint32_t at) {
+    float r;
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];" : "=f"(r) : "r"(at) : "memory");
+    return r;
+}
+__device__ __forceinline__ void tc_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void tc_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void tc_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tc_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+
+__device__ __forceinline__ bool elect_one() {
+    uint32_t yes;
+    asm volatile("{ .reg .pred p; elect.sync _|p, 0xffffffff; selp.u32 %0, 1, 0, p; }" : "=r"(yes));
+    return yes != 0;
+}
+
+// A piece of an item, in the order in which every role walks the CTA's range.
+struct Piece {
+    int b, h, mt, t0, t1, rows;
+};
+struct Walk {
+    long long x, x1, base;
+    int b;
+    Share sh;
+    __device__ bool next(const AttentionArgs& a, int tile_rows, Piece* p) {
+        if (x >= x1) return false;
+        while (x >= base + sh.units(a.c.heads)) {
+            base += sh.units(a.c.heads);
+            sh = share_of(a, ++b, tile_rows, kTcUnit);
+        }
+        const long long r = x - base;
+        const int item = (int)(r / sh.tiles);
+        p->b = b;
+        p->t0 = (int)(r - (long long)item * sh.tiles);
+        p->h = item / sh.mts;
+        p->mt = item - p->h * sh.mts;
+        p->t1 = (int)min((long long)sh.tiles, p->t0 + (x1 - x));
+        p->rows = min(tile_rows, sh.n * a.group - p->mt * tile_rows);
+        x += p->t1 - p->t0;
+        return true;
+    }
+};
+
+template <typename T, int DP, int ROWS>
+__global__ void __launch_bounds__(kTcThreads, 1) kv_wide_kernel(const AttentionArgs a) {
+    using L = Tc<DP, ROWS>;
+    constexpr int S = L::kStages, CH = DP / 8;
+    // Weights in two halves (P = hi + lo) where the tensor pipe waits for memory anyway.
+    constexpr bool kLo = ROWS == 128;
+    extern __shared__ __align__(1024) char smem_tc[];  // the swizzle counts from 1024
+    __shared__ TcBars bars;
+    __shared__ long long s_scan[kTcThreads / 32];
+    __shared__ long long s_start;
+    __shared__ int s_b, s_gave_up, s_bad_piece[4], s_par[kMaxN];
+    __shared__ uint64_t s_anc[kMaxN];
+    __shared__ uint32_t s_tmem, s_wild[6][4];
+    __shared__ float2 s_ml[128];
+    const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
+    const Cache& c = a.c;
+    const uint32_t sq = saddr(smem_tc);  // queries, then stages of k, then of v
+    const uint32_t sk = sq + L::kQ, sv = sk + S * L::kTile;
+
+    if (tid == 0) {
+        bar_init(&bars.q_full, 128);
+        bar_init(&bars.q_empty, 1);
+        bar_init(&bars.drain, 1);
+        bar_init(&bars.epi_done, 256);
+        for (int i = 0; i < S; ++i) {
+            bar_init(&bars.k_full[i], 128);
+            bar_init(&bars.k_empty[i], 1);
+            bar_init(&bars.v_full[i], 128);
+            bar_init(&bars.v_empty[i], 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            bar_init(&bars.s_full[i], 1);
+            bar_init(&bars.p_full[i], 128);
+            bar_init(&bars.pv_done[i], 1);
+        }
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        s_gave_up = 0;
+    }
+    if (tid < 4) s_bad_piece[tid] = -1;
+    if (w == 12) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;"
+                     ::"r"(saddr(&s_tmem)), "r"(512) : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+    }
+    cudaGridDependencySynchronize();
+    cudaTriggerProgrammaticLaunchCompletion();
+
+    Walk walk;
+    {
+        const int per = (a.B + kTcThreads - 1) / kTcThreads;
+        const int b0 = min(a.B, tid * per), b1 = min(a.B, b0 + per);
+        long long sum = 0;
+        for (int b = b0; b < b1; ++b) sum += share_of(a, b, ROWS, kTcUnit).units(c.heads);
+        long long inc = sum;
+        for (int k = 1; k < 32; k <<= 1) {
+            const long long y = __shfl_up_sync(~0u, inc, k);
+            if (lane >= k) inc += y;
+        }
+        if (lane == 31) s_scan[w] = inc;
+        tc_before();
+        __syncthreads();
+        tc_after();
+        long long W = 0, before = inc - sum;
+        for (int i = 0; i < kTcThreads / 32; ++i) {
+            W += s_scan[i];
+            if (i < w) before += s_scan[i];
+        }
+        const int P = ranges_of(W, a.ctas);
+        walk.x = (int)blockIdx.x < P ? range_start(W, P, blockIdx.x) : W;
+        walk.x1 = (int)blockIdx.x < P ? range_start(W, P, blockIdx.x + 1) : W;
+        if (blockIdx.x == 0 || (walk.x >= before && walk.x < before + sum)) {
+            long long at = before;
+            for (int b = b0; b < b1; ++b) {
+                const long long u = share_of(a, b, ROWS, kTcUnit).units(c.heads);
+                if (walk.x >= at && walk.x < at + u) s_b = b, s_start = at;
+                if (blockIdx.x == 0) a.prefix[b] = at;
+                at += u;
+            }
+            if (blockIdx.x == 0 && tid == 0) a.prefix[a.B] = W;
+        }
+        __syncthreads();
+        walk.b = walk.x < walk.x1 ? s_b : 0;
+        walk.base = walk.x < walk.x1 ? s_start : 0;
+        walk.sh = share_of(a, walk.b, ROWS, kTcUnit);
+    }
+    const uint32_t tmem = s_tmem;
+    volatile int* gave_up = &s_gave_up;
+    Piece p;
+
+    if (w >= 8 && w < 12) {
+        // ------------------------------------------------ loads
+        const int lt = tid - 256, lw = lt >> 5;
+        const int dch = c.dim / 8;
+        long long tile = 0;
+        int pieces = 0;
+        bool ok = true;  // once a wait gave up: no more copies, the barriers among the warps stay
+        while (walk.next(a, ROWS, &p)) {
+            if (walk.sh.bad) continue;
+            const int len = walk.sh.len, total = len + walk.sh.n;
+            // queries: rows of the item, zeros past them
+            ok = ok && warp_wait(&bars.q_empty, (pieces & 1) ^ 1, gave_up);
+            for (int i = lt; ok && i < ROWS * CH; i += 128) {
+                const int row = i / CH, ch = i % CH, R = p.mt * ROWS + row;
+                const bool take = row < p.rows && ch < dch;
+                const int j = R / a.group, g = R - j * a.group;
+                const T* q = (const T*)a.q + (take ? p.b * a.qb + j * a.qt +
+                                  (long long)(p.h * a.group + g) * a.qh + ch * 8 : 0);
+                const int r = row & 127;
+                cp_async16(sq + (row >> 7) * L::kTile + (ch >> 3) * 16384 + r * 128 +
+                               (((ch & 7) ^ (r & 7)) << 4), q, take);
+            }
+            bar_arrive_copies(&bars.q_full);
+
+            const char* kb = c.k + p.h * c.head_stride;
+            const char* vb = c.v + p.h * c.head_stride;
+            const int32_t* table = c.table + (long long)p.b * c.table_width;
+            // this lane looks up row 32 lw + lane of a tile
+            auto page_of = [&](int t) -> int {
+                const long long s = (long long)t * kTcUnit + lw * 32 + lane;
+                return t < p.t1 && s < total ? __ldg(table + (s >> c.page_shift)) : -1;
+            };
+            int page = page_of(p.t0);
+            for (int t = p.t0; t < p.t1; ++t, ++tile) {
+                const long long s = (long long)t * kTcUnit + lw * 32 + lane;
+                long long off = -1;
+                if (s < total) {
+                    if ((unsigned)page < (unsigned)c.num_pages)
+                        off = page * c.page_stride +
+                              (s & ((1 << c.page_shift) - 1)) * c.slot_stride;
+                    else
+                        s_bad_piece[pieces & 3] = pieces;
+                }
+                page = page_of(t + 1);
+                const int st = (int)(tile % S);
+                const uint32_t again = (uint32_t)(tile / S & 1) ^ 1;
+                const bool tail = (long long)(t + 1) * kTcUnit > len + 1;
+#pragma unroll 1
+                for (int kv = 0; kv < 2; ++kv) {
+                    ok = ok && warp_wait(kv ? &bars.v_empty[st] : &bars.k_empty[st], again, gave_up);
+                    const uint32_t dst = (kv ? sv : sk) + st * L::kTile;
+                    const char* src = kv ? vb : kb;
+                    constexpr int kRows = 32 / CH;  // rows per instruction of a warp: 2 or 4
+#pragma unroll
+                    for (int i = 0; i < 32 / kRows; ++i) {
+                        const int rl = i * kRows + lane / CH, ch = lane % CH;
+                        const long long f = __shfl_sync(~0u, off, rl);
+                        const bool take = f >= 0 && ch < dch;
+                        const int r = lw * 32 + rl;
+                        if (ok)
+                            cp_async16(dst + (ch >> 3) * 16384 + r * 128 +
+                                           (((ch & 7) ^ (r & 7)) << 4),
+                                       src + (take ? f + ch * 16 : 0), take);
+                    }
+                    if (kv && tail) {
+                        // A masked entry may hold anything, but 0 times NaN is NaN: new tokens'
+                        // values that are not finite are zeroed here and added row by row.
+                        asm volatile("cp.async.wait_all;" ::: "memory");
+                        named_sync(2, 128);
+                        if (lt < 4) s_wild[st][lt] = 0;
+                        named_sync(2, 128);
+                        const int r = lt;  // a row per thread
+                        const long long slot = (long long)t * kTcUnit + r;
+                        if (slot > len && slot < total) {
+                            constexpr uint32_t e = std::is_same<T, __half>::value ? 0x7c00u
+                                                                                  : 0x7f80u;
+                            bool f = false;
+                            for (int ch = 0; ch < dch; ++ch) {
+                                uint32_t v[4];
+                                asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
+                                             : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3])
+                                             : "r"(dst + (ch >> 3) * 16384 + r * 128 +
+                                                   (((ch & 7) ^ (r & 7)) << 4)) : "memory");
+#pragma unroll
+                                for (int k = 0; k < 4; ++k)
+                                    f |= (v[k] & e) == e || (v[k] >> 16 & e) == e;
+                            }
+                            if (f) {
+                                atomicOr(&s_wild[st][r >> 5], 1u << (r & 31));
+                                for (int ch = 0; ch < CH; ++ch)
+                                    asm volatile("st.shared.v4.b32 [%0], {%1,%1,%1,%1};" ::"r"(
+                                        dst + (ch >> 3) * 16384 + r * 128 +
+                                        (((ch & 7) ^ (r & 7)) << 4)), "r"(0) : "memory");
+                            }
+                        }
+                        bar_arrive(&bars.v_full[st]);
+                    } else {
+                        bar_arrive_copies(kv ? &bars.v_full[st] : &bars.k_full[st]);
+                    }
+                }
+            }
+            ++pieces;
+        }
+        asm volatile("cp.async.wait_all;" ::: "memory");
+    } else if (w >= 12) {
+        // ------------------------------------------------ products
+        if (w == 12) {
+            constexpr uint32_t kPv = product<T>(DP, true);
+            constexpr uint32_t kPanel = DP > 64 ? 16384 : 1024;  // one panel: not used
+            // scores times the sign of the scale: the largest is then the one to look for
+            const uint32_t qk = product<T>(128, false) | (a.scale < 0.0f ? 1u << 13 : 0u);
+            long long tiles = 0;  // of earlier pieces
+            uint32_t pieces = 0, p_phase = 0;
+            bool ok = true;
+            while (ok && walk.next(a, ROWS, &p)) {
+                if (walk.sh.bad) continue;
+                const bool two = p.rows > 128;
+                const int nt = p.t1 - p.t0, jobs = two ? 2 * nt : nt;
+                ok = warp_wait(&bars.q_full, pieces & 1, gave_up);
+                // Job i belongs to stream i & 1.  Its scores take the place of the weights of job
+                // i - 2, whose product comes before them; products of one thread run in order.
+                // Scores go first, so that each stream's product and next scores are issued
+                // together and the streams take turns.
+                int ns = 0, np = 0, idle = 0;  // scores and outputs issued; polls in vain
+                uint64_t since = 0;
+                while (ok && np < jobs) {
+                    const int sst = ns & 1, pst = np & 1;
+                    const long long stile = tiles + (two ? ns >> 1 : ns);
+                    const long long ptile = tiles + (two ? np >> 1 : np);
+                    const int ks = (int)(stile % S), vs = (int)(ptile % S);
+                    if (ns < jobs && ns < np + 2 &&
+                        warp_test(&bars.k_full[ks], (uint32_t)(stile / S & 1))) {
+                        // the copies wrote through the generic proxy, the products read through
+                        // the asynchronous one
+                        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                        tc_after();
+                        const uint64_t qa = operand(sq + (two ? sst * L::kTile : 0), 16384);
+                        const uint64_t ka = operand(sk + ks * L::kTile, 16384);
+                        if (elect_one()) {
+#pragma unroll
+                            for (int k = 0; k < DP / 16; ++k) {
+                                // in 16 bytes: a panel, 16 elements of a row
+                                const uint64_t at = (k >> 2) * (16384 >> 4) + (k & 3) * 2;
+                                tc_mma(tmem + sst * 128, qa + at, ka + at, qk, k > 0);
+                            }
+                            tc_commit(&bars.s_full[sst]);
+                            if (!two || sst == 1) tc_commit(&bars.k_empty[ks]);
+                            if (ns == jobs - 1) tc_commit(&bars.q_empty);
+                        }
+                        __syncwarp();
+                        ++ns;
+                        idle = 0;
+                    } else if (np < ns && warp_test(&bars.p_full[pst], p_phase >> pst & 1) &&
+                               warp_test(&bars.v_full[vs], (uint32_t)(ptile / S & 1))) {
+                        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                        tc_after();
+                        const uint64_t va = operand(sv + vs * L::kTile, kPanel);
+                        const uint32_t sd = tmem + pst * 128, od = tmem + 256 + pst * DP;
+                        if (elect_one()) {
+#pragma unroll
+                            for (int k = 0; k < 8; ++k)
+                                tc_mma_t(od, sd + (k >> 1) * 32 + (k & 1) * 8, va + k * 128, kPv,
+                                         true);
+                            if constexpr (kLo) {
+#pragma unroll
+                                for (int k = 0; k < 8; ++k)
+                                    tc_mma_t(od, sd + (k >> 1) * 32 + 16 + (k & 1) * 8,
+                                             va + k * 128, kPv, true);
+                            }
+                            tc_commit(&bars.pv_done[pst]);
+                            if (!two || pst == 1) tc_commit(&bars.v_empty[vs]);
+                        }
+                        __syncwarp();
+                        p_phase ^= 1u << pst;
+                        ++np;
+                        idle = 0;
+                    } else if ((++idle & 63) == 0) {
+                        const uint64_t now = nanoseconds();
+                        if (idle == 64) since = now;
+                        ok = __all_sync(~0u, !*gave_up && now - since < kGiveUp);
+                        if (!ok) *gave_up = 1;
+                    }
+                }
+                tiles += nt;
+                ++pieces;
+            }
+            if (!ok) {  // products in flight end before the tensor memory goes back
+                volatile int none = 0;
+                if (elect_one()) tc_commit(&bars.drain);
+                __syncwarp();
+                warp_wait(&bars.drain, 0, &none);
+            }
+        }
+    } else {
+        // ------------------------------------------------ weights: a row per thread
+        const int st = w >> 2, r = tid & 127;
+        const uint32_t mine = tmem + ((uint32_t)(w & 3) * 32 << 16);
+        const uint32_t sc = mine + st * 128, oc = mine + 256 + st * DP;
+        uint32_t s_phase = 0, pv = 0;  // phases of the scores; products waited for
+        long long tiles = 0;
+        int pieces = 0, anc_of = -1;
+        bool tree_bad = false, ok = true;  // a wait that gave up skips the rest, not the barriers
+        while (walk.next(a, ROWS, &p)) {
+            const Share& sh = walk.sh;
+            const bool two = p.rows > 128;
+            const int row = two ? st * 128 + r : r, R = p.mt * ROWS + row;
+            const int j = min(R / a.group, sh.n - 1), g = R - R / a.group * a.group;
+            const bool live = row < p.rows;
+            T* out = (T*)a.out + (((long long)p.b * a.N + j) * a.q_heads + p.h * a.group + g) * c.dim;
+            if (sh.bad) {
+                if (tid == 0) mark(a.status, p.b, SV_DEV_BAD_LENGTH);
+                if (live && (two || st == 0))
+                    for (int d = 0; d < c.dim; ++d) out[d] = Conv<T>::from(NAN);
+                __syncwarp();
+                continue;
+            }
+            const int len = sh.len, nt = p.t1 - p.t0, jobs = two ? 2 * nt : nt;
+            if ((long long)p.t1 * kTcUnit > len && anc_of != p.b) {
+                named_sync(1, 256);
+                int f = 0;
+                if (a.parents && tid < sh.n) {
+                    const int q = a.parents[(long long)p.b * a.N + tid];
+                    s_par[tid] = q;
+                    f = tid > 0 && (q < 0 || q >= tid);
+                }
+                // any bad parent: every thread learns it from the barrier's reduction
+                asm volatile("{ .reg .pred p, q; setp.ne.b32 p, %1, 0; "
+                             "barrier.cta.red.or.pred q, 1, 256, p; selp.s32 %0, 1, 0, q; }"
+                             : "=r"(f) : "r"(f) : "memory");
+                if (tid < sh.n) {
+                    uint64_t m = 0;
+                    if (!a.parents)
+                        m = tid == 64 ? ~0ull : (1ull << tid) - 1;
+                    else if (!f)
+                        for (int i = tid; i > 0; i = s_par[i]) m |= 1ull << (i - 1);
+                    s_anc[tid] = m;
+                }
+                named_sync(1, 256);
+                anc_of = p.b;
+                tree_bad = f;
+                if (f && tid == 0) mark(a.status, p.b, SV_DEV_BAD_TREE);
+            }
+            const bool nan_rows = tree_bad && anc_of == p.b;
+            const uint64_t anc = anc_of == p.b ? s_anc[j] : 0;
+            const float unit = fabsf(a.scale) * 1.4426950408889634f;  // the products carry the sign
+            const bool busy = (two ? st * 128 : 0) + (w & 3) * 32 < p.rows;  // rows in this warp
+            float l = 0.0f, ref = -INFINITY;
+            int done = 0;  // jobs of this stream
+            // the outputs of the piece before have been read; this one's start at zero
+            ok = ok && warp_wait(&bars.epi_done, (pieces & 1) ^ 1, gave_up);
+            tc_after();
+            {
+                float zero[32];
+#pragma unroll
+                for (int e = 0; e < 32; ++e) zero[e] = 0.0f;
+#pragma unroll
+                for (int k = 0; k < DP; k += 32) tc_st32(oc + k, zero);
+                tc_wait_st();
+            }
+            for (int i = st; ok && i < jobs; i += 2, ++done) {
+                const int t = p.t0 + (two ? i >> 1 : i);
+                ok = warp_wait(&bars.s_full[st], s_phase, gave_up);
+                s_phase ^= 1;
+                if (!ok) break;
+                tc_after();
+                if (!busy) {  // rows that nothing comes of: any weights will do
+                    tc_before();
+                    bar_arrive(&bars.p_full[st]);
+                    continue;
+                }
+                const bool tail = (long long)(t + 1) * kTcUnit > len + 1;
+                uint32_t see[4];  // of the tile's slots, those that this row sees
+                if (tail) {
+                    const int rel = t * kTcUnit - len;  // slot 0 of the tile among the new tokens
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const int at = rel + 32 * k - 1;  // bit of anc for the word's first slot
+                        see[k] = at >= 64    ? 0u
+                                 : at >= 0   ? (uint32_t)(anc >> at)
+                                 : at > -32  ? (uint32_t)(anc << -at) | ((1u << -at) - 1)
+                                             : ~0u;
+                    }
+                }
+                // Once for the maximum, once for the weights: the scores stay in tensor memory
+                // rather than in 128 registers.
+                float top = -INFINITY;
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    float s[64];
+                    tc_ld32(s, sc + 64 * k);
+                    tc_ld32(s + 32, sc + 64 * k + 32);
+                    tc_wait_ld();
+                    if (tail) {
+#pragma unroll
+                        for (int e = 0; e < 64; ++e)
+                            if (!(see[2 * k + (e >> 5)] >> (e & 31) & 1)) s[e] = -INFINITY;
+                    }
+                    float m[4] = {s[0], s[1], s[2], s[3]};
+#pragma unroll
+                    for (int e = 4; e < 64; ++e) m[e & 3] = fmaxf(m[e & 3], s[e]);
+                    top = fmaxf(fmaxf(top, fmaxf(m[0], m[1])), fmaxf(m[2], m[3]));
+                }
+                const float mx = top == -INFINITY ? -INFINITY : top * unit;
+                // The reference follows the maximum only when that has grown by 2^8.
+                const bool grow = mx > ref + 8.0f;
+                bool waited = false;  // for the product before this one
+                if (__any_sync(~0u, grow)) {
+                    const float f = grow ? ex2(ref - mx) : 1.0f;
+                    if (grow) ref = mx;
+                    l *= f;
+                    if (done > 0) {
+                        ok = warp_wait(&bars.pv_done[st], (pv + done - 1) & 1, gave_up);
+                        waited = true;
+                        tc_after();
+#pragma unroll 1
+                        for (int k = 0; k < DP; k += 32) {
+                            float o[32];
+                            tc_ld32(o, oc + k);
+                            tc_wait_ld();
+#pragma unroll
+                            for (int e = 0; e < 32; ++e) o[e] *= f;
+                            tc_st32(oc + k, o);
+                        }
+                        tc_wait_st();
+                    }
+                }
+                const float less = ref == -INFINITY ? 0.0f : ref;
+                if (tail) {
+                    const long long tile = tiles + (two ? i >> 1 : i);
+                    const int vs = (int)(tile % S);
+                    ok = ok && warp_wait(&bars.v_full[vs], (uint32_t)(tile / S & 1), gave_up);
+#pragma unroll 1
+                    for (int sl = 0; ok && sl < 128; ++sl) {
+                        if (!(s_wild[vs][sl >> 5] >> (sl & 31) & 1)) continue;
+                        if (done > 0 && !waited) {
+                            ok = warp_wait(&bars.pv_done[st], (pv + done - 1) & 1, gave_up);
+                            waited = true;
+                            tc_after();
+                        }
+                        const int n = t * kTcUnit + sl - len;  // the new token, >= 1
+                        const float x = tc_ld1(sc + sl);
+                        tc_wait_ld();
+                        const bool mine_too = sees(anc, n);
+                        const float pw = mine_too ? ex2(x * unit - less) : 0.0f;
+                        const long long at = slot_offset(c, p.b, len + n);
+                        const T* v = (const T*)(c.v + (at < 0 ? 0 : at) + p.h * c.head_stride);
+#pragma unroll 1
+                        for (int k = 0; k < c.dim; k += 16) {
+                            float o[16];
+                            tc_ld16(o, oc + k);
+                            tc_wait_ld();
+                            if (mine_too && at >= 0) {
+#pragma unroll
+                                for (int e = 0; e < 16; ++e) o[e] += pw * Conv<T>::to(v[k + e]);
+                            }
+                            __syncwarp();
+                            tc_st16(oc + k, o);
+                            tc_wait_st();
+                        }
+                    }
+                }
+                // Weights take the place of their own scores: of 32 columns, 16 hold the high
+                // halves in pairs and 16 the low ones.
+                float sum[4] = {0, 0, 0, 0};
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    float x[32], y[16];
+                    tc_ld32(x, sc + 32 * k);
+                    tc_wait_ld();
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) x[e] = ex2(fmaf(x[e], unit, -less));
+                    if (tail) {
+#pragma unroll
+                        for (int e = 0; e < 32; ++e)
+                            if (!(see[k] >> e & 1)) x[e] = 0.0f;
+                    }
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) sum[e & 3] += x[e];
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) {
+                        const uint32_t h = pair<T>(x[2 * e], x[2 * e + 1]);
+                        y[e] = __uint_as_float(h);
+                        if constexpr (kLo) {
+                            const float2 f = unpair<T>(h);
+                            x[e] = __uint_as_float(pair<T>(x[2 * e] - f.x, x[2 * e + 1] - f.y));
+                        }
+                    }
+                    tc_st16(sc + 32 * k, y);
+                    if constexpr (kLo) tc_st16(sc + 32 * k + 16, x);
+                }
+                l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+                tc_wait_st();
+                tc_before();
+                bar_arrive(&bars.p_full[st]);
+            }
+            // the stream's last product
+            if (ok && done > 0) ok = warp_wait(&bars.pv_done[st], (pv + done - 1) & 1, gave_up);
+            pv += done;
+            tc_after();
+            bool nan_piece = nan_rows || s_bad_piece[pieces & 3] == pieces || !ok;
+            if (nan_piece && !nan_rows && ok && tid == 0) mark(a.status, p.b, SV_DEV_BAD_PAGE);
+            if (!ok && tid == 0) mark(a.status, p.b, SV_DEV_TIMEOUT);
+            const bool whole = p.t0 == 0 && p.t1 == sh.tiles;
+            float f0 = 1.0f, f1 = 0.0f;  // shares of the two streams where they are joined
+            if (!two) {
+                if (st == 1) s_ml[r] = make_float2(ref, l);
+                tc_before();
+                named_sync(1, 256);
+                tc_after();
+                if (st == 0 && jobs > 1) {
+                    const float2 o = s_ml[r];
+                    const float top = fmaxf(ref, o.x), less = top == -INFINITY ? 0.0f : top;
+                    f0 = ex2(ref - less);
+                    f1 = ex2(o.x - less);
+                    l = l * f0 + o.y * f1;
+                    ref = top;
+                }
+            }
+            if (two || st == 0) {
+                if (nan_piece) l = NAN;
+                const long long part = (2 * (long long)blockIdx.x + (p.t0 == 0 ? 1 : 0)) * ROWS + row;
+                const float inv = 1.0f / l;
+#pragma unroll 1
+                for (int k = 0; k < DP; k += 32) {
+                    float o[32];
+                    tc_ld32(o, oc + k);
+                    tc_wait_ld();
+                    if (!two) {
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) o[e] *= f0;
+                        if (jobs > 1) {
+                            float y[32];
+                            tc_ld32(y, oc + DP + k);
+                            tc_wait_ld();
+#pragma unroll
+                            for (int e = 0; e < 32; ++e) o[e] += y[e] * f1;
+                        }
+                    }
+                    if (live && !whole) {
+#pragma unroll
+                        for (int e = 0; e < 32; e += 4)
+                            *reinterpret_cast<float4*>(a.part_o + part * DP + k + e) =
+                                make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+                    } else if (live) {
+#pragma unroll
+                        for (int e = 0; e < 32; e += 8) {
+                            if (k + e >= c.dim) continue;
+                            uint32_t y[4];
+#pragma unroll
+                            for (int q = 0; q < 4; ++q)
+                                y[q] = pair<T>(o[e + 2 * q] * inv, o[e + 2 * q + 1] * inv);
+                            *reinterpret_cast<uint4*>(out + k + e) = make_uint4(y[0], y[1], y[2], y[3]);
+                        }
+                    }
+                    __syncwarp();
+                }
+                if (live && !whole) a.part_ml[part] = make_float2(ref, l);
+            }
+            tc_before();
+            bar_arrive(&bars.epi_done);
+            tiles += nt;
+            ++pieces;
+        }
+    }
+    tc_before();
+    __syncthreads();
+    tc_after();
+    if (w == 12)
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512));
+}
+
 // Adds up the pieces of the items that more than one range holds: sum over pieces of
 // 2^(m - max) (o, l), then o / l.  A CTA of four warps per four rows of an item (a warp each), or
 // per row (the warps share its pieces) where the host expects many pieces per item.
 template <typename T, int DP>
-__global__ void __launch_bounds__(128) kv_join_kernel(const AttentionArgs a, int rows, int mts_max,
-                                                      int warps) {
+__global__ void __launch_bounds__(128) kv_join_kernel(const AttentionArgs a, int rows, int unit,
+                                                      int mts_max, int warps) {
     __shared__ float4 s_o[4][DP / 4];
     const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
     const Cache& c = a.c;
     cudaGridDependencySynchronize();
     const int mt = blockIdx.x % mts_max, bh = blockIdx.x / mts_max;
     const int h = bh % c.heads, b = bh / c.heads;
-    const Share sh = share_of(a, b, rows);
+    const Share sh = share_of(a, b, rows, unit);
     if (mt >= sh.mts) return;
     const long long W = a.prefix[a.B];
     const long long from = a.prefix[b] + (long long)(h * sh.mts + mt) * sh.tiles;
@@ -1056,9 +1821,34 @@ static auto with_split(sv_dtype dtype, sv_dtype cache, int dim, int rows, F f) {
     return cache == SV_E4M3 ? sized(__half(), __nv_fp8_e4m3()) : sized(__half(), __half());
 }
 
-// Shared memory of every split kernel, once per device.
-static cudaError_t split_setup() {
+// The same for the wide kernel: tiles of 128 rows, or of two times 128.
+template <typename F> static auto with_wide(sv_dtype dtype, int dim, int rows, F f) {
+    auto sized = [&](auto t) {
+        using T = decltype(t);
+        if (dim <= 64)
+            return rows <= 128 ? f(kv_wide_kernel<T, 64, 128>, kv_join_kernel<T, 64>,
+                                   Tc<64, 128>::kSmem)
+                               : f(kv_wide_kernel<T, 64, 256>, kv_join_kernel<T, 64>,
+                                   Tc<64, 256>::kSmem);
+        return rows <= 128 ? f(kv_wide_kernel<T, 128, 128>, kv_join_kernel<T, 128>,
+                               Tc<128, 128>::kSmem)
+                           : f(kv_wide_kernel<T, 128, 256>, kv_join_kernel<T, 128>,
+                               Tc<128, 256>::kSmem);
+    };
+    return dtype == SV_BF16 ? sized(__nv_bfloat16()) : sized(__half());
+}
+
+// Shared memory of every attention kernel, once per device.
+static cudaError_t attention_setup() {
     cudaError_t e = cudaSuccess;
+    for (sv_dtype t : {SV_BF16, SV_F16})
+        for (int dim : {64, 128})
+            for (int rows : {128, 256})
+                if (e == cudaSuccess)
+                    e = with_wide(t, dim, rows, [](auto k, auto, int smem) {
+                        return cudaFuncSetAttribute(
+                            k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+                    });
     for (sv_dtype t : {SV_BF16, SV_F16})
         for (bool f8 : {false, true})
             for (int dim : {64, 128})
@@ -1088,7 +1878,7 @@ static sv_status device_ok(int* sms) {
         if (major == 10 && minor == 3 &&
             cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
             return SV_ERR_CUDA;
-        if (n > 0 && split_setup() != cudaSuccess) return SV_ERR_CUDA;
+        if (n > 0 && attention_setup() != cudaSuccess) return SV_ERR_CUDA;
         known[dev] = n;
     }
     if (known[dev] < 0) return SV_ERR_UNSUPPORTED;
@@ -1096,14 +1886,17 @@ static sv_status device_ok(int* sms) {
     return SV_OK;
 }
 
-// The workspace: units before each sequence, then two pieces of up to 32 rows per CTA.
+// The workspace: units before each sequence, then two pieces of a row tile per CTA.
 struct AttentionWs { size_t part_o, part_ml, bytes; };
-static AttentionWs attention_ws(int B, int dim) {
-    const size_t dp = dim <= 64 ? 64 : 128, rows = (size_t)2 * kMaxCtas * 32;
+static AttentionWs attention_ws(int B, int rows, int dim) {
+    const size_t dp = dim <= 64 ? 64 : 128;
+    const size_t split = (size_t)2 * kMaxCtas * (rows <= 16 ? 16 : 32);
+    const size_t wide = rows <= 32 ? 0 : (size_t)2 * kTcMaxCtas * (rows <= 128 ? 128 : 256);
+    const size_t held = split > wide ? split : wide;
     AttentionWs l;
     l.part_o = ((size_t)(B + 1) * 8 + 255) / 256 * 256;
-    l.part_ml = l.part_o + rows * dp * 4;
-    l.bytes = l.part_ml + rows * 8;
+    l.part_ml = l.part_o + held * dp * 4;
+    l.bytes = l.part_ml + held * 8;
     return l;
 }
 
@@ -1258,7 +2051,7 @@ size_t spec_kv_attention_workspace_size(int B, int N, int q_heads, int heads, in
     if (B < 0 || B > kMaxB || N < 1 || N > kMaxN || heads < 1 || q_heads < 1 || q_heads % heads ||
         q_heads > kMaxQHeads || dim < 16 || dim > kMaxDim || dim % 16)
         return 0;
-    return attention_ws(B, dim).bytes;
+    return attention_ws(B, N * (q_heads / heads), dim).bytes;
 }
 
 sv_status spec_kv_attention(const sv_kv_cache* cache, const void* q, const sv_strides* q_strides,
@@ -1293,14 +2086,19 @@ sv_status spec_kv_attention(const sv_kv_cache* cache, const void* q, const sv_st
     a.q_heads = q_heads;
     a.group = q_heads / cache->heads;
     a.B = B;
-    const int rows = N * a.group, tile = rows <= 16 ? 16 : 32;
+    // Few rows: mma.sync, which then waits for memory only.  More: tcgen05.
+    const int rows = N * a.group;
+    const bool wide = rows > 32 && cache->dtype != SV_E4M3;
+    const int tile = wide ? (rows <= 128 ? 128 : 256) : rows <= 16 ? 16 : 32;
+    const int unit = wide ? kTcUnit : kUnit;
     const int mts = (rows + tile - 1) / tile;
     if ((long double)B * cache->heads * mts *
-            ((double)cache->table_width * cache->page_size / kUnit + 1) >= (long double)(1ll << 50))
+            ((double)cache->table_width * cache->page_size / unit + 1) >= (long double)(1ll << 50))
         return SV_ERR_UNSUPPORTED;
     if ((long long)B * cache->heads * mts >= (1ll << 31)) return SV_ERR_UNSUPPORTED;  // grid size
-    a.ctas = 2 * sms < kMaxCtas ? 2 * sms : kMaxCtas;
-    const AttentionWs l = attention_ws(B, cache->dim);
+    const int most = wide ? kTcMaxCtas : kMaxCtas, fit = wide ? sms : 2 * sms;
+    a.ctas = fit < most ? fit : most;
+    const AttentionWs l = attention_ws(B, rows, cache->dim);
     a.prefix = (long long*)ws;
     a.part_o = (float*)((char*)ws + l.part_o);
     a.part_ml = (float2*)((char*)ws + l.part_ml);
@@ -1309,22 +2107,23 @@ sv_status spec_kv_attention(const sv_kv_cache* cache, const void* q, const sv_st
     cudaLaunchAttribute pdl;
     pdl.id = cudaLaunchAttributeProgrammaticStreamSerialization;
     pdl.val.programmaticStreamSerializationAllowed = 1;
-    const cudaError_t e = with_split(dtype, cache->dtype, cache->dim, rows, [&](auto split, auto join,
-                                                                               int smem) {
+    auto launch = [&](auto kernel, auto join, int smem) {
         cudaLaunchConfig_t cfg = {};
         cfg.gridDim = dim3(a.ctas);
-        cfg.blockDim = dim3(kSplitThreads);
+        cfg.blockDim = dim3(wide ? kTcThreads : kSplitThreads);
         cfg.dynamicSmemBytes = smem;
         cfg.stream = stream;
         cfg.attrs = &pdl;
         cfg.numAttrs = 1;
-        cudaError_t r = cudaLaunchKernelEx(&cfg, split, a);
+        cudaError_t r = cudaLaunchKernelEx(&cfg, kernel, a);
         if (r != cudaSuccess) return r;
         cfg.gridDim = dim3(B * cache->heads * mts, warps == 4 ? tile : tile / 4);
         cfg.blockDim = dim3(128);
         cfg.dynamicSmemBytes = 0;
-        return cudaLaunchKernelEx(&cfg, join, a, tile, mts, warps);
-    });
+        return cudaLaunchKernelEx(&cfg, join, a, tile, unit, mts, warps);
+    };
+    const cudaError_t e = wide ? with_wide(dtype, cache->dim, rows, launch)
+                               : with_split(dtype, cache->dtype, cache->dim, rows, launch);
     return e == cudaSuccess ? SV_OK : SV_ERR_CUDA;
 }
 

@@ -24,7 +24,7 @@ import torch
 from . import specverify as sv
 
 SV_F16, SV_E4M3 = 2, 3
-SV_DEV_BAD_PAGE, SV_DEV_BAD_LENGTH = 0x80, 0x100
+SV_DEV_BAD_PAGE, SV_DEV_BAD_LENGTH, SV_DEV_TIMEOUT = 0x80, 0x100, 0x200
 
 EXPORTS = ("spec_kv_rope_turns", "spec_kv_append", "spec_kv_attention_workspace_size",
            "spec_kv_attention", "spec_kv_commit")
