@@ -4,6 +4,8 @@
 
 #include "specverify_kv.h"
 
+#include <cuda.h>
+#include <cudaTypedefs.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
@@ -303,6 +305,86 @@ __device__ __forceinline__ int range_of(long long W, int P, long long x) {
     return (int)(((x + 1) * P - 1) / W);
 }
 
+// A CTA's range as pieces of items, in order: sequence, key head, row tile, units t0 .. t1 - 1.
+struct Piece {
+    int b, h, mt, t0, t1, rows;
+};
+struct Walk {
+    long long left;  // units of the range still to come
+    int b, item, t0;
+    Share sh;
+    __device__ __forceinline__ bool next(const AttentionArgs& a, int rows, int unit, Piece* p) {
+        if (left <= 0) return false;
+        while (item >= a.c.heads * sh.mts) {
+            sh = share_of(a, ++b, rows, unit);
+            item = 0;
+        }
+        p->b = b;
+        p->h = item / sh.mts;
+        p->mt = item - p->h * sh.mts;
+        p->t0 = t0;
+        p->t1 = (int)min((long long)sh.tiles, t0 + left);
+        p->rows = min(rows, sh.n * a.group - p->mt * rows);
+        left -= p->t1 - t0;
+        ++item;
+        t0 = 0;
+        return true;
+    }
+};
+struct Start {
+    long long at;
+    int b;
+};
+
+// The range of this CTA: units before each sequence (a scan over the batch; CTA 0 leaves it for
+// the join), their sum W, range blockIdx.x of the min(ctas, W) that W is cut into.
+template <int THREADS>
+__device__ __forceinline__ Walk start_walk(const AttentionArgs& a, int rows, int unit,
+                                           long long* s_scan, Start* s_start) {
+    const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
+    const int per = (a.B + THREADS - 1) / THREADS;
+    const int b0 = min(a.B, tid * per), b1 = min(a.B, b0 + per);
+    long long sum = 0;
+    for (int b = b0; b < b1; ++b) sum += share_of(a, b, rows, unit).units(a.c.heads);
+    long long inc = sum;
+    for (int k = 1; k < 32; k <<= 1) {
+        const long long y = __shfl_up_sync(~0u, inc, k);
+        if (lane >= k) inc += y;
+    }
+    if (lane == 31) s_scan[w] = inc;
+    __syncthreads();
+    long long W = 0, before = inc - sum;
+    for (int i = 0; i < THREADS / 32; ++i) {
+        W += s_scan[i];
+        if (i < w) before += s_scan[i];
+    }
+    const int P = ranges_of(W, a.ctas);
+    const bool some = W > 0 && (int)blockIdx.x < P;
+    const long long x = some ? range_start(W, P, blockIdx.x) : 0;
+    const bool here = some && x >= before && x < before + sum;
+    if (blockIdx.x == 0 || here) {
+        long long at = before;
+        for (int b = b0; b < b1; ++b) {
+            const long long u = share_of(a, b, rows, unit).units(a.c.heads);
+            if (here && x >= at && x < at + u) *s_start = Start{at, b};
+            if (blockIdx.x == 0) a.prefix[b] = at;
+            at += u;
+        }
+        if (blockIdx.x == 0 && tid == 0) a.prefix[a.B] = W;
+    }
+    __syncthreads();
+    Walk k = {};
+    if (some) {
+        k.left = range_start(W, P, blockIdx.x + 1) - x;
+        k.b = s_start->b;
+        k.sh = share_of(a, k.b, rows, unit);
+        const long long r = x - s_start->at;
+        k.item = (int)(r / k.sh.tiles);
+        k.t0 = (int)(r - (long long)k.item * k.sh.tiles);
+    }
+    return k;
+}
+
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool take) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
                  "r"(take ? 16 : 0));
@@ -349,6 +431,27 @@ template <typename M> __device__ __forceinline__ float2 unpair(uint32_t w) {
         return __half22float2(reinterpret_cast<const __half2&>(w));
     else
         return __bfloat1622float2(reinterpret_cast<const __nv_bfloat162&>(w));
+}
+// The high half of a pair that a low half will make up for: bf16 by leaving off bits.
+template <typename M> __device__ __forceinline__ uint32_t cut(float x, float y) {
+    if constexpr (std::is_same<M, __half>::value) return pair<M>(x, y);
+    else return __byte_perm(__float_as_uint(x), __float_as_uint(y), 0x7632);
+}
+// Two fp32 operations in one instruction.
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+    float2 d;
+    asm("{ .reg .b64 a, b, c; mov.b64 a, {%2, %3}; mov.b64 b, {%4, %5}; mov.b64 c, {%6, %7}; "
+        "fma.rn.f32x2 a, a, b, c; mov.b64 {%0, %1}, a; }"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+    return d;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+    float2 d;
+    asm("{ .reg .b64 a, b; mov.b64 a, {%2, %3}; mov.b64 b, {%4, %5}; "
+        "add.rn.f32x2 a, a, b; mov.b64 {%0, %1}, a; }"
+        : "=f"(d.x), "=f"(d.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return d;
 }
 // Two e4m3 bytes (the low half of w) as two halves: exact.
 __device__ __forceinline__ uint32_t widen(uint32_t w) {
@@ -402,8 +505,8 @@ __global__ void __launch_bounds__(kSplitThreads, 2) kv_split_kernel(const Attent
     constexpr int S = St::kStages, KS = DP / 16, NT = DP / 8, ROWS = MI * 16;
     extern __shared__ __align__(128) char smem[];
     __shared__ long long s_scan[4];
-    __shared__ long long s_start;
-    __shared__ int s_b, s_par[kMaxN];
+    __shared__ Start s_start;
+    __shared__ int s_par[kMaxN];
     __shared__ uint64_t s_anc[kMaxN];
     const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5, t4 = lane & 3;
     const Cache& c = a.c;
@@ -411,57 +514,15 @@ __global__ void __launch_bounds__(kSplitThreads, 2) kv_split_kernel(const Attent
     cudaGridDependencySynchronize();
     cudaTriggerProgrammaticLaunchCompletion();
 
-    // Units before each sequence (a scan over the batch), the total, and where this range starts.
-    long long W, x0, x1;
-    {
-        const int per = (a.B + kSplitThreads - 1) / kSplitThreads;
-        const int b0 = min(a.B, tid * per), b1 = min(a.B, b0 + per);
-        long long sum = 0;
-        for (int b = b0; b < b1; ++b) sum += share_of(a, b, ROWS, kUnit).units(c.heads);
-        long long inc = sum;
-        for (int k = 1; k < 32; k <<= 1) {
-            const long long y = __shfl_up_sync(~0u, inc, k);
-            if (lane >= k) inc += y;
-        }
-        if (lane == 31) s_scan[w] = inc;
-        __syncthreads();
-        W = s_scan[0] + s_scan[1] + s_scan[2] + s_scan[3];
-        long long before = inc - sum;
-        for (int i = 0; i < w; ++i) before += s_scan[i];
-        const int P = ranges_of(W, a.ctas);
-        x0 = (int)blockIdx.x < P ? range_start(W, P, blockIdx.x) : W;
-        x1 = (int)blockIdx.x < P ? range_start(W, P, blockIdx.x + 1) : W;
-        long long at = before;
-        if (blockIdx.x == 0 || (x0 >= before && x0 < before + sum)) {
-            for (int b = b0; b < b1; ++b) {
-                const long long u = share_of(a, b, ROWS, kUnit).units(c.heads);
-                if (x0 >= at && x0 < at + u) s_b = b, s_start = at;
-                if (blockIdx.x == 0) a.prefix[b] = at;
-                at += u;
-            }
-            if (blockIdx.x == 0 && tid == 0) a.prefix[a.B] = W;
-        }
-        __syncthreads();
-    }
-    if (x0 >= x1) return;
-
-    int b = s_b;
-    long long base = s_start;  // units before sequence b
-    Share sh = share_of(a, b, ROWS, kUnit);
+    Walk walk = start_walk<kSplitThreads>(a, ROWS, kUnit, s_scan, &s_start);
+    const Share& sh = walk.sh;
     const uint32_t ring = (uint32_t)__cvta_generic_to_shared(smem) + w * S * St::kBytes;
     int anc_of = -1;  // the sequence whose ancestors s_anc holds
 
-    for (long long x = x0; x < x1;) {
-        while (x >= base + sh.units(c.heads)) {
-            base += sh.units(c.heads);
-            sh = share_of(a, ++b, ROWS, kUnit);
-        }
-        const long long r = x - base;
-        const int item = (int)(r / sh.tiles), t0 = (int)(r - (long long)item * sh.tiles);
-        const int h = item / sh.mts, mt = item - h * sh.mts;
-        const int t1 = (int)min((long long)sh.tiles, t0 + (x1 - x));
-        const int len = sh.len, total = len + sh.n, rows = min(ROWS, sh.n * a.group - mt * ROWS);
-        x += t1 - t0;
+    Piece piece;
+    while (walk.next(a, ROWS, kUnit, &piece)) {
+        const int b = piece.b, h = piece.h, mt = piece.mt, t0 = piece.t0, t1 = piece.t1;
+        const int len = sh.len, total = len + sh.n, rows = piece.rows;
         bool bad = sh.bad;
         if (bad && tid == 0) mark(a.status, b, SV_DEV_BAD_LENGTH);
 
@@ -891,9 +952,9 @@ __global__ void __launch_bounds__(kSplitThreads, 2) kv_split_kernel(const Attent
 //
 // With more query rows per key head than mma.sync keeps up with, the products run on tcgen05.mma:
 // 128 rows by 128 slots, scores, weights and outputs in tensor memory.  One CTA per SM; its warps
-// have roles: 4 load keys and values (16-byte asynchronous copies through the page table into
-// 128-byte-swizzled panels of 64 elements), one thread issues the products, 2 x 4 hold one query
-// row per thread and turn scores into weights.  Two streams of scores alternate on the tensor
+// have roles: one loads keys and one values (TMA, a box per page and panel of 64 elements, which
+// swizzles rows of 128 bytes), two queries, one issues the products, 2 x 4 hold one query row per
+// thread and turn scores into weights.  Two streams of scores alternate on the tensor
 // pipe, so that one is multiplied while the other is exponentiated: two tiles of 128 rows over
 // the same slots, or, when the rows fit one tile, every other 128 slots of it (joined at the
 // end).  Work is cut into ranges and joined as for the split kernel, in units of 128 slots.
@@ -905,13 +966,16 @@ constexpr int kTcMaxCtas = 152;
 template <int DP, int ROWS> struct Tc {
     static constexpr int kTile = 128 * DP * 2;          // bytes of 128 keys, values or queries
     static constexpr int kQ = ROWS / 128 * kTile;
-    static constexpr int kFit = (224 * 1024 - kQ) / (2 * kTile);  // the static part: below 3 KiB
-    static constexpr int kStages = kFit > 6 ? 6 : kFit;  // of keys and values each
-    static constexpr int kSmem = kQ + 2 * kStages * kTile;
+    // Stages: what fits beside the queries (the static part stays below 3 KiB), the odd one for
+    // keys, which are wanted first.
+    static constexpr int kFit = (224 * 1024 - kQ) / kTile;
+    static constexpr int kK = kFit >= 12 ? 6 : (kFit + 1) / 2;
+    static constexpr int kV = kFit >= 12 ? 6 : kFit / 2;
+    static constexpr int kSmem = kQ + (kK + kV) * kTile;
 };
 
 struct TcBars {
-    uint64_t q_full, q_empty, epi_done, drain;
+    uint64_t q_full, q_empty, epi_done, drain, v_land;
     uint64_t k_full[6], k_empty[6], v_full[6], v_empty[6];
     uint64_t s_full[2], p_full[2], pv_done[2];
 };
@@ -924,6 +988,19 @@ __device__ __forceinline__ void bar_init(uint64_t* bar, int count) {
 }
 __device__ __forceinline__ void bar_arrive(uint64_t* bar) {
     asm volatile("mbarrier.arrive.shared.b64 _, [%0];" ::"r"(saddr(bar)) : "memory");
+}
+// Arrives, expecting so many bytes of bulk copies besides.
+__device__ __forceinline__ void bar_expect(uint64_t* bar, uint32_t bytes) {
+    asm volatile("mbarrier.arrive.expect_tx.shared.b64 _, [%0], %1;" ::"r"(saddr(bar)), "r"(bytes)
+                 : "memory");
+}
+// One box of the cache: 64 elements from x of head h in slots from s on of page p.
+__device__ __forceinline__ void tma_page(uint32_t dst, const CUtensorMap* map, int x, int h, int s,
+                                         int p, uint64_t* bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
+        "[%0], [%1, {%2, %3, %4, %5}], [%6];"
+        ::"r"(dst), "l"(map), "r"(x), "r"(h), "r"(s), "r"(p), "r"(saddr(bar)) : "memory");
 }
 // Arrives when this thread's asynchronous copies so far have landed.
 __device__ __forceinline__ void bar_arrive_copies(uint64_t* bar) {
@@ -1065,63 +1142,35 @@ __device__ __forceinline__ bool elect_one() {
     return yes != 0;
 }
 
-// A piece of an item, in the order in which every role walks the CTA's range.
-struct Piece {
-    int b, h, mt, t0, t1, rows;
-};
-struct Walk {
-    long long x, x1, base;
-    int b;
-    Share sh;
-    __device__ bool next(const AttentionArgs& a, int tile_rows, Piece* p) {
-        if (x >= x1) return false;
-        while (x >= base + sh.units(a.c.heads)) {
-            base += sh.units(a.c.heads);
-            sh = share_of(a, ++b, tile_rows, kTcUnit);
-        }
-        const long long r = x - base;
-        const int item = (int)(r / sh.tiles);
-        p->b = b;
-        p->t0 = (int)(r - (long long)item * sh.tiles);
-        p->h = item / sh.mts;
-        p->mt = item - p->h * sh.mts;
-        p->t1 = (int)min((long long)sh.tiles, p->t0 + (x1 - x));
-        p->rows = min(tile_rows, sh.n * a.group - p->mt * tile_rows);
-        x += p->t1 - p->t0;
-        return true;
-    }
-};
-
 template <typename T, int DP, int ROWS>
-__global__ void __launch_bounds__(kTcThreads, 1) kv_wide_kernel(const AttentionArgs a) {
+__global__ void __launch_bounds__(kTcThreads, 1)
+    kv_wide_kernel(const AttentionArgs a, const __grid_constant__ CUtensorMap kmap,
+                   const __grid_constant__ CUtensorMap vmap) {
     using L = Tc<DP, ROWS>;
-    constexpr int S = L::kStages, CH = DP / 8;
+    constexpr int SK = L::kK, SV = L::kV, CH = DP / 8;
     // Weights in two halves (P = hi + lo) where the tensor pipe waits for memory anyway.
     constexpr bool kLo = ROWS == 128;
     extern __shared__ __align__(1024) char smem_tc[];  // the swizzle counts from 1024
     __shared__ TcBars bars;
     __shared__ long long s_scan[kTcThreads / 32];
-    __shared__ long long s_start;
-    __shared__ int s_b, s_gave_up, s_bad_piece[4], s_par[kMaxN];
+    __shared__ Start s_start;
+    __shared__ int s_gave_up, s_bad_piece[8], s_par[kMaxN];
     __shared__ uint64_t s_anc[kMaxN];
     __shared__ uint32_t s_tmem, s_wild[6][4];
     __shared__ float2 s_ml[128];
     const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
     const Cache& c = a.c;
     const uint32_t sq = saddr(smem_tc);  // queries, then stages of k, then of v
-    const uint32_t sk = sq + L::kQ, sv = sk + S * L::kTile;
+    const uint32_t sk = sq + L::kQ, sv = sk + SK * L::kTile;
 
     if (tid == 0) {
-        bar_init(&bars.q_full, 128);
+        bar_init(&bars.q_full, 64);
         bar_init(&bars.q_empty, 1);
         bar_init(&bars.drain, 1);
         bar_init(&bars.epi_done, 256);
-        for (int i = 0; i < S; ++i) {
-            bar_init(&bars.k_full[i], 128);
-            bar_init(&bars.k_empty[i], 1);
-            bar_init(&bars.v_full[i], 128);
-            bar_init(&bars.v_empty[i], 1);
-        }
+        bar_init(&bars.v_land, 1);
+        for (int i = 0; i < SK; ++i) bar_init(&bars.k_full[i], 1), bar_init(&bars.k_empty[i], 1);
+        for (int i = 0; i < SV; ++i) bar_init(&bars.v_full[i], 1), bar_init(&bars.v_empty[i], 1);
         for (int i = 0; i < 2; ++i) {
             bar_init(&bars.s_full[i], 1);
             bar_init(&bars.p_full[i], 128);
@@ -1130,7 +1179,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv_wide_kernel(const AttentionA
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         s_gave_up = 0;
     }
-    if (tid < 4) s_bad_piece[tid] = -1;
+    if (tid < 8) s_bad_piece[tid] = -1;
     if (w == 12) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;"
                      ::"r"(saddr(&s_tmem)), "r"(512) : "memory");
@@ -1139,154 +1188,128 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv_wide_kernel(const AttentionA
     cudaGridDependencySynchronize();
     cudaTriggerProgrammaticLaunchCompletion();
 
-    Walk walk;
-    {
-        const int per = (a.B + kTcThreads - 1) / kTcThreads;
-        const int b0 = min(a.B, tid * per), b1 = min(a.B, b0 + per);
-        long long sum = 0;
-        for (int b = b0; b < b1; ++b) sum += share_of(a, b, ROWS, kTcUnit).units(c.heads);
-        long long inc = sum;
-        for (int k = 1; k < 32; k <<= 1) {
-            const long long y = __shfl_up_sync(~0u, inc, k);
-            if (lane >= k) inc += y;
-        }
-        if (lane == 31) s_scan[w] = inc;
-        tc_before();
-        __syncthreads();
-        tc_after();
-        long long W = 0, before = inc - sum;
-        for (int i = 0; i < kTcThreads / 32; ++i) {
-            W += s_scan[i];
-            if (i < w) before += s_scan[i];
-        }
-        const int P = ranges_of(W, a.ctas);
-        walk.x = (int)blockIdx.x < P ? range_start(W, P, blockIdx.x) : W;
-        walk.x1 = (int)blockIdx.x < P ? range_start(W, P, blockIdx.x + 1) : W;
-        if (blockIdx.x == 0 || (walk.x >= before && walk.x < before + sum)) {
-            long long at = before;
-            for (int b = b0; b < b1; ++b) {
-                const long long u = share_of(a, b, ROWS, kTcUnit).units(c.heads);
-                if (walk.x >= at && walk.x < at + u) s_b = b, s_start = at;
-                if (blockIdx.x == 0) a.prefix[b] = at;
-                at += u;
-            }
-            if (blockIdx.x == 0 && tid == 0) a.prefix[a.B] = W;
-        }
-        __syncthreads();
-        walk.b = walk.x < walk.x1 ? s_b : 0;
-        walk.base = walk.x < walk.x1 ? s_start : 0;
-        walk.sh = share_of(a, walk.b, ROWS, kTcUnit);
-    }
+    tc_before();
+    Walk walk = start_walk<kTcThreads>(a, ROWS, kTcUnit, s_scan, &s_start);
+    tc_after();
     const uint32_t tmem = s_tmem;
     volatile int* gave_up = &s_gave_up;
     Piece p;
 
     if (w >= 8 && w < 12) {
-        // ------------------------------------------------ loads
-        const int lt = tid - 256, lw = lt >> 5;
-        const int dch = c.dim / 8;
-        long long tile = 0;
-        int pieces = 0;
+        // ------------------------------------------------ loads: a warp keys, a warp values
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+        const bool vals = w > 8;  // warps 10 and 11 only help to look values through
+        const int lt = tid - 288, stages = vals ? SV : SK;
+        const CUtensorMap* const map = vals ? &vmap : &kmap;
+        // A page is one box per panel (its first 128 slots where it is larger): this lane's page
+        // of a tile.
+        const int shift = min(c.page_shift, 7), boxes = kTcUnit >> shift;
+        const uint32_t bytes = (128u << shift) * (DP / 64);  // per page
+        int pieces = 0, st = 0;
+        uint32_t again = 1, landed = 0;  // parities: the stage's last release; tails landed
         bool ok = true;  // once a wait gave up: no more copies, the barriers among the warps stay
-        while (walk.next(a, ROWS, &p)) {
+        while (walk.next(a, ROWS, kTcUnit, &p)) {
             if (walk.sh.bad) continue;
             const int len = walk.sh.len, total = len + walk.sh.n;
-            // queries: rows of the item, zeros past them
-            ok = ok && warp_wait(&bars.q_empty, (pieces & 1) ^ 1, gave_up);
-            for (int i = lt; ok && i < ROWS * CH; i += 128) {
-                const int row = i / CH, ch = i % CH, R = p.mt * ROWS + row;
-                const bool take = row < p.rows && ch < dch;
-                const int j = R / a.group, g = R - j * a.group;
-                const T* q = (const T*)a.q + (take ? p.b * a.qb + j * a.qt +
-                                  (long long)(p.h * a.group + g) * a.qh + ch * 8 : 0);
-                const int r = row & 127;
-                cp_async16(sq + (row >> 7) * L::kTile + (ch >> 3) * 16384 + r * 128 +
-                               (((ch & 7) ^ (r & 7)) << 4), q, take);
-            }
-            bar_arrive_copies(&bars.q_full);
-
-            const char* kb = c.k + p.h * c.head_stride;
-            const char* vb = c.v + p.h * c.head_stride;
             const int32_t* table = c.table + (long long)p.b * c.table_width;
-            // this lane looks up row 32 lw + lane of a tile
             auto page_of = [&](int t) -> int {
-                const long long s = (long long)t * kTcUnit + lw * 32 + lane;
-                return t < p.t1 && s < total ? __ldg(table + (s >> c.page_shift)) : -1;
+                const long long s = (long long)t * kTcUnit + ((long long)lane << shift);
+                return w < 10 && lane < boxes && t < p.t1 && s < total
+                           ? __ldg(table + (s >> c.page_shift)) : -1;
             };
             int page = page_of(p.t0);
-            for (int t = p.t0; t < p.t1; ++t, ++tile) {
-                const long long s = (long long)t * kTcUnit + lw * 32 + lane;
-                long long off = -1;
-                if (s < total) {
-                    if ((unsigned)page < (unsigned)c.num_pages)
-                        off = page * c.page_stride +
-                              (s & ((1 << c.page_shift) - 1)) * c.slot_stride;
-                    else
-                        s_bad_piece[pieces & 3] = pieces;
-                }
-                page = page_of(t + 1);
-                const int st = (int)(tile % S);
-                const uint32_t again = (uint32_t)(tile / S & 1) ^ 1;
-                const bool tail = (long long)(t + 1) * kTcUnit > len + 1;
-#pragma unroll 1
-                for (int kv = 0; kv < 2; ++kv) {
-                    ok = ok && warp_wait(kv ? &bars.v_empty[st] : &bars.k_empty[st], again, gave_up);
-                    const uint32_t dst = (kv ? sv : sk) + st * L::kTile;
-                    const char* src = kv ? vb : kb;
-                    constexpr int kRows = 32 / CH;  // rows per instruction of a warp: 2 or 4
+            for (int t = p.t0; t < p.t1; ++t) {
+                const long long s = (long long)t * kTcUnit + ((long long)lane << shift);
+                const uint32_t dst = (vals ? sv : sk) + st * L::kTile;
+                const bool tail = vals && (long long)(t + 1) * kTcUnit > len + 1;
+                uint64_t* const full = tail ? &bars.v_land : vals ? &bars.v_full[st] : &bars.k_full[st];
+                if (w < 10) {
+                    const bool want = lane < boxes && s < total;
+                    const bool good = want && (unsigned)page < (unsigned)c.num_pages;
+                    if (want && !good) s_bad_piece[pieces & 7] = pieces;
+                    const int pg = page;
+                    page = page_of(t + 1);
+                    ok = ok && warp_wait(vals ? &bars.v_empty[st] : &bars.k_empty[st], again, gave_up);
+                    const uint32_t n = __popc(__ballot_sync(~0u, good));
+                    if (ok) {
+                        if (lane == 0) bar_expect(full, n * bytes);
+                        __syncwarp();
+                        if (good) {
+                            const int slot = (int)(s & ((1 << c.page_shift) - 1));
 #pragma unroll
-                    for (int i = 0; i < 32 / kRows; ++i) {
-                        const int rl = i * kRows + lane / CH, ch = lane % CH;
-                        const long long f = __shfl_sync(~0u, off, rl);
-                        const bool take = f >= 0 && ch < dch;
-                        const int r = lw * 32 + rl;
-                        if (ok)
-                            cp_async16(dst + (ch >> 3) * 16384 + r * 128 +
-                                           (((ch & 7) ^ (r & 7)) << 4),
-                                       src + (take ? f + ch * 16 : 0), take);
-                    }
-                    if (kv && tail) {
-                        // A masked entry may hold anything, but 0 times NaN is NaN: new tokens'
-                        // values that are not finite are zeroed here and added row by row.
-                        asm volatile("cp.async.wait_all;" ::: "memory");
-                        named_sync(2, 128);
-                        if (lt < 4) s_wild[st][lt] = 0;
-                        named_sync(2, 128);
-                        const int r = lt;  // a row per thread
-                        const long long slot = (long long)t * kTcUnit + r;
-                        if (slot > len && slot < total) {
-                            constexpr uint32_t e = std::is_same<T, __half>::value ? 0x7c00u
-                                                                                  : 0x7f80u;
-                            bool f = false;
-                            for (int ch = 0; ch < dch; ++ch) {
-                                uint32_t v[4];
-                                asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
-                                             : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3])
-                                             : "r"(dst + (ch >> 3) * 16384 + r * 128 +
-                                                   (((ch & 7) ^ (r & 7)) << 4)) : "memory");
-#pragma unroll
-                                for (int k = 0; k < 4; ++k)
-                                    f |= (v[k] & e) == e || (v[k] >> 16 & e) == e;
-                            }
-                            if (f) {
-                                atomicOr(&s_wild[st][r >> 5], 1u << (r & 31));
-                                for (int ch = 0; ch < CH; ++ch)
-                                    asm volatile("st.shared.v4.b32 [%0], {%1,%1,%1,%1};" ::"r"(
-                                        dst + (ch >> 3) * 16384 + r * 128 +
-                                        (((ch & 7) ^ (r & 7)) << 4)), "r"(0) : "memory");
-                            }
+                            for (int q = 0; q < DP / 64; ++q)
+                                tma_page(dst + q * 16384 + (lane << shift) * 128, map, q * 64, p.h,
+                                         slot, pg, full);
                         }
-                        bar_arrive(&bars.v_full[st]);
-                    } else {
-                        bar_arrive_copies(kv ? &bars.v_full[st] : &bars.k_full[st]);
                     }
                 }
+                if (tail) {
+                    // A masked entry may hold anything, but 0 times NaN is NaN: what lies behind
+                    // the last token is zeroed here, and so are new tokens' values that are not
+                    // finite; those are added row by row.
+                    ok = ok && warp_wait(&bars.v_land, landed, gave_up);
+                    landed ^= 1;
+                    if (lt < 4) s_wild[st][lt] = 0;
+                    named_sync(2, 96);
+#pragma unroll 1
+                    for (int r = lt; r < 128; r += 96) {  // a row per thread
+                        const long long slot = (long long)t * kTcUnit + r;
+                        if (slot <= len) continue;
+                        constexpr uint32_t e = std::is_same<T, __half>::value ? 0x7c00u : 0x7f80u;
+                        bool f = slot >= total;
+#pragma unroll 4
+                        for (int k = 0; k < CH; ++k) {
+                            uint32_t v[4];
+                            asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
+                                         : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3])
+                                         : "r"(dst + (k >> 3) * 16384 + r * 128 +
+                                               (((k & 7) ^ (r & 7)) << 4)) : "memory");
+#pragma unroll
+                            for (int q = 0; q < 4; ++q)
+                                f |= (v[q] & e) == e || (v[q] >> 16 & e) == e;
+                        }
+                        if (!f) continue;
+                        if (slot < total) atomicOr(&s_wild[st][r >> 5], 1u << (r & 31));
+#pragma unroll 4
+                        for (int k = 0; k < CH; ++k)
+                            asm volatile("st.shared.v4.b32 [%0], {%1,%1,%1,%1};" ::"r"(
+                                dst + (k >> 3) * 16384 + r * 128 + (((k & 7) ^ (r & 7)) << 4)),
+                                "r"(0) : "memory");
+                    }
+                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                    named_sync(2, 96);
+                    if (lt == 0) bar_arrive(&bars.v_full[st]);
+                }
+                if (++st == stages) st = 0, again ^= 1;
             }
             ++pieces;
         }
-        asm volatile("cp.async.wait_all;" ::: "memory");
     } else if (w >= 12) {
         // ------------------------------------------------ products
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+        if (w == 13 || w == 14) {
+            // queries: rows of the item, zeros past them
+            const int lt = tid & 31 | (w - 13) << 5, dch = c.dim / 8;
+            int pieces = 0;
+            bool ok = true;
+            while (ok && walk.next(a, ROWS, kTcUnit, &p)) {
+                if (walk.sh.bad) continue;
+                ok = warp_wait(&bars.q_empty, (pieces & 1) ^ 1, gave_up);
+#pragma unroll 4
+                for (int i = lt; ok && i < ROWS * CH; i += 64) {
+                    const int row = i / CH, ch = i % CH, R = p.mt * ROWS + row, r = row & 127;
+                    const bool take = row < p.rows && ch < dch;
+                    const int j = R / a.group, g = R - j * a.group;
+                    const T* q = (const T*)a.q + (take ? p.b * a.qb + j * a.qt +
+                                      (long long)(p.h * a.group + g) * a.qh + ch * 8 : 0);
+                    cp_async16(sq + (row >> 7) * L::kTile + (ch >> 3) * 16384 + r * 128 +
+                                   (((ch & 7) ^ (r & 7)) << 4), q, take);
+                }
+                bar_arrive_copies(&bars.q_full);
+                ++pieces;
+            }
+            asm volatile("cp.async.wait_all;" ::: "memory");
+        }
         if (w == 12) {
             constexpr uint32_t kPv = product<T>(DP, true);
             constexpr uint32_t kPanel = DP > 64 ? 16384 : 1024;  // one panel: not used
@@ -1295,11 +1318,14 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv_wide_kernel(const AttentionA
             long long tiles = 0;  // of earlier pieces
             uint32_t pieces = 0, p_phase = 0;
             bool ok = true;
-            while (ok && walk.next(a, ROWS, &p)) {
+            while (ok && walk.next(a, ROWS, kTcUnit, &p)) {
                 if (walk.sh.bad) continue;
                 const bool two = p.rows > 128;
                 const int nt = p.t1 - p.t0, jobs = two ? 2 * nt : nt;
                 ok = warp_wait(&bars.q_full, pieces & 1, gave_up);
+                // threads copied the queries through the generic proxy, the products read them
+                // through the asynchronous one
+                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                 // Job i belongs to stream i & 1.  Its scores take the place of the weights of job
                 // i - 2, whose product comes before them; products of one thread run in order.
                 // Scores go first, so that each stream's product and next scores are issued
@@ -1310,12 +1336,9 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv_wide_kernel(const AttentionA
                     const int sst = ns & 1, pst = np & 1;
                     const long long stile = tiles + (two ? ns >> 1 : ns);
                     const long long ptile = tiles + (two ? np >> 1 : np);
-                    const int ks = (int)(stile % S), vs = (int)(ptile % S);
+                    const int ks = (int)(stile % SK), vs = (int)(ptile % SV);
                     if (ns < jobs && ns < np + 2 &&
-                        warp_test(&bars.k_full[ks], (uint32_t)(stile / S & 1))) {
-                        // the copies wrote through the generic proxy, the products read through
-                        // the asynchronous one
-                        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                        warp_test(&bars.k_full[ks], (uint32_t)(stile / SK & 1))) {
                         tc_after();
                         const uint64_t qa = operand(sq + (two ? sst * L::kTile : 0), 16384);
                         const uint64_t ka = operand(sk + ks * L::kTile, 16384);
@@ -1334,8 +1357,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv_wide_kernel(const AttentionA
                         ++ns;
                         idle = 0;
                     } else if (np < ns && warp_test(&bars.p_full[pst], p_phase >> pst & 1) &&
-                               warp_test(&bars.v_full[vs], (uint32_t)(ptile / S & 1))) {
-                        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                               warp_test(&bars.v_full[vs], (uint32_t)(ptile / SV & 1))) {
                         tc_after();
                         const uint64_t va = operand(sv + vs * L::kTile, kPanel);
                         const uint32_t sd = tmem + pst * 128, od = tmem + 256 + pst * DP;
@@ -1376,6 +1398,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv_wide_kernel(const AttentionA
         }
     } else {
         // ------------------------------------------------ weights: a row per thread
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 184;");
         const int st = w >> 2, r = tid & 127;
         const uint32_t mine = tmem + ((uint32_t)(w & 3) * 32 << 16);
         const uint32_t sc = mine + st * 128, oc = mine + 256 + st * DP;
@@ -1383,7 +1406,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv_wide_kernel(const AttentionA
         long long tiles = 0;
         int pieces = 0, anc_of = -1;
         bool tree_bad = false, ok = true;  // a wait that gave up skips the rest, not the barriers
-        while (walk.next(a, ROWS, &p)) {
+        while (walk.next(a, ROWS, kTcUnit, &p)) {
             const Share& sh = walk.sh;
             const bool two = p.rows > 128;
             const int row = two ? st * 128 + r : r, R = p.mt * ROWS + row;
@@ -1464,25 +1487,23 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv_wide_kernel(const AttentionA
                                              : ~0u;
                     }
                 }
-                // Once for the maximum, once for the weights: the scores stay in tensor memory
-                // rather than in 128 registers.
-                float top = -INFINITY;
+                float x[128];
 #pragma unroll
-                for (int k = 0; k < 2; ++k) {
-                    float s[64];
-                    tc_ld32(s, sc + 64 * k);
-                    tc_ld32(s + 32, sc + 64 * k + 32);
-                    tc_wait_ld();
-                    if (tail) {
+                for (int k = 0; k < 128; k += 32) tc_ld32(x + k, sc + k);
+                tc_wait_ld();
+                if (tail) {
 #pragma unroll
-                        for (int e = 0; e < 64; ++e)
-                            if (!(see[2 * k + (e >> 5)] >> (e & 31) & 1)) s[e] = -INFINITY;
-                    }
-                    float m[4] = {s[0], s[1], s[2], s[3]};
-#pragma unroll
-                    for (int e = 4; e < 64; ++e) m[e & 3] = fmaxf(m[e & 3], s[e]);
-                    top = fmaxf(fmaxf(top, fmaxf(m[0], m[1])), fmaxf(m[2], m[3]));
+                    for (int e = 0; e < 128; ++e)
+                        if (!(see[e >> 5] >> (e & 31) & 1)) x[e] = -INFINITY;
                 }
+                float m[4] = {x[0], x[1], x[2], x[3]};
+#pragma unroll
+                for (int e = 4; e < 124; e += 8)
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) m[k] = fmaxf(fmaxf(m[k], x[e + k]), x[e + k + 4]);
+#pragma unroll
+                for (int k = 0; k < 4; ++k) m[k] = fmaxf(m[k], x[124 + k]);
+                const float top = fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]));
                 const float mx = top == -INFINITY ? -INFINITY : top * unit;
                 // The reference follows the maximum only when that has grown by 2^8.
                 const bool grow = mx > ref + 8.0f;
@@ -1496,13 +1517,13 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv_wide_kernel(const AttentionA
                         waited = true;
                         tc_after();
 #pragma unroll 1
-                        for (int k = 0; k < DP; k += 32) {
-                            float o[32];
-                            tc_ld32(o, oc + k);
+                        for (int k = 0; k < DP; k += 16) {
+                            float o[16];
+                            tc_ld16(o, oc + k);
                             tc_wait_ld();
 #pragma unroll
-                            for (int e = 0; e < 32; ++e) o[e] *= f;
-                            tc_st32(oc + k, o);
+                            for (int e = 0; e < 16; ++e) o[e] *= f;
+                            tc_st16(oc + k, o);
                         }
                         tc_wait_st();
                     }
@@ -1510,8 +1531,8 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv_wide_kernel(const AttentionA
                 const float less = ref == -INFINITY ? 0.0f : ref;
                 if (tail) {
                     const long long tile = tiles + (two ? i >> 1 : i);
-                    const int vs = (int)(tile % S);
-                    ok = ok && warp_wait(&bars.v_full[vs], (uint32_t)(tile / S & 1), gave_up);
+                    const int vs = (int)(tile % SV);
+                    ok = ok && warp_wait(&bars.v_full[vs], (uint32_t)(tile / SV & 1), gave_up);
 #pragma unroll 1
                     for (int sl = 0; ok && sl < 128; ++sl) {
                         if (!(s_wild[vs][sl >> 5] >> (sl & 31) & 1)) continue;
@@ -1521,10 +1542,10 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv_wide_kernel(const AttentionA
                             tc_after();
                         }
                         const int n = t * kTcUnit + sl - len;  // the new token, >= 1
-                        const float x = tc_ld1(sc + sl);
+                        const float y = tc_ld1(sc + sl);
                         tc_wait_ld();
                         const bool mine_too = sees(anc, n);
-                        const float pw = mine_too ? ex2(x * unit - less) : 0.0f;
+                        const float pw = mine_too ? ex2(y * unit - less) : 0.0f;
                         const long long at = slot_offset(c, p.b, len + n);
                         const T* v = (const T*)(c.v + (at < 0 ? 0 : at) + p.h * c.head_stride);
 #pragma unroll 1
@@ -1544,34 +1565,35 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv_wide_kernel(const AttentionA
                 }
                 // Weights take the place of their own scores: of 32 columns, 16 hold the high
                 // halves in pairs and 16 the low ones.
-                float sum[4] = {0, 0, 0, 0};
+                float2 sum[2] = {{0, 0}, {0, 0}};
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
-                    float x[32], y[16];
-                    tc_ld32(x, sc + 32 * k);
-                    tc_wait_ld();
-#pragma unroll
-                    for (int e = 0; e < 32; ++e) x[e] = ex2(fmaf(x[e], unit, -less));
-                    if (tail) {
-#pragma unroll
-                        for (int e = 0; e < 32; ++e)
-                            if (!(see[k] >> e & 1)) x[e] = 0.0f;
-                    }
-#pragma unroll
-                    for (int e = 0; e < 32; ++e) sum[e & 3] += x[e];
+                    float y[32];
 #pragma unroll
                     for (int e = 0; e < 16; ++e) {
-                        const uint32_t h = pair<T>(x[2 * e], x[2 * e + 1]);
-                        y[e] = __uint_as_float(h);
+                        float2 v = fma2(make_float2(x[32 * k + 2 * e], x[32 * k + 2 * e + 1]),
+                                        make_float2(unit, unit), make_float2(-less, -less));
+                        v.x = ex2(v.x);
+                        v.y = ex2(v.y);
+                        if (tail) {
+                            if (!(see[k] >> (2 * e) & 1)) v.x = 0.0f;
+                            if (!(see[k] >> (2 * e + 1) & 1)) v.y = 0.0f;
+                        }
+                        sum[e & 1] = add2(sum[e & 1], v);
                         if constexpr (kLo) {
+                            const uint32_t h = cut<T>(v.x, v.y);
                             const float2 f = unpair<T>(h);
-                            x[e] = __uint_as_float(pair<T>(x[2 * e] - f.x, x[2 * e + 1] - f.y));
+                            const float2 d = add2(v, make_float2(-f.x, -f.y));
+                            y[e] = __uint_as_float(h);
+                            y[16 + e] = __uint_as_float(pair<T>(d.x, d.y));
+                        } else {
+                            y[e] = __uint_as_float(pair<T>(v.x, v.y));
                         }
                     }
-                    tc_st16(sc + 32 * k, y);
-                    if constexpr (kLo) tc_st16(sc + 32 * k + 16, x);
+                    if constexpr (kLo) tc_st32(sc + 32 * k, y);
+                    else tc_st16(sc + 32 * k, y);
                 }
-                l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+                l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
                 tc_wait_st();
                 tc_before();
                 bar_arrive(&bars.p_full[st]);
@@ -1580,7 +1602,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) kv_wide_kernel(const AttentionA
             if (ok && done > 0) ok = warp_wait(&bars.pv_done[st], (pv + done - 1) & 1, gave_up);
             pv += done;
             tc_after();
-            bool nan_piece = nan_rows || s_bad_piece[pieces & 3] == pieces || !ok;
+            bool nan_piece = nan_rows || s_bad_piece[pieces & 7] == pieces || !ok;
             if (nan_piece && !nan_rows && ok && tid == 0) mark(a.status, p.b, SV_DEV_BAD_PAGE);
             if (!ok && tid == 0) mark(a.status, p.b, SV_DEV_TIMEOUT);
             const bool whole = p.t0 == 0 && p.t1 == sh.tiles;
@@ -1796,6 +1818,7 @@ __global__ void __launch_bounds__(kCommitThreads) kv_commit_kernel(const CommitA
 
 // ---------------------------------------------------------------- host
 
+static int elem_bytes(sv_dtype t) { return t == SV_E4M3 ? 1 : 2; }
 static bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
 
 // Calls f with the types and sizes of the split kernel that these sizes take: 16 query rows
@@ -1838,6 +1861,33 @@ template <typename F> static auto with_wide(sv_dtype dtype, int dim, int rows, F
     return dtype == SV_BF16 ? sized(__nv_bfloat16()) : sized(__half());
 }
 
+// A cache tensor as the TMA sees it: element, head, slot, page.
+static bool cache_map(CUtensorMap* map, void* base, const sv_kv_cache* c) {
+    static PFN_cuTensorMapEncodeTiled_v12000 encode = [] {
+        void* f = nullptr;
+        cudaDriverEntryPointQueryResult found;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault,
+                                             &found) != cudaSuccess ||
+            found != cudaDriverEntryPointSuccess)
+            f = nullptr;
+        return (PFN_cuTensorMapEncodeTiled_v12000)f;
+    }();
+    if (!encode) return false;
+    const int e = elem_bytes(c->dtype);
+    const cuuint64_t dims[4] = {(cuuint64_t)c->dim, (cuuint64_t)c->heads, (cuuint64_t)c->page_size,
+                                (cuuint64_t)c->num_pages};
+    const cuuint64_t strides[3] = {(cuuint64_t)c->head_stride * e, (cuuint64_t)c->slot_stride * e,
+                                   (cuuint64_t)c->page_stride * e};
+    const cuuint32_t box[4] = {64, 1, (cuuint32_t)(c->page_size < 128 ? c->page_size : 128), 1};
+    const cuuint32_t step[4] = {1, 1, 1, 1};
+    return encode(map,
+                  c->dtype == SV_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
+                                      : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
+                  4, base, dims, strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                  CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 // Shared memory of every attention kernel, once per device.
 static cudaError_t attention_setup() {
     cudaError_t e = cudaSuccess;
@@ -1846,8 +1896,15 @@ static cudaError_t attention_setup() {
             for (int rows : {128, 256})
                 if (e == cudaSuccess)
                     e = with_wide(t, dim, rows, [](auto k, auto, int smem) {
-                        return cudaFuncSetAttribute(
-                            k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+                        // the roles' shares (256 threads of 184, 256 of 72) are those of a launch
+                        // with 128 each: with fewer the larger share would be waited for
+                        cudaFuncAttributes f;
+                        cudaError_t r = cudaFuncGetAttributes(&f, k);
+                        if (r == cudaSuccess && f.numRegs != 128) r = cudaErrorInvalidConfiguration;
+                        return r != cudaSuccess
+                                   ? r
+                                   : cudaFuncSetAttribute(
+                                         k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
                     });
     for (sv_dtype t : {SV_BF16, SV_F16})
         for (bool f8 : {false, true})
@@ -1899,8 +1956,6 @@ static AttentionWs attention_ws(int B, int rows, int dim) {
     l.bytes = l.part_ml + held * 8;
     return l;
 }
-
-static int elem_bytes(sv_dtype t) { return t == SV_E4M3 ? 1 : 2; }
 
 // scales: the call needs the scales of a float8 cache.
 static sv_status check_cache(const sv_kv_cache* c, bool scales, Cache* out) {
@@ -2086,9 +2141,13 @@ sv_status spec_kv_attention(const sv_kv_cache* cache, const void* q, const sv_st
     a.q_heads = q_heads;
     a.group = q_heads / cache->heads;
     a.B = B;
-    // Few rows: mma.sync, which then waits for memory only.  More: tcgen05.
+    // Few rows: mma.sync, which then waits for memory only.  More: tcgen05, where a page fills
+    // whole rows of the swizzle.
     const int rows = N * a.group;
-    const bool wide = rows > 32 && cache->dtype != SV_E4M3;
+    const bool wide = rows > 32 && cache->dtype != SV_E4M3 && cache->page_size >= 8;
+    CUtensorMap kmap, vmap;
+    if (wide && (!cache_map(&kmap, cache->k, cache) || !cache_map(&vmap, cache->v, cache)))
+        return SV_ERR_CUDA;
     const int tile = wide ? (rows <= 128 ? 128 : 256) : rows <= 16 ? 16 : 32;
     const int unit = wide ? kTcUnit : kUnit;
     const int mts = (rows + tile - 1) / tile;
@@ -2115,7 +2174,12 @@ sv_status spec_kv_attention(const sv_kv_cache* cache, const void* q, const sv_st
         cfg.stream = stream;
         cfg.attrs = &pdl;
         cfg.numAttrs = 1;
-        cudaError_t r = cudaLaunchKernelEx(&cfg, kernel, a);
+        cudaError_t r;
+        if constexpr (std::is_same<decltype(kernel), void (*)(const AttentionArgs)>::value ||
+                      std::is_same<decltype(kernel), void (*)(AttentionArgs)>::value)
+            r = cudaLaunchKernelEx(&cfg, kernel, a);
+        else
+            r = cudaLaunchKernelEx(&cfg, kernel, a, kmap, vmap);
         if (r != cudaSuccess) return r;
         cfg.gridDim = dim3(B * cache->heads * mts, warps == 4 ? tile : tile / 4);
         cfg.blockDim = dim3(128);
