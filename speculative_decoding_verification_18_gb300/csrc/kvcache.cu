@@ -1315,8 +1315,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             constexpr uint32_t kPanel = DP > 64 ? 16384 : 1024;  // one panel: not used
             // scores times the sign of the scale: the largest is then the one to look for
             const uint32_t qk = product<T>(128, false) | (a.scale < 0.0f ? 1u << 13 : 0u);
-            long long tiles = 0;  // of earlier pieces
-            uint32_t pieces = 0, p_phase = 0;
+            int ks = 0, vs = 0;  // stages and parities of the next tiles of keys and of values
+            uint32_t k_phase = 0, v_phase = 0, pieces = 0, p_phase = 0;
             bool ok = true;
             while (ok && walk.next(a, ROWS, kTcUnit, &p)) {
                 if (walk.sh.bad) continue;
@@ -1331,15 +1331,12 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 // Scores go first, so that each stream's product and next scores are issued
                 // together and the streams take turns.
                 int ns = 0, np = 0, idle = 0;  // scores and outputs issued; polls in vain
+                bool k_ready = false;          // the next tile of keys: asked for ahead of time
                 uint64_t since = 0;
                 while (ok && np < jobs) {
                     const int sst = ns & 1, pst = np & 1;
-                    const long long stile = tiles + (two ? ns >> 1 : ns);
-                    const long long ptile = tiles + (two ? np >> 1 : np);
-                    const int ks = (int)(stile % SK), vs = (int)(ptile % SV);
-                    if (ns < jobs && ns < np + 2 &&
-                        warp_test(&bars.k_full[ks], (uint32_t)(stile / SK & 1))) {
-                        tc_after();
+                    if (!k_ready && ns < jobs) k_ready = warp_test(&bars.k_full[ks], k_phase);
+                    if (k_ready && ns < jobs && ns < np + 2) {
                         const uint64_t qa = operand(sq + (two ? sst * L::kTile : 0), 16384);
                         const uint64_t ka = operand(sk + ks * L::kTile, 16384);
                         if (elect_one()) {
@@ -1354,10 +1351,14 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                             if (ns == jobs - 1) tc_commit(&bars.q_empty);
                         }
                         __syncwarp();
+                        if (!two || sst == 1) {
+                            k_ready = false;
+                            if (++ks == SK) ks = 0, k_phase ^= 1;
+                        }
                         ++ns;
                         idle = 0;
                     } else if (np < ns && warp_test(&bars.p_full[pst], p_phase >> pst & 1) &&
-                               warp_test(&bars.v_full[vs], (uint32_t)(ptile / SV & 1))) {
+                               warp_test(&bars.v_full[vs], v_phase)) {
                         tc_after();
                         const uint64_t va = operand(sv + vs * L::kTile, kPanel);
                         const uint32_t sd = tmem + pst * 128, od = tmem + 256 + pst * DP;
@@ -1376,6 +1377,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                             if (!two || pst == 1) tc_commit(&bars.v_empty[vs]);
                         }
                         __syncwarp();
+                        if ((!two || pst == 1) && ++vs == SV) vs = 0, v_phase ^= 1;
                         p_phase ^= 1u << pst;
                         ++np;
                         idle = 0;
@@ -1386,7 +1388,6 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                         if (!ok) *gave_up = 1;
                     }
                 }
-                tiles += nt;
                 ++pieces;
             }
             if (!ok) {  // products in flight end before the tensor memory goes back
