@@ -1,10 +1,10 @@
-"""Thin ctypes binding of the paged key-value cache calls (include/specverify_kv.h):
+"""Thin binding of the paged key-value cache calls (include/specverify_kv.h):
 ``spec_kv_append``, ``spec_kv_attention`` and ``spec_kv_commit``.
 
 Like specverify.py it only marshals arguments: torch CUDA tensors on the current
 device, launches on the current torch stream unless ``stream`` is given, no CPU
-fallback.  Shapes, types and layouts are checked here (ValueError / TypeError);
-everything else by the library (SpecVerifyError).
+fallback.  Shapes, types and layouts are checked on the way, in csrc/kvbind.cpp
+(ValueError / TypeError); everything else by the library (SpecVerifyError).
 
 One round of a layer, and the commit of all layers after the verdict::
 
@@ -18,6 +18,9 @@ One round of a layer, and the commit of all layers after the verdict::
 from __future__ import annotations
 
 import ctypes
+import importlib.machinery
+import importlib.util
+import os
 
 import torch
 
@@ -40,38 +43,37 @@ class _Cache(ctypes.Structure):
                                                "dim", "dtype")])
 
 
-class _Strides(ctypes.Structure):
-    """sv_strides."""
-    _fields_ = [("batch", ctypes.c_int64), ("token", ctypes.c_int64), ("head", ctypes.c_int64)]
-
-
 class _Rope(ctypes.Structure):
     """sv_rope."""
     _fields_ = [("turns", ctypes.c_void_p), ("rot_dim", ctypes.c_int),
                 ("interleaved", ctypes.c_int), ("magnitude", ctypes.c_float)]
 
 
-_lib = None
+BIND = os.path.join(sv.HERE, "_kvbind.so")
+_lib = _bind = None
 
 
 def load():
     """The library with the cache calls declared (raises if it has not been built)."""
-    global _lib
+    global _lib, _bind
     if _lib is not None:
         return _lib
     lib = sv.load()
-    P, I, F, Z, L, D = (ctypes.c_void_p, ctypes.c_int, ctypes.c_float, ctypes.c_size_t,
-                        ctypes.c_int64, ctypes.c_double)
+    P, I, Z, D = ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t, ctypes.c_double
     lib.spec_kv_rope_turns.argtypes = [I, D, D, D, D, D, P]
-    lib.spec_kv_append.argtypes = [P, P, P, P, P, P, P, I, P, P, P, I, I, I, P, P, P]
     lib.spec_kv_attention_workspace_size.argtypes = [I, I, I, I, I]
     lib.spec_kv_attention_workspace_size.restype = Z
-    lib.spec_kv_attention.argtypes = [P, P, P, I, P, P, P, F, I, I, I, P, P, Z, P, P]
-    lib.spec_kv_commit.argtypes = [P, I, L, P, P, P, I, I, P, P, P]
-    for n in EXPORTS:
-        if n != "spec_kv_attention_workspace_size":
-            getattr(lib, n).restype = I
-    _lib = lib
+    lib.spec_kv_rope_turns.restype = I
+    if not os.path.exists(BIND):
+        raise ImportError(f"_kvbind.so is not built ({BIND}); run "
+                          "speculative_decoding_verification_18_gb300.build.build() first")
+    loader = importlib.machinery.ExtensionFileLoader("_kvbind", BIND)
+    bind = importlib.util.module_from_spec(importlib.util.spec_from_loader("_kvbind", loader))
+    loader.exec_module(bind)
+    address = lambda f: ctypes.cast(f, P).value
+    bind.bind(address(lib.spec_kv_append), address(lib.spec_kv_attention),
+              address(lib.spec_kv_commit))
+    _lib, _bind = lib, bind
     return lib
 
 
@@ -94,30 +96,6 @@ def _vector(t, name, shape, dtype=torch.int32):
         raise ValueError(f"{name} must be contiguous")
     _on_device(t, name)
     return t.data_ptr()
-
-
-def _status(t, B):
-    """status: int32 or uint32 [B]; only its bits matter."""
-    if t is not None and t.dtype not in (torch.int32, torch.uint32):
-        raise TypeError(f"status must be int32 or uint32, not {t.dtype}")
-    return None if t is None else _vector(t, "status", (B,), t.dtype)
-
-
-def _tokens(t, name, B, N, heads, dim, dtype):
-    """(pointer, sv_strides) of a [B, N, heads, dim] tensor with contiguous dim."""
-    if t.dtype != dtype:
-        raise TypeError(f"{name} must be {dtype}, not {t.dtype}")
-    if t.shape != (B, N, heads, dim):
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, not {(B, N, heads, dim)}")
-    if t.stride(3) != 1:
-        raise ValueError(f"the last dimension of {name} must be contiguous")
-    _on_device(t, name)
-    sb, st, sh, _ = t.stride()
-    # the stride of a dimension of one entry means nothing: the contiguous one
-    sh = sh if heads > 1 else dim
-    st = st if N > 1 else heads * sh
-    sb = sb if B > 1 else N * st
-    return t.data_ptr(), ctypes.byref(_Strides(sb, st, sh))
 
 
 class PagedCache:
@@ -168,18 +146,17 @@ class PagedCache:
             self._layers.append(_Cache(k.data_ptr() + at, v.data_ptr() + at, tp, *scales, sp, ss,
                                        sh, pages, page_size, table.shape[1], heads, dim,
                                        _TYPES[k.dtype]))
-        self._refs = [ctypes.byref(c) for c in self._layers]
+        load()
+        self._addresses = [ctypes.addressof(c) for c in self._layers]
+        self._rows, self._device = table.shape[0], k.get_device()
 
     def layer(self, i):
-        if self.k_scale is None and self.dtype == torch.float8_e4m3fn:
-            raise ValueError("a float8_e4m3fn cache needs k_scale and v_scale here")
+        """Address of the sv_kv_cache of layer i."""
         if not 0 <= i < self.layers:
             raise ValueError(f"layer {i} of {self.layers}")
-        return self._refs[i]
-
-    def rows(self, B):
-        if self.table.shape[0] != B:
-            raise ValueError(f"the table has {self.table.shape[0]} sequences, not {B}")
+        if self.k_scale is None and self.dtype == torch.float8_e4m3fn:
+            raise ValueError("a float8_e4m3fn cache needs k_scale and v_scale here")
+        return self._addresses[i]
 
 
 class Rope:
@@ -196,42 +173,20 @@ class Rope:
         self.turns = host.to(device or "cuda")
         self.rot_dim, self.interleaved, self.magnitude = rot_dim, bool(interleaved), magnitude
         self._c = _Rope(self.turns.data_ptr(), rot_dim, int(self.interleaved), float(magnitude))
-        self._ref = ctypes.byref(self._c)
+        self._address = ctypes.addressof(self._c)
 
 
 def spec_kv_append(cache, k, v, kv_len, q=None, q_out=None, rope=None, parents=None, num_new=None,
                    status=None, layer=0, stream=None):
     """Rotate the new tokens' q and k [B, N, heads, dim] by `rope` (None: not at all) and write
     k and v behind the kv_len[b] cached entries; q_out (contiguous, may be q) gets the queries."""
-    if k.dim() != 4:
-        raise ValueError("k must be [B, N, heads, dim]")
-    B, N, H, D = k.shape
-    if (H, D) != (cache.heads, cache.dim):
-        raise ValueError(f"k has {H} heads of {D}, the cache {cache.heads} of {cache.dim}")
-    cache.rows(B)
-    kp, ks = _tokens(k, "k", B, N, H, D, k.dtype)
-    vp, vs = _tokens(v, "v", B, N, H, D, k.dtype)
-    if (vs._obj.batch, vs._obj.token, vs._obj.head) != (ks._obj.batch, ks._obj.token,
-                                                       ks._obj.head):
-        raise ValueError("k and v must have the same strides")
-    if k.dtype not in (torch.bfloat16, torch.float16):
-        raise TypeError(f"k must be bfloat16 or float16, not {k.dtype}")
-    qp = qs = op = None
-    hq = H
-    if q is not None:
-        hq = q.shape[2] if q.dim() == 4 else 0
-        qp, qs = _tokens(q, "q", B, N, hq, D, k.dtype)
-        if q_out is None:
-            raise ValueError("q needs q_out")
-        op = _vector(q_out, "q_out", (B, N, hq, D), k.dtype)
     if rope is not None:
         _on_device(rope.turns, "rope")
-    st = load().spec_kv_append(cache.layer(layer), rope and rope._ref, qp, qs, kp, vp, ks,
-                               _TYPES[k.dtype], _vector(kv_len, "kv_len", (B,)),
-                               _vector(num_new, "num_new", (B,)),
-                               _vector(parents, "parents", (B, N)), B, N, hq, op,
-                               _status(status, B), sv._stream(stream))
-    sv._check(st, "spec_kv_append")
+    st = _bind.append(cache.layer(layer), cache._rows, cache._device, k, v, kv_len, q, q_out,
+                      None if rope is None else rope._address, parents, num_new, status,
+                      None if stream is None else sv._stream(stream))
+    if st:
+        sv._check(st, "spec_kv_append")
 
 
 def spec_kv_attention_workspace_size(B, N, q_heads, heads, dim) -> int:
@@ -250,23 +205,10 @@ def spec_kv_attention(cache, q, kv_len, out, ws, scale, parents=None, num_new=No
                       layer=0, stream=None):
     """Attention of the new tokens' q [B, N, q_heads, dim] over the kv_len[b] cached entries and
     their own ancestors' -> out (contiguous).  ws: attention_workspace(...)."""
-    if q.dim() != 4:
-        raise ValueError("q must be [B, N, q_heads, dim]")
-    B, N, hq, D = q.shape
-    if D != cache.dim:
-        raise ValueError(f"q has heads of {D}, the cache of {cache.dim}")
-    if q.dtype not in (torch.bfloat16, torch.float16):
-        raise TypeError(f"q must be bfloat16 or float16, not {q.dtype}")
-    cache.rows(B)
-    qp, qs = _tokens(q, "q", B, N, hq, D, q.dtype)
-    st = load().spec_kv_attention(cache.layer(layer), qp, qs, _TYPES[q.dtype],
-                                  _vector(kv_len, "kv_len", (B,)),
-                                  _vector(num_new, "num_new", (B,)),
-                                  _vector(parents, "parents", (B, N)), float(scale), B, N, hq,
-                                  _vector(out, "out", (B, N, hq, D), q.dtype),
-                                  _vector(ws, "ws", ws.shape, torch.uint8), ws.numel(),
-                                  _status(status, B), sv._stream(stream))
-    sv._check(st, "spec_kv_attention")
+    st = _bind.attention(cache.layer(layer), cache._rows, cache._device, q, kv_len, out, ws, scale,
+                         parents, num_new, status, None if stream is None else sv._stream(stream))
+    if st:
+        sv._check(st, "spec_kv_attention")
 
 
 def spec_kv_commit(cache, kv_len, num_accepted, kv_len_out, out_nodes=None, status=None,
@@ -274,13 +216,8 @@ def spec_kv_commit(cache, kv_len, num_accepted, kv_len_out, out_nodes=None, stat
     """Move the accepted nodes' entries of every layer behind the committed ones;
     kv_len_out = kv_len + num_accepted + 1.  out_nodes [B, N] as spec_verify_tree writes it;
     None for a chain."""
-    B = kv_len.shape[0]
-    cache.rows(B)
-    N = 65 if out_nodes is None else out_nodes.shape[-1]
-    st = load().spec_kv_commit(cache._refs[0], cache.layers, cache.layer_stride,
-                               _vector(kv_len, "kv_len", (B,)),
-                               _vector(out_nodes, "out_nodes", (B, N)),
-                               _vector(num_accepted, "num_accepted", (B,)), B, N,
-                               _vector(kv_len_out, "kv_len_out", (B,)), _status(status, B),
-                               sv._stream(stream))
-    sv._check(st, "spec_kv_commit")
+    st = _bind.commit(cache._addresses[0], cache._rows, cache._device, cache.layers,
+                      cache.layer_stride, kv_len, num_accepted, kv_len_out, out_nodes, status,
+                      None if stream is None else sv._stream(stream))
+    if st:
+        sv._check(st, "spec_kv_commit")

@@ -16,8 +16,17 @@ from conftest import ROOT
 def kv():
     from speculative_decoding_verification_18_gb300 import build, kvcache
     build.build()
-    kvcache.load()
+    lib = kvcache.load()
+    P, I, F, Z, L = (ctypes.c_void_p, ctypes.c_int, ctypes.c_float, ctypes.c_size_t, ctypes.c_int64)
+    lib.spec_kv_append.argtypes = [P, P, P, P, P, P, P, I, P, P, P, I, I, I, P, P, P]
+    lib.spec_kv_attention.argtypes = [P, P, P, I, P, P, P, F, I, I, I, P, P, Z, P, P]
+    lib.spec_kv_commit.argtypes = [P, I, L, P, P, P, I, I, P, P, P]
     return kvcache
+
+
+class Strides(ctypes.Structure):
+    """sv_strides."""
+    _fields_ = [("batch", ctypes.c_int64), ("token", ctypes.c_int64), ("head", ctypes.c_int64)]
 
 
 P = 4096  # a 16-byte-aligned fake address: never dereferenced on these paths
@@ -61,7 +70,7 @@ def test_workspace_size(kv):
 
 def test_append_argument_errors(kv):
     from speculative_decoding_verification_18_gb300 import specverify as sv
-    st = kv._Strides(64 * 6, 64 * 6, 64)
+    st = Strides(64 * 6, 64 * 6, 64)
 
     def call(cache=None, rope=None, q=P, qs=st, k=P, v=P, ks=st, dtype=sv.SV_BF16, kv_len=P,
              num_new=None, parents=None, B=2, N=3, hq=4, out=2 * P, status=None):
@@ -79,7 +88,7 @@ def test_append_argument_errors(kv):
                       (dict(hq=0), 1), (dict(hq=1026), 3), (dict(k=P + 2), 1), (dict(q=P + 2), 1),
                       (dict(out=P + 2), 1), (dict(kv_len=P + 4), 1), (dict(num_new=P + 4), 1),
                       (dict(parents=P + 4), 1), (dict(status=P + 4), 1), (dict(out=P), 1),
-                      (dict(qs=kv._Strides(64, 64, 4)), 1), (dict(ks=kv._Strides(64, -64, 64)), 1),
+                      (dict(qs=Strides(64, 64, 4)), 1), (dict(ks=Strides(64, -64, 64)), 1),
                       (dict(rope=kv._Rope(None, 64, 0, 1.0)), 1),
                       (dict(rope=kv._Rope(P, 63, 0, 1.0)), 1),
                       (dict(rope=kv._Rope(P, 66, 0, 1.0)), 1),
@@ -94,7 +103,7 @@ def test_append_argument_errors(kv):
 
 def test_attention_argument_errors(kv):
     from speculative_decoding_verification_18_gb300 import specverify as sv
-    st = kv._Strides(64 * 12, 64 * 4, 64)
+    st = Strides(64 * 12, 64 * 4, 64)
     need = kv.spec_kv_attention_workspace_size(2, 3, 4, 2, 64)
 
     def call(cache=None, q=P, qs=st, dtype=sv.SV_BF16, kv_len=P, num_new=None, parents=None,
@@ -113,7 +122,7 @@ def test_attention_argument_errors(kv):
                       (dict(q=P + 8), 1), (dict(out=P + 8), 1), (dict(ws=P + 8), 1),
                       (dict(ws=None), 2), (dict(wsb=need - 1), 2), (dict(num_new=P + 4), 1),
                       (dict(status=P + 4), 1), (dict(parents=P + 4), 1),
-                      (dict(qs=kv._Strides(64, 64, 4)), 1)):
+                      (dict(qs=Strides(64, 64, 4)), 1)):
         assert call(**bad) == code, bad
     assert call(B=0) == 0
 
