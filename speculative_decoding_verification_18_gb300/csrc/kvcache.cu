@@ -51,8 +51,73 @@ template <> struct Conv<__nv_fp8_e4m3> {
     static __device__ __nv_fp8_e4m3 from(float x) { return __nv_fp8_e4m3(x); }
 };
 
-// V elements of type T moved as one access (2 V or V bytes, aligned to them).
-template <typename T, int V> struct alignas(sizeof(T) * V) Vec { T x[V]; };
+// Two values as a pair of type M in one word (x low), rounded to nearest.
+template <typename M> __device__ __forceinline__ uint32_t pair(float x, float y) {
+    if constexpr (std::is_same<M, __half>::value) {
+        const __half2 h = __floats2half2_rn(x, y);
+        return reinterpret_cast<const uint32_t&>(h);
+    } else {
+        const __nv_bfloat162 h = __floats2bfloat162_rn(x, y);
+        return reinterpret_cast<const uint32_t&>(h);
+    }
+}
+template <typename M> __device__ __forceinline__ float2 unpair(uint32_t w) {
+    if constexpr (std::is_same<M, __half>::value)
+        return __half22float2(reinterpret_cast<const __half2&>(w));
+    else
+        return __bfloat1622float2(reinterpret_cast<const __nv_bfloat162&>(w));
+}
+
+// V values of a 16-bit type as one access of 2 V bytes (V = 8, 4 or 1), in words.
+template <int V> struct Words { uint32_t w[V > 1 ? V / 2 : 1]; };
+template <int V> __device__ __forceinline__ Words<V> get(const void* p) {
+    Words<V> r;
+    if constexpr (V == 8) {
+        const uint4 x = *reinterpret_cast<const uint4*>(p);
+        r.w[0] = x.x, r.w[1] = x.y, r.w[2] = x.z, r.w[3] = x.w;
+    } else if constexpr (V == 4) {
+        const uint2 x = *reinterpret_cast<const uint2*>(p);
+        r.w[0] = x.x, r.w[1] = x.y;
+    } else {
+        r.w[0] = *reinterpret_cast<const uint16_t*>(p);
+    }
+    return r;
+}
+template <int V> __device__ __forceinline__ void put(void* p, const Words<V>& r) {
+    if constexpr (V == 8)
+        *reinterpret_cast<uint4*>(p) = make_uint4(r.w[0], r.w[1], r.w[2], r.w[3]);
+    else if constexpr (V == 4)
+        *reinterpret_cast<uint2*>(p) = make_uint2(r.w[0], r.w[1]);
+    else
+        *reinterpret_cast<uint16_t*>(p) = (uint16_t)r.w[0];
+}
+template <typename T, int V> __device__ __forceinline__ void widen_to(float* f, const Words<V>& r) {
+#pragma unroll
+    for (int i = 0; i < V; i += 2) {
+        const float2 x = unpair<T>(r.w[i / 2]);
+        f[i] = x.x;
+        if (V > 1) f[i + 1] = x.y;
+    }
+}
+// V floats rounded to CT and written: 2 V or (float8: to nearest, saturating) V bytes.
+template <typename CT, int V> __device__ __forceinline__ void round_to(void* p, const float* f) {
+    if constexpr (sizeof(CT) == 2) {
+        Words<V> r;
+#pragma unroll
+        for (int i = 0; i < V; i += 2) r.w[i / 2] = pair<CT>(f[i], V > 1 ? f[i + 1] : 0.0f);
+        put<V>(p, r);
+    } else {
+        uint32_t w[V > 4 ? 2 : 1] = {};
+#pragma unroll
+        for (int i = 0; i < V; i += 2)
+            w[i / 4] |= (uint32_t)__nv_cvt_float2_to_fp8x2(
+                            make_float2(f[i], V > 1 ? f[i + 1] : 0.0f), __NV_SATFINITE, __NV_E4M3)
+                        << (i % 4 * 8);
+        if constexpr (V == 8) *reinterpret_cast<uint2*>(p) = make_uint2(w[0], w[1]);
+        else if constexpr (V == 4) *reinterpret_cast<uint32_t*>(p) = w[0];
+        else *reinterpret_cast<uint8_t*>(p) = (uint8_t)w[0];
+    }
+}
 
 // ---------------------------------------------------------------- sequences
 
@@ -94,151 +159,153 @@ struct AppendArgs {
     const int32_t* num_new;
     const int32_t* parents;
     uint32_t* status;
-    int N, q_heads;
+    int N, q_heads, run;  // tokens per CTA
 };
 
-constexpr int kAppendThreads = 256;
+constexpr int kAppendThreads = 320;  // at most
+constexpr int kAppendHeads = 2;   // heads per thread in flight
+constexpr int kAppendTokens = 4;  // at most so many tokens per CTA
 
-// One CTA per new token: it forms the token's cosines and sines once, in shared
-// memory, and turns every head with them.  The angle is position * rate modulo
-// one turn in 64-bit integers (exact), so far positions lose nothing; its top 32
-// bits become the argument of sincospi.  V pairs of a head per step: 2 V elements
-// of 2 bytes read and written in 16-byte accesses when V = 8.  Bound by memory:
-// each query, key and value is read once and written once.
-template <typename T, typename CT, int V>
-__global__ void __launch_bounds__(kAppendThreads) kv_append_kernel(const AppendArgs a) {
-    __shared__ float2 s_cs[kMaxDim / 2];
+// One CTA per run of new tokens of a sequence.  A thread owns the same 2 V elements (V rotated
+// pairs, or 2 V elements that are not rotated) of every blockDim.y-th head, queries, keys and
+// values in one row.  It asks for its first heads before anything else; the lengths, the pages
+// and the angles of the run arrive while they are under way, and each next token's heads while
+// the one before is turned and written.  The angle is position * rate modulo one turn in 64-bit
+// integers (exact), so far positions lose nothing; its top 32 bits become the argument of
+// sincospi.  Accesses are of 16 bytes where V = 8.  Bound by memory: each query, key and value is
+// read once and written once.
+template <typename T, typename CT, int V, bool INTERLEAVED>
+__global__ void __launch_bounds__(kAppendThreads, 2) kv_append_kernel(const AppendArgs a) {
+    __shared__ float2 s_cs[kAppendTokens][kMaxDim / 2];
+    __shared__ long long s_place[kAppendTokens];
     __shared__ int s_par[kMaxN];
-    const int b = blockIdx.y, j = blockIdx.x, tid = threadIdx.x;
+    const int b = blockIdx.y, j0 = blockIdx.x * a.run, w = threadIdx.x;
+    const int tid = threadIdx.y * blockDim.x + w, threads = blockDim.x * blockDim.y;
     const Cache& c = a.c;
+    struct Heads { Words<V> x0[kAppendHeads], x1[kAppendHeads]; };
+    const int half = a.rot / 2, D = c.dim, qn = a.q ? a.q_heads : 0, heads = qn + 2 * c.heads;
+    const bool turns = w < half / V;
+    const int e0 = turns && !INTERLEAVED ? w * V : 2 * w * V;
+    const int e1 = turns && !INTERLEAVED ? e0 + half : e0 + V;
+    auto load = [&](Heads& x, int j, int h0) {
+#pragma unroll
+        for (int i = 0; i < kAppendHeads; ++i) {
+            const int h = h0 + i * blockDim.y;
+            if (h >= heads) continue;
+            const T* src = h < qn ? (const T*)a.q + b * a.qb + j * a.qt + h * a.qh
+                           : h < qn + c.heads
+                               ? (const T*)a.k + b * a.kb + j * a.kt + (h - qn) * a.kh
+                               : (const T*)a.v + b * a.kb + j * a.kt + (h - qn - c.heads) * a.kh;
+            x.x0[i] = get<V>(src + e0);
+            x.x1[i] = get<V>(src + e1);
+        }
+    };
+    Heads now, next;
+    load(now, j0, threadIdx.y);
+
     int len;
     const int n = new_tokens(a.kv_len, a.num_new, b, a.N, c, &len);
     if (n < 0) {
-        if (j == 0 && tid == 0) mark(a.status, b, SV_DEV_BAD_LENGTH);
+        if (j0 == 0 && tid == 0) mark(a.status, b, SV_DEV_BAD_LENGTH);
         return;
     }
-    if (j >= n) return;
-    int depth = j;
+    const int j1 = min(n, j0 + a.run);
+    if (j0 >= j1) return;
+    if (tid < j1 - j0) {
+        s_place[tid] = slot_offset(c, b, len + j0 + tid);
+        if (s_place[tid] < 0) mark(a.status, b, SV_DEV_BAD_PAGE);
+    }
     if (a.parents) {
         int bad = 0;
-        for (int i = tid; i < n; i += kAppendThreads) {
+        for (int i = tid; i < n; i += threads) {
             const int p = a.parents[(long long)b * a.N + i];
             s_par[i] = p;
             bad |= i > 0 && (p < 0 || p >= i);
         }
         if (__syncthreads_or(bad)) {
-            if (j == 0 && tid == 0) mark(a.status, b, SV_DEV_BAD_TREE);
+            if (j0 == 0 && tid == 0) mark(a.status, b, SV_DEV_BAD_TREE);
             return;
         }
-        depth = 0;
-        for (int i = j; i > 0; i = s_par[i]) ++depth;
     }
-    const int half = a.rot / 2;
-    const uint64_t pos = (uint64_t)len + depth;
-    for (int i = tid; i < half; i += kAppendThreads) {
-        const int32_t t = (int32_t)((pos * a.turns[i]) >> 32);
+    for (int i = tid; i < half * (j1 - j0); i += threads) {
+        const int t = i / half, e = i - t * half;
+        int depth = j0 + t;
+        if (a.parents) {
+            depth = 0;
+            for (int k = j0 + t; k > 0; k = s_par[k]) ++depth;
+        }
+        const int32_t turn = (int32_t)((((uint64_t)len + depth) * a.turns[e]) >> 32);
         float s, co;
-        sincospif((float)t * 4.656612873077393e-10f, &s, &co);  // 2^-31: half turns
-        s_cs[i] = make_float2(co * a.magnitude, s * a.magnitude);
+        sincospif((float)turn * 4.656612873077393e-10f, &s, &co);  // 2^-31: half turns
+        s_cs[t][e] = make_float2(co * a.magnitude, s * a.magnitude);
     }
-    const long long place = slot_offset(c, b, len + j);
-    if (place < 0 && tid == 0) mark(a.status, b, SV_DEV_BAD_PAGE);
     __syncthreads();
 
-    // Units of a head: rot/2/V rotated ones (2 V elements each), then the rest in
-    // steps of V; of a value head: dim/V steps.
-    const int D = c.dim, turn_units = half / V, units = turn_units + (D - a.rot) / V;
-    const int qn = a.q ? a.q_heads : 0;
-    const int heads = qn + c.heads;
-    using VT = Vec<T, V>;
-    using VC = Vec<CT, V>;
-    for (int u = tid; u < heads * units; u += kAppendThreads) {
-        const int h = u / units, w = u - h * units;
-        const bool is_q = h < qn;
-        const T* src = is_q ? (const T*)a.q + b * a.qb + j * a.qt + h * a.qh
-                            : (const T*)a.k + b * a.kb + j * a.kt + (h - qn) * a.kh;
-        int e0, e1;
-        float r0[V], r1[V];
-        const bool turns = w < turn_units;
-        if (turns) {
-            e0 = a.interleaved ? 2 * w * V : w * V;
-            e1 = a.interleaved ? e0 + V : e0 + half;
-        } else {
-            e0 = a.rot + (w - turn_units) * V;
-            e1 = e0;
-        }
-        const VT x0 = *reinterpret_cast<const VT*>(src + e0);
+    auto write = [&](const Heads& x, int j, int h0) {
+        const long long place = s_place[j - j0];
+        float2 cs[V];
 #pragma unroll
-        for (int i = 0; i < V; ++i) r0[i] = Conv<T>::to(x0.x[i]);
-        if (turns) {
-            const VT x1 = *reinterpret_cast<const VT*>(src + e1);
+        for (int i = 0; i < V; ++i) cs[i] = turns ? s_cs[j - j0][w * V + i] : make_float2(1.0f, 0.0f);
 #pragma unroll
-            for (int i = 0; i < V; ++i) r1[i] = Conv<T>::to(x1.x[i]);
-            if (a.interleaved) {
+        for (int i = 0; i < kAppendHeads; ++i) {
+            const int h = h0 + i * blockDim.y;
+            if (h >= heads) continue;
+            const bool is_q = h < qn, is_v = h >= qn + c.heads;
+            const int ch = is_v ? h - qn - c.heads : h - qn;  // head of the cache
+            if (!is_q && place < 0) continue;
+            if (is_v && sizeof(CT) == sizeof(T)) {  // moved bit by bit
+                CT* dst = (CT*)(c.v + place + ch * c.head_stride);
+                put<V>(dst + e0, x.x0[i]);
+                put<V>(dst + e1, x.x1[i]);
+                continue;
+            }
+            float r[2 * V];
+            widen_to<T, V>(r, x.x0[i]);
+            widen_to<T, V>(r + V, x.x1[i]);
+            if (turns && !is_v) {
 #pragma unroll
-                for (int i = 0; i < V; ++i) {
-                    const float2 cs = s_cs[w * V + i];
-                    // pair i of the unit: elements 2i and 2i + 1 of its 2 V
-                    float& x = 2 * i < V ? r0[2 * i < V ? 2 * i : 0] : r1[2 * i < V ? 0 : 2 * i - V];
-                    float& y = 2 * i + 1 < V ? r0[2 * i + 1 < V ? 2 * i + 1 : 0]
-                                             : r1[2 * i + 1 < V ? 0 : 2 * i + 1 - V];
-                    const float p = x * cs.x - y * cs.y;
-                    y = y * cs.x + x * cs.y;
-                    x = p;
+                for (int k = 0; k < V; ++k) {
+                    // the pair's places among the thread's 2 V elements
+                    float& u = r[INTERLEAVED ? 2 * k : k];
+                    float& v = r[INTERLEAVED ? 2 * k + 1 : V + k];
+                    const float p = u * cs[k].x - v * cs[k].y;
+                    v = v * cs[k].x + u * cs[k].y;
+                    u = p;
                 }
+            }
+            if (is_q) {
+                T* dst = (T*)a.q_out + (((long long)b * a.N + j) * a.q_heads + h) * D;
+                round_to<T, V>(dst + e0, r);
+                round_to<T, V>(dst + e1, r + V);
             } else {
+                CT* dst = (CT*)((is_v ? c.v : c.k) + place + ch * c.head_stride);
+                if constexpr (sizeof(CT) == 1) {
+                    // times the reciprocal, which is off by half a step more than the quotient;
+                    // the quotient itself where there is no finite one
+                    const float scale = (is_v ? c.v_scale : c.k_scale)[ch];
+                    const float inverse = __fdiv_rn(1.0f, scale);
+                    if (fabsf(inverse) <= 3.0e38f) {
 #pragma unroll
-                for (int i = 0; i < V; ++i) {
-                    const float2 cs = s_cs[w * V + i];
-                    const float p = r0[i] * cs.x - r1[i] * cs.y;
-                    r1[i] = r1[i] * cs.x + r0[i] * cs.y;
-                    r0[i] = p;
+                        for (int k = 0; k < 2 * V; ++k) r[k] *= inverse;
+                    } else {
+#pragma unroll
+                        for (int k = 0; k < 2 * V; ++k) r[k] = __fdiv_rn(r[k], scale);
+                    }
                 }
+                round_to<CT, V>(dst + e0, r);
+                round_to<CT, V>(dst + e1, r + V);
             }
         }
-        if (is_q) {
-            T* dst = (T*)a.q_out + (((long long)b * a.N + j) * a.q_heads + h) * D;
-            VT y;
-#pragma unroll
-            for (int i = 0; i < V; ++i) y.x[i] = Conv<T>::from(r0[i]);
-            *reinterpret_cast<VT*>(dst + e0) = y;
-            if (turns) {
-#pragma unroll
-                for (int i = 0; i < V; ++i) y.x[i] = Conv<T>::from(r1[i]);
-                *reinterpret_cast<VT*>(dst + e1) = y;
-            }
-        } else if (place >= 0) {
-            CT* dst = (CT*)(c.k + place + (h - qn) * c.head_stride);
-            const float ks = c.k_scale ? c.k_scale[h - qn] : 1.0f;
-            VC y;
-#pragma unroll
-            for (int i = 0; i < V; ++i)
-                y.x[i] = Conv<CT>::from(c.k_scale ? __fdiv_rn(r0[i], ks) : r0[i]);
-            *reinterpret_cast<VC*>(dst + e0) = y;
-            if (turns) {
-#pragma unroll
-                for (int i = 0; i < V; ++i)
-                    y.x[i] = Conv<CT>::from(c.k_scale ? __fdiv_rn(r1[i], ks) : r1[i]);
-                *reinterpret_cast<VC*>(dst + e1) = y;
-            }
+    };
+    for (int j = j0; j < j1; ++j) {
+        if (j + 1 < j1) load(next, j + 1, threadIdx.y);
+        write(now, j, threadIdx.y);
+        for (int h0 = threadIdx.y + kAppendHeads * blockDim.y; h0 < heads;
+             h0 += kAppendHeads * blockDim.y) {
+            load(now, j, h0);
+            write(now, j, h0);
         }
-    }
-    if (place < 0) return;
-    constexpr int W = 8;  // dim is a multiple of 16
-    for (int u = tid; u < c.heads * (D / W); u += kAppendThreads) {
-        const int h = u / (D / W), e = (u - h * (D / W)) * W;
-        const T* src = (const T*)a.v + b * a.kb + j * a.kt + h * a.kh + e;
-        const Vec<T, W> x = *reinterpret_cast<const Vec<T, W>*>(src);
-        CT* dst = (CT*)(c.v + place + h * c.head_stride) + e;
-        if constexpr (sizeof(CT) == sizeof(T)) {
-            *reinterpret_cast<Vec<T, W>*>(dst) = x;
-        } else {
-            const float vs = c.v_scale[h];
-            Vec<CT, W> y;
-#pragma unroll
-            for (int i = 0; i < W; ++i) y.x[i] = Conv<CT>::from(__fdiv_rn(Conv<T>::to(x.x[i]), vs));
-            *reinterpret_cast<Vec<CT, W>*>(dst) = y;
-        }
+        now = next;
     }
 }
 
@@ -415,22 +482,6 @@ __device__ __forceinline__ float ex2(float x) {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
-}
-// Two values as a pair of type M in one word (x low), rounded to nearest.
-template <typename M> __device__ __forceinline__ uint32_t pair(float x, float y) {
-    if constexpr (std::is_same<M, __half>::value) {
-        const __half2 h = __floats2half2_rn(x, y);
-        return reinterpret_cast<const uint32_t&>(h);
-    } else {
-        const __nv_bfloat162 h = __floats2bfloat162_rn(x, y);
-        return reinterpret_cast<const uint32_t&>(h);
-    }
-}
-template <typename M> __device__ __forceinline__ float2 unpair(uint32_t w) {
-    if constexpr (std::is_same<M, __half>::value)
-        return __half22float2(reinterpret_cast<const __half2&>(w));
-    else
-        return __bfloat1622float2(reinterpret_cast<const __nv_bfloat162&>(w));
 }
 // The high half of a pair that a low half will make up for: bf16 by leaving off bits.
 template <typename M> __device__ __forceinline__ uint32_t cut(float x, float y) {
@@ -1751,69 +1802,80 @@ struct CommitArgs {
     uint32_t* status;
     int N, units;  // 16-byte units of one slot's entry, all heads
     int head_units;
+    int planes, run;  // layers' keys and values; how many of them a CTA takes
 };
 
 constexpr int kCommitThreads = 128;
 constexpr int kCommitBatch = 8;
 
-// One CTA per sequence, layer, keys or values.  Each thread owns one 16-byte
-// column of the entries and moves it for all accepted nodes in order, eight at a
-// time: the sources of a batch are read before any of its targets is written,
-// and since a_i >= i is increasing, no target is the source of a later batch.
-// Bound by memory (or, for a few rows, by latency): every moved entry is read
-// once and written once.
+// One CTA per sequence and run of planes (a layer's keys or values).  Accepted nodes increase, so
+// those that stay where they are (node i + 1 in place i) come first and the rest moves.  Each
+// thread owns one 16-byte column of the entries; for each plane it moves the column of all nodes
+// in order, eight moves at a time (of several planes, where one has fewer): the sources of a batch
+// are read before any of its targets is written, and since a_i >= i increases, no target is the
+// source of a later batch.  Bound by memory (or, for a few rows, by the chain node - page -
+// entry): every moved entry is read once and written once.
 __global__ void __launch_bounds__(kCommitThreads) kv_commit_kernel(const CommitArgs a) {
     __shared__ long long s_src[kMaxN], s_dst[kMaxN];
     const int b = blockIdx.z, tid = threadIdx.x;
     const Cache& c = a.c;
     const int n = a.num_accepted[b], len = a.kv_len[b];
+    // (asked for before n is known: the row has N nodes)
+    const int32_t* nodes = a.out_nodes + (long long)b * a.N;
+    const int node = a.out_nodes && tid < a.N ? nodes[tid] : 0;
+    const int before = a.out_nodes && tid > 0 && tid < a.N ? nodes[tid - 1] : 0;
     const bool first = blockIdx.x == 0 && blockIdx.y == 0 && tid == 0;
-    uint32_t bad = 0;
     const long long cap = (long long)c.table_width << c.page_shift;
+    uint32_t bad = 0;
+    int stay = 0;
     if (n < -1 || n >= a.N || len < 0 || (long long)len + n + 1 > cap) {
         bad = SV_DEV_BAD_LENGTH;
     } else if (n > 0 && a.out_nodes) {
         int f = 0;
+        const bool stays = tid < n && node == tid + 1;
         if (tid < n) {
-            const int32_t* nodes = a.out_nodes + (long long)b * a.N;
-            const int x = nodes[tid], before = tid ? nodes[tid - 1] : 0;
-            // the last slot within the table bounds them all
-            if (x <= before || x >= a.N) {
+            if (node <= before || node >= a.N) {
                 f = SV_DEV_BAD_TREE;
-            } else if ((long long)len + x >= cap) {
+            } else if ((long long)len + node >= cap) {
                 f = SV_DEV_BAD_LENGTH;
-            } else {
-                const bool stays = x == tid + 1;
-                s_src[tid] = stays ? 0 : slot_offset(c, b, len + x);
-                s_dst[tid] = stays ? -1 : slot_offset(c, b, len + tid + 1);
-                if (!stays && (s_src[tid] < 0 || s_dst[tid] < 0)) f = SV_DEV_BAD_PAGE;
+            } else if (!stays) {
+                s_src[tid] = slot_offset(c, b, len + node);
+                s_dst[tid] = slot_offset(c, b, len + tid + 1);
+                if (s_src[tid] < 0 || s_dst[tid] < 0) f = SV_DEV_BAD_PAGE;
             }
         }
-        bad = __syncthreads_or(f & SV_DEV_BAD_TREE)     ? SV_DEV_BAD_TREE
-              : __syncthreads_or(f & SV_DEV_BAD_LENGTH) ? SV_DEV_BAD_LENGTH
-              : __syncthreads_or(f)                     ? SV_DEV_BAD_PAGE
-                                                        : 0;
+        stay = __syncthreads_count(stays);
+        if (__syncthreads_or(f))
+            bad = __syncthreads_or(f & SV_DEV_BAD_TREE)     ? SV_DEV_BAD_TREE
+                  : __syncthreads_or(f & SV_DEV_BAD_LENGTH) ? SV_DEV_BAD_LENGTH
+                                                            : SV_DEV_BAD_PAGE;
     }
     if (first) {
         if (bad) mark(a.status, b, bad);
         a.kv_len_out[b] = bad ? len : len + n + 1;
     }
     if (bad || n <= 0 || !a.out_nodes) return;
-    char* base = (blockIdx.y & 1 ? c.v : c.k) + (long long)(blockIdx.y >> 1) * a.layer_stride;
     const int u = blockIdx.x * kCommitThreads + tid;
     if (u >= a.units) return;
     const int h = u / a.head_units;
-    base += h * c.head_stride + (u - h * a.head_units) * 16;
-    for (int i0 = 0; i0 < n; i0 += kCommitBatch) {
+    const long long column = h * c.head_stride + (u - h * a.head_units) * 16;
+    const int p0 = blockIdx.y * a.run, p1 = min(a.planes, p0 + a.run);
+    int plane = p0, move = stay;
+    while (plane < p1 && stay < n) {
         uint4 x[kCommitBatch];
+        char* to[kCommitBatch];
+#pragma unroll
+        for (int i = 0; i < kCommitBatch; ++i) {
+            to[i] = nullptr;
+            if (plane >= p1) continue;
+            char* base = (plane & 1 ? c.v : c.k) + (plane >> 1) * a.layer_stride + column;
+            x[i] = *reinterpret_cast<const uint4*>(base + s_src[move]);
+            to[i] = base + s_dst[move];
+            if (++move == n) move = stay, ++plane;
+        }
 #pragma unroll
         for (int i = 0; i < kCommitBatch; ++i)
-            if (i0 + i < n && s_dst[i0 + i] >= 0)
-                x[i] = *reinterpret_cast<const uint4*>(base + s_src[i0 + i]);
-#pragma unroll
-        for (int i = 0; i < kCommitBatch; ++i)
-            if (i0 + i < n && s_dst[i0 + i] >= 0)
-                *reinterpret_cast<uint4*>(base + s_dst[i0 + i]) = x[i];
+            if (to[i]) *reinterpret_cast<uint4*>(to[i]) = x[i];
     }
 }
 
@@ -2005,15 +2067,26 @@ static sv_status check_tokens(const sv_kv_cache* c, sv_dtype dtype, const int32_
 }
 
 template <typename T, typename CT>
-static void launch_append(const AppendArgs& a, int B, cudaStream_t s) {
-    const dim3 grid(a.N, B);
-    // whole 16-byte accesses when the rotated and the remaining part allow it
-    if (a.rot % 16 == 0)
-        kv_append_kernel<T, CT, 8><<<grid, kAppendThreads, 0, s>>>(a);
-    else if (a.rot % 8 == 0)
-        kv_append_kernel<T, CT, 4><<<grid, kAppendThreads, 0, s>>>(a);
+static void launch_append(AppendArgs& a, int B, int sms, cudaStream_t s) {
+    // whole 16-byte accesses when the rotated part allows it
+    const int V = a.rot % 16 == 0 ? 8 : a.rot % 8 == 0 ? 4 : 1;
+    const int units = a.c.dim / (2 * V), heads = (a.q ? a.q_heads : 0) + 2 * a.c.heads;
+    // A head per thread where that makes a small block, else two (and more passes past that).
+    const int want = heads * units <= 256 ? heads : (heads + kAppendHeads - 1) / kAppendHeads;
+    const int side_by_side = want < kAppendThreads / units ? want : kAppendThreads / units;
+    // Runs of tokens once there are more of them than CTAs resident twice over: a run pays its
+    // chain of lengths, pages and angles once (16640 tokens of 80 heads: a token per CTA 179 us,
+    // four 120 us); fewer tokens are spread over the SMs.
+    const long long tokens = (long long)a.N * B / (6ll * sms);
+    a.run = tokens < 1 ? 1 : tokens > kAppendTokens ? kAppendTokens : (int)tokens;
+    const dim3 grid((a.N + a.run - 1) / a.run, B), block(units, side_by_side);
+    auto go = [&](auto kernel) { kernel<<<grid, block, 0, s>>>(a); };
+    if (V == 8)
+        a.interleaved ? go(kv_append_kernel<T, CT, 8, true>) : go(kv_append_kernel<T, CT, 8, false>);
+    else if (V == 4)
+        a.interleaved ? go(kv_append_kernel<T, CT, 4, true>) : go(kv_append_kernel<T, CT, 4, false>);
     else
-        kv_append_kernel<T, CT, 1><<<grid, kAppendThreads, 0, s>>>(a);
+        a.interleaved ? go(kv_append_kernel<T, CT, 1, true>) : go(kv_append_kernel<T, CT, 1, false>);
 }
 
 static sv_status launched() { return cudaGetLastError() == cudaSuccess ? SV_OK : SV_ERR_CUDA; }
@@ -2091,14 +2164,14 @@ sv_status spec_kv_append(const sv_kv_cache* cache, const sv_rope* rope, const vo
     a.q_heads = q_heads;
     if (dtype == SV_BF16) {
         if (cache->dtype == SV_E4M3)
-            launch_append<__nv_bfloat16, __nv_fp8_e4m3>(a, B, stream);
+            launch_append<__nv_bfloat16, __nv_fp8_e4m3>(a, B, sms, stream);
         else
-            launch_append<__nv_bfloat16, __nv_bfloat16>(a, B, stream);
+            launch_append<__nv_bfloat16, __nv_bfloat16>(a, B, sms, stream);
     } else {
         if (cache->dtype == SV_E4M3)
-            launch_append<__half, __nv_fp8_e4m3>(a, B, stream);
+            launch_append<__half, __nv_fp8_e4m3>(a, B, sms, stream);
         else
-            launch_append<__half, __half>(a, B, stream);
+            launch_append<__half, __half>(a, B, sms, stream);
     }
     return launched();
 }
@@ -2222,7 +2295,12 @@ sv_status spec_kv_commit(const sv_kv_cache* cache, int layers, int64_t layer_str
     a.N = N;
     a.head_units = cache->dim * e / 16;
     a.units = cache->heads * a.head_units;
-    const dim3 grid((a.units + kCommitThreads - 1) / kCommitThreads, 2 * layers, B);
+    // Few CTAs per SM more than are resident: a CTA's chain node - page is paid once per run.
+    const long long ctas = (a.units + kCommitThreads - 1) / kCommitThreads;
+    a.planes = 2 * layers;
+    a.run = (int)((a.planes * ctas * B + 16ll * sms - 1) / (16ll * sms));
+    a.run = a.run < 1 ? 1 : a.run > a.planes ? a.planes : a.run;
+    const dim3 grid((unsigned)ctas, (a.planes + a.run - 1) / a.run, B);
     kv_commit_kernel<<<grid, kCommitThreads, 0, stream>>>(a);
     return launched();
 }
