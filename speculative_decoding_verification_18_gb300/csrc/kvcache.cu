@@ -504,12 +504,10 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
         : "=f"(d.x), "=f"(d.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
     return d;
 }
-// Two e4m3 bytes (the low half of w) as two halves: exact.
-__device__ __forceinline__ uint32_t widen(uint32_t w) {
-    uint32_t r;
-    asm("{ .reg .b16 lo, hi; mov.b32 {lo, hi}, %1; cvt.rn.f16x2.e4m3x2 %0, lo; }"
-        : "=r"(r) : "r"(w));
-    return r;
+// Four e4m3 bytes as two pairs of halves (bytes 0 and 1, bytes 2 and 3): exact.
+__device__ __forceinline__ void widen(uint32_t& low, uint32_t& high, uint32_t w) {
+    asm("{ .reg .b16 l, h; mov.b32 {l, h}, %2; cvt.rn.f16x2.e4m3x2 %0, l; "
+        "cvt.rn.f16x2.e4m3x2 %1, h; }" : "=r"(low), "=r"(high) : "r"(w));
 }
 
 // Layout of a warp's stage: 16 keys, then 16 values, rows of DP elements whose 16-byte chunks
@@ -529,45 +527,61 @@ template <typename CT, int DP> struct Stage {
     }
 };
 
-template <typename CT, int DP, int MI> constexpr int split_smem() {
-    const int ring = 4 * Stage<CT, DP>::kStages * Stage<CT, DP>::kBytes;
-    const int merge = 4 * MI * 16 * (DP + 8) * 4 + 4 * MI * 16 * 8;
-    return ring > merge ? ring : merge;
-}
-
 // Whether node j's row may look at new token i of the sequence (bit i - 1 of its ancestors).
 __device__ __forceinline__ bool sees(uint64_t anc, int i) { return i == 0 || (anc >> (i - 1) & 1); }
 
-// Rows of a CTA: MI * 16.  Each of the four warps walks its own 16 slots of every unit, with its
-// own ring of stages filled by 16-byte asynchronous copies, its own running maximum, sum and
-// output; no barrier inside a piece.  The four are joined in shared memory at a piece's end.
-// Matrix products by mma.sync: with at most 32 rows the tensor pipe has time to spare (measured
-// against the memory's share of a stage), and the weights may take two products: P = hi + lo,
-// two 16-bit halves, so that rounding the weights costs nothing next to rounding the result.
-// float8 caches become halves on the way into the registers (exact), with a power of two taken
-// out of each query row so that a bfloat16 query fits a half too; their weights are single
-// halves, four bits finer than a bfloat16 result.
-template <typename T, typename CT, int DP, int MI>
-__global__ void __launch_bounds__(kSplitThreads, 2) kv_split_kernel(const AttentionArgs a) {
+// Rows of a CTA: WM * 16, at most 32.  Each of the four slot groups walks its own 16 slots of
+// every unit, with its own ring of stages filled by 16-byte asynchronous copies; in it a warp per
+// 16 rows keeps its own running maximum, sum and output (one warp: no barrier inside a piece; two
+// share the ring and meet once per stage, and keep their queries in shared memory, so that 16
+// warps fit an SM).  The four groups are joined in shared memory at a piece's end.  Matrix
+// products by mma.sync: with at most 32 rows the tensor pipe has time to spare, and the weights
+// may take two products: P = hi + lo, two 16-bit halves, so that rounding the weights costs
+// nothing next to rounding the result.  float8 caches become halves on the way into the registers
+// (exact), with a power of two taken out of each query row so that a bfloat16 query fits a half
+// too; their weights are single halves, four bits finer than a bfloat16 result.
+template <typename CT, int DP, int WM> struct Split {
+    using St = Stage<CT, DP>;
+    static constexpr int kRows = WM * 16, kPitch = DP + 8;  // floats: rows eight banks apart
+    static constexpr int kRing = 4 * St::kStages * St::kBytes;
+    static constexpr int kMerge = 4 * kRows * kPitch * 4 + 4 * kRows * 8;
+    static constexpr int kBody = kRing > kMerge ? kRing : kMerge;
+    static constexpr int kSmem = kBody + (WM > 1 ? kRows * DP * 2 : 0);  // + queries
+};
+
+template <typename T, typename CT, int DP, int WM>
+__global__ void __launch_bounds__(kSplitThreads * WM, 2) kv_split_kernel(const AttentionArgs a) {
     constexpr bool kF8 = sizeof(CT) == 1;
     using M = typename std::conditional<kF8, __half, T>::type;  // type of the products
-    constexpr bool kLo = !kF8 || std::is_same<T, __half>::value;
+    constexpr bool kFit = !kF8 || std::is_same<T, __half>::value;  // queries are of it already
+    constexpr bool kLo = kFit;
     using St = Stage<CT, DP>;
-    constexpr int S = St::kStages, KS = DP / 16, NT = DP / 8, ROWS = MI * 16;
+    using L = Split<CT, DP, WM>;
+    constexpr int S = St::kStages, KS = DP / 16, NT = DP / 8, ROWS = L::kRows;
+    constexpr int THREADS = kSplitThreads * WM;
     extern __shared__ __align__(128) char smem[];
-    __shared__ long long s_scan[4];
+    __shared__ long long s_scan[THREADS / 32];
     __shared__ Start s_start;
     __shared__ int s_par[kMaxN];
     __shared__ uint64_t s_anc[kMaxN];
-    const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5, t4 = lane & 3;
+    const int tid = threadIdx.x, lane = tid & 31, t4 = lane & 3;
+    const int w = tid >> 5 & 3, wm = tid >> 7;  // slot group, row tile
     const Cache& c = a.c;
+    auto group_sync = [&]() {
+        if constexpr (WM == 1)
+            __syncwarp();
+        else
+            asm volatile("bar.sync %0, %1;" ::"r"(1 + w), "r"(32 * WM) : "memory");
+    };
 
     cudaGridDependencySynchronize();
     cudaTriggerProgrammaticLaunchCompletion();
 
-    Walk walk = start_walk<kSplitThreads>(a, ROWS, kUnit, s_scan, &s_start);
+    Walk walk = start_walk<THREADS>(a, ROWS, kUnit, s_scan, &s_start);
     const Share& sh = walk.sh;
-    const uint32_t ring = (uint32_t)__cvta_generic_to_shared(smem) + w * S * St::kBytes;
+    const uint32_t base = (uint32_t)__cvta_generic_to_shared(smem);
+    const uint32_t ring = base + w * S * St::kBytes;
+    const uint32_t queries = base + L::kBody + wm * KS * 512 + lane * 16;
     int anc_of = -1;  // the sequence whose ancestors s_anc holds
 
     Piece piece;
@@ -582,7 +596,7 @@ __global__ void __launch_bounds__(kSplitThreads, 2) kv_split_kernel(const Attent
             __syncthreads();
             int f = 0;
             if (a.parents)
-                for (int i = tid; i < sh.n; i += kSplitThreads) {
+                for (int i = tid; i < sh.n; i += THREADS) {
                     const int p = a.parents[(long long)b * a.N + i];
                     s_par[i] = p;
                     f |= i > 0 && (p < 0 || p >= i);
@@ -606,77 +620,17 @@ __global__ void __launch_bounds__(kSplitThreads, 2) kv_split_kernel(const Attent
             }
         }
 
-        // Queries as the A operand: thread (row lane / 4, + 8; elements by lane % 4).
-        uint32_t qa[MI][KS][4];
-        float mul[MI][2];  // from a product to the exponent (base 2)
-        const float unit = a.scale * 1.4426950408889634f * (kF8 ? c.k_scale[h] : 1.0f);
-#pragma unroll
-        for (int mi = 0; mi < MI; ++mi) {
-#pragma unroll
-            for (int half = 0; half < 2; ++half) {
-                const int row = mi * 16 + half * 8 + (lane >> 2), R = mt * ROWS + row;
-                const int j = R / a.group, g = R - j * a.group;
-                const bool live = row < rows && !bad;
-                const T* q = (const T*)a.q + (live ? b * a.qb + j * a.qt +
-                                                         (long long)(h * a.group + g) * a.qh : 0);
-                float top = 0.0f;
-#pragma unroll
-                for (int ks = 0; ks < KS; ++ks) {
-                    // float8: 16 consecutive elements of a block of 64 per thread, 4 per step
-                    const int e0 = kF8 ? (ks >> 2) * 64 + t4 * 16 + (ks & 3) * 4 : ks * 16 + t4 * 2;
-                    const int e1 = kF8 ? e0 + 2 : e0 + 8;
-                    const bool in = live && (kF8 ? e0 : ks * 16) < c.dim;
-                    const uint32_t w0 = in ? __ldg((const uint32_t*)(q + e0)) : 0u;
-                    const uint32_t w1 = in ? __ldg((const uint32_t*)(q + e1)) : 0u;
-                    qa[mi][ks][half] = w0;
-                    qa[mi][ks][half + 2] = w1;
-                    if constexpr (kF8 && !std::is_same<T, __half>::value) {
-                        const float2 f0 = unpair<T>(w0), f1 = unpair<T>(w1);
-                        top = fmaxf(fmaxf(top, fmaxf(fabsf(f0.x), fabsf(f0.y))),
-                                    fmaxf(fabsf(f1.x), fabsf(f1.y)));
-                    }
-                }
-                mul[mi][half] = unit;
-                if constexpr (kF8 && !std::is_same<T, __half>::value) {
-                    top = fmaxf(top, __shfl_xor_sync(~0u, top, 1));
-                    top = fmaxf(top, __shfl_xor_sync(~0u, top, 2));
-                    // the row's largest element becomes 2^8 .. 2^9: what then falls below the
-                    // smallest half is 2^-33 of it
-                    int e = top > 0.0f && top < INFINITY ? ilogbf(top) - 8 : 0;
-                    e = max(-100, min(100, e));
-                    const float down = exp2f((float)-e);
-                    mul[mi][half] = unit * exp2f((float)e);
-#pragma unroll
-                    for (int ks = 0; ks < KS; ++ks)
-#pragma unroll
-                        for (int k = half; k < 4; k += 2) {
-                            const float2 f = unpair<T>(qa[mi][ks][k]);
-                            qa[mi][ks][k] = pair<__half>(f.x * down, f.y * down);
-                        }
-                }
-            }
-        }
-
-        float o[MI][NT][4], l[MI][2], mr[MI][2];
-#pragma unroll
-        for (int mi = 0; mi < MI; ++mi) {
-            l[mi][0] = l[mi][1] = 0.0f;
-            mr[mi][0] = mr[mi][1] = -INFINITY;
-#pragma unroll
-            for (int k = 0; k < NT; ++k) o[mi][k][0] = o[mi][k][1] = o[mi][k][2] = o[mi][k][3] = 0.0f;
-        }
-        bool bad_page = false;
-
         const char* kb = c.k + h * c.head_stride;
         const char* vb = c.v + h * c.head_stride;
         const int32_t* table = c.table + (long long)b * c.table_width;
         const int my = w * 16 + (lane & 15);  // the slot of a unit whose page this lane looks up
         const int dch = c.dim * (int)sizeof(CT) / 16;
+        bool bad_page = false;
         auto page_of = [&](int t) -> int {
             const int s = t * kUnit + my;
             return t < t1 && s < total ? __ldg(table + (s >> c.page_shift)) : -1;
         };
-        auto issue = [&](int t, int page) {
+        auto issue = [&](int t, int stage, int page) {
             const int s = t * kUnit + my;
             long long off = -1;
             if (t < t1 && s < total) {
@@ -686,11 +640,13 @@ __global__ void __launch_bounds__(kSplitThreads, 2) kv_split_kernel(const Attent
                     bad_page = true;
             }
             if (t < t1) {
-                const uint32_t dst = ring + (t - t0) % S * St::kBytes;
-                constexpr int kRows = 32 / St::kChunks;
+                const uint32_t dst = ring + stage * St::kBytes;
+                constexpr int kRows = 32 / St::kChunks;  // rows per instruction
+                constexpr int kMine = 16 / kRows / WM;
 #pragma unroll
-                for (int i = 0; i < 16 / kRows; ++i) {
-                    const int row = i * kRows + lane / St::kChunks, ch = lane % St::kChunks;
+                for (int i = 0; i < kMine; ++i) {
+                    const int row = (i * WM + wm) * kRows + lane / St::kChunks;
+                    const int ch = lane % St::kChunks;
                     const long long f = __shfl_sync(~0u, off, row);
                     const bool take = f >= 0 && ch < dch;
                     const long long at = take ? f + ch * 16 : 0;
@@ -707,120 +663,186 @@ __global__ void __launch_bounds__(kSplitThreads, 2) kv_split_kernel(const Attent
             for (int i = 0; i < S - 1; ++i) first[i] = page_of(t0 + i);
             page = page_of(t0 + S - 1);
 #pragma unroll
-            for (int i = 0; i < S - 1; ++i) issue(t0 + i, first[i]);
+            for (int i = 0; i < S - 1; ++i) issue(t0 + i, i, first[i]);
         }
 
+        // Queries as the A operand: thread (row lane / 4, + 8; elements by lane % 4), with the
+        // sign of the scale, so that the largest product is the largest exponent.
+        uint32_t qa[KS][4];
+        float mul[2];  // from a product to the exponent (base 2); never 0, for 0 * -inf is NaN
+        const float unit = fabsf(a.scale) * 1.4426950408889634f * (kF8 ? c.k_scale[h] : 1.0f);
+        const uint32_t sign = a.scale < 0.0f ? 0x80008000u : 0u;
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+            const int row = wm * 16 + half * 8 + (lane >> 2), R = mt * ROWS + row;
+            const int j = R / a.group, g = R - j * a.group;
+            const bool live = row < rows && !bad;
+            const T* q = (const T*)a.q + (live ? b * a.qb + j * a.qt +
+                                                     (long long)(h * a.group + g) * a.qh : 0);
+            float top = 0.0f;
+#pragma unroll
+            for (int ks = 0; ks < KS; ++ks) {
+                // float8: 16 consecutive elements of a block of 64 per thread, 4 per step
+                const int e0 = kF8 ? (ks >> 2) * 64 + t4 * 16 + (ks & 3) * 4 : ks * 16 + t4 * 2;
+                const int e1 = kF8 ? e0 + 2 : e0 + 8;
+                const bool in = live && (kF8 ? e0 : ks * 16) < c.dim;
+                const uint32_t w0 = in ? __ldg((const uint32_t*)(q + e0)) ^ sign : 0u;
+                const uint32_t w1 = in ? __ldg((const uint32_t*)(q + e1)) ^ sign : 0u;
+                qa[ks][half] = w0;
+                qa[ks][half + 2] = w1;
+                if constexpr (!kFit) {
+                    const float2 f0 = unpair<T>(w0), f1 = unpair<T>(w1);
+                    top = fmaxf(fmaxf(top, fmaxf(fabsf(f0.x), fabsf(f0.y))),
+                                fmaxf(fabsf(f1.x), fabsf(f1.y)));
+                }
+            }
+            mul[half] = fmaxf(unit, 1e-37f);
+            if constexpr (!kFit) {
+                top = fmaxf(top, __shfl_xor_sync(~0u, top, 1));
+                top = fmaxf(top, __shfl_xor_sync(~0u, top, 2));
+                // the row's largest element becomes 2^8 .. 2^9: what then falls below the smallest
+                // half is 2^-33 of it
+                int e = top > 0.0f && top < INFINITY ? ilogbf(top) - 8 : 0;
+                e = max(-100, min(100, e));
+                const float down = exp2f((float)-e);
+                mul[half] = fmaxf(unit * exp2f((float)e), 1e-37f);
+#pragma unroll
+                for (int ks = 0; ks < KS; ++ks)
+#pragma unroll
+                    for (int k = half; k < 4; k += 2) {
+                        const float2 f = unpair<T>(qa[ks][k]);
+                        qa[ks][k] = pair<__half>(f.x * down, f.y * down);
+                    }
+            }
+        }
+        if constexpr (WM > 1) {  // kept in shared memory, as each lane will want them
+            if (w == 0)
+#pragma unroll
+                for (int ks = 0; ks < KS; ++ks)
+                    asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(queries + ks * 512),
+                                 "r"(qa[ks][0]), "r"(qa[ks][1]), "r"(qa[ks][2]), "r"(qa[ks][3])
+                                 : "memory");
+            __syncthreads();
+        }
+        auto query = [&](int ks, uint32_t (&f)[4]) {
+            if constexpr (WM > 1)
+                asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
+                             : "=r"(f[0]), "=r"(f[1]), "=r"(f[2]), "=r"(f[3])
+                             : "r"(queries + ks * 512) : "memory");
+            else
+                for (int k = 0; k < 4; ++k) f[k] = qa[ks][k];
+        };
+
+        float o[NT][4], l[2] = {0.0f, 0.0f}, mr[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+        for (int k = 0; k < NT; ++k) o[k][0] = o[k][1] = o[k][2] = o[k][3] = 0.0f;
+
+        int stage = 0;
         for (int t = t0; t < t1 && !bad; ++t) {
             asm volatile("cp.async.wait_group %0;" ::"n"(S - 2) : "memory");
-            __syncwarp();
-            issue(t + S - 1, page);
+            group_sync();
+            issue(t + S - 1, stage == 0 ? S - 1 : stage - 1, page);
             page = page_of(t + S);
+            const uint32_t kt = ring + stage * St::kBytes, vt = kt + 16 * St::kPitch;
+            stage = stage == S - 1 ? 0 : stage + 1;
             const int slot0 = t * kUnit + w * 16;
             if (slot0 >= total) continue;
-            const uint32_t kt = ring + (t - t0) % S * St::kBytes, vt = kt + 16 * St::kPitch;
 
             // Scores: 16 slots = two tiles of 8 columns.
-            float s[MI][2][4];
+            float s[2][4];
 #pragma unroll
-            for (int mi = 0; mi < MI; ++mi)
-#pragma unroll
-                for (int k = 0; k < 4; ++k) s[mi][0][k] = s[mi][1][k] = 0.0f;
+            for (int k = 0; k < 4; ++k) s[0][k] = s[1][k] = 0.0f;
             if constexpr (!kF8) {
 #pragma unroll
                 for (int ks = 0; ks < KS; ++ks) {
-                    uint32_t f[4];
+                    uint32_t f[4], q[4];
                     const int row = (lane & 7) + (lane >> 4) * 8, ch = ks * 2 + (lane >> 3 & 1);
                     ldsm4(f, kt + St::at(row, ch));
-#pragma unroll
-                    for (int mi = 0; mi < MI; ++mi) {
-                        mma<M>(s[mi][0], qa[mi][ks], f[0], f[1]);
-                        mma<M>(s[mi][1], qa[mi][ks], f[2], f[3]);
-                    }
+                    query(ks, q);
+                    mma<M>(s[0], q, f[0], f[1]);
+                    mma<M>(s[1], q, f[2], f[3]);
                 }
             } else {
 #pragma unroll
-                for (int kb4 = 0; kb4 < DP / 64; ++kb4)
+                for (int kb4 = 0; kb4 < DP / 64; ++kb4) {
+                    uint32_t f[2][4];
 #pragma unroll
-                    for (int nt = 0; nt < 2; ++nt) {
-                        uint32_t f[4];
-                        const uint32_t at = kt + St::at(nt * 8 + (lane >> 2), kb4 * 4 + t4);
+                    for (int nt = 0; nt < 2; ++nt)
                         asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
-                                     : "=r"(f[0]), "=r"(f[1]), "=r"(f[2]), "=r"(f[3])
-                                     : "r"(at) : "memory");
-#pragma unroll
-                        for (int k = 0; k < 4; ++k) {
-                            const uint32_t b0 = widen(f[k]), b1 = widen(f[k] >> 16);
-#pragma unroll
-                            for (int mi = 0; mi < MI; ++mi)
-                                mma<M>(s[mi][nt], qa[mi][kb4 * 4 + k], b0, b1);
-                        }
-                    }
-            }
-            const bool fresh = slot0 + 16 > len;  // new tokens or the end are among the 16
-#pragma unroll
-            for (int mi = 0; mi < MI; ++mi) {
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    s[mi][0][k] *= mul[mi][k >> 1];
-                    s[mi][1][k] *= mul[mi][k >> 1];
-                }
-                if (fresh) {
-#pragma unroll
-                    for (int half = 0; half < 2; ++half) {
-                        const int R = mt * ROWS + mi * 16 + half * 8 + (lane >> 2);
-                        const uint64_t anc = s_anc[min(R / a.group, sh.n - 1)];
-#pragma unroll
-                        for (int k = 0; k < 4; ++k) {
-                            const int i = slot0 + (k >> 1) * 8 + t4 * 2 + (k & 1) - len;
-                            if (i >= 0 && (i >= sh.n || !sees(anc, i)))
-                                s[mi][k >> 1][half * 2 + (k & 1)] = -INFINITY;
-                        }
-                    }
-                }
-                // The reference of a row follows its maximum only when that has grown by 2^8:
-                // weights stay below 2^8 and the output is rarely rescaled.
-                float mx[2];
-#pragma unroll
-                for (int half = 0; half < 2; ++half) {
-                    mx[half] = fmaxf(fmaxf(s[mi][0][half * 2], s[mi][0][half * 2 + 1]),
-                                     fmaxf(s[mi][1][half * 2], s[mi][1][half * 2 + 1]));
-                    mx[half] = fmaxf(mx[half], __shfl_xor_sync(~0u, mx[half], 1));
-                    mx[half] = fmaxf(mx[half], __shfl_xor_sync(~0u, mx[half], 2));
-                }
-                const bool grow0 = mx[0] > mr[mi][0] + 8.0f, grow1 = mx[1] > mr[mi][1] + 8.0f;
-                if (__any_sync(~0u, grow0 || grow1)) {
-                    const float f0 = grow0 ? ex2(mr[mi][0] - mx[0]) : 1.0f;
-                    const float f1 = grow1 ? ex2(mr[mi][1] - mx[1]) : 1.0f;
-                    if (grow0) mr[mi][0] = mx[0];
-                    if (grow1) mr[mi][1] = mx[1];
-                    l[mi][0] *= f0;
-                    l[mi][1] *= f1;
-#pragma unroll
-                    for (int k = 0; k < NT; ++k) {
-                        o[mi][k][0] *= f0;
-                        o[mi][k][1] *= f0;
-                        o[mi][k][2] *= f1;
-                        o[mi][k][3] *= f1;
-                    }
-                }
-#pragma unroll
-                for (int half = 0; half < 2; ++half) {
-                    const float ref = mr[mi][half] == -INFINITY ? 0.0f : mr[mi][half];
+                                     : "=r"(f[nt][0]), "=r"(f[nt][1]), "=r"(f[nt][2]),
+                                       "=r"(f[nt][3])
+                                     : "r"(kt + St::at(nt * 8 + (lane >> 2), kb4 * 4 + t4))
+                                     : "memory");
 #pragma unroll
                     for (int k = 0; k < 4; ++k) {
-                        float& p = s[mi][k >> 1][half * 2 + (k & 1)];
-                        p = ex2(p - ref);
-                        l[mi][half] += p;
+                        uint32_t q[4];
+                        query(kb4 * 4 + k, q);
+#pragma unroll
+                        for (int nt = 0; nt < 2; ++nt) {
+                            uint32_t b0, b1;
+                            widen(b0, b1, f[nt][k]);
+                            mma<M>(s[nt], q, b0, b1);
+                        }
                     }
+                }
+            }
+            const bool fresh = slot0 + 16 > len;  // new tokens or the end are among the 16
+            if (fresh) {
+#pragma unroll
+                for (int half = 0; half < 2; ++half) {
+                    const int R = mt * ROWS + wm * 16 + half * 8 + (lane >> 2);
+                    const uint64_t anc = s_anc[min(R / a.group, sh.n - 1)];
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const int i = slot0 + (k >> 1) * 8 + t4 * 2 + (k & 1) - len;
+                        if (i >= 0 && (i >= sh.n || !sees(anc, i)))
+                            s[k >> 1][half * 2 + (k & 1)] = -INFINITY;
+                    }
+                }
+            }
+            // The reference of a row follows its maximum only when that has grown by 2^8: weights
+            // stay below 2^8 and the output is rarely rescaled.
+            float mx[2];
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+                float m = fmaxf(fmaxf(s[0][half * 2], s[0][half * 2 + 1]),
+                                fmaxf(s[1][half * 2], s[1][half * 2 + 1]));
+                m = fmaxf(m, __shfl_xor_sync(~0u, m, 1));
+                m = fmaxf(m, __shfl_xor_sync(~0u, m, 2));
+                mx[half] = m * mul[half];
+            }
+            const bool grow0 = mx[0] > mr[0] + 8.0f, grow1 = mx[1] > mr[1] + 8.0f;
+            if (__any_sync(~0u, grow0 || grow1)) {
+                const float f0 = grow0 ? ex2(mr[0] - mx[0]) : 1.0f;
+                const float f1 = grow1 ? ex2(mr[1] - mx[1]) : 1.0f;
+                if (grow0) mr[0] = mx[0];
+                if (grow1) mr[1] = mx[1];
+                l[0] *= f0;
+                l[1] *= f1;
+#pragma unroll
+                for (int k = 0; k < NT; ++k) {
+                    o[k][0] *= f0;
+                    o[k][1] *= f0;
+                    o[k][2] *= f1;
+                    o[k][3] *= f1;
+                }
+            }
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+                const float ref = mr[half] == -INFINITY ? 0.0f : mr[half];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    float& p = s[k >> 1][half * 2 + (k & 1)];
+                    p = ex2(fmaf(p, mul[half], -ref));
+                    l[half] += p;
                 }
             }
             if (fresh) {
                 // A masked entry may hold anything, but 0 times NaN is NaN: values that are not
                 // finite are taken out of the product and added for the rows that see them.
-                uint32_t wild = 0;
+                bool f = false;
                 const int row = lane >> 1;
                 if (slot0 + row > len && slot0 + row < total) {
-                    bool f = false;
                     for (int ch = (lane & 1); ch < dch; ch += 2) {
                         uint32_t v[4];
                         asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
@@ -837,67 +859,65 @@ __global__ void __launch_bounds__(kSplitThreads, 2) kv_split_kernel(const Attent
                             }
                         }
                     }
-                    wild = f;
                 }
-                wild = __ballot_sync(~0u, wild != 0);
+                const uint32_t wild = __ballot_sync(~0u, f);  // (the same in the group's warps)
                 for (int rw = 0; wild != 0 && rw < 16; ++rw) {
                     if (!(wild >> (2 * rw) & 3)) continue;
                     const int i = slot0 + rw - len;
                     const int from = (lane & ~3) | (rw & 7) >> 1;
 #pragma unroll
-                    for (int mi = 0; mi < MI; ++mi)
+                    for (int half = 0; half < 2; ++half) {
+                        const float pe = rw < 8 ? s[0][half * 2] : s[1][half * 2];
+                        const float po = rw < 8 ? s[0][half * 2 + 1] : s[1][half * 2 + 1];
+                        const float p = __shfl_sync(~0u, rw & 1 ? po : pe, from);
+                        const int R = mt * ROWS + wm * 16 + half * 8 + (lane >> 2);
+                        if (sees(s_anc[min(R / a.group, sh.n - 1)], i)) {
 #pragma unroll
-                        for (int half = 0; half < 2; ++half) {
-                            const float pe = rw < 8 ? s[mi][0][half * 2] : s[mi][1][half * 2];
-                            const float po = rw < 8 ? s[mi][0][half * 2 + 1] : s[mi][1][half * 2 + 1];
-                            const float p = __shfl_sync(~0u, rw & 1 ? po : pe, from);
-                            const int R = mt * ROWS + mi * 16 + half * 8 + (lane >> 2);
-                            if (sees(s_anc[min(R / a.group, sh.n - 1)], i)) {
+                            for (int k = 0; k < NT; ++k)
 #pragma unroll
-                                for (int k = 0; k < NT; ++k)
-#pragma unroll
-                                    for (int e = 0; e < 2; ++e) {
-                                        const int d = kF8 ? (k >> 1) * 16 + t4 * 4 + e * 2 + (k & 1)
-                                                          : k * 8 + t4 * 2 + e;
-                                        const int by = d * (int)sizeof(CT);
-                                        const CT* v = reinterpret_cast<const CT*>(
-                                            smem + (vt + St::at(rw, by >> 4) + (by & 15) -
-                                                    (uint32_t)__cvta_generic_to_shared(smem)));
-                                        o[mi][k][half * 2 + e] += p * Conv<CT>::to(*v);
-                                    }
-                            }
+                                for (int e = 0; e < 2; ++e) {
+                                    const int d = kF8 ? (k >> 1) * 16 + t4 * 4 + e * 2 + (k & 1)
+                                                      : k * 8 + t4 * 2 + e;
+                                    const int by = d * (int)sizeof(CT);
+                                    const CT* v = reinterpret_cast<const CT*>(
+                                        smem + (vt + St::at(rw, by >> 4) + (by & 15) - base));
+                                    o[k][half * 2 + e] += p * Conv<CT>::to(*v);
+                                }
                         }
-                    __syncwarp();
-                    for (int ch = lane; ch < St::kChunks; ch += 32)
-                        asm volatile("st.shared.v4.b32 [%0], {%1,%1,%1,%1};" ::"r"(
-                                         vt + St::at(rw, ch)), "r"(0) : "memory");
-                    __syncwarp();
-                }
-            }
-            uint32_t pa[MI][4], pl[MI][4];
-#pragma unroll
-            for (int mi = 0; mi < MI; ++mi)
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    const float u = s[mi][k >> 1][(k & 1) * 2], v = s[mi][k >> 1][(k & 1) * 2 + 1];
-                    pa[mi][k] = pair<M>(u, v);
-                    if constexpr (kLo) {
-                        const float2 f = unpair<M>(pa[mi][k]);
-                        pl[mi][k] = pair<M>(u - f.x, v - f.y);
+                        __syncwarp();
                     }
                 }
+                if (wild) {
+                    group_sync();  // every warp of the group has added its own
+                    for (int rw = 0; rw < 16; ++rw)
+                        if (wild >> (2 * rw) & 3)
+                            for (int ch = lane; ch < St::kChunks; ch += 32)
+                                asm volatile("st.shared.v4.b32 [%0], {%1,%1,%1,%1};" ::"r"(
+                                                 vt + St::at(rw, ch)), "r"(0) : "memory");
+                    group_sync();
+                }
+            }
+            uint32_t pa[4], pl[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const float u = s[k >> 1][(k & 1) * 2], v = s[k >> 1][(k & 1) * 2 + 1];
+                if constexpr (kLo) {
+                    pa[k] = cut<M>(u, v);
+                    const float2 f = unpair<M>(pa[k]);
+                    pl[k] = pair<M>(u - f.x, v - f.y);
+                } else {
+                    pa[k] = pair<M>(u, v);
+                }
+            }
             if constexpr (!kF8) {
 #pragma unroll
                 for (int dt = 0; dt < KS; ++dt) {
                     uint32_t f[4];
                     ldsm4t(f, vt + St::at(lane & 15, dt * 2 + (lane >> 4)));
-#pragma unroll
-                    for (int mi = 0; mi < MI; ++mi) {
-                        mma<M>(o[mi][2 * dt], pa[mi], f[0], f[1]);
-                        mma<M>(o[mi][2 * dt + 1], pa[mi], f[2], f[3]);
-                        mma<M>(o[mi][2 * dt], pl[mi], f[0], f[1]);
-                        mma<M>(o[mi][2 * dt + 1], pl[mi], f[2], f[3]);
-                    }
+                    mma<M>(o[2 * dt], pa, f[0], f[1]);
+                    mma<M>(o[2 * dt + 1], pa, f[2], f[3]);
+                    mma<M>(o[2 * dt], pl, f[0], f[1]);
+                    mma<M>(o[2 * dt + 1], pl, f[2], f[3]);
                 }
             } else {
                 // a word: elements 2i and 2i + 1 of two slots; the even elements make one tile of
@@ -908,18 +928,14 @@ __global__ void __launch_bounds__(kSplitThreads, 2) kv_split_kernel(const Attent
                     ldsm4t(f, vt + St::at(lane & 15, dt * 2 + (lane >> 4)));
 #pragma unroll
                     for (int k = 0; k < 2; ++k) {
-                        const uint32_t e0 = widen(__byte_perm(f[2 * k], 0, 0x20));
-                        const uint32_t e1 = widen(__byte_perm(f[2 * k + 1], 0, 0x20));
-                        const uint32_t o0 = widen(__byte_perm(f[2 * k], 0, 0x31));
-                        const uint32_t o1 = widen(__byte_perm(f[2 * k + 1], 0, 0x31));
-#pragma unroll
-                        for (int mi = 0; mi < MI; ++mi) {
-                            mma<M>(o[mi][4 * dt + 2 * k], pa[mi], e0, e1);
-                            mma<M>(o[mi][4 * dt + 2 * k + 1], pa[mi], o0, o1);
-                            if constexpr (kLo) {
-                                mma<M>(o[mi][4 * dt + 2 * k], pl[mi], e0, e1);
-                                mma<M>(o[mi][4 * dt + 2 * k + 1], pl[mi], o0, o1);
-                            }
+                        uint32_t e0, e1, o0, o1;
+                        widen(e0, o0, __byte_perm(f[2 * k], 0, 0x3120));
+                        widen(e1, o1, __byte_perm(f[2 * k + 1], 0, 0x3120));
+                        mma<M>(o[4 * dt + 2 * k], pa, e0, e1);
+                        mma<M>(o[4 * dt + 2 * k + 1], pa, o0, o1);
+                        if constexpr (kLo) {
+                            mma<M>(o[4 * dt + 2 * k], pl, e0, e1);
+                            mma<M>(o[4 * dt + 2 * k + 1], pl, o0, o1);
                         }
                     }
                 }
@@ -932,38 +948,36 @@ __global__ void __launch_bounds__(kSplitThreads, 2) kv_split_kernel(const Attent
             bad = true;
         }
 
-        // Join the four warps.
+        // Join the four groups.
         float* so = reinterpret_cast<float*>(smem);
-        constexpr int kP = DP + 8;  // rows of eight banks apart
+        constexpr int kP = L::kPitch;
         float2* sml = reinterpret_cast<float2*>(so + 4 * ROWS * kP);
 #pragma unroll
-        for (int mi = 0; mi < MI; ++mi)
+        for (int half = 0; half < 2; ++half) {
+            const int row = wm * 16 + half * 8 + (lane >> 2);
+            float sum = l[half];
+            sum += __shfl_xor_sync(~0u, sum, 1);
+            sum += __shfl_xor_sync(~0u, sum, 2);
+            if (t4 == 0) sml[w * ROWS + row] = make_float2(mr[half], sum);
+            float* dst = so + (w * ROWS + row) * kP;
+            if constexpr (!kF8) {
 #pragma unroll
-            for (int half = 0; half < 2; ++half) {
-                const int row = mi * 16 + half * 8 + (lane >> 2);
-                float sum = l[mi][half];
-                sum += __shfl_xor_sync(~0u, sum, 1);
-                sum += __shfl_xor_sync(~0u, sum, 2);
-                if (t4 == 0) sml[w * ROWS + row] = make_float2(mr[mi][half], sum);
-                float* dst = so + (w * ROWS + row) * kP;
-                if constexpr (!kF8) {
+                for (int k = 0; k < NT; ++k)
+                    *reinterpret_cast<float2*>(dst + k * 8 + t4 * 2) =
+                        make_float2(o[k][half * 2], o[k][half * 2 + 1]);
+            } else {
 #pragma unroll
-                    for (int k = 0; k < NT; ++k)
-                        *reinterpret_cast<float2*>(dst + k * 8 + t4 * 2) =
-                            make_float2(o[mi][k][half * 2], o[mi][k][half * 2 + 1]);
-                } else {
-#pragma unroll
-                    for (int k = 0; k < NT; k += 2)
-                        *reinterpret_cast<float4*>(dst + k * 8 + t4 * 4) =
-                            make_float4(o[mi][k][half * 2], o[mi][k + 1][half * 2],
-                                        o[mi][k][half * 2 + 1], o[mi][k + 1][half * 2 + 1]);
-                }
+                for (int k = 0; k < NT; k += 2)
+                    *reinterpret_cast<float4*>(dst + k * 8 + t4 * 4) =
+                        make_float4(o[k][half * 2], o[k + 1][half * 2], o[k][half * 2 + 1],
+                                    o[k + 1][half * 2 + 1]);
             }
+        }
         __syncthreads();
         const bool whole = t0 == 0 && t1 == sh.tiles;
         const long long part = 2 * blockIdx.x + (t0 == 0 ? 1 : 0);
         const float vs = kF8 ? c.v_scale[h] : 1.0f;
-        for (int i = tid; i < rows * (DP / 4); i += kSplitThreads) {
+        for (int i = tid; i < rows * (DP / 4); i += THREADS) {
             const int row = i / (DP / 4), d = i % (DP / 4) * 4;
             float2 ml[4];
             float top = -INFINITY;
@@ -973,22 +987,22 @@ __global__ void __launch_bounds__(kSplitThreads, 2) kv_split_kernel(const Attent
                 top = fmaxf(top, ml[k].x);
             }
             const float ref = top == -INFINITY ? 0.0f : top;
-            float L = 0.0f;
+            float sum = 0.0f;
             float4 y = make_float4(0, 0, 0, 0);
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
                 const float f = ex2(ml[k].x - ref);
                 const float4 v = *reinterpret_cast<const float4*>(so + (k * ROWS + row) * kP + d);
-                L += ml[k].y * f;
+                sum += ml[k].y * f;
                 y.x += v.x * f, y.y += v.y * f, y.z += v.z * f, y.w += v.w * f;
             }
-            if (bad) L = NAN;
+            if (bad) sum = NAN;
             if (!whole) {
                 *reinterpret_cast<float4*>(a.part_o + (part * ROWS + row) * DP + d) = y;
-                if (d == 0) a.part_ml[part * ROWS + row] = make_float2(top, L);
+                if (d == 0) a.part_ml[part * ROWS + row] = make_float2(top, sum);
             } else if (d < c.dim) {
                 const int R = mt * ROWS + row, j = R / a.group, g = R - j * a.group;
-                const float f = vs / L;
+                const float f = vs / sum;
                 T* dst = (T*)a.out +
                          (((long long)b * a.N + j) * a.q_heads + h * a.group + g) * c.dim + d;
                 *reinterpret_cast<uint2*>(dst) =
@@ -1014,21 +1028,26 @@ constexpr int kTcThreads = 512;
 constexpr int kTcUnit = 128;  // slots
 constexpr int kTcMaxCtas = 152;
 
-template <int DP, int ROWS> struct Tc {
+template <int DP, int ROWS, bool F8> struct Tc {
     static constexpr int kTile = 128 * DP * 2;          // bytes of 128 keys, values or queries
     static constexpr int kQ = ROWS / 128 * kTile;
     // Stages: what fits beside the queries (the static part stays below 3 KiB), the odd one for
-    // keys, which are wanted first.
+    // keys, which are wanted first.  float8: half as many stages of 16-bit operands, and what is
+    // left for the bytes they are made of.
     static constexpr int kFit = (224 * 1024 - kQ) / kTile;
-    static constexpr int kK = kFit >= 12 ? 6 : (kFit + 1) / 2;
-    static constexpr int kV = kFit >= 12 ? 6 : kFit / 2;
-    static constexpr int kSmem = kQ + (kK + kV) * kTile;
+    static constexpr int kK = F8 ? (DP <= 64 ? 4 : 2) : kFit >= 12 ? 6 : (kFit + 1) / 2;
+    static constexpr int kV = F8 ? (DP <= 64 ? 4 : 2) : kFit >= 12 ? 6 : kFit / 2;
+    static constexpr int kRaw = 128 * DP;               // bytes of 128 float8 keys or values
+    static constexpr int kRawFit = (224 * 1024 - kQ - (kK + kV) * kTile) / (2 * kRaw);
+    static constexpr int kRaws = !F8 ? 0 : kRawFit > 4 ? 4 : kRawFit;  // of each
+    static constexpr int kSmem = kQ + (kK + kV) * kTile + 2 * kRaws * kRaw;
 };
 
 struct TcBars {
     uint64_t q_full, q_empty, epi_done, drain, v_land;
     uint64_t k_full[6], k_empty[6], v_full[6], v_empty[6];
     uint64_t s_full[2], p_full[2], pv_done[2];
+    uint64_t r_full[2][4], r_empty[2][4];  // float8 keys, values as they came
 };
 
 __device__ __forceinline__ uint32_t saddr(const void* p) {
@@ -1193,14 +1212,21 @@ __device__ __forceinline__ bool elect_one() {
     return yes != 0;
 }
 
-template <typename T, int DP, int ROWS>
+// float8 caches: the bytes land in stages of their own, and the four loading warps turn them into
+// halves (exact) in the products' layout; a power of two is taken out of each bfloat16 query row
+// so that it fits halves too, as in the split kernel.
+template <typename T, typename CT, int DP, int ROWS>
 __global__ void __launch_bounds__(kTcThreads, 1)
     kv_wide_kernel(const AttentionArgs a, const __grid_constant__ CUtensorMap kmap,
                    const __grid_constant__ CUtensorMap vmap) {
-    using L = Tc<DP, ROWS>;
+    constexpr bool kF8 = sizeof(CT) == 1;
+    using M = typename std::conditional<kF8, __half, T>::type;  // type of the products
+    constexpr bool kFit = !kF8 || std::is_same<T, __half>::value;  // queries are of it already
+    using L = Tc<DP, ROWS, kF8>;
     constexpr int SK = L::kK, SV = L::kV, CH = DP / 8;
-    // Weights in two halves (P = hi + lo) where the tensor pipe waits for memory anyway.
-    constexpr bool kLo = ROWS == 128;
+    // Weights in two halves (P = hi + lo) where the tensor pipe waits for memory anyway, unless
+    // single ones are four bits finer than the result.
+    constexpr bool kLo = ROWS == 128 && kFit;
     extern __shared__ __align__(1024) char smem_tc[];  // the swizzle counts from 1024
     __shared__ TcBars bars;
     __shared__ long long s_scan[kTcThreads / 32];
@@ -1209,10 +1235,11 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     __shared__ uint64_t s_anc[kMaxN];
     __shared__ uint32_t s_tmem, s_wild[6][4];
     __shared__ float2 s_ml[128];
+    __shared__ int8_t s_exp[2][ROWS];  // powers of two taken out of the queries, by piece parity
     const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
     const Cache& c = a.c;
     const uint32_t sq = saddr(smem_tc);  // queries, then stages of k, then of v
-    const uint32_t sk = sq + L::kQ, sv = sk + SK * L::kTile;
+    const uint32_t sk = sq + L::kQ, sv = sk + SK * L::kTile, sr = sv + SV * L::kTile;
 
     if (tid == 0) {
         bar_init(&bars.q_full, 64);
@@ -1220,8 +1247,13 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         bar_init(&bars.drain, 1);
         bar_init(&bars.epi_done, 256);
         bar_init(&bars.v_land, 1);
-        for (int i = 0; i < SK; ++i) bar_init(&bars.k_full[i], 1), bar_init(&bars.k_empty[i], 1);
-        for (int i = 0; i < SV; ++i) bar_init(&bars.v_full[i], 1), bar_init(&bars.v_empty[i], 1);
+        constexpr int kFill = kF8 ? 128 : 1;
+        for (int i = 0; i < SK; ++i) bar_init(&bars.k_full[i], kFill), bar_init(&bars.k_empty[i], 1);
+        for (int i = 0; i < SV; ++i) bar_init(&bars.v_full[i], kFill), bar_init(&bars.v_empty[i], 1);
+        for (int i = 0; i < 2 * L::kRaws; ++i) {
+            bar_init(&bars.r_full[i & 1][i >> 1], 1);
+            bar_init(&bars.r_empty[i & 1][i >> 1], 128);
+        }
         for (int i = 0; i < 2; ++i) {
             bar_init(&bars.s_full[i], 1);
             bar_init(&bars.p_full[i], 128);
@@ -1246,7 +1278,93 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     volatile int* gave_up = &s_gave_up;
     Piece p;
 
-    if (w >= 8 && w < 12) {
+    if (kF8 && w >= 8 && w < 12) {
+        // ------------------------------------------------ float8: bytes into halves
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+        constexpr int kCh = DP / 16, R = L::kRaws > 0 ? L::kRaws : 1;  // 16-byte chunks of a row
+        const int lt = tid - 256;
+        int rs = 0, ds = 0;  // stages of bytes, of halves (keys and values have as many)
+        uint32_t r_phase = 0, again = 1;
+        bool ok = true;
+        while (walk.next(a, ROWS, kTcUnit, &p)) {
+            if (walk.sh.bad) continue;
+            const int len = walk.sh.len, total = len + walk.sh.n;
+            for (int t = p.t0; t < p.t1; ++t) {
+#pragma unroll 1
+                for (int kv = 0; kv < 2; ++kv) {
+                    const bool tail = kv && (long long)(t + 1) * kTcUnit > len + 1;
+                    ok = ok && warp_wait(&bars.r_full[kv][rs], r_phase, gave_up);
+                    ok = ok && warp_wait(kv ? &bars.v_empty[ds] : &bars.k_empty[ds], again, gave_up);
+                    if (tail) {
+                        named_sync(2, 128);
+                        if (lt < 4) s_wild[ds][lt] = 0;
+                        named_sync(2, 128);
+                    }
+                    const uint32_t src = sr + (2 * rs + kv) * L::kRaw;
+                    const uint32_t dst = (kv ? sv : sk) + ds * L::kTile;
+                    auto read = [&](int i, uint32_t (&v)[4]) {
+                        asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
+                                     : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3])
+                                     : "r"(src + i * 16) : "memory");
+                    };
+                    // Two 16-byte units per chunk; the lanes of the second panel write theirs in
+                    // the other order, so that no two meet in a bank.
+                    auto write = [&](int i, const uint32_t (&v)[4]) {
+                        const int r = i / kCh, ch = i % kCh, flip = ch >> 2 & 1;
+                        const uint32_t row = dst + (ch >> 2) * 16384 + r * 128;
+#pragma unroll
+                        for (int k = 0; k < 2; ++k) {
+                            const int u = k ^ flip;
+                            uint32_t y[4];
+                            widen(y[0], y[1], u ? v[2] : v[0]);
+                            widen(y[2], y[3], u ? v[3] : v[1]);
+                            asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(
+                                row + (((2 * ch + u & 7) ^ (r & 7)) << 4)),
+                                "r"(y[0]), "r"(y[1]), "r"(y[2]), "r"(y[3]) : "memory");
+                        }
+                    };
+                    if (!tail) {
+#pragma unroll 1
+                        for (int i = lt; i < 128 * kCh; i += 512) {
+                            uint32_t v[4][4];
+#pragma unroll
+                            for (int k = 0; k < 4; ++k) read(i + 128 * k, v[k]);
+#pragma unroll
+                            for (int k = 0; k < 4; ++k) write(i + 128 * k, v[k]);
+                        }
+                    } else {
+                        // behind the last token: zeros; new tokens' NaN are zeroed here and added
+                        // row by row
+#pragma unroll 1
+                        for (int i = lt; i < 128 * kCh; i += 128) {
+                            uint32_t v[4];
+                            read(i, v);
+                            const int r = i / kCh;
+                            const long long slot = (long long)t * kTcUnit + r;
+                            bool wild = false;
+#pragma unroll
+                            for (int k = 0; k < 4; ++k) {
+                                if (slot >= total) v[k] = 0;
+#pragma unroll
+                                for (int e = 0; e < 32; e += 8)
+                                    if (slot > len && (v[k] >> e & 0x7f) == 0x7f) {
+                                        wild = true;
+                                        v[k] &= ~(0xffu << e);
+                                    }
+                            }
+                            if (wild) atomicOr(&s_wild[ds][r >> 5], 1u << (r & 31));
+                            write(i, v);
+                        }
+                    }
+                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                    bar_arrive(&bars.r_empty[kv][rs]);
+                    bar_arrive(kv ? &bars.v_full[ds] : &bars.k_full[ds]);
+                }
+                if (++rs == R) rs = 0, r_phase ^= 1;
+                if (++ds == SK) ds = 0, again ^= 1;
+            }
+        }
+    } else if (!kF8 && w >= 8 && w < 12) {
         // ------------------------------------------------ loads: a warp keys, a warp values
         asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
         const bool vals = w > 8;  // warps 10 and 11 only help to look values through
@@ -1338,6 +1456,46 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     } else if (w >= 12) {
         // ------------------------------------------------ products
         asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+        if (kF8 && w == 15) {
+            // float8: bytes of keys and values, a box per page
+            const int shift = min(c.page_shift, 7), boxes = kTcUnit >> shift;
+            constexpr int R = L::kRaws > 0 ? L::kRaws : 1;
+            int pieces = 0, rs = 0;
+            uint32_t again = 1;
+            bool ok = true;
+            while (ok && walk.next(a, ROWS, kTcUnit, &p)) {
+                if (walk.sh.bad) continue;
+                const int total = walk.sh.len + walk.sh.n;
+                const int32_t* table = c.table + (long long)p.b * c.table_width;
+                auto page_of = [&](int t) -> int {
+                    const long long s = (long long)t * kTcUnit + ((long long)lane << shift);
+                    return lane < boxes && t < p.t1 && s < total
+                               ? __ldg(table + (s >> c.page_shift)) : -1;
+                };
+                int page = page_of(p.t0);
+                for (int t = p.t0; ok && t < p.t1; ++t) {
+                    const long long s = (long long)t * kTcUnit + ((long long)lane << shift);
+                    const bool want = lane < boxes && s < total;
+                    const bool good = want && (unsigned)page < (unsigned)c.num_pages;
+                    if (want && !good) s_bad_piece[pieces & 7] = pieces;
+                    const int pg = page, slot = (int)(s & ((1 << c.page_shift) - 1));
+                    page = page_of(t + 1);
+                    const uint32_t bytes = __popc(__ballot_sync(~0u, good)) * ((uint32_t)DP << shift);
+                    for (int kv = 0; ok && kv < 2; ++kv) {
+                        ok = warp_wait(&bars.r_empty[kv][rs], again, gave_up);
+                        if (!ok) break;
+                        if (lane == 0) bar_expect(&bars.r_full[kv][rs], bytes);
+                        __syncwarp();
+                        if (good)
+                            tma_page(sr + (2 * rs + kv) * L::kRaw + (lane << shift) * DP,
+                                     kv ? &vmap : &kmap, 0, p.h, slot, pg, &bars.r_full[kv][rs]);
+                        __syncwarp();
+                    }
+                    if (++rs == R) rs = 0, again ^= 1;
+                }
+                ++pieces;
+            }
+        }
         if (w == 13 || w == 14) {
             // queries: rows of the item, zeros past them
             const int lt = tid & 31 | (w - 13) << 5, dch = c.dim / 8;
@@ -1346,26 +1504,72 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             while (ok && walk.next(a, ROWS, kTcUnit, &p)) {
                 if (walk.sh.bad) continue;
                 ok = warp_wait(&bars.q_empty, (pieces & 1) ^ 1, gave_up);
-#pragma unroll 4
-                for (int i = lt; ok && i < ROWS * CH; i += 64) {
-                    const int row = i / CH, ch = i % CH, R = p.mt * ROWS + row, r = row & 127;
-                    const bool take = row < p.rows && ch < dch;
+                auto query = [&](int row) {
+                    const int R = p.mt * ROWS + (row < p.rows ? row : 0);
                     const int j = R / a.group, g = R - j * a.group;
-                    const T* q = (const T*)a.q + (take ? p.b * a.qb + j * a.qt +
-                                      (long long)(p.h * a.group + g) * a.qh + ch * 8 : 0);
-                    cp_async16(sq + (row >> 7) * L::kTile + (ch >> 3) * 16384 + r * 128 +
-                                   (((ch & 7) ^ (r & 7)) << 4), q, take);
+                    return (const T*)a.q + p.b * a.qb + j * a.qt +
+                           (long long)(p.h * a.group + g) * a.qh;
+                };
+                auto place = [&](int row, int ch) {
+                    const int r = row & 127;
+                    return sq + (row >> 7) * L::kTile + (ch >> 3) * 16384 + r * 128 +
+                           (((ch & 7) ^ (r & 7)) << 4);
+                };
+                if constexpr (kFit) {
+#pragma unroll 4
+                    for (int i = lt; ok && i < ROWS * CH; i += 64) {
+                        const int row = i / CH, ch = i % CH;
+                        const bool take = row < p.rows && ch < dch;
+                        cp_async16(place(row, ch), query(row) + (take ? ch * 8 : 0), take);
+                    }
+                    if (kF8)
+                        for (int row = lt; row < ROWS; row += 64) s_exp[pieces & 1][row] = 0;
+                    asm volatile("cp.async.wait_all;" ::: "memory");
+                } else {
+                    // eight lanes per row: its largest element becomes 2^8 .. 2^9; what then falls
+                    // below the smallest half is 2^-33 of it
+                    for (int row = lt >> 3; ok && row < ROWS; row += 8) {
+                        const T* q = query(row);
+                        Words<8> x[CH / 8];
+                        float top = 0.0f;
+#pragma unroll
+                        for (int k = 0; k < CH / 8; ++k) {
+                            const int ch = k * 8 + (lane & 7);
+                            x[k] = Words<8>{};
+                            if (row < p.rows && ch < dch) x[k] = get<8>(q + ch * 8);
+                            float f[8];
+                            widen_to<T, 8>(f, x[k]);
+#pragma unroll
+                            for (int e = 0; e < 8; ++e) top = fmaxf(top, fabsf(f[e]));
+                        }
+                        for (int k = 4; k; k >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, k));
+                        int e2 = top > 0.0f && top < INFINITY ? ilogbf(top) - 8 : 0;
+                        e2 = max(-100, min(100, e2));
+                        const float down = exp2f((float)-e2);
+                        if ((lane & 7) == 0) s_exp[pieces & 1][row] = (int8_t)e2;
+#pragma unroll
+                        for (int k = 0; k < CH / 8; ++k) {
+                            float f[8];
+                            widen_to<T, 8>(f, x[k]);
+                            asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(
+                                place(row, k * 8 + (lane & 7))),
+                                "r"(pair<__half>(f[0] * down, f[1] * down)),
+                                "r"(pair<__half>(f[2] * down, f[3] * down)),
+                                "r"(pair<__half>(f[4] * down, f[5] * down)),
+                                "r"(pair<__half>(f[6] * down, f[7] * down)) : "memory");
+                        }
+                    }
                 }
-                bar_arrive_copies(&bars.q_full);
+                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                bar_arrive(&bars.q_full);
                 ++pieces;
             }
-            asm volatile("cp.async.wait_all;" ::: "memory");
         }
         if (w == 12) {
-            constexpr uint32_t kPv = product<T>(DP, true);
+            constexpr uint32_t kPv = product<M>(DP, true);
             constexpr uint32_t kPanel = DP > 64 ? 16384 : 1024;  // one panel: not used
             // scores times the sign of the scale: the largest is then the one to look for
-            const uint32_t qk = product<T>(128, false) | (a.scale < 0.0f ? 1u << 13 : 0u);
+            const uint32_t qk = product<M>(128, false) | (a.scale < 0.0f ? 1u << 13 : 0u);
             int ks = 0, vs = 0;  // stages and parities of the next tiles of keys and of values
             uint32_t k_phase = 0, v_phase = 0, pieces = 0, p_phase = 0;
             bool ok = true;
@@ -1374,9 +1578,6 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 const bool two = p.rows > 128;
                 const int nt = p.t1 - p.t0, jobs = two ? 2 * nt : nt;
                 ok = warp_wait(&bars.q_full, pieces & 1, gave_up);
-                // threads copied the queries through the generic proxy, the products read them
-                // through the asynchronous one
-                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                 // Job i belongs to stream i & 1.  Its scores take the place of the weights of job
                 // i - 2, whose product comes before them; products of one thread run in order.
                 // Scores go first, so that each stream's product and next scores are issued
@@ -1500,7 +1701,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             }
             const bool nan_rows = tree_bad && anc_of == p.b;
             const uint64_t anc = anc_of == p.b ? s_anc[j] : 0;
-            const float unit = fabsf(a.scale) * 1.4426950408889634f;  // the products carry the sign
+            // from a score to an exponent of two; the products carry the sign
+            const float unit0 = fabsf(a.scale) * 1.4426950408889634f * (kF8 ? c.k_scale[p.h] : 1.0f);
+            float unit = unit0;
             const bool busy = (two ? st * 128 : 0) + (w & 3) * 32 < p.rows;  // rows in this warp
             float l = 0.0f, ref = -INFINITY;
             int done = 0;  // jobs of this stream
@@ -1521,6 +1724,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 s_phase ^= 1;
                 if (!ok) break;
                 tc_after();
+                if (!kFit && done == 0) unit = unit0 * exp2f((float)s_exp[pieces & 1][row]);
                 if (!busy) {  // rows that nothing comes of: any weights will do
                     tc_before();
                     bar_arrive(&bars.p_full[st]);
@@ -1599,7 +1803,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                         const bool mine_too = sees(anc, n);
                         const float pw = mine_too ? ex2(y * unit - less) : 0.0f;
                         const long long at = slot_offset(c, p.b, len + n);
-                        const T* v = (const T*)(c.v + (at < 0 ? 0 : at) + p.h * c.head_stride);
+                        const CT* v = (const CT*)(c.v + (at < 0 ? 0 : at) + p.h * c.head_stride);
 #pragma unroll 1
                         for (int k = 0; k < c.dim; k += 16) {
                             float o[16];
@@ -1607,7 +1811,11 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                             tc_wait_ld();
                             if (mine_too && at >= 0) {
 #pragma unroll
-                                for (int e = 0; e < 16; ++e) o[e] += pw * Conv<T>::to(v[k + e]);
+                                for (int e = 0; e < 16; ++e) {
+                                    const float y = Conv<CT>::to(v[k + e]);
+                                    // (of float8 rows only what is not finite was zeroed)
+                                    if (!kF8 || y != y) o[e] += pw * y;
+                                }
                             }
                             __syncwarp();
                             tc_st16(oc + k, o);
@@ -1633,13 +1841,13 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                         }
                         sum[e & 1] = add2(sum[e & 1], v);
                         if constexpr (kLo) {
-                            const uint32_t h = cut<T>(v.x, v.y);
-                            const float2 f = unpair<T>(h);
+                            const uint32_t h = cut<M>(v.x, v.y);
+                            const float2 f = unpair<M>(h);
                             const float2 d = add2(v, make_float2(-f.x, -f.y));
                             y[e] = __uint_as_float(h);
-                            y[16 + e] = __uint_as_float(pair<T>(d.x, d.y));
+                            y[16 + e] = __uint_as_float(pair<M>(d.x, d.y));
                         } else {
-                            y[e] = __uint_as_float(pair<T>(v.x, v.y));
+                            y[e] = __uint_as_float(pair<M>(v.x, v.y));
                         }
                     }
                     if constexpr (kLo) tc_st32(sc + 32 * k, y);
@@ -1676,7 +1884,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             if (two || st == 0) {
                 if (nan_piece) l = NAN;
                 const long long part = (2 * (long long)blockIdx.x + (p.t0 == 0 ? 1 : 0)) * ROWS + row;
-                const float inv = 1.0f / l;
+                const float inv = (kF8 ? c.v_scale[p.h] : 1.0f) / l;
 #pragma unroll 1
                 for (int k = 0; k < DP; k += 32) {
                     float o[32];
@@ -1893,13 +2101,13 @@ static auto with_split(sv_dtype dtype, sv_dtype cache, int dim, int rows, F f) {
         using CT = decltype(ct);
         if (dim <= 64)
             return rows <= 16 ? f(kv_split_kernel<T, CT, 64, 1>, kv_join_kernel<T, 64>,
-                                  split_smem<CT, 64, 1>())
+                                  Split<CT, 64, 1>::kSmem)
                               : f(kv_split_kernel<T, CT, 64, 2>, kv_join_kernel<T, 64>,
-                                  split_smem<CT, 64, 2>());
+                                  Split<CT, 64, 2>::kSmem);
         return rows <= 16 ? f(kv_split_kernel<T, CT, 128, 1>, kv_join_kernel<T, 128>,
-                              split_smem<CT, 128, 1>())
+                              Split<CT, 128, 1>::kSmem)
                           : f(kv_split_kernel<T, CT, 128, 2>, kv_join_kernel<T, 128>,
-                              split_smem<CT, 128, 2>());
+                              Split<CT, 128, 2>::kSmem);
     };
     if (dtype == SV_BF16)
         return cache == SV_E4M3 ? sized(__nv_bfloat16(), __nv_fp8_e4m3())
@@ -1908,20 +2116,26 @@ static auto with_split(sv_dtype dtype, sv_dtype cache, int dim, int rows, F f) {
 }
 
 // The same for the wide kernel: tiles of 128 rows, or of two times 128.
-template <typename F> static auto with_wide(sv_dtype dtype, int dim, int rows, F f) {
-    auto sized = [&](auto t) {
+template <typename F>
+static auto with_wide(sv_dtype dtype, sv_dtype cache, int dim, int rows, F f) {
+    auto sized = [&](auto t, auto ct) {
         using T = decltype(t);
+        using CT = decltype(ct);
+        constexpr bool F8 = sizeof(CT) == 1;
         if (dim <= 64)
-            return rows <= 128 ? f(kv_wide_kernel<T, 64, 128>, kv_join_kernel<T, 64>,
-                                   Tc<64, 128>::kSmem)
-                               : f(kv_wide_kernel<T, 64, 256>, kv_join_kernel<T, 64>,
-                                   Tc<64, 256>::kSmem);
-        return rows <= 128 ? f(kv_wide_kernel<T, 128, 128>, kv_join_kernel<T, 128>,
-                               Tc<128, 128>::kSmem)
-                           : f(kv_wide_kernel<T, 128, 256>, kv_join_kernel<T, 128>,
-                               Tc<128, 256>::kSmem);
+            return rows <= 128 ? f(kv_wide_kernel<T, CT, 64, 128>, kv_join_kernel<T, 64>,
+                                   Tc<64, 128, F8>::kSmem)
+                               : f(kv_wide_kernel<T, CT, 64, 256>, kv_join_kernel<T, 64>,
+                                   Tc<64, 256, F8>::kSmem);
+        return rows <= 128 ? f(kv_wide_kernel<T, CT, 128, 128>, kv_join_kernel<T, 128>,
+                               Tc<128, 128, F8>::kSmem)
+                           : f(kv_wide_kernel<T, CT, 128, 256>, kv_join_kernel<T, 128>,
+                               Tc<128, 256, F8>::kSmem);
     };
-    return dtype == SV_BF16 ? sized(__nv_bfloat16()) : sized(__half());
+    if (dtype == SV_BF16)
+        return cache == SV_E4M3 ? sized(__nv_bfloat16(), __nv_fp8_e4m3())
+                                : sized(__nv_bfloat16(), __nv_bfloat16());
+    return cache == SV_E4M3 ? sized(__half(), __nv_fp8_e4m3()) : sized(__half(), __half());
 }
 
 // A cache tensor as the TMA sees it: element, head, slot, page.
@@ -1941,34 +2155,38 @@ static bool cache_map(CUtensorMap* map, void* base, const sv_kv_cache* c) {
                                 (cuuint64_t)c->num_pages};
     const cuuint64_t strides[3] = {(cuuint64_t)c->head_stride * e, (cuuint64_t)c->slot_stride * e,
                                    (cuuint64_t)c->page_stride * e};
-    const cuuint32_t box[4] = {64, 1, (cuuint32_t)(c->page_size < 128 ? c->page_size : 128), 1};
+    // rows of 128 bytes, swizzled, for the products; float8 rows whole, as they are
+    const bool f8 = c->dtype == SV_E4M3;
+    const cuuint32_t box[4] = {f8 && c->dim > 64 ? 128u : 64u, 1,
+                               (cuuint32_t)(c->page_size < 128 ? c->page_size : 128), 1};
     const cuuint32_t step[4] = {1, 1, 1, 1};
     return encode(map,
-                  c->dtype == SV_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
-                                      : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
+                  f8                    ? CU_TENSOR_MAP_DATA_TYPE_UINT8
+                  : c->dtype == SV_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
+                                        : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
                   4, base, dims, strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                  CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  f8 ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B,
+                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 // Shared memory of every attention kernel, once per device.
 static cudaError_t attention_setup() {
     cudaError_t e = cudaSuccess;
-    for (sv_dtype t : {SV_BF16, SV_F16})
-        for (int dim : {64, 128})
-            for (int rows : {128, 256})
-                if (e == cudaSuccess)
-                    e = with_wide(t, dim, rows, [](auto k, auto, int smem) {
-                        // the roles' shares (256 threads of 184, 256 of 72) are those of a launch
-                        // with 128 each: with fewer the larger share would be waited for
-                        cudaFuncAttributes f;
-                        cudaError_t r = cudaFuncGetAttributes(&f, k);
-                        if (r == cudaSuccess && f.numRegs != 128) r = cudaErrorInvalidConfiguration;
-                        return r != cudaSuccess
-                                   ? r
-                                   : cudaFuncSetAttribute(
-                                         k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-                    });
+    for (int i = 0; i < 16 && e == cudaSuccess; ++i) {
+        const sv_dtype t = i & 1 ? SV_F16 : SV_BF16;
+        e = with_wide(t, i & 2 ? SV_E4M3 : t, i & 4 ? 128 : 64, i & 8 ? 256 : 128,
+                      [](auto k, auto, int smem) {
+            // the roles' shares (256 threads of 184, 256 of 72) are those of a launch with 128
+            // each: with fewer the larger share would be waited for
+            cudaFuncAttributes f;
+            cudaError_t r = cudaFuncGetAttributes(&f, k);
+            if (r == cudaSuccess && f.numRegs != 128) r = cudaErrorInvalidConfiguration;
+            return r != cudaSuccess ? r
+                                    : cudaFuncSetAttribute(
+                                          k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        });
+    }
     for (sv_dtype t : {SV_BF16, SV_F16})
         for (bool f8 : {false, true})
             for (int dim : {64, 128})
@@ -2218,7 +2436,7 @@ sv_status spec_kv_attention(const sv_kv_cache* cache, const void* q, const sv_st
     // Few rows: mma.sync, which then waits for memory only.  More: tcgen05, where a page fills
     // whole rows of the swizzle.
     const int rows = N * a.group;
-    const bool wide = rows > 32 && cache->dtype != SV_E4M3 && cache->page_size >= 8;
+    const bool wide = rows > 32 && cache->page_size >= 8;
     CUtensorMap kmap, vmap;
     if (wide && (!cache_map(&kmap, cache->k, cache) || !cache_map(&vmap, cache->v, cache)))
         return SV_ERR_CUDA;
@@ -2243,7 +2461,7 @@ sv_status spec_kv_attention(const sv_kv_cache* cache, const void* q, const sv_st
     auto launch = [&](auto kernel, auto join, int smem) {
         cudaLaunchConfig_t cfg = {};
         cfg.gridDim = dim3(a.ctas);
-        cfg.blockDim = dim3(wide ? kTcThreads : kSplitThreads);
+        cfg.blockDim = dim3(wide ? kTcThreads : kSplitThreads * tile / 16);
         cfg.dynamicSmemBytes = smem;
         cfg.stream = stream;
         cfg.attrs = &pdl;
@@ -2260,7 +2478,7 @@ sv_status spec_kv_attention(const sv_kv_cache* cache, const void* q, const sv_st
         cfg.dynamicSmemBytes = 0;
         return cudaLaunchKernelEx(&cfg, join, a, tile, unit, mts, warps);
     };
-    const cudaError_t e = wide ? with_wide(dtype, cache->dim, rows, launch)
+    const cudaError_t e = wide ? with_wide(dtype, cache->dtype, cache->dim, rows, launch)
                                : with_split(dtype, cache->dtype, cache->dim, rows, launch);
     return e == cudaSuccess ? SV_OK : SV_ERR_CUDA;
 }
