@@ -47,8 +47,6 @@ template <> struct Conv<__half> {
 };
 template <> struct Conv<__nv_fp8_e4m3> {
     static __device__ float to(__nv_fp8_e4m3 x) { return float(x); }
-    // round to nearest, saturating at +-448 (infinities too); NaN stays NaN
-    static __device__ __nv_fp8_e4m3 from(float x) { return __nv_fp8_e4m3(x); }
 };
 
 // Two values as a pair of type M in one word (x low), rounded to nearest.
@@ -452,6 +450,39 @@ __device__ __forceinline__ Walk start_walk(const AttentionArgs& a, int rows, int
     return k;
 }
 
+// Clusters of CTAs, one per item.
+constexpr int kCluster = 8;
+__device__ __forceinline__ int cluster_rank() {
+    int r;
+    asm volatile("mov.u32 %0, %cluster_ctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive;\nbarrier.cluster.wait;" ::: "memory");
+}
+// The same place in the shared memory of CTA k of the cluster.
+template <typename P> __device__ __forceinline__ const P* cluster_at(P* p, int k) {
+    uint64_t r;
+    asm volatile("mapa.u64 %0, %1, %2;" : "=l"(r) : "l"(p), "r"(k));
+    return reinterpret_cast<const P*>(r);
+}
+// The part of its cluster's item that this CTA takes: equal shares of the units, perhaps none.
+// False for an item that the sequence does not have (fewer tokens than the launch counts on).
+__device__ __forceinline__ bool item_piece(const AttentionArgs& a, int rows, int unit, Share* sh,
+                                           Piece* p) {
+    const int mts = (a.N * a.group + rows - 1) / rows, item = blockIdx.x / kCluster;
+    p->mt = item % mts;
+    p->h = item / mts % a.c.heads;
+    p->b = item / mts / a.c.heads;
+    *sh = share_of(a, p->b, rows, unit);
+    if (p->mt >= sh->mts) return false;
+    const int rank = cluster_rank();
+    p->t0 = (int)((long long)sh->tiles * rank / kCluster);
+    p->t1 = (int)((long long)sh->tiles * (rank + 1) / kCluster);
+    p->rows = min(rows, sh->n * a.group - p->mt * rows);
+    return true;
+}
+
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool take) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
                  "r"(take ? 16 : 0));
@@ -545,11 +576,17 @@ template <typename CT, int DP, int WM> struct Split {
     static constexpr int kRows = WM * 16, kPitch = DP + 8;  // floats: rows eight banks apart
     static constexpr int kRing = 4 * St::kStages * St::kBytes;
     static constexpr int kMerge = 4 * kRows * kPitch * 4 + 4 * kRows * 8;
-    static constexpr int kBody = kRing > kMerge ? kRing : kMerge;
+    static constexpr int kShare = kRows * DP * 4 + kRows * 8;  // a cluster's CTA's own sums
+    static constexpr int kBody = kRing > kMerge + kShare ? kRing : kMerge + kShare;
     static constexpr int kSmem = kBody + (WM > 1 ? kRows * DP * 2 : 0);  // + queries
 };
 
-template <typename T, typename CT, int DP, int WM>
+//
+// CLUSTER: a cluster of kCluster CTAs per item instead, each with an equal share of its units,
+// joined through distributed shared memory: one launch and no workspace, for calls of few items
+// and short contexts, whose time is latency (one sequence of 700 positions: 8.4 us with the join
+// kernel, 5.6 us so).
+template <typename T, typename CT, int DP, int WM, bool CLUSTER>
 __global__ void __launch_bounds__(kSplitThreads * WM, 2) kv_split_kernel(const AttentionArgs a) {
     constexpr bool kF8 = sizeof(CT) == 1;
     using M = typename std::conditional<kF8, __half, T>::type;  // type of the products
@@ -577,7 +614,8 @@ __global__ void __launch_bounds__(kSplitThreads * WM, 2) kv_split_kernel(const A
     cudaGridDependencySynchronize();
     cudaTriggerProgrammaticLaunchCompletion();
 
-    Walk walk = start_walk<THREADS>(a, ROWS, kUnit, s_scan, &s_start);
+    Walk walk = {};
+    if constexpr (!CLUSTER) walk = start_walk<THREADS>(a, ROWS, kUnit, s_scan, &s_start);
     const Share& sh = walk.sh;
     const uint32_t base = (uint32_t)__cvta_generic_to_shared(smem);
     const uint32_t ring = base + w * S * St::kBytes;
@@ -585,7 +623,8 @@ __global__ void __launch_bounds__(kSplitThreads * WM, 2) kv_split_kernel(const A
     int anc_of = -1;  // the sequence whose ancestors s_anc holds
 
     Piece piece;
-    while (walk.next(a, ROWS, kUnit, &piece)) {
+    while (CLUSTER ? item_piece(a, ROWS, kUnit, &walk.sh, &piece)
+                   : walk.next(a, ROWS, kUnit, &piece)) {
         const int b = piece.b, h = piece.h, mt = piece.mt, t0 = piece.t0, t1 = piece.t1;
         const int len = sh.len, total = len + sh.n, rows = piece.rows;
         bool bad = sh.bad;
@@ -974,9 +1013,12 @@ __global__ void __launch_bounds__(kSplitThreads * WM, 2) kv_split_kernel(const A
             }
         }
         __syncthreads();
-        const bool whole = t0 == 0 && t1 == sh.tiles;
+        const bool whole = !CLUSTER && t0 == 0 && t1 == sh.tiles;
         const long long part = 2 * blockIdx.x + (t0 == 0 ? 1 : 0);
         const float vs = kF8 ? c.v_scale[h] : 1.0f;
+        // (cluster: this CTA's share, behind what its groups left)
+        float* const mine = so + L::kMerge / 4;
+        float2* const mine_ml = reinterpret_cast<float2*>(mine + ROWS * DP);
         for (int i = tid; i < rows * (DP / 4); i += THREADS) {
             const int row = i / (DP / 4), d = i % (DP / 4) * 4;
             float2 ml[4];
@@ -997,7 +1039,10 @@ __global__ void __launch_bounds__(kSplitThreads * WM, 2) kv_split_kernel(const A
                 y.x += v.x * f, y.y += v.y * f, y.z += v.z * f, y.w += v.w * f;
             }
             if (bad) sum = NAN;
-            if (!whole) {
+            if constexpr (CLUSTER) {
+                *reinterpret_cast<float4*>(mine + row * DP + d) = y;
+                if (d == 0) mine_ml[row] = make_float2(top, sum);
+            } else if (!whole) {
                 *reinterpret_cast<float4*>(a.part_o + (part * ROWS + row) * DP + d) = y;
                 if (d == 0) a.part_ml[part * ROWS + row] = make_float2(top, sum);
             } else if (d < c.dim) {
@@ -1008,6 +1053,41 @@ __global__ void __launch_bounds__(kSplitThreads * WM, 2) kv_split_kernel(const A
                 *reinterpret_cast<uint2*>(dst) =
                     make_uint2(pair<T>(y.x * f, y.y * f), pair<T>(y.z * f, y.w * f));
             }
+        }
+        if constexpr (CLUSTER) {
+            // Every CTA adds up its share of the elements of all eight.
+            cluster_sync();
+            for (int i = cluster_rank() * THREADS + tid; i < rows * (DP / 4);
+                 i += kCluster * THREADS) {
+                const int row = i / (DP / 4), d = i % (DP / 4) * 4;
+                if (d >= c.dim) continue;
+                float2 ml[kCluster];
+                float4 v[kCluster];
+                float top = -INFINITY;
+#pragma unroll
+                for (int k = 0; k < kCluster; ++k) {
+                    ml[k] = *cluster_at(mine_ml + row, k);
+                    v[k] = *reinterpret_cast<const float4*>(cluster_at(mine + row * DP + d, k));
+                    top = fmaxf(top, ml[k].x);
+                }
+                const float ref = top == -INFINITY ? 0.0f : top;
+                float sum = 0.0f;
+                float4 y = make_float4(0, 0, 0, 0);
+#pragma unroll
+                for (int k = 0; k < kCluster; ++k) {
+                    const float f = ex2(ml[k].x - ref);
+                    sum += ml[k].y * f;
+                    y.x += v[k].x * f, y.y += v[k].y * f, y.z += v[k].z * f, y.w += v[k].w * f;
+                }
+                const int R = mt * ROWS + row, j = R / a.group, g = R - j * a.group;
+                const float f = vs / sum;
+                T* dst = (T*)a.out +
+                         (((long long)b * a.N + j) * a.q_heads + h * a.group + g) * c.dim + d;
+                *reinterpret_cast<uint2*>(dst) =
+                    make_uint2(pair<T>(y.x * f, y.y * f), pair<T>(y.z * f, y.w * f));
+            }
+            cluster_sync();  // nobody leaves while its share is being read
+            break;           // an item is all there is
         }
         __syncthreads();
     }
@@ -1071,10 +1151,6 @@ __device__ __forceinline__ void tma_page(uint32_t dst, const CUtensorMap* map, i
         "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
         "[%0], [%1, {%2, %3, %4, %5}], [%6];"
         ::"r"(dst), "l"(map), "r"(x), "r"(h), "r"(s), "r"(p), "r"(saddr(bar)) : "memory");
-}
-// Arrives when this thread's asynchronous copies so far have landed.
-__device__ __forceinline__ void bar_arrive_copies(uint64_t* bar) {
-    asm volatile("cp.async.mbarrier.arrive.noinc.shared.b64 [%0];" ::"r"(saddr(bar)) : "memory");
 }
 constexpr uint64_t kGiveUp = 2000000000;  // two seconds
 __device__ __forceinline__ uint64_t nanoseconds() {
@@ -2015,6 +2091,7 @@ struct CommitArgs {
 
 constexpr int kCommitThreads = 128;
 constexpr int kCommitBatch = 8;
+constexpr int kCommitResident = 8;  // CTAs per SM
 
 // One CTA per sequence and run of planes (a layer's keys or values).  Accepted nodes increase, so
 // those that stay where they are (node i + 1 in place i) come first and the rest moves.  Each
@@ -2023,7 +2100,7 @@ constexpr int kCommitBatch = 8;
 // are read before any of its targets is written, and since a_i >= i increases, no target is the
 // source of a later batch.  Bound by memory (or, for a few rows, by the chain node - page -
 // entry): every moved entry is read once and written once.
-__global__ void __launch_bounds__(kCommitThreads) kv_commit_kernel(const CommitArgs a) {
+__global__ void __launch_bounds__(kCommitThreads, kCommitResident) kv_commit_kernel(const CommitArgs a) {
     __shared__ long long s_src[kMaxN], s_dst[kMaxN];
     const int b = blockIdx.z, tid = threadIdx.x;
     const Cache& c = a.c;
@@ -2063,12 +2140,15 @@ __global__ void __launch_bounds__(kCommitThreads) kv_commit_kernel(const CommitA
         a.kv_len_out[b] = bad ? len : len + n + 1;
     }
     if (bad || n <= 0 || !a.out_nodes) return;
-    const int u = blockIdx.x * kCommitThreads + tid;
-    if (u >= a.units) return;
+    // entries shorter than the block: planes side by side
+    const int side = a.units < kCommitThreads ? kCommitThreads / a.units : 1;
+    const int lane = a.units < kCommitThreads ? tid / a.units : 0;
+    const int u = blockIdx.x * kCommitThreads + tid - lane * a.units;
+    if (u >= a.units || lane >= side) return;
     const int h = u / a.head_units;
     const long long column = h * c.head_stride + (u - h * a.head_units) * 16;
     const int p0 = blockIdx.y * a.run, p1 = min(a.planes, p0 + a.run);
-    int plane = p0, move = stay;
+    int plane = p0 + lane, move = stay;
     while (plane < p1 && stay < n) {
         uint4 x[kCommitBatch];
         char* to[kCommitBatch];
@@ -2079,7 +2159,7 @@ __global__ void __launch_bounds__(kCommitThreads) kv_commit_kernel(const CommitA
             char* base = (plane & 1 ? c.v : c.k) + (plane >> 1) * a.layer_stride + column;
             x[i] = *reinterpret_cast<const uint4*>(base + s_src[move]);
             to[i] = base + s_dst[move];
-            if (++move == n) move = stay, ++plane;
+            if (++move == n) move = stay, plane += side;
         }
 #pragma unroll
         for (int i = 0; i < kCommitBatch; ++i)
@@ -2094,19 +2174,19 @@ static bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 
 
 // Calls f with the types and sizes of the split kernel that these sizes take: 16 query rows
 // of a key head per CTA, or 32 where there are more (one CTA then reads each key once for all).
-template <typename F>
+template <bool CLUSTER, typename F>
 static auto with_split(sv_dtype dtype, sv_dtype cache, int dim, int rows, F f) {
     auto sized = [&](auto t, auto ct) {
         using T = decltype(t);
         using CT = decltype(ct);
         if (dim <= 64)
-            return rows <= 16 ? f(kv_split_kernel<T, CT, 64, 1>, kv_join_kernel<T, 64>,
+            return rows <= 16 ? f(kv_split_kernel<T, CT, 64, 1, CLUSTER>, kv_join_kernel<T, 64>,
                                   Split<CT, 64, 1>::kSmem)
-                              : f(kv_split_kernel<T, CT, 64, 2>, kv_join_kernel<T, 64>,
+                              : f(kv_split_kernel<T, CT, 64, 2, CLUSTER>, kv_join_kernel<T, 64>,
                                   Split<CT, 64, 2>::kSmem);
-        return rows <= 16 ? f(kv_split_kernel<T, CT, 128, 1>, kv_join_kernel<T, 128>,
+        return rows <= 16 ? f(kv_split_kernel<T, CT, 128, 1, CLUSTER>, kv_join_kernel<T, 128>,
                               Split<CT, 128, 1>::kSmem)
-                          : f(kv_split_kernel<T, CT, 128, 2>, kv_join_kernel<T, 128>,
+                          : f(kv_split_kernel<T, CT, 128, 2, CLUSTER>, kv_join_kernel<T, 128>,
                               Split<CT, 128, 2>::kSmem);
     };
     if (dtype == SV_BF16)
@@ -2136,6 +2216,14 @@ static auto with_wide(sv_dtype dtype, sv_dtype cache, int dim, int rows, F f) {
         return cache == SV_E4M3 ? sized(__nv_bfloat16(), __nv_fp8_e4m3())
                                 : sized(__nv_bfloat16(), __nv_bfloat16());
     return cache == SV_E4M3 ? sized(__half(), __nv_fp8_e4m3()) : sized(__half(), __half());
+}
+
+// Whether a call takes a cluster per item: when all its clusters are resident at once and a CTA's
+// share of the longest context that the table can hold is at most 16 units (1024 slots).
+static bool small_call(int B, int heads, int rows, int slots, int sms) {
+    const long long items = (long long)B * heads * ((rows + (rows <= 16 ? 15 : 31)) /
+                                                    (rows <= 16 ? 16 : 32));
+    return items * kCluster <= 2 * sms && slots <= kCluster * 16 * kUnit;
 }
 
 // A cache tensor as the TMA sees it: element, head, slot, page.
@@ -2191,11 +2279,15 @@ static cudaError_t attention_setup() {
         for (bool f8 : {false, true})
             for (int dim : {64, 128})
                 for (int rows : {16, 32})
-                    if (e == cudaSuccess)
-                        e = with_split(t, f8 ? SV_E4M3 : t, dim, rows, [](auto k, auto, int smem) {
+                    if (e == cudaSuccess) {
+                        auto set = [](auto k, auto, int smem) {
                             return cudaFuncSetAttribute(
                                 k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-                        });
+                        };
+                        const sv_dtype ct = f8 ? SV_E4M3 : t;
+                        e = with_split<false>(t, ct, dim, rows, set);
+                        if (e == cudaSuccess) e = with_split<true>(t, ct, dim, rows, set);
+                    }
     return e;
 }
 
@@ -2433,10 +2525,12 @@ sv_status spec_kv_attention(const sv_kv_cache* cache, const void* q, const sv_st
     a.q_heads = q_heads;
     a.group = q_heads / cache->heads;
     a.B = B;
-    // Few rows: mma.sync, which then waits for memory only.  More: tcgen05, where a page fills
-    // whole rows of the swizzle.
+    // Few items over short contexts: a cluster each, in one launch.  Else few rows: mma.sync,
+    // which then waits for memory only; more: tcgen05, where a page fills whole groups of eight
+    // rows of the swizzle.
     const int rows = N * a.group;
-    const bool wide = rows > 32 && cache->page_size >= 8;
+    const bool cluster = small_call(B, cache->heads, rows, cache->table_width * cache->page_size, sms);
+    const bool wide = !cluster && rows > 32 && cache->page_size >= 8;
     CUtensorMap kmap, vmap;
     if (wide && (!cache_map(&kmap, cache->k, cache) || !cache_map(&vmap, cache->v, cache)))
         return SV_ERR_CUDA;
@@ -2455,31 +2549,36 @@ sv_status spec_kv_attention(const sv_kv_cache* cache, const void* q, const sv_st
     a.part_ml = (float2*)((char*)ws + l.part_ml);
     // Pieces per item, if all sequences were alike: with many, the warps of a CTA share a row.
     const int warps = a.ctas >= 8 * (long long)B * cache->heads * mts ? 4 : 1;
-    cudaLaunchAttribute pdl;
-    pdl.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    pdl.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchAttribute attrs[2];
+    attrs[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attrs[0].val.programmaticStreamSerializationAllowed = 1;
+    attrs[1].id = cudaLaunchAttributeClusterDimension;
+    attrs[1].val.clusterDim.x = kCluster;
+    attrs[1].val.clusterDim.y = attrs[1].val.clusterDim.z = 1;
     auto launch = [&](auto kernel, auto join, int smem) {
         cudaLaunchConfig_t cfg = {};
-        cfg.gridDim = dim3(a.ctas);
+        cfg.gridDim = dim3(cluster ? B * cache->heads * mts * kCluster : a.ctas);
         cfg.blockDim = dim3(wide ? kTcThreads : kSplitThreads * tile / 16);
         cfg.dynamicSmemBytes = smem;
         cfg.stream = stream;
-        cfg.attrs = &pdl;
-        cfg.numAttrs = 1;
+        cfg.attrs = attrs;
+        cfg.numAttrs = cluster ? 2 : 1;
         cudaError_t r;
         if constexpr (std::is_same<decltype(kernel), void (*)(const AttentionArgs)>::value ||
                       std::is_same<decltype(kernel), void (*)(AttentionArgs)>::value)
             r = cudaLaunchKernelEx(&cfg, kernel, a);
         else
             r = cudaLaunchKernelEx(&cfg, kernel, a, kmap, vmap);
-        if (r != cudaSuccess) return r;
+        if (r != cudaSuccess || cluster) return r;
+        cfg.numAttrs = 1;
         cfg.gridDim = dim3(B * cache->heads * mts, warps == 4 ? tile : tile / 4);
         cfg.blockDim = dim3(128);
         cfg.dynamicSmemBytes = 0;
         return cudaLaunchKernelEx(&cfg, join, a, tile, unit, mts, warps);
     };
     const cudaError_t e = wide ? with_wide(dtype, cache->dtype, cache->dim, rows, launch)
-                               : with_split(dtype, cache->dtype, cache->dim, rows, launch);
+                    : cluster ? with_split<true>(dtype, cache->dtype, cache->dim, rows, launch)
+                              : with_split<false>(dtype, cache->dtype, cache->dim, rows, launch);
     return e == cudaSuccess ? SV_OK : SV_ERR_CUDA;
 }
 
@@ -2513,11 +2612,14 @@ sv_status spec_kv_commit(const sv_kv_cache* cache, int layers, int64_t layer_str
     a.N = N;
     a.head_units = cache->dim * e / 16;
     a.units = cache->heads * a.head_units;
-    // Few CTAs per SM more than are resident: a CTA's chain node - page is paid once per run.
+    // As many CTAs as are resident at once: a CTA's chain node - page is paid once per run.
     const long long ctas = (a.units + kCommitThreads - 1) / kCommitThreads;
     a.planes = 2 * layers;
-    a.run = (int)((a.planes * ctas * B + 16ll * sms - 1) / (16ll * sms));
-    a.run = a.run < 1 ? 1 : a.run > a.planes ? a.planes : a.run;
+    a.run = (int)(((long long)a.planes * ctas * B + kCommitResident * sms - 1) /
+                  (kCommitResident * sms));
+    const int side = a.units < kCommitThreads ? kCommitThreads / a.units : 1;
+    a.run = a.run < side ? side : a.run;
+    a.run = a.run > a.planes ? a.planes : a.run;
     const dim3 grid((unsigned)ctas, (a.planes + a.run - 1) / a.run, B);
     kv_commit_kernel<<<grid, kCommitThreads, 0, stream>>>(a);
     return launched();

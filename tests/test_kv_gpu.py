@@ -42,11 +42,13 @@ def tree(N, form, g):
 
 
 class Round:
-    """One layer's cache and new tokens on the CPU; to() gives the device's copies.  Slots that
-    no sequence holds are NaN (or, in a float8 cache, its NaN), tables of shared pools shuffled."""
+    """One layer's cache and new tokens on the CPU; paged() makes the device's copies.  Slots that
+    no sequence holds are NaN (or, in a float8 cache, its NaN), tables of shared pools shuffled.
+    far: the table has room for more than 8192 slots, which calls of few sequences take another
+    way than tables for short contexts."""
 
     def __init__(self, lens, N, form="chain", counts=None, heads=2, group=4, dim=64, page=16,
-                 dtype=BF, cache=None, order="slot", seed=0, spread=1.5, extra=1):
+                 dtype=BF, cache=None, order="slot", seed=0, spread=1.5, extra=1, far=False):
         g = torch.Generator().manual_seed(seed)
         self.g, self.N, self.heads, self.group, self.dim, self.page = g, N, heads, group, dim, page
         self.dtype, self.cache = dtype, cache or dtype
@@ -60,6 +62,9 @@ class Round:
         width = max(1, max((l + N + page - 1) // page for l in lens)) + extra
         pages = B * width + 1
         self.table = torch.randperm(pages, generator=g)[:B * width].view(B, width).to(torch.int32)
+        if far:  # a table for long contexts, whose entries past the held pages mean nothing
+            self.table = torch.cat([self.table, torch.full((B, 8192 // page + 1), -1,
+                                                           dtype=torch.int32)], dim=1)
         shape = (pages, page, heads, dim)
         lay = (lambda x: x) if order == "slot" else (
             lambda x: x.transpose(1, 2).contiguous().transpose(1, 2))
@@ -111,87 +116,95 @@ class Round:
 TYPES = [(BF, BF), (HF, HF), (BF, E4M3), (HF, E4M3)]
 
 
+@pytest.mark.parametrize("far", [False, True])
 # ---------------------------------------------------------------- attention
 
 @pytest.mark.parametrize("dtype,cache", TYPES)
 @pytest.mark.parametrize("dim", [16, 64, 80, 96, 128])
 @pytest.mark.parametrize("order", ["slot", "head"])
-def test_attention_types_and_heads(kv, dtype, cache, dim, order):
+def test_attention_types_and_heads(kv, far, dtype, cache, dim, order):
     r = Round([37, 0, 130, 64], 3, heads=3, group=2, dim=dim, dtype=dtype, cache=cache,
-              order=order, seed=dim)
+              order=order, seed=dim, far=far)
     out, status = r.attend(kv)
     assert status == [0] * 4
     r.check(out)
 
 
+@pytest.mark.parametrize("far", [False, True])
 @pytest.mark.parametrize("N,form", [(1, "chain"), (2, "chain"), (17, "chain"), (65, "chain"),
                                     (5, "tree"), (16, "tree"), (40, "tree"), (65, "tree"),
                                     (65, "star"), (33, "star")])
 @pytest.mark.parametrize("heads,group", [(1, 1), (2, 8), (1, 5)])
-def test_attention_chains_and_trees(kv, N, form, heads, group):
-    r = Round([100, 7, 0], N, form, heads=heads, group=group, dim=64, seed=N)
+def test_attention_chains_and_trees(kv, far, N, form, heads, group):
+    r = Round([100, 7, 0], N, form, heads=heads, group=group, dim=64, seed=N, far=far)
     out, status = r.attend(kv)
     assert status == [0] * 3
     r.check(out)
 
 
+@pytest.mark.parametrize("far", [False, True])
 @pytest.mark.parametrize("page", [1, 2, 16, 64, 256])
 @pytest.mark.parametrize("N", [1, 6])
-def test_attention_lengths_around_borders(kv, page, N):
+def test_attention_lengths_around_borders(kv, far, page, N):
     lens = [0, 1, 15, 16, 17, 31, 63, 64, 65, 127, 128, 129, 191, 255, 256, 257]
-    r = Round(lens, N, heads=1, group=3, dim=64, page=page, seed=page)
+    r = Round(lens, N, heads=1, group=3, dim=64, page=page, seed=page, far=far)
     out, status = r.attend(kv)
     assert status == [0] * len(lens)
     r.check(out)
 
 
+@pytest.mark.parametrize("far", [False, True])
 @pytest.mark.parametrize("dtype,cache", TYPES)
 @pytest.mark.parametrize("N,group,form", [(1, 4, "chain"), (4, 8, "tree"), (16, 8, "tree"),
                                           (33, 7, "tree")])
-def test_attention_split_over_a_long_cache(kv, dtype, cache, N, group, form):
+def test_attention_split_over_a_long_cache(kv, far, dtype, cache, N, group, form):
     """One sequence, long enough for every SM to hold a part of it, and a short one beside it."""
     r = Round([5003, 40], N, form, heads=1, group=group, dim=128, dtype=dtype, cache=cache,
-              page=32, seed=N)
+              page=32, seed=N, far=far)
     out, status = r.attend(kv)
     assert status == [0, 0]
     r.check(out)
 
 
+@pytest.mark.parametrize("far", [False, True])
 @pytest.mark.parametrize("N,group,form", [(6, 4, "chain"), (16, 8, "tree"), (20, 8, "tree")])
-def test_attention_ragged_counts(kv, N, group, form):
+def test_attention_ragged_counts(kv, far, N, group, form):
     counts = [N, 0, 1, N // 2, N - 1, 0, 2]
     r = Round([50, 60, 0, 129, 300, 0, 16], N, form, counts=counts, heads=2, group=group,
-              dim=64, seed=3)
+              dim=64, seed=3, far=far)
     out, status = r.attend(kv)
     assert status == [0] * 7
     r.check(out)
 
 
+@pytest.mark.parametrize("far", [False, True])
 @pytest.mark.parametrize("B", [1, 150, 700])
 @pytest.mark.parametrize("N,group", [(1, 2), (12, 8)])
-def test_attention_many_sequences(kv, B, N, group):
+def test_attention_many_sequences(kv, far, B, N, group):
     """Every third sequence has nothing new, every fourth nothing cached."""
     g = torch.Generator().manual_seed(B)
     lens = [0 if b % 4 == 3 else int(torch.randint(0, 40, (1,), generator=g)) for b in range(B)]
     counts = [0 if b % 3 == 2 else 1 + b % N for b in range(B)]
-    r = Round(lens, N, "tree", counts=counts, heads=1, group=group, dim=16, page=8, seed=B)
+    r = Round(lens, N, "tree", counts=counts, heads=1, group=group, dim=16, page=8, seed=B, far=far)
     out, status = r.attend(kv)
     assert status == [0] * B
     r.check(out)
 
 
-def test_attention_without_work(kv):
-    r = Round([5, 9], 4, counts=[0, 0])
+@pytest.mark.parametrize("far", [False, True])
+def test_attention_without_work(kv, far):
+    r = Round([5, 9], 4, counts=[0, 0], far=far)
     out, status = r.attend(kv)
     assert status == [0, 0] and bool((out == 7.0).all())
 
 
+@pytest.mark.parametrize("far", [False, True])
 @pytest.mark.parametrize("dtype,cache", TYPES)
 @pytest.mark.parametrize("N,group,form", [(7, 4, "star"), (16, 8, "tree"), (40, 8, "tree")])
-def test_attention_masked_places_may_hold_anything(kv, dtype, cache, N, group, form):
+def test_attention_masked_places_may_hold_anything(kv, far, dtype, cache, N, group, form):
     """A leaf whose key and value are NaN or infinite changes its own row only."""
     r = Round([70, 33, 0, 128], N, form, heads=2, group=group, dim=64, dtype=dtype, cache=cache,
-              seed=5)
+              seed=5, far=far)
     clean_k, clean_v = r.k.clone(), r.v.clone()
     for b, bad in enumerate((math.nan, math.inf, -math.inf, math.nan)):
         p, s = kv_plain.slots(r.table[b], r.page, int(r.lens[b]) + N)[-1]  # node N - 1: a leaf
@@ -209,10 +222,11 @@ def test_attention_masked_places_may_hold_anything(kv, dtype, cache, N, group, f
     assert bool((err <= bound[:, :N - 1]).all())
 
 
-def test_attention_lowest_and_large_scores(kv):
+@pytest.mark.parametrize("far", [False, True])
+def test_attention_lowest_and_large_scores(kv, far):
     """Keys so large that scores reach +-60000 and differ by thousands; one key whose scores are
     the type's lowest: weights are one-hot or exactly shared, never NaN."""
-    r = Round([200, 64, 3], 3, heads=1, group=2, dim=16, spread=1.0, seed=8)
+    r = Round([200, 64, 3], 3, heads=1, group=2, dim=16, spread=1.0, seed=8, far=far)
     for b in range(3):
         for i, (p, s) in enumerate(kv_plain.slots(r.table[b], r.page, int(r.lens[b]))):
             if i % 3 == 0:
@@ -229,9 +243,10 @@ def test_attention_lowest_and_large_scores(kv):
     assert float(tell.double().mean()) > 0.2 and bool((err <= bound)[tell].all())
 
 
-def test_attention_rows_that_overflow_are_nan_and_stay_alone(kv):
+@pytest.mark.parametrize("far", [False, True])
+def test_attention_rows_that_overflow_are_nan_and_stay_alone(kv, far):
     """A query of infinities gives NaN in its own row; the others keep their values."""
-    r = Round([90, 30], 4, heads=1, group=2, dim=64, seed=2)
+    r = Round([90, 30], 4, heads=1, group=2, dim=64, seed=2, far=far)
     r.q[0, 1, 0] = math.inf
     out, _ = r.attend(kv)
     assert bool(torch.isnan(out[0, 1, 0].float()).all())
@@ -243,9 +258,10 @@ def test_attention_rows_that_overflow_are_nan_and_stay_alone(kv):
     assert bool((err <= bound).all())
 
 
+@pytest.mark.parametrize("far", [False, True])
 @pytest.mark.parametrize("scale", [0.0, -0.3, 1e-30])
-def test_attention_scales(kv, scale):
-    r = Round([40, 70], 4, "tree", seed=4)
+def test_attention_scales(kv, far, scale):
+    r = Round([40, 70], 4, "tree", seed=4, far=far)
     r.scale = scale
     out, _ = r.attend(kv)
     r.check(out)
@@ -264,11 +280,12 @@ def test_attention_shared_prefix_and_strided_queries(kv):
     r.check(out.cpu())
 
 
-def test_attention_bad_data(kv):
+@pytest.mark.parametrize("far", [False, True])
+def test_attention_bad_data(kv, far):
     """Bad lengths, counts, trees and pages: NaN rows and the bit, the others untouched by it."""
     N = 6
     r = Round([40, 50, 60, 70, 80, 33, 20, 90], N, "tree", counts=[6, 6, 6, 6, 6, 6, 3, 6],
-              heads=2, group=3, dim=64, seed=9, extra=0)
+              heads=2, group=3, dim=64, seed=9, extra=0, far=far)
     clean = (r.lens.clone(), r.counts.clone(), r.parents.clone(), r.table.clone())
     width = r.table.shape[1] * r.page
     r.lens[0] = -1
@@ -290,10 +307,11 @@ def test_attention_bad_data(kv):
     assert bool((out[6, 3:] == 7.0).all())
 
 
+@pytest.mark.parametrize("far", [False, True])
 @pytest.mark.parametrize("N,group", [(1, 4), (16, 8), (24, 8)])
-def test_attention_bad_page_far_from_the_end(kv, N, group):
+def test_attention_bad_page_far_from_the_end(kv, far, N, group):
     """The bad page is in one part of a split sequence; every row of it is NaN."""
-    r = Round([4000, 100], N, "tree", heads=1, group=group, dim=64, seed=1)
+    r = Round([4000, 100], N, "tree", heads=1, group=group, dim=64, seed=1, far=far)
     good = r.table.clone()
     r.table[0, 3] = -1
     out, status = r.attend(kv)
@@ -324,9 +342,10 @@ def test_attention_offsets_past_32_bits(kv):
     r.check(out.cpu())
 
 
-def test_attention_repeats_bit_for_bit(kv):
+@pytest.mark.parametrize("far", [False, True])
+def test_attention_repeats_bit_for_bit(kv, far):
     """The split does not depend on timing: the same call gives the same bits."""
-    r = Round([3000, 10, 777], 5, "tree", heads=2, group=4, dim=128, seed=11)
+    r = Round([3000, 10, 777], 5, "tree", heads=2, group=4, dim=128, seed=11, far=far)
     first, _ = r.attend(kv)
     for _ in range(3):
         assert torch.equal(r.attend(kv)[0], first)
