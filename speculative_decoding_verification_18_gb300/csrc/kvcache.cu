@@ -1158,13 +1158,6 @@ __device__ __forceinline__ uint64_t nanoseconds() {
     asm volatile("mov.u64 %0, %globaltimer;" : "=l"(now));
     return now;
 }
-// Whether a phase is complete, for a whole warp.
-__device__ __forceinline__ bool warp_test(uint64_t* bar, uint32_t parity) {
-    uint32_t done;
-    asm volatile("{ .reg .pred p; mbarrier.test_wait.parity.shared.b64 p, [%1], %2; "
-                 "selp.u32 %0, 1, 0, p; }" : "=r"(done) : "r"(saddr(bar)), "r"(parity) : "memory");
-    return __all_sync(~0u, done != 0);
-}
 // Waits for a phase of a barrier, two seconds at most, and no longer once another wait has given
 // up; false when it gave up.
 __device__ __forceinline__ bool bar_wait(uint64_t* bar, uint32_t parity, volatile int* gave_up) {
@@ -1638,11 +1631,13 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 ++pieces;
             }
         }
-        if (w == 12) {
+        if (w == 12 && elect_one()) {
             constexpr uint32_t kPv = product<M>(DP, true);
             constexpr uint32_t kPanel = DP > 64 ? 16384 : 1024;  // one panel: not used
             // scores times the sign of the scale: the largest is then the one to look for
             const uint32_t qk = product<M>(128, false) | (a.scale < 0.0f ? 1u << 13 : 0u);
+            const uint64_t qd = operand(sq, 16384), kd = operand(sk, 16384), vd = operand(sv, kPanel);
+            constexpr int kStep = L::kTile >> 4;  // a tile further in a descriptor
             int ks = 0, vs = 0;  // stages and parities of the next tiles of keys and of values
             uint32_t k_phase = 0, v_phase = 0, pieces = 0, p_phase = 0;
             bool ok = true;
@@ -1650,72 +1645,59 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 if (walk.sh.bad) continue;
                 const bool two = p.rows > 128;
                 const int nt = p.t1 - p.t0, jobs = two ? 2 * nt : nt;
-                ok = warp_wait(&bars.q_full, pieces & 1, gave_up);
+                ok = bar_wait(&bars.q_full, pieces & 1, gave_up);
                 // Job i belongs to stream i & 1.  Its scores take the place of the weights of job
                 // i - 2, whose product comes before them; products of one thread run in order.
-                // Scores go first, so that each stream's product and next scores are issued
-                // together and the streams take turns.
-                int ns = 0, np = 0, idle = 0;  // scores and outputs issued; polls in vain
-                bool k_ready = false;          // the next tile of keys: asked for ahead of time
-                uint64_t since = 0;
-                while (ok && np < jobs) {
-                    const int sst = ns & 1, pst = np & 1;
-                    if (!k_ready && ns < jobs) k_ready = warp_test(&bars.k_full[ks], k_phase);
-                    if (k_ready && ns < jobs && ns < np + 2) {
-                        const uint64_t qa = operand(sq + (two ? sst * L::kTile : 0), 16384);
-                        const uint64_t ka = operand(sk + ks * L::kTile, 16384);
-                        if (elect_one()) {
+                // Each stream's product and next scores are issued together, so that the streams
+                // take turns.
+                auto scores = [&](int i) {
+                    const int st = i & 1;
+                    if (!two || st == 0) ok = ok && bar_wait(&bars.k_full[ks], k_phase, gave_up);
+                    if (!ok) return;
+                    const uint64_t qa = qd + (two ? st * kStep : 0), ka = kd + ks * kStep;
 #pragma unroll
-                            for (int k = 0; k < DP / 16; ++k) {
-                                // in 16 bytes: a panel, 16 elements of a row
-                                const uint64_t at = (k >> 2) * (16384 >> 4) + (k & 3) * 2;
-                                tc_mma(tmem + sst * 128, qa + at, ka + at, qk, k > 0);
-                            }
-                            tc_commit(&bars.s_full[sst]);
-                            if (!two || sst == 1) tc_commit(&bars.k_empty[ks]);
-                            if (ns == jobs - 1) tc_commit(&bars.q_empty);
-                        }
-                        __syncwarp();
-                        if (!two || sst == 1) {
-                            k_ready = false;
-                            if (++ks == SK) ks = 0, k_phase ^= 1;
-                        }
-                        ++ns;
-                        idle = 0;
-                    } else if (np < ns && warp_test(&bars.p_full[pst], p_phase >> pst & 1) &&
-                               warp_test(&bars.v_full[vs], v_phase)) {
-                        tc_after();
-                        const uint64_t va = operand(sv + vs * L::kTile, kPanel);
-                        const uint32_t sd = tmem + pst * 128, od = tmem + 256 + pst * DP;
-                        if (elect_one()) {
-#pragma unroll
-                            for (int k = 0; k < 8; ++k)
-                                tc_mma_t(od, sd + (k >> 1) * 32 + (k & 1) * 8, va + k * 128, kPv,
-                                         true);
-                            tc_commit(&bars.pv_done[pst]);
-                            if (!two || pst == 1) tc_commit(&bars.v_empty[vs]);
-                        }
-                        __syncwarp();
-                        if ((!two || pst == 1) && ++vs == SV) vs = 0, v_phase ^= 1;
-                        p_phase ^= 1u << pst;
-                        ++np;
-                        idle = 0;
-                    } else if ((++idle & 63) == 0) {
-                        const uint64_t now = nanoseconds();
-                        if (idle == 64) since = now;
-                        ok = __all_sync(~0u, !*gave_up && now - since < kGiveUp);
-                        if (!ok) *gave_up = 1;
+                    for (int k = 0; k < DP / 16; ++k) {
+                        // in 16 bytes: a panel, 16 elements of a row
+                        const uint64_t at = (k >> 2) * (16384 >> 4) + (k & 3) * 2;
+                        tc_mma(tmem + st * 128, qa + at, ka + at, qk, k > 0);
                     }
+                    tc_commit(&bars.s_full[st]);
+                    if (!two || st == 1) {
+                        tc_commit(&bars.k_empty[ks]);
+                        if (++ks == SK) ks = 0, k_phase ^= 1;
+                    }
+                    if (i == jobs - 1) tc_commit(&bars.q_empty);
+                };
+                if (ok) scores(0);
+                if (ok && jobs > 1) scores(1);
+                for (int i = 0; ok && i < jobs; ++i) {
+                    const int st = i & 1;
+                    if (!two || st == 0) ok = bar_wait(&bars.v_full[vs], v_phase, gave_up);
+                    ok = ok && bar_wait(&bars.p_full[st], p_phase >> st & 1, gave_up);
+                    p_phase ^= 1u << st;
+                    if (!ok) break;
+                    tc_after();
+                    const uint64_t va = vd + vs * kStep;
+                    const uint32_t pd = tmem + st * 128, od = tmem + 256 + st * DP;
+#pragma unroll
+                    for (int k = 0; k < 8; ++k)
+                        tc_mma_t(od, pd + (k >> 1) * 32 + (k & 1) * 8, va + k * 128, kPv, true);
+                    tc_commit(&bars.pv_done[st]);
+                    if (!two || st == 1) {
+                        tc_commit(&bars.v_empty[vs]);
+                        if (++vs == SV) vs = 0, v_phase ^= 1;
+                    }
+                    if (i + 2 < jobs) scores(i + 2);
                 }
                 ++pieces;
             }
             if (!ok) {  // products in flight end before the tensor memory goes back
                 volatile int none = 0;
-                if (elect_one()) tc_commit(&bars.drain);
-                __syncwarp();
-                warp_wait(&bars.drain, 0, &none);
+                tc_commit(&bars.drain);
+                bar_wait(&bars.drain, 0, &none);
             }
         }
+        __syncwarp();
     } else {
         // ------------------------------------------------ weights: a row per thread
         asm volatile("setmaxnreg.inc.sync.aligned.u32 184;");
