@@ -333,7 +333,8 @@ struct AttentionArgs {
     int B, N, q_heads, group;
     int ctas;             // ranges
     long long* prefix;    // workspace: [B + 1] units before each sequence
-    float* part_o;        // workspace: [2 * ctas, rows, DP]
+    float* part_o;        // workspace: [2 * ctas, rows, DP], or of the wide kernel
+                          // [2 * ctas, DP / 4, rows, 4]: there a thread holds a row
     float2* part_ml;      // workspace: [2 * ctas, rows] maximum (base 2) and sum
 };
 
@@ -1925,7 +1926,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             }
             if (two || st == 0) {
                 if (nan_piece) l = NAN;
-                const long long part = (2 * (long long)blockIdx.x + (p.t0 == 0 ? 1 : 0)) * ROWS + row;
+                const long long part = 2 * (long long)blockIdx.x + (p.t0 == 0 ? 1 : 0);
                 const float inv = (kF8 ? c.v_scale[p.h] : 1.0f) / l;
 #pragma unroll 1
                 for (int k = 0; k < DP; k += 32) {
@@ -1946,7 +1947,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                     if (live && !whole) {
 #pragma unroll
                         for (int e = 0; e < 32; e += 4)
-                            *reinterpret_cast<float4*>(a.part_o + part * DP + k + e) =
+                            *reinterpret_cast<float4*>(
+                                a.part_o + ((part * (DP / 4) + (k + e) / 4) * ROWS + row) * 4) =
                                 make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
                     } else if (live) {
 #pragma unroll
@@ -1961,7 +1963,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                     }
                     __syncwarp();
                 }
-                if (live && !whole) a.part_ml[part] = make_float2(ref, l);
+                if (live && !whole) a.part_ml[part * ROWS + row] = make_float2(ref, l);
             }
             tc_before();
             bar_arrive(&bars.epi_done);
@@ -1980,15 +1982,15 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 // 2^(m - max) (o, l), then o / l.  A CTA of four warps per four rows of an item (a warp each), or
 // per row (the warps share its pieces) where the host expects many pieces per item.
 template <typename T, int DP>
-__global__ void __launch_bounds__(128) kv_join_kernel(const AttentionArgs a, int rows, int unit,
-                                                      int mts_max, int warps) {
+__global__ void __launch_bounds__(128) kv_join_kernel(const AttentionArgs a, int rows, int mts_max,
+                                                      int warps) {
     __shared__ float4 s_o[4][DP / 4];
     const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
     const Cache& c = a.c;
     cudaGridDependencySynchronize();
     const int mt = blockIdx.x % mts_max, bh = blockIdx.x / mts_max;
     const int h = bh % c.heads, b = bh / c.heads;
-    const Share sh = share_of(a, b, rows, unit);
+    const Share sh = share_of(a, b, rows, kUnit);
     if (mt >= sh.mts) return;
     const long long W = a.prefix[a.B];
     const long long from = a.prefix[b] + (long long)(h * sh.mts + mt) * sh.tiles;
@@ -2036,6 +2038,66 @@ __global__ void __launch_bounds__(128) kv_join_kernel(const AttentionArgs a, int
     const int R = mt * rows + row, j = R / a.group, g = R - j * a.group;
     const float f = (c.v_scale ? c.v_scale[h] : 1.0f) / L;
     T* dst = (T*)a.out + (((long long)b * a.N + j) * a.q_heads + h * a.group + g) * c.dim + lane * 4;
+    *reinterpret_cast<uint2*>(dst) =
+        make_uint2(pair<T>(y.x * f, y.y * f), pair<T>(y.z * f, y.w * f));
+}
+
+// The same for pieces of the wide kernel: a warp takes 32 rows by four elements, so that what it
+// reads lies together, as it was written; the four warps of a CTA neighbouring elements, or (many
+// pieces) a quarter of the pieces each.
+template <typename T, int DP>
+__global__ void __launch_bounds__(128) kv_wide_join_kernel(const AttentionArgs a, int rows,
+                                                           int mts_max, int warps) {
+    __shared__ float s_y[3][32][5];
+    const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+    const Cache& c = a.c;
+    cudaGridDependencySynchronize();
+    const int mt = blockIdx.x % mts_max, bh = blockIdx.x / mts_max;
+    const int h = bh % c.heads, b = bh / c.heads;
+    const Share sh = share_of(a, b, rows, kTcUnit);
+    if (mt >= sh.mts) return;
+    const long long W = a.prefix[a.B];
+    const long long from = a.prefix[b] + (long long)(h * sh.mts + mt) * sh.tiles;
+    const int P = ranges_of(W, a.ctas);
+    const int c0 = range_of(W, P, from), c1 = range_of(W, P, from + sh.tiles - 1);
+    if (c0 == c1) return;
+    const int cols = DP / 4 / (warps == 4 ? 1 : 4);  // blocks of four elements, or of sixteen
+    const int row = blockIdx.y / cols * 32 + lane;
+    const int d4 = warps == 4 ? blockIdx.y % cols : blockIdx.y % cols * 4 + w;
+    const bool live = row < min(rows, sh.n * a.group - mt * rows) && d4 * 4 < c.dim;
+    if (warps == 1 && !live) return;
+    auto at = [&](int i) { return (long long)(2 * i + (i == c0 ? 1 : 0)); };
+    float top = -INFINITY, L = 0.0f;
+    float4 y = make_float4(0, 0, 0, 0);
+    if (live) {
+#pragma unroll 8
+        for (int i = c0; i <= c1; ++i) top = fmaxf(top, a.part_ml[at(i) * rows + row].x);
+        const float ref = top == -INFINITY ? 0.0f : top;
+#pragma unroll 8
+        for (int i = c0 + (warps == 4 ? w : 0); i <= c1; i += warps) {
+            const float2 ml = a.part_ml[at(i) * rows + row];
+            const float f = ex2(ml.x - ref);
+            const float4 v = *reinterpret_cast<const float4*>(
+                a.part_o + ((at(i) * (DP / 4) + d4) * rows + row) * 4);
+            L += ml.y * f;
+            y.x += v.x * f, y.y += v.y * f, y.z += v.z * f, y.w += v.w * f;
+        }
+    }
+    if (warps == 4) {
+        if (w) {
+            float* to = s_y[w - 1][lane];
+            to[0] = y.x, to[1] = y.y, to[2] = y.z, to[3] = y.w, to[4] = L;
+        }
+        __syncthreads();
+        if (w || !live) return;
+        for (int k = 0; k < 3; ++k) {
+            const float* of = s_y[k][lane];
+            y.x += of[0], y.y += of[1], y.z += of[2], y.w += of[3], L += of[4];
+        }
+    }
+    const int R = mt * rows + row, j = R / a.group, g = R - j * a.group;
+    const float f = (c.v_scale ? c.v_scale[h] : 1.0f) / L;
+    T* dst = (T*)a.out + (((long long)b * a.N + j) * a.q_heads + h * a.group + g) * c.dim + d4 * 4;
     *reinterpret_cast<uint2*>(dst) =
         make_uint2(pair<T>(y.x * f, y.y * f), pair<T>(y.z * f, y.w * f));
 }
@@ -2169,13 +2231,13 @@ static auto with_wide(sv_dtype dtype, sv_dtype cache, int dim, int rows, F f) {
         using CT = decltype(ct);
         constexpr bool F8 = sizeof(CT) == 1;
         if (dim <= 64)
-            return rows <= 128 ? f(kv_wide_kernel<T, CT, 64, 128>, kv_join_kernel<T, 64>,
+            return rows <= 128 ? f(kv_wide_kernel<T, CT, 64, 128>, kv_wide_join_kernel<T, 64>,
                                    Tc<64, 128, F8>::kSmem)
-                               : f(kv_wide_kernel<T, CT, 64, 256>, kv_join_kernel<T, 64>,
+                               : f(kv_wide_kernel<T, CT, 64, 256>, kv_wide_join_kernel<T, 64>,
                                    Tc<64, 256, F8>::kSmem);
-        return rows <= 128 ? f(kv_wide_kernel<T, CT, 128, 128>, kv_join_kernel<T, 128>,
+        return rows <= 128 ? f(kv_wide_kernel<T, CT, 128, 128>, kv_wide_join_kernel<T, 128>,
                                Tc<128, 128, F8>::kSmem)
-                           : f(kv_wide_kernel<T, CT, 128, 256>, kv_join_kernel<T, 128>,
+                           : f(kv_wide_kernel<T, CT, 128, 256>, kv_wide_join_kernel<T, 128>,
                                Tc<128, 256, F8>::kSmem);
     };
     if (dtype == SV_BF16)
@@ -2537,10 +2599,11 @@ sv_status spec_kv_attention(const sv_kv_cache* cache, const void* q, const sv_st
             r = cudaLaunchKernelEx(&cfg, kernel, a, kmap, vmap);
         if (r != cudaSuccess || cluster) return r;
         cfg.numAttrs = 1;
-        cfg.gridDim = dim3(B * cache->heads * mts, warps == 4 ? tile : tile / 4);
         cfg.blockDim = dim3(128);
         cfg.dynamicSmemBytes = 0;
-        return cudaLaunchKernelEx(&cfg, join, a, tile, unit, mts, warps);
+        const int parts = wide ? tile / 32 * (cache->dim <= 64 ? 16 : 32) : tile;
+        cfg.gridDim = dim3(B * cache->heads * mts, warps == 4 ? parts : parts / 4);
+        return cudaLaunchKernelEx(&cfg, join, a, tile, mts, warps);
     };
     const cudaError_t e = wide ? with_wide(dtype, cache->dtype, cache->dim, rows, launch)
                     : cluster ? with_split<true>(dtype, cache->dtype, cache->dim, rows, launch)
