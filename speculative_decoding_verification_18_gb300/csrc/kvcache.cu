@@ -332,7 +332,9 @@ struct AttentionArgs {
     float scale;
     int B, N, q_heads, group;
     int ctas;             // ranges
-    long long* prefix;    // workspace: [B + 1] units before each sequence
+    int mts;              // row tiles of an item's head, counted for N tokens
+    int2* ends;           // workspace: [B, heads, mts] first and last range of an item's pieces
+                          // (-1: one range has all of it and wrote the output)
     float* part_o;        // workspace: [2 * ctas, rows, DP], or of the wide kernel
                           // [2 * ctas, DP / 4, rows, 4]: there a thread holds a row
     float2* part_ml;      // workspace: [2 * ctas, rows] maximum (base 2) and sum
@@ -367,9 +369,6 @@ __device__ __forceinline__ int ranges_of(long long W, int ctas) {
 __device__ __forceinline__ long long range_start(long long W, int P, int c) {
     return W / P * c + W % P * c / P;
 }
-__device__ __forceinline__ int range_of(long long W, int P, long long x) {
-    return (int)(((x + 1) * P - 1) / W);
-}
 
 // A CTA's range as pieces of items, in order: sequence, key head, row tile, units t0 .. t1 - 1.
 struct Piece {
@@ -402,8 +401,15 @@ struct Start {
     int b;
 };
 
-// The range of this CTA: units before each sequence (a scan over the batch; CTA 0 leaves it for
-// the join), their sum W, range blockIdx.x of the min(ctas, W) that W is cut into.
+// Says where the pieces of an item are, for the join: the piece that starts it, or ends it.
+__device__ __forceinline__ void tell_ends(const AttentionArgs& a, const Piece& p, int tiles) {
+    int2* e = a.ends + ((long long)p.b * a.c.heads + p.h) * a.mts + p.mt;
+    if (p.t0 == 0) e->x = p.t1 == tiles ? -1 : (int)blockIdx.x;
+    else if (p.t1 == tiles) e->y = (int)blockIdx.x;
+}
+
+// The range of this CTA: units before each sequence (a scan over the batch), their sum W, range
+// blockIdx.x of the min(ctas, W) that W is cut into.
 template <int THREADS>
 __device__ __forceinline__ Walk start_walk(const AttentionArgs& a, int rows, int unit,
                                            long long* s_scan, Start* s_start) {
@@ -428,15 +434,13 @@ __device__ __forceinline__ Walk start_walk(const AttentionArgs& a, int rows, int
     const bool some = W > 0 && (int)blockIdx.x < P;
     const long long x = some ? range_start(W, P, blockIdx.x) : 0;
     const bool here = some && x >= before && x < before + sum;
-    if (blockIdx.x == 0 || here) {
+    if (here) {
         long long at = before;
         for (int b = b0; b < b1; ++b) {
             const long long u = share_of(a, b, rows, unit).units(a.c.heads);
-            if (here && x >= at && x < at + u) *s_start = Start{at, b};
-            if (blockIdx.x == 0) a.prefix[b] = at;
+            if (x >= at && x < at + u) *s_start = Start{at, b};
             at += u;
         }
-        if (blockIdx.x == 0 && tid == 0) a.prefix[a.B] = W;
     }
     __syncthreads();
     Walk k = {};
@@ -628,6 +632,7 @@ __global__ void __launch_bounds__(kSplitThreads * WM, 2) kv_split_kernel(const A
                    : walk.next(a, ROWS, kUnit, &piece)) {
         const int b = piece.b, h = piece.h, mt = piece.mt, t0 = piece.t0, t1 = piece.t1;
         const int len = sh.len, total = len + sh.n, rows = piece.rows;
+        if (!CLUSTER && tid == 0) tell_ends(a, piece, sh.tiles);
         bool bad = sh.bad;
         if (bad && tid == 0) mark(a.status, b, SV_DEV_BAD_LENGTH);
 
@@ -1715,6 +1720,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             const int row = two ? st * 128 + r : r, R = p.mt * ROWS + row;
             const int j = min(R / a.group, sh.n - 1), g = R - R / a.group * a.group;
             const bool live = row < p.rows;
+            if (tid == 0) tell_ends(a, p, sh.tiles);
             T* out = (T*)a.out + (((long long)p.b * a.N + j) * a.q_heads + p.h * a.group + g) * c.dim;
             if (sh.bad) {
                 if (tid == 0) mark(a.status, p.b, SV_DEV_BAD_LENGTH);
@@ -1982,21 +1988,17 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 // 2^(m - max) (o, l), then o / l.  A CTA of four warps per four rows of an item (a warp each), or
 // per row (the warps share its pieces) where the host expects many pieces per item.
 template <typename T, int DP>
-__global__ void __launch_bounds__(128) kv_join_kernel(const AttentionArgs a, int rows, int mts_max,
-                                                      int warps) {
+__global__ void __launch_bounds__(128) kv_join_kernel(const AttentionArgs a, int rows, int warps) {
     __shared__ float4 s_o[4][DP / 4];
     const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
     const Cache& c = a.c;
     cudaGridDependencySynchronize();
-    const int mt = blockIdx.x % mts_max, bh = blockIdx.x / mts_max;
+    const int mt = blockIdx.x % a.mts, bh = blockIdx.x / a.mts;
     const int h = bh % c.heads, b = bh / c.heads;
+    const int2 ends = a.ends[blockIdx.x];  // (not written for an item that is not there)
     const Share sh = share_of(a, b, rows, kUnit);
-    if (mt >= sh.mts) return;
-    const long long W = a.prefix[a.B];
-    const long long from = a.prefix[b] + (long long)(h * sh.mts + mt) * sh.tiles;
-    const int P = ranges_of(W, a.ctas);
-    const int c0 = range_of(W, P, from), c1 = range_of(W, P, from + sh.tiles - 1);
-    if (c0 == c1) return;
+    if (mt >= sh.mts || ends.x < 0) return;
+    const int c0 = ends.x, c1 = ends.y;
     const int row = warps == 1 ? blockIdx.y * 4 + w : blockIdx.y;
     const int live = min(rows, sh.n * a.group - mt * rows);
     const bool mine = row < live;
@@ -2047,20 +2049,17 @@ __global__ void __launch_bounds__(128) kv_join_kernel(const AttentionArgs a, int
 // pieces) a quarter of the pieces each.
 template <typename T, int DP>
 __global__ void __launch_bounds__(128) kv_wide_join_kernel(const AttentionArgs a, int rows,
-                                                           int mts_max, int warps) {
+                                                           int warps) {
     __shared__ float s_y[3][32][5];
     const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
     const Cache& c = a.c;
     cudaGridDependencySynchronize();
-    const int mt = blockIdx.x % mts_max, bh = blockIdx.x / mts_max;
+    const int mt = blockIdx.x % a.mts, bh = blockIdx.x / a.mts;
     const int h = bh % c.heads, b = bh / c.heads;
+    const int2 ends = a.ends[blockIdx.x];  // (not written for an item that is not there)
     const Share sh = share_of(a, b, rows, kTcUnit);
-    if (mt >= sh.mts) return;
-    const long long W = a.prefix[a.B];
-    const long long from = a.prefix[b] + (long long)(h * sh.mts + mt) * sh.tiles;
-    const int P = ranges_of(W, a.ctas);
-    const int c0 = range_of(W, P, from), c1 = range_of(W, P, from + sh.tiles - 1);
-    if (c0 == c1) return;
+    if (mt >= sh.mts || ends.x < 0) return;
+    const int c0 = ends.x, c1 = ends.y;
     const int cols = DP / 4 / (warps == 4 ? 1 : 4);  // blocks of four elements, or of sixteen
     const int row = blockIdx.y / cols * 32 + lane;
     const int d4 = warps == 4 ? blockIdx.y % cols : blockIdx.y % cols * 4 + w;
@@ -2344,15 +2343,16 @@ static sv_status device_ok(int* sms) {
     return SV_OK;
 }
 
-// The workspace: units before each sequence, then two pieces of a row tile per CTA.
+// The workspace: where the pieces of each item are (tiles of at least 16 rows, of 32 where there
+// are more), then two pieces of a row tile per CTA.
 struct AttentionWs { size_t part_o, part_ml, bytes; };
-static AttentionWs attention_ws(int B, int rows, int dim) {
-    const size_t dp = dim <= 64 ? 64 : 128;
+static AttentionWs attention_ws(int B, int heads, int rows, int dim) {
+    const size_t dp = dim <= 64 ? 64 : 128, items = (size_t)B * heads * ((rows + 31) / 32);
     const size_t split = (size_t)2 * kMaxCtas * (rows <= 16 ? 16 : 32);
     const size_t wide = rows <= 32 ? 0 : (size_t)2 * kTcMaxCtas * (rows <= 128 ? 128 : 256);
     const size_t held = split > wide ? split : wide;
     AttentionWs l;
-    l.part_o = ((size_t)(B + 1) * 8 + 255) / 256 * 256;
+    l.part_o = (items * sizeof(int2) + 255) / 256 * 256;
     l.part_ml = l.part_o + held * dp * 4;
     l.bytes = l.part_ml + held * 8;
     return l;
@@ -2518,7 +2518,7 @@ size_t spec_kv_attention_workspace_size(int B, int N, int q_heads, int heads, in
     if (B < 0 || B > kMaxB || N < 1 || N > kMaxN || heads < 1 || q_heads < 1 || q_heads % heads ||
         q_heads > kMaxQHeads || dim < 16 || dim > kMaxDim || dim % 16)
         return 0;
-    return attention_ws(B, N * (q_heads / heads), dim).bytes;
+    return attention_ws(B, heads, N * (q_heads / heads), dim).bytes;
 }
 
 sv_status spec_kv_attention(const sv_kv_cache* cache, const void* q, const sv_strides* q_strides,
@@ -2571,8 +2571,9 @@ sv_status spec_kv_attention(const sv_kv_cache* cache, const void* q, const sv_st
     if ((long long)B * cache->heads * mts >= (1ll << 31)) return SV_ERR_UNSUPPORTED;  // grid size
     const int most = wide ? kTcMaxCtas : kMaxCtas, fit = wide ? sms : 2 * sms;
     a.ctas = fit < most ? fit : most;
-    const AttentionWs l = attention_ws(B, rows, cache->dim);
-    a.prefix = (long long*)ws;
+    const AttentionWs l = attention_ws(B, cache->heads, rows, cache->dim);
+    a.mts = mts;
+    a.ends = (int2*)ws;
     a.part_o = (float*)((char*)ws + l.part_o);
     a.part_ml = (float2*)((char*)ws + l.part_ml);
     // Pieces per item, if all sequences were alike: with many, the warps of a CTA share a row.
@@ -2603,7 +2604,7 @@ sv_status spec_kv_attention(const sv_kv_cache* cache, const void* q, const sv_st
         cfg.dynamicSmemBytes = 0;
         const int parts = wide ? tile / 32 * (cache->dim <= 64 ? 16 : 32) : tile;
         cfg.gridDim = dim3(B * cache->heads * mts, warps == 4 ? parts : parts / 4);
-        return cudaLaunchKernelEx(&cfg, join, a, tile, mts, warps);
+        return cudaLaunchKernelEx(&cfg, join, a, tile, warps);
     };
     const cudaError_t e = wide ? with_wide(dtype, cache->dtype, cache->dim, rows, launch)
                     : cluster ? with_split<true>(dtype, cache->dtype, cache->dim, rows, launch)
