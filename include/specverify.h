@@ -72,7 +72,7 @@ typedef enum {
     SV_ERR_UNSUPPORTED = 3,  /* sizes beyond the limits above, or no sm_103a device */
     SV_ERR_CUDA = 4,         /* a CUDA runtime call failed (launch, copy) */
     SV_ERR_DATA = 5,         /* device-detected bad data (spec_verify_read_status) */
-    SV_ERR_TIMEOUT = 6       /* reserved: no device-side wait exists in this version */
+    SV_ERR_TIMEOUT = 6       /* reserved: no call returns it */
 } sv_status;
 
 typedef enum { SV_BF16 = 0, SV_F32 = 1 } sv_dtype;

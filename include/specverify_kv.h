@@ -136,7 +136,8 @@ size_t spec_kv_attention_workspace_size(int B, int N, int q_heads, int heads, in
  * ancestors.  Query head h reads key head h / (q_heads / heads).
  *   q    [B, N, q_heads, dim], SV_BF16 or SV_F16, strides q_strides; the cache
  *        has the same type, or SV_E4M3.
- *   out  [B, N, q_heads, dim] contiguous (written), the type of q.
+ *   out  [B, N, q_heads, dim] contiguous (written), the type of q; it must not
+ *        overlap q.
  * Entries that a node does not attend to take no part, whatever they hold.  The
  * sums are fp32.  Workspace as for the other calls (no initialisation; calls that
  * share one must not overlap).  Every row of a sequence with a bad length, tree or page is
@@ -155,8 +156,8 @@ sv_status spec_kv_attention(const sv_kv_cache* cache, const void* q, const sv_st
  *                 writes them, or NULL for a chain (nothing moves).
  *   num_accepted  [B] int32: how many of them; -1 (an invalid sequence): nothing
  *                 moves and kv_len_out = kv_len.
- *   kv_len_out    [B] int32 (written): kv_len + num_accepted + 1.  Must not be
- *                 kv_len.
+ *   kv_len_out    [B] int32 (written): kv_len + num_accepted + 1.  Must not
+ *                 overlap kv_len or num_accepted.
  * A sequence whose accepted nodes are not increasing within [1, N)
  * (SV_DEV_BAD_TREE), whose num_accepted is outside [-1, N - 1] or whose slots
  * lie beyond the table (SV_DEV_BAD_LENGTH) or that needs a bad page stays as it

@@ -2253,7 +2253,8 @@ static bool small_call(int B, int heads, int rows, int slots, int sms) {
     return items * kCluster <= 2 * sms && slots <= kCluster * 16 * kUnit;
 }
 
-// A cache tensor as the TMA sees it: element, head, slot, page.
+// A cache tensor as the TMA sees it: element, head, slot, page.  False where it does not take the
+// strides (2^40 bytes and more).
 static bool cache_map(CUtensorMap* map, void* base, const sv_kv_cache* c) {
     static PFN_cuTensorMapEncodeTiled_v12000 encode = [] {
         void* f = nullptr;
@@ -2380,6 +2381,8 @@ static sv_status check_cache(const sv_kv_cache* c, bool scales, Cache* out) {
                  c->num_pages, __builtin_ctz(c->page_size), c->table_width, c->heads, c->dim};
     return SV_OK;
 }
+
+static bool overlap(const int32_t* a, const int32_t* b, int n) { return a < b + n && b < a + n; }
 
 static bool strides_ok(const sv_strides* s) {
     if (!s) return false;
@@ -2558,10 +2561,9 @@ sv_status spec_kv_attention(const sv_kv_cache* cache, const void* q, const sv_st
     // rows of the swizzle.
     const int rows = N * a.group;
     const bool cluster = small_call(B, cache->heads, rows, cache->table_width * cache->page_size, sms);
-    const bool wide = !cluster && rows > 32 && cache->page_size >= 8;
     CUtensorMap kmap, vmap;
-    if (wide && (!cache_map(&kmap, cache->k, cache) || !cache_map(&vmap, cache->v, cache)))
-        return SV_ERR_CUDA;
+    const bool wide = !cluster && rows > 32 && cache->page_size >= 8 &&
+                      cache_map(&kmap, cache->k, cache) && cache_map(&vmap, cache->v, cache);
     const int tile = wide ? (rows <= 128 ? 128 : 256) : rows <= 16 ? 16 : 32;
     const int unit = wide ? kTcUnit : kUnit;
     const int mts = (rows + tile - 1) / tile;
@@ -2630,7 +2632,9 @@ sv_status spec_kv_commit(const sv_kv_cache* cache, int layers, int64_t layer_str
         !aligned16(kv_len_out) || !aligned16(status))
         return SV_ERR_INVALID_ARG;
     if (B == 0) return SV_OK;
-    if (kv_len_out == kv_len) return SV_ERR_INVALID_ARG;
+    // a CTA may still read a sequence's length or count when another writes its new length
+    if (overlap(kv_len_out, kv_len, B) || overlap(kv_len_out, num_accepted, B))
+        return SV_ERR_INVALID_ARG;
     int sms;
     if ((st = device_ok(&sms)) != SV_OK) return st;
     a.layer_stride = layers > 1 ? layer_stride * e : 0;

@@ -149,6 +149,7 @@ class PagedCache:
         load()
         self._addresses = [ctypes.addressof(c) for c in self._layers]
         self._rows, self._device = table.shape[0], k.get_device()
+        self._held = (k, v, table, k_scale, v_scale)  # whatever becomes of the attributes
 
     def layer(self, i):
         """Address of the sv_kv_cache of layer i."""
@@ -174,6 +175,7 @@ class Rope:
         self.rot_dim, self.interleaved, self.magnitude = rot_dim, bool(interleaved), magnitude
         self._c = _Rope(self.turns.data_ptr(), rot_dim, int(self.interleaved), float(magnitude))
         self._address = ctypes.addressof(self._c)
+        self._held = self.turns
 
 
 def spec_kv_append(cache, k, v, kv_len, q=None, q_out=None, rope=None, parents=None, num_new=None,

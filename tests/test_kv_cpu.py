@@ -139,8 +139,9 @@ def test_commit_argument_errors(kv):
         assert call(cache=cache_struct(kv, **bad)) == code, bad
     for bad, code in ((dict(layers=0), 1), (dict(layers=40000), 3), (dict(stride=8), 1),
                       (dict(stride=65), 1), (dict(kv_len=None), 1), (dict(acc=None), 1),
-                      (dict(out=None), 1), (dict(out=P), 1), (dict(B=-1), 1), (dict(N=0), 1),
-                      (dict(N=66), 3), (dict(nodes=P + 4), 1), (dict(acc=P + 4), 1),
+                      (dict(out=None), 1), (dict(out=P), 1), (dict(out=P + 16, B=9), 1),
+                      (dict(acc=2 * P, out=2 * P + 16, B=9), 1),
+                      (dict(B=-1), 1), (dict(N=0), 1), (dict(N=66), 3), (dict(nodes=P + 4), 1), (dict(acc=P + 4), 1),
                       (dict(out=P + 4), 1), (dict(status=P + 4), 1)):
         assert call(**bad) == code, bad
     assert call(B=0) == 0

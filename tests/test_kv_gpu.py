@@ -736,3 +736,71 @@ def test_whole_rounds(kv, capture):
             assert logits[toks[t + 1]] + 2 * slack.max() >= logits.max()
             told += int((logits < logits.max() - 2 * slack.max()).sum())
     assert told > 0 and sum(sum(n) for n in s["took"]) > 0
+
+
+FIRST = """
+import sys
+sys.path[:0] = [{root!r}, {tests!r}]
+import torch, kv_plain
+from test_kv_gpu import Round
+from speculative_decoding_verification_18_gb300 import kvcache as kv
+for N, far in ((1, False), (1, True), (16, True)):
+    r = Round([300, 40], N, "tree", heads=1, group=8, dim=128, seed=N, far=far)
+    c, q, lens, par = r.paged(kv), r.q.cuda(), r.lens.cuda(), r.parents.cuda()
+    out, ws = torch.full_like(q, 7.0), kv.attention_workspace(c, 2, N, 8)
+    acc, new = torch.zeros_like(lens), torch.zeros_like(lens)
+    k = torch.stack([r.k[r.table[b, (int(r.lens[b]) + j) // r.page].item(),
+                         (int(r.lens[b]) + j) % r.page] for b in range(2) for j in range(N)])
+    v = torch.stack([r.v[r.table[b, (int(r.lens[b]) + j) // r.page].item(),
+                         (int(r.lens[b]) + j) % r.page] for b in range(2) for j in range(N)])
+    k, v = k.view(2, N, 1, 128).cuda(), v.view(2, N, 1, 128).cuda()
+    stream, graph = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph, stream=stream):
+        kv.spec_kv_append(c, k, v, lens, parents=par)
+        kv.spec_kv_attention(c, q, lens, out, ws, r.scale, parents=par)
+        kv.spec_kv_commit(c, lens, acc, new)
+    for _ in range(2):
+        out.fill_(7.0)
+        graph.replay()
+        torch.cuda.synchronize()
+        r.check(out.cpu())
+        assert new.cpu().tolist() == [301, 41]
+print("captured")
+"""
+
+
+def test_first_calls_of_a_process_inside_a_capture(kv):
+    """Nothing that the calls set up on a device needs an eager call first."""
+    import os
+    import subprocess
+    import sys
+    tests = os.path.dirname(os.path.abspath(__file__))
+    code = FIRST.format(root=os.path.dirname(tests), tests=tests)
+    got = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=300)
+    assert got.returncode == 0 and "captured" in got.stdout, got.stderr[-2000:]
+
+
+def test_two_graphs_share_a_workspace(kv):
+    """Two captured calls of different sizes on one workspace, replayed in turn on one stream."""
+    a = Round([3000, 50], 16, "tree", heads=1, group=8, dim=128, seed=1, far=True)
+    b = Round([400, 5, 77], 2, heads=1, group=8, dim=128, seed=2, far=True)
+    n = max(kv.spec_kv_attention_workspace_size(r.B, r.N, 8, 1, 128) for r in (a, b))
+    ws = torch.full((n,), 255, dtype=torch.uint8, device="cuda")
+    held = []
+    for r in (a, b):
+        c, q, lens = r.paged(kv), r.q.cuda(), r.lens.cuda()
+        par = None if r.parents is None else r.parents.cuda()
+        out = torch.full_like(q, 7.0)
+        graph = torch.cuda.CUDAGraph()
+        torch.cuda.synchronize()
+        with torch.cuda.graph(graph, stream=torch.cuda.Stream()):
+            kv.spec_kv_attention(c, q, lens, out, ws, r.scale, parents=par)
+        held.append((r, graph, out, (c, q, lens, par)))
+    for _ in range(3):
+        for r, graph, out, _ in held:
+            out.fill_(7.0)
+            graph.replay()
+        torch.cuda.synchronize()
+        for r, graph, out, _ in held:
+            r.check(out.cpu())
