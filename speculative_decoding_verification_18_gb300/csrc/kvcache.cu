@@ -344,12 +344,17 @@ constexpr int kUnit = 64;          // slots of a unit: 16 per warp
 constexpr int kSplitThreads = 128;
 constexpr int kMaxCtas = 304;      // two per SM
 
-// One sequence's share of the work, for row tiles of `rows` rows.
+// One sequence's share of the work, for row tiles of `rows` rows.  A unit of a tile of 256 rows
+// weighs as two where more than 128 of them are there: it takes both streams' time.
 struct Share {
     int len, n, tiles, mts;
+    int last;  // weight of the last row tile's units; the others weigh `full`
     bool bad;
-    __device__ long long units(int heads) const { return (long long)heads * mts * tiles; }
+    __device__ long long units(int heads, int full) const {
+        return (long long)heads * tiles * (mts > 0 ? full * (mts - 1) + last : 0);
+    }
 };
+__device__ __forceinline__ constexpr int full_weight(int rows) { return rows > 128 ? 2 : 1; }
 
 __device__ __forceinline__ Share share_of(const AttentionArgs& a, int b, int rows, int unit) {
     Share s;
@@ -358,12 +363,13 @@ __device__ __forceinline__ Share share_of(const AttentionArgs& a, int b, int row
     if (s.bad) s.n = a.N;  // one unit per item: its rows become NaN
     s.tiles = s.bad ? 1 : (int)(((long long)s.len + s.n + unit - 1) / unit);
     s.mts = (s.n * a.group + rows - 1) / rows;
+    s.last = s.n * a.group - (s.mts - 1) * rows > 128 ? 2 : 1;
     return s;
 }
 
-// Ranges that W units are cut into: none of them is empty.
-__device__ __forceinline__ int ranges_of(long long W, int ctas) {
-    return (int)min((long long)ctas, max(W, 1ll));
+// Ranges that units of total weight W are cut into: each has a whole unit at least.
+__device__ __forceinline__ int ranges_of(long long W, int ctas, int full) {
+    return (int)min((long long)ctas, max(W / full, 1ll));
 }
 // Range c of P equal ranges of W units starts at floor(c W / P).
 __device__ __forceinline__ long long range_start(long long W, int P, int c) {
@@ -375,25 +381,32 @@ struct Piece {
     int b, h, mt, t0, t1, rows;
 };
 struct Walk {
-    long long left;  // units of the range still to come
-    int b, item, t0;
+    long long left;  // weight of the range still to come
+    long long at;    // weight of the item before the range's part of it
+    int b, item;
     Share sh;
     __device__ __forceinline__ bool next(const AttentionArgs& a, int rows, int unit, Piece* p) {
-        if (left <= 0) return false;
-        while (item >= a.c.heads * sh.mts) {
-            sh = share_of(a, ++b, rows, unit);
-            item = 0;
+        const int full = full_weight(rows);
+        for (;;) {
+            if (left <= 0) return false;
+            while (item >= a.c.heads * sh.mts) {
+                sh = share_of(a, ++b, rows, unit);
+                item = 0;
+            }
+            p->b = b;
+            p->h = item / sh.mts;
+            p->mt = item - p->h * sh.mts;
+            // (a unit of weight two belongs to the range that its first half is in)
+            const int w = full == 1 || p->mt < sh.mts - 1 ? full : sh.last;
+            const long long to = min((long long)sh.tiles * w, at + left);
+            p->t0 = (int)((at + w - 1) / w);
+            p->t1 = (int)((to + w - 1) / w);
+            p->rows = min(rows, sh.n * a.group - p->mt * rows);
+            left -= to - at;
+            ++item;
+            at = 0;
+            if (p->t0 < p->t1) return true;
         }
-        p->b = b;
-        p->h = item / sh.mts;
-        p->mt = item - p->h * sh.mts;
-        p->t0 = t0;
-        p->t1 = (int)min((long long)sh.tiles, t0 + left);
-        p->rows = min(rows, sh.n * a.group - p->mt * rows);
-        left -= p->t1 - t0;
-        ++item;
-        t0 = 0;
-        return true;
     }
 };
 struct Start {
@@ -408,16 +421,16 @@ __device__ __forceinline__ void tell_ends(const AttentionArgs& a, const Piece& p
     else if (p.t1 == tiles) e->y = (int)blockIdx.x;
 }
 
-// The range of this CTA: units before each sequence (a scan over the batch), their sum W, range
-// blockIdx.x of the min(ctas, W) that W is cut into.
+// The range of this CTA: weight of the units before each sequence (a scan over the batch), their
+// sum W, range blockIdx.x of those that W is cut into.
 template <int THREADS>
 __device__ __forceinline__ Walk start_walk(const AttentionArgs& a, int rows, int unit,
                                            long long* s_scan, Start* s_start) {
-    const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
+    const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5, full = full_weight(rows);
     const int per = (a.B + THREADS - 1) / THREADS;
     const int b0 = min(a.B, tid * per), b1 = min(a.B, b0 + per);
     long long sum = 0;
-    for (int b = b0; b < b1; ++b) sum += share_of(a, b, rows, unit).units(a.c.heads);
+    for (int b = b0; b < b1; ++b) sum += share_of(a, b, rows, unit).units(a.c.heads, full);
     long long inc = sum;
     for (int k = 1; k < 32; k <<= 1) {
         const long long y = __shfl_up_sync(~0u, inc, k);
@@ -430,14 +443,14 @@ __device__ __forceinline__ Walk start_walk(const AttentionArgs& a, int rows, int
         W += s_scan[i];
         if (i < w) before += s_scan[i];
     }
-    const int P = ranges_of(W, a.ctas);
+    const int P = ranges_of(W, a.ctas, full);
     const bool some = W > 0 && (int)blockIdx.x < P;
     const long long x = some ? range_start(W, P, blockIdx.x) : 0;
     const bool here = some && x >= before && x < before + sum;
     if (here) {
         long long at = before;
         for (int b = b0; b < b1; ++b) {
-            const long long u = share_of(a, b, rows, unit).units(a.c.heads);
+            const long long u = share_of(a, b, rows, unit).units(a.c.heads, full);
             if (x >= at && x < at + u) *s_start = Start{at, b};
             at += u;
         }
@@ -448,9 +461,12 @@ __device__ __forceinline__ Walk start_walk(const AttentionArgs& a, int rows, int
         k.left = range_start(W, P, blockIdx.x + 1) - x;
         k.b = s_start->b;
         k.sh = share_of(a, k.b, rows, unit);
-        const long long r = x - s_start->at;
-        k.item = (int)(r / k.sh.tiles);
-        k.t0 = (int)(r - (long long)k.item * k.sh.tiles);
+        const long long r = x - s_start->at, head = k.sh.units(1, full);
+        const long long tile = (long long)k.sh.tiles * full;  // weight of an item but the last
+        const int h = (int)(r / head);
+        const int mt = (int)min((r - h * head) / tile, (long long)k.sh.mts - 1);
+        k.item = h * k.sh.mts + mt;
+        k.at = r - h * head - mt * tile;
     }
     return k;
 }
