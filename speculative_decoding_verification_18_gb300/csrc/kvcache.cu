@@ -1148,7 +1148,7 @@ template <int DP, int ROWS, bool F8> struct Tc {
 struct TcBars {
     uint64_t q_full, q_empty, epi_done, drain, v_land;
     uint64_t k_full[6], k_empty[6], v_full[6], v_empty[6];
-    uint64_t s_full[2], p_full[2], pv_done[2];
+    uint64_t s_full[2], p_full[2][2], pv_done[2];  // weights: a barrier per half of the slots
     uint64_t r_full[2][4], r_empty[2][4];  // float8 keys, values as they came
 };
 
@@ -1344,7 +1344,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         }
         for (int i = 0; i < 2; ++i) {
             bar_init(&bars.s_full[i], 1);
-            bar_init(&bars.p_full[i], 128);
+            bar_init(&bars.p_full[i][0], 128);
+            bar_init(&bars.p_full[i][1], 128);
             bar_init(&bars.pv_done[i], 1);
         }
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -1695,15 +1696,19 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 for (int i = 0; ok && i < jobs; ++i) {
                     const int st = i & 1;
                     if (!two || st == 0) ok = bar_wait(&bars.v_full[vs], v_phase, gave_up);
-                    ok = ok && bar_wait(&bars.p_full[st], p_phase >> st & 1, gave_up);
-                    p_phase ^= 1u << st;
-                    if (!ok) break;
-                    tc_after();
                     const uint64_t va = vd + vs * kStep;
                     const uint32_t pd = tmem + st * 128, od = tmem + 256 + st * DP;
 #pragma unroll
-                    for (int k = 0; k < 8; ++k)
-                        tc_mma_t(od, pd + (k >> 1) * 32 + (k & 1) * 8, va + k * 128, kPv, true);
+                    for (int half = 0; half < 2; ++half) {
+                        ok = ok && bar_wait(&bars.p_full[st][half], p_phase >> st & 1, gave_up);
+                        if (!ok) break;
+                        tc_after();
+#pragma unroll
+                        for (int k = 4 * half; k < 4 * half + 4; ++k)
+                            tc_mma_t(od, pd + (k >> 1) * 32 + (k & 1) * 8, va + k * 128, kPv, true);
+                    }
+                    p_phase ^= 1u << st;
+                    if (!ok) break;
                     tc_commit(&bars.pv_done[st]);
                     if (!two || st == 1) {
                         tc_commit(&bars.v_empty[vs]);
@@ -1799,7 +1804,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 if (!kFit && done == 0) unit = unit0 * exp2f((float)s_exp[pieces & 1][row]);
                 if (!busy) {  // rows that nothing comes of: any weights will do
                     tc_before();
-                    bar_arrive(&bars.p_full[st]);
+                    bar_arrive(&bars.p_full[st][0]);
+                    bar_arrive(&bars.p_full[st][1]);
                     continue;
                 }
                 const bool tail = (long long)(t + 1) * kTcUnit > len + 1;
@@ -1917,11 +1923,13 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                         y[e] = __uint_as_float(pair<M>(v.x, v.y));
                     }
                     tc_st16(sc + 32 * k, y);
+                    if (k & 1) {  // half of the slots: their product may begin
+                        tc_wait_st();
+                        tc_before();
+                        bar_arrive(&bars.p_full[st][k >> 1]);
+                    }
                 }
                 l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
-                tc_wait_st();
-                tc_before();
-                bar_arrive(&bars.p_full[st]);
             }
             // the stream's last product
             if (ok && done > 0) ok = warp_wait(&bars.pv_done[st], (pv + done - 1) & 1, gave_up);
