@@ -171,7 +171,7 @@ constexpr int kAppendTokens = 4;  // at most so many tokens per CTA
 // the one before is turned and written.  The angle is position * rate modulo one turn in 64-bit
 // integers (exact), so far positions lose nothing; its top 32 bits become the argument of
 // sincospi.  Accesses are of 16 bytes where V = 8.  Bound by memory: each query, key and value is
-// read once and written once.
+// read once and written once (256 x 65 tokens of 80 heads of 128: 119 us, 5.7 TB/s).
 template <typename T, typename CT, int V, bool INTERLEAVED>
 __global__ void __launch_bounds__(kAppendThreads, 2) kv_append_kernel(const AppendArgs a) {
     __shared__ float2 s_cs[kAppendTokens][kMaxDim / 2];
@@ -243,7 +243,8 @@ __global__ void __launch_bounds__(kAppendThreads, 2) kv_append_kernel(const Appe
         const long long place = s_place[j - j0];
         float2 cs[V];
 #pragma unroll
-        for (int i = 0; i < V; ++i) cs[i] = turns ? s_cs[j - j0][w * V + i] : make_float2(1.0f, 0.0f);
+        for (int i = 0; i < V; ++i)
+            cs[i] = turns ? s_cs[j - j0][w * V + i] : make_float2(1.0f, 0.0f);
 #pragma unroll
         for (int i = 0; i < kAppendHeads; ++i) {
             const int h = h0 + i * blockDim.y;
@@ -591,7 +592,10 @@ __device__ __forceinline__ bool sees(uint64_t anc, int i) { return i == 0 || (an
 // may take two products: P = hi + lo, two 16-bit halves, so that rounding the weights costs
 // nothing next to rounding the result.  float8 caches become halves on the way into the registers
 // (exact), with a power of two taken out of each query row so that a bfloat16 query fits a half
-// too; their weights are single halves, four bits finer than a bfloat16 result.
+// too; their weights are single halves, four bits finer than a bfloat16 result.  Bound by memory
+// up to 16 rows (64 sequences of 4000-8000 slots, one token, 32 query and 8 key heads of 128:
+// 245 us, 6.5 TB/s; the same over float8, 96 sequences: 211 us, 5.6 TB/s), by conversions and
+// fixed latencies over float8 with 32 (96 sequences, 24 rows: 362 us, 3.4 TB/s).
 template <typename CT, int DP, int WM> struct Split {
     using St = Stage<CT, DP>;
     static constexpr int kRows = WM * 16, kPitch = DP + 8;  // floats: rows eight banks apart
@@ -1125,6 +1129,11 @@ __global__ void __launch_bounds__(kSplitThreads * WM, 2) kv_split_kernel(const A
 // pipe, so that one is multiplied while the other is exponentiated: two tiles of 128 rows over
 // the same slots, or, when the rows fit one tile, every other 128 slots of it (joined at the
 // end).  Work is cut into ranges and joined as for the split kernel, in units of 128 slots.
+// Measured: 32 trees of 16 nodes, 128 rows per key head, 6000-12000 slots: 230 us, 5.4 TB/s (the
+// chain scores - weights - product of a stream, 5000 cycles, hides all but a fifth of the memory's
+// time); 8 trees of 65 nodes over 16000-33000 slots: 507 us, 861 TFLOP/s (the products: 128 x 128
+// of two shared-memory operands takes all of that memory's bandwidth, 780 cycles where the tensor
+// pipe alone would need 512).
 
 constexpr int kTcThreads = 512;
 constexpr int kTcUnit = 128;  // slots
@@ -1210,8 +1219,8 @@ __device__ __forceinline__ void named_sync(int id, int threads) {
 // group of eight rows to the next; `panel`: bytes between panels of 64 elements, used where the
 // operand's contiguous dimension is not the summed one (values: rows are slots).
 __device__ __forceinline__ uint64_t operand(uint32_t at, uint32_t panel) {
-    return (uint64_t)(at >> 4 & 0x3fff) | (uint64_t)(panel >> 4) << 16 | (uint64_t)(1024 >> 4) << 32 |
-           (uint64_t)1 << 46 | (uint64_t)2 << 61;
+    return (uint64_t)(at >> 4 & 0x3fff) | (uint64_t)(panel >> 4) << 16 |
+           (uint64_t)(1024 >> 4) << 32 | (uint64_t)1 << 46 | (uint64_t)2 << 61;
 }
 // Instruction descriptor: 128 x N, fp32 sums of bf16 or fp16 products; `rows`: the second
 // operand's contiguous dimension is N.
@@ -1220,7 +1229,8 @@ template <typename T> __device__ constexpr uint32_t product(int N, bool rows) {
     return 1u << 4 | type << 7 | type << 10 | (rows ? 1u << 16 : 0u) | (uint32_t)(N >> 3) << 17 |
            (128u >> 4) << 24;
 }
-__device__ __forceinline__ void tc_mma(uint32_t d, uint64_t a, uint64_t b, uint32_t desc, bool add) {
+__device__ __forceinline__ void tc_mma(uint32_t d, uint64_t a, uint64_t b, uint32_t desc,
+                                       bool add) {
     asm volatile("{ .reg .pred p; setp.ne.b32 p, %4, 0; "
                  "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p; }"
                  ::"r"(d), "l"(a), "l"(b), "r"(desc), "r"((int)add) : "memory");
@@ -1238,8 +1248,9 @@ __device__ __forceinline__ void tc_commit(uint64_t* bar) {
 // 32 columns of this thread's lane of tensor memory, as floats.
 __device__ __forceinline__ void tc_ld32(float* r, uint32_t at) {
     asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
-        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, "
+        "%11, %12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, "
+        "%28, %29, %30, %31}, [%32];"
         : "=f"(r[0]), "=f"(r[1]), "=f"(r[2]), "=f"(r[3]), "=f"(r[4]), "=f"(r[5]),
           "=f"(r[6]), "=f"(r[7]), "=f"(r[8]), "=f"(r[9]), "=f"(r[10]), "=f"(r[11]),
           "=f"(r[12]), "=f"(r[13]), "=f"(r[14]), "=f"(r[15]), "=f"(r[16]), "=f"(r[17]),
@@ -1250,8 +1261,9 @@ __device__ __forceinline__ void tc_ld32(float* r, uint32_t at) {
 }
 __device__ __forceinline__ void tc_st32(uint32_t at, const float* r) {
     asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, "
-        "%17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};"
+        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, "
+        "%10, %11, %12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, "
+        "%27, %28, %29, %30, %31, %32};"
         ::"r"(at), "f"(r[0]), "f"(r[1]), "f"(r[2]), "f"(r[3]), "f"(r[4]), "f"(r[5]), "f"(r[6]),
           "f"(r[7]), "f"(r[8]), "f"(r[9]), "f"(r[10]), "f"(r[11]), "f"(r[12]),
           "f"(r[13]), "f"(r[14]), "f"(r[15]), "f"(r[16]), "f"(r[17]), "f"(r[18]),
@@ -1289,13 +1301,22 @@ __device__ __forceinline__ void tc_st16(uint32_t at, const float* r) {
 }
 __device__ __forceinline__ float tc_ld1(uint32_t at) {
     float r;
-    asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];" : "=f"(r) : "r"(at) : "memory");
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];"
+                 : "=f"(r) : "r"(at) : "memory");
     return r;
 }
-__device__ __forceinline__ void tc_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
-__device__ __forceinline__ void tc_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
-__device__ __forceinline__ void tc_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
-__device__ __forceinline__ void tc_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tc_wait_ld() {
+    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void tc_wait_st() {
+    asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void tc_before() {
+    asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+}
+__device__ __forceinline__ void tc_after() {
+    asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+}
 
 __device__ __forceinline__ bool elect_one() {
     uint32_t yes;
@@ -1336,8 +1357,14 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         bar_init(&bars.epi_done, 256);
         bar_init(&bars.v_land, 1);
         constexpr int kFill = kF8 ? 128 : 1;
-        for (int i = 0; i < SK; ++i) bar_init(&bars.k_full[i], kFill), bar_init(&bars.k_empty[i], 1);
-        for (int i = 0; i < SV; ++i) bar_init(&bars.v_full[i], kFill), bar_init(&bars.v_empty[i], 1);
+        for (int i = 0; i < SK; ++i) {
+            bar_init(&bars.k_full[i], kFill);
+            bar_init(&bars.k_empty[i], 1);
+        }
+        for (int i = 0; i < SV; ++i) {
+            bar_init(&bars.v_full[i], kFill);
+            bar_init(&bars.v_empty[i], 1);
+        }
         for (int i = 0; i < 2 * L::kRaws; ++i) {
             bar_init(&bars.r_full[i & 1][i >> 1], 1);
             bar_init(&bars.r_empty[i & 1][i >> 1], 128);
@@ -1383,7 +1410,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 for (int kv = 0; kv < 2; ++kv) {
                     const bool tail = kv && (long long)(t + 1) * kTcUnit > len + 1;
                     ok = ok && warp_wait(&bars.r_full[kv][rs], r_phase, gave_up);
-                    ok = ok && warp_wait(kv ? &bars.v_empty[ds] : &bars.k_empty[ds], again, gave_up);
+                    ok = ok &&
+                         warp_wait(kv ? &bars.v_empty[ds] : &bars.k_empty[ds], again, gave_up);
                     if (tail) {
                         named_sync(2, 128);
                         if (lt < 4) s_wild[ds][lt] = 0;
@@ -1480,14 +1508,17 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 const long long s = (long long)t * kTcUnit + ((long long)lane << shift);
                 const uint32_t dst = (vals ? sv : sk) + st * L::kTile;
                 const bool tail = vals && (long long)(t + 1) * kTcUnit > len + 1;
-                uint64_t* const full = tail ? &bars.v_land : vals ? &bars.v_full[st] : &bars.k_full[st];
+                uint64_t* const full = tail   ? &bars.v_land
+                                       : vals ? &bars.v_full[st]
+                                              : &bars.k_full[st];
                 if (w < 10) {
                     const bool want = lane < boxes && s < total;
                     const bool good = want && (unsigned)page < (unsigned)c.num_pages;
                     if (want && !good) s_bad_piece[pieces & 7] = pieces;
                     const int pg = page;
                     page = page_of(t + 1);
-                    ok = ok && warp_wait(vals ? &bars.v_empty[st] : &bars.k_empty[st], again, gave_up);
+                    ok = ok &&
+                         warp_wait(vals ? &bars.v_empty[st] : &bars.k_empty[st], again, gave_up);
                     const uint32_t n = __popc(__ballot_sync(~0u, good));
                     if (ok) {
                         if (lane == 0) bar_expect(full, n * bytes);
@@ -1569,7 +1600,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                     if (want && !good) s_bad_piece[pieces & 7] = pieces;
                     const int pg = page, slot = (int)(s & ((1 << c.page_shift) - 1));
                     page = page_of(t + 1);
-                    const uint32_t bytes = __popc(__ballot_sync(~0u, good)) * ((uint32_t)DP << shift);
+                    const uint32_t bytes =
+                        __popc(__ballot_sync(~0u, good)) * ((uint32_t)DP << shift);
                     for (int kv = 0; ok && kv < 2; ++kv) {
                         ok = warp_wait(&bars.r_empty[kv][rs], again, gave_up);
                         if (!ok) break;
@@ -1659,7 +1691,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             constexpr uint32_t kPanel = DP > 64 ? 16384 : 1024;  // one panel: not used
             // scores times the sign of the scale: the largest is then the one to look for
             const uint32_t qk = product<M>(128, false) | (a.scale < 0.0f ? 1u << 13 : 0u);
-            const uint64_t qd = operand(sq, 16384), kd = operand(sk, 16384), vd = operand(sv, kPanel);
+            const uint64_t qd = operand(sq, 16384), kd = operand(sk, 16384);
+            const uint64_t vd = operand(sv, kPanel);
             constexpr int kStep = L::kTile >> 4;  // a tile further in a descriptor
             int ks = 0, vs = 0;  // stages and parities of the next tiles of keys and of values
             uint32_t k_phase = 0, v_phase = 0, pieces = 0, p_phase = 0;
@@ -1742,7 +1775,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             const int j = min(R / a.group, sh.n - 1), g = R - R / a.group * a.group;
             const bool live = row < p.rows;
             if (tid == 0) tell_ends(a, p, sh.tiles);
-            T* out = (T*)a.out + (((long long)p.b * a.N + j) * a.q_heads + p.h * a.group + g) * c.dim;
+            T* out = (T*)a.out +
+                     (((long long)p.b * a.N + j) * a.q_heads + p.h * a.group + g) * c.dim;
             if (sh.bad) {
                 if (tid == 0) mark(a.status, p.b, SV_DEV_BAD_LENGTH);
                 if (live && (two || st == 0))
@@ -1779,7 +1813,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             const bool nan_rows = tree_bad && anc_of == p.b;
             const uint64_t anc = anc_of == p.b ? s_anc[j] : 0;
             // from a score to an exponent of two; the products carry the sign
-            const float unit0 = fabsf(a.scale) * 1.4426950408889634f * (kF8 ? c.k_scale[p.h] : 1.0f);
+            const float unit0 =
+                fabsf(a.scale) * 1.4426950408889634f * (kF8 ? c.k_scale[p.h] : 1.0f);
             float unit = unit0;
             const bool busy = (two ? st * 128 : 0) + (w & 3) * 32 < p.rows;  // rows in this warp
             float l = 0.0f, ref = -INFINITY;
@@ -1988,7 +2023,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 #pragma unroll
                             for (int q = 0; q < 4; ++q)
                                 y[q] = pair<T>(o[e + 2 * q] * inv, o[e + 2 * q + 1] * inv);
-                            *reinterpret_cast<uint4*>(out + k + e) = make_uint4(y[0], y[1], y[2], y[3]);
+                            *reinterpret_cast<uint4*>(out + k + e) =
+                                make_uint4(y[0], y[1], y[2], y[3]);
                         }
                     }
                     __syncwarp();
@@ -2063,7 +2099,8 @@ __global__ void __launch_bounds__(128) kv_join_kernel(const AttentionArgs a, int
     if (!mine || lane * 4 >= c.dim) return;
     const int R = mt * rows + row, j = R / a.group, g = R - j * a.group;
     const float f = (c.v_scale ? c.v_scale[h] : 1.0f) / L;
-    T* dst = (T*)a.out + (((long long)b * a.N + j) * a.q_heads + h * a.group + g) * c.dim + lane * 4;
+    T* dst =
+        (T*)a.out + (((long long)b * a.N + j) * a.q_heads + h * a.group + g) * c.dim + lane * 4;
     *reinterpret_cast<uint2*>(dst) =
         make_uint2(pair<T>(y.x * f, y.y * f), pair<T>(y.z * f, y.w * f));
 }
@@ -2150,8 +2187,10 @@ constexpr int kCommitResident = 8;  // CTAs per SM
 // in order, eight moves at a time (of several planes, where one has fewer): the sources of a batch
 // are read before any of its targets is written, and since a_i >= i increases, no target is the
 // source of a later batch.  Bound by memory (or, for a few rows, by the chain node - page -
-// entry): every moved entry is read once and written once.
-__global__ void __launch_bounds__(kCommitThreads, kCommitResident) kv_commit_kernel(const CommitArgs a) {
+// entry): every moved entry is read once and written once (256 trees of 65 nodes, 16 float8
+// layers: 34 us, 4.8 TB/s; one layer of one tree 3.1 us).
+__global__ void __launch_bounds__(kCommitThreads, kCommitResident)
+    kv_commit_kernel(const CommitArgs a) {
     __shared__ long long s_src[kMaxN], s_dst[kMaxN];
     const int b = blockIdx.z, tid = threadIdx.x;
     const Cache& c = a.c;
@@ -2447,11 +2486,14 @@ static void launch_append(AppendArgs& a, int B, int sms, cudaStream_t s) {
     const dim3 grid((a.N + a.run - 1) / a.run, B), block(units, side_by_side);
     auto go = [&](auto kernel) { kernel<<<grid, block, 0, s>>>(a); };
     if (V == 8)
-        a.interleaved ? go(kv_append_kernel<T, CT, 8, true>) : go(kv_append_kernel<T, CT, 8, false>);
+        a.interleaved ? go(kv_append_kernel<T, CT, 8, true>)
+                      : go(kv_append_kernel<T, CT, 8, false>);
     else if (V == 4)
-        a.interleaved ? go(kv_append_kernel<T, CT, 4, true>) : go(kv_append_kernel<T, CT, 4, false>);
+        a.interleaved ? go(kv_append_kernel<T, CT, 4, true>)
+                      : go(kv_append_kernel<T, CT, 4, false>);
     else
-        a.interleaved ? go(kv_append_kernel<T, CT, 1, true>) : go(kv_append_kernel<T, CT, 1, false>);
+        a.interleaved ? go(kv_append_kernel<T, CT, 1, true>)
+                      : go(kv_append_kernel<T, CT, 1, false>);
 }
 
 static sv_status launched() { return cudaGetLastError() == cudaSuccess ? SV_OK : SV_ERR_CUDA; }
@@ -2584,7 +2626,8 @@ sv_status spec_kv_attention(const sv_kv_cache* cache, const void* q, const sv_st
     // which then waits for memory only; more: tcgen05, where a page fills whole groups of eight
     // rows of the swizzle.
     const int rows = N * a.group;
-    const bool cluster = small_call(B, cache->heads, rows, cache->table_width * cache->page_size, sms);
+    const bool cluster =
+        small_call(B, cache->heads, rows, cache->table_width * cache->page_size, sms);
     CUtensorMap kmap, vmap;
     const bool wide = !cluster && rows > 32 && cache->page_size >= 8 &&
                       cache_map(&kmap, cache->k, cache) && cache_map(&vmap, cache->v, cache);
