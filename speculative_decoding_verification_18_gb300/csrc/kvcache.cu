@@ -1224,7 +1224,7 @@ __device__ __forceinline__ uint64_t operand(uint32_t at, uint32_t panel) {
 }
 // Instruction descriptor: 128 x N, fp32 sums of bf16 or fp16 products; `rows`: the second
 // operand's contiguous dimension is N.
-template <typename T> __device__ constexpr uint32_t product(int N, bool rows) {
+template <typename T> __device__ __forceinline__ constexpr uint32_t product(int N, bool rows) {
     const uint32_t type = std::is_same<T, __half>::value ? 0u : 1u;
     return 1u << 4 | type << 7 | type << 10 | (rows ? 1u << 16 : 0u) | (uint32_t)(N >> 3) << 17 |
            (128u >> 4) << 24;
@@ -1687,7 +1687,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             }
         }
         if (w == 12 && elect_one()) {
-            constexpr uint32_t kPv = product<M>(DP, true);
+            const uint32_t pv = product<M>(c.dim, true);  // the elements that heads have
             constexpr uint32_t kPanel = DP > 64 ? 16384 : 1024;  // one panel: not used
             // scores times the sign of the scale: the largest is then the one to look for
             const uint32_t qk = product<M>(128, false) | (a.scale < 0.0f ? 1u << 13 : 0u);
@@ -1713,6 +1713,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                     const uint64_t qa = qd + (two ? st * kStep : 0), ka = kd + ks * kStep;
 #pragma unroll
                     for (int k = 0; k < DP / 16; ++k) {
+                        if (k * 16 >= c.dim) break;
                         // in 16 bytes: a panel, 16 elements of a row
                         const uint64_t at = (k >> 2) * (16384 >> 4) + (k & 3) * 2;
                         tc_mma(tmem + st * 128, qa + at, ka + at, qk, k > 0);
@@ -1738,7 +1739,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                         tc_after();
 #pragma unroll
                         for (int k = 4 * half; k < 4 * half + 4; ++k)
-                            tc_mma_t(od, pd + (k >> 1) * 32 + (k & 1) * 8, va + k * 128, kPv, true);
+                            tc_mma_t(od, pd + (k >> 1) * 32 + (k & 1) * 8, va + k * 128, pv, true);
                     }
                     p_phase ^= 1u << st;
                     if (!ok) break;

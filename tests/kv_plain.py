@@ -44,7 +44,9 @@ def attention(q, k, v, table, kv_len, counts, parents, scale, k_scale=None, v_sc
     score's error: (dim + 8) additions and products, each within 2^-23 (the tensor cores cut,
     rather than round, some bits) of sum_d |q_d k_d|, times |scale|; plus 2^-20 for the exponential
     and the running sums' rescaling, and 2^-23 per 64 positions for the sums' length.  Rounding
-    the result adds u of the result's type."""
+    the result adds u of the result's type.  Halves (fp16 results; the weights of fp16 and float8
+    caches, relative to the largest) are rounded to steps of 2^-24 at the finest: half of one of
+    the result's, and of every weight's times |v|."""
     B, N, HQ, D = q.shape
     H = k.shape[2]
     out = torch.full((B, N, HQ, D), math.nan, dtype=torch.float64)
@@ -54,7 +56,8 @@ def attention(q, k, v, table, kv_len, counts, parents, scale, k_scale=None, v_sc
         n, m = int(kv_len[b]), int(counts[b])
         up = paths(None if parents is None else parents[b], N)
         for h in range(H):
-            ks, vs = entries(k, k_scale, table[b], n + m, h), entries(v, v_scale, table[b], n + m, h)
+            ks = entries(k, k_scale, table[b], n + m, h)
+            vs = entries(v, v_scale, table[b], n + m, h)
             for j in range(m):
                 see = torch.tensor(list(range(n)) + sorted(n + i for i in up[j]))
                 kk, vv = ks[see], vs[see]
@@ -68,6 +71,8 @@ def attention(q, k, v, table, kv_len, counts, parents, scale, k_scale=None, v_sc
                     d = u + (D + 8) * 2.0 ** -23 * abs(scale) * float((kk.abs() @ x.abs()).max()) \
                         + 2.0 ** -20 + (len(see) / 64 + 1) * 2.0 ** -23
                     bound[at] = 2 * d * (p @ vv.abs()) + u * o.abs() + 1e-30
+                    if q.dtype == torch.float16 or k.dtype == E4M3:
+                        bound[at] += 2.0 ** -25 * (1 + vv.abs().sum(0))
                     spread[at] = ((p * p) @ (vv * vv)).sqrt() + o.abs()
     return out, bound, spread
 
