@@ -334,8 +334,9 @@ struct AttentionArgs {
     int B, N, q_heads, group;
     int ctas;             // ranges
     int mts;              // row tiles of an item's head, counted for N tokens
-    int2* ends;           // workspace: [B, heads, mts] first and last range of an item's pieces
-                          // (-1: one range has all of it and wrote the output)
+    int* started;         // workspace: [ctas] the item that a range starts and another goes on
+                          // with, or -1: there is at most one, its last
+    int* ended;           // workspace: [B, heads, mts] the range that ends an item begun by another
     float* part_o;        // workspace: [2 * ctas, rows, DP], or of the wide kernel
                           // [2 * ctas, DP / 4, rows, 4]: there a thread holds a row
     float2* part_ml;      // workspace: [2 * ctas, rows] maximum (base 2) and sum
@@ -415,11 +416,11 @@ struct Start {
     int b;
 };
 
-// Says where the pieces of an item are, for the join: the piece that starts it, or ends it.
+// Says where the pieces of an item are, for the join.
 __device__ __forceinline__ void tell_ends(const AttentionArgs& a, const Piece& p, int tiles) {
-    int2* e = a.ends + ((long long)p.b * a.c.heads + p.h) * a.mts + p.mt;
-    if (p.t0 == 0) e->x = p.t1 == tiles ? -1 : (int)blockIdx.x;
-    else if (p.t1 == tiles) e->y = (int)blockIdx.x;
+    const int item = (p.b * a.c.heads + p.h) * a.mts + p.mt;
+    if (p.t0 == 0 && p.t1 < tiles) a.started[blockIdx.x] = item;
+    if (p.t0 > 0 && p.t1 == tiles) a.ended[item] = blockIdx.x;
 }
 
 // The range of this CTA: weight of the units before each sequence (a scan over the batch), their
@@ -444,6 +445,7 @@ __device__ __forceinline__ Walk start_walk(const AttentionArgs& a, int rows, int
         W += s_scan[i];
         if (i < w) before += s_scan[i];
     }
+    if (tid == 0) a.started[blockIdx.x] = -1;  // until it starts one that it does not end
     const int P = ranges_of(W, a.ctas, full);
     const bool some = W > 0 && (int)blockIdx.x < P;
     const long long x = some ? range_start(W, P, blockIdx.x) : 0;
@@ -595,7 +597,7 @@ __device__ __forceinline__ bool sees(uint64_t anc, int i) { return i == 0 || (an
 // too; their weights are single halves, four bits finer than a bfloat16 result.  Bound by memory
 // up to 16 rows (64 sequences of 4000-8000 slots, one token, 32 query and 8 key heads of 128:
 // 245 us, 6.5 TB/s; the same over float8, 96 sequences: 211 us, 5.6 TB/s), by conversions and
-// fixed latencies over float8 with 32 (96 sequences, 24 rows: 362 us, 3.4 TB/s).
+// fixed latencies over float8 with 32 (96 sequences, 24 rows: 352 us, 3.5 TB/s).
 template <typename CT, int DP, int WM> struct Split {
     using St = Stage<CT, DP>;
     static constexpr int kRows = WM * 16, kPitch = DP + 8;  // floats: rows eight banks apart
@@ -656,35 +658,6 @@ __global__ void __launch_bounds__(kSplitThreads * WM, 2) kv_split_kernel(const A
         bool bad = sh.bad;
         if (bad && tid == 0) mark(a.status, b, SV_DEV_BAD_LENGTH);
 
-        // The ancestors of every node, where this piece reaches the new tokens.
-        if (!bad && (long long)t1 * kUnit > len && anc_of != b) {
-            __syncthreads();
-            int f = 0;
-            if (a.parents)
-                for (int i = tid; i < sh.n; i += THREADS) {
-                    const int p = a.parents[(long long)b * a.N + i];
-                    s_par[i] = p;
-                    f |= i > 0 && (p < 0 || p >= i);
-                }
-            f = __syncthreads_or(f);
-            if (tid < sh.n) {
-                uint64_t m = 0;
-                if (!a.parents)
-                    m = tid == 64 ? ~0ull : (1ull << tid) - 1;
-                else if (!f)
-                    for (int i = tid; i > 0; i = s_par[i]) m |= 1ull << (i - 1);
-                s_anc[tid] = m;
-            }
-            __syncthreads();
-            if (f) {
-                bad = true;
-                if (tid == 0) mark(a.status, b, SV_DEV_BAD_TREE);
-                anc_of = -1;
-            } else {
-                anc_of = b;
-            }
-        }
-
         const char* kb = c.k + h * c.head_stride;
         const char* vb = c.v + h * c.head_stride;
         const int32_t* table = c.table + (long long)b * c.table_width;
@@ -729,6 +702,36 @@ __global__ void __launch_bounds__(kSplitThreads * WM, 2) kv_split_kernel(const A
             page = page_of(t0 + S - 1);
 #pragma unroll
             for (int i = 0; i < S - 1; ++i) issue(t0 + i, i, first[i]);
+        }
+
+        // With the first slots on their way: the ancestors of every node, where this piece reaches
+        // the new tokens.
+        if (!bad && (long long)t1 * kUnit > len && anc_of != b) {
+            __syncthreads();
+            int f = 0;
+            if (a.parents)
+                for (int i = tid; i < sh.n; i += THREADS) {
+                    const int p = a.parents[(long long)b * a.N + i];
+                    s_par[i] = p;
+                    f |= i > 0 && (p < 0 || p >= i);
+                }
+            f = __syncthreads_or(f);
+            if (tid < sh.n) {
+                uint64_t m = 0;
+                if (!a.parents)
+                    m = tid == 64 ? ~0ull : (1ull << tid) - 1;
+                else if (!f)
+                    for (int i = tid; i > 0; i = s_par[i]) m |= 1ull << (i - 1);
+                s_anc[tid] = m;
+            }
+            __syncthreads();
+            if (f) {
+                bad = true;
+                if (tid == 0) mark(a.status, b, SV_DEV_BAD_TREE);
+                anc_of = -1;
+            } else {
+                anc_of = b;
+            }
         }
 
         // Queries as the A operand: thread (row lane / 4, + 8; elements by lane % 4), with the
@@ -1129,9 +1132,9 @@ __global__ void __launch_bounds__(kSplitThreads * WM, 2) kv_split_kernel(const A
 // pipe, so that one is multiplied while the other is exponentiated: two tiles of 128 rows over
 // the same slots, or, when the rows fit one tile, every other 128 slots of it (joined at the
 // end).  Work is cut into ranges and joined as for the split kernel, in units of 128 slots.
-// Measured: 32 trees of 16 nodes, 128 rows per key head, 6000-12000 slots: 230 us, 5.4 TB/s (the
+// Measured: 32 trees of 16 nodes, 128 rows per key head, 6000-12000 slots: 229 us, 5.4 TB/s (the
 // chain scores - weights - product of a stream, 5000 cycles, hides all but a fifth of the memory's
-// time); 8 trees of 65 nodes over 16000-33000 slots: 507 us, 861 TFLOP/s (the products: 128 x 128
+// time); 8 trees of 65 nodes over 16000-33000 slots: 500 us, 873 TFLOP/s (the products: 128 x 128
 // of two shared-memory operands takes all of that memory's bandwidth, 780 cycles where the tensor
 // pipe alone would need 512).
 
@@ -2045,8 +2048,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512));
 }
 
-// Adds up the pieces of the items that more than one range holds: sum over pieces of
-// 2^(m - max) (o, l), then o / l.  A CTA of four warps per four rows of an item (a warp each), or
+// Adds up the pieces of the items that more than one range holds, at most one per range that
+// starts one: sum over pieces of 2^(m - max) (o, l), then o / l.  A CTA of four warps per four rows of an item (a warp each), or
 // per row (the warps share its pieces) where the host expects many pieces per item.
 template <typename T, int DP>
 __global__ void __launch_bounds__(128) kv_join_kernel(const AttentionArgs a, int rows, int warps) {
@@ -2054,12 +2057,11 @@ __global__ void __launch_bounds__(128) kv_join_kernel(const AttentionArgs a, int
     const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
     const Cache& c = a.c;
     cudaGridDependencySynchronize();
-    const int mt = blockIdx.x % a.mts, bh = blockIdx.x / a.mts;
-    const int h = bh % c.heads, b = bh / c.heads;
-    const int2 ends = a.ends[blockIdx.x];  // (not written for an item that is not there)
+    const int item = a.started[blockIdx.x];
+    if (item < 0) return;
+    const int mt = item % a.mts, h = item / a.mts % c.heads, b = item / a.mts / c.heads;
+    const int c0 = blockIdx.x, c1 = a.ended[item];
     const Share sh = share_of(a, b, rows, kUnit);
-    if (mt >= sh.mts || ends.x < 0) return;
-    const int c0 = ends.x, c1 = ends.y;
     const int row = warps == 1 ? blockIdx.y * 4 + w : blockIdx.y;
     const int live = min(rows, sh.n * a.group - mt * rows);
     const bool mine = row < live;
@@ -2116,12 +2118,11 @@ __global__ void __launch_bounds__(128) kv_wide_join_kernel(const AttentionArgs a
     const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
     const Cache& c = a.c;
     cudaGridDependencySynchronize();
-    const int mt = blockIdx.x % a.mts, bh = blockIdx.x / a.mts;
-    const int h = bh % c.heads, b = bh / c.heads;
-    const int2 ends = a.ends[blockIdx.x];  // (not written for an item that is not there)
+    const int item = a.started[blockIdx.x];
+    if (item < 0) return;
+    const int mt = item % a.mts, h = item / a.mts % c.heads, b = item / a.mts / c.heads;
+    const int c0 = blockIdx.x, c1 = a.ended[item];
     const Share sh = share_of(a, b, rows, kTcUnit);
-    if (mt >= sh.mts || ends.x < 0) return;
-    const int c0 = ends.x, c1 = ends.y;
     const int cols = DP / 4 / (warps == 4 ? 1 : 4);  // blocks of four elements, or of sixteen
     const int row = blockIdx.y / cols * 32 + lane;
     const int d4 = warps == 4 ? blockIdx.y % cols : blockIdx.y % cols * 4 + w;
@@ -2408,8 +2409,8 @@ static sv_status device_ok(int* sms) {
     return SV_OK;
 }
 
-// The workspace: where the pieces of each item are (tiles of at least 16 rows, of 32 where there
-// are more), then two pieces of a row tile per CTA.
+// The workspace: where items are cut (tiles of at least 16 rows, of 32 where there are more), then
+// two pieces of a row tile per CTA.
 struct AttentionWs { size_t part_o, part_ml, bytes; };
 static AttentionWs attention_ws(int B, int heads, int rows, int dim) {
     const size_t dp = dim <= 64 ? 64 : 128, items = (size_t)B * heads * ((rows + 31) / 32);
@@ -2417,7 +2418,7 @@ static AttentionWs attention_ws(int B, int heads, int rows, int dim) {
     const size_t wide = rows <= 32 ? 0 : (size_t)2 * kTcMaxCtas * (rows <= 128 ? 128 : 256);
     const size_t held = split > wide ? split : wide;
     AttentionWs l;
-    l.part_o = (items * sizeof(int2) + 255) / 256 * 256;
+    l.part_o = ((items + kMaxCtas) * sizeof(int) + 255) / 256 * 256;
     l.part_ml = l.part_o + held * dp * 4;
     l.bytes = l.part_ml + held * 8;
     return l;
@@ -2629,8 +2630,13 @@ sv_status spec_kv_attention(const sv_kv_cache* cache, const void* q, const sv_st
     const int rows = N * a.group;
     const bool cluster =
         small_call(B, cache->heads, rows, cache->table_width * cache->page_size, sms);
+    // Float8 over short contexts stays with mma.sync up to 64 rows: pieces of one or two units, and
+    // no halves to make (100 sequences of 64 rows over at most 128 slots 38 against 62 us, 2048
+    // slots 135 against 146, 4096 slots 215 against 200).
+    const int slots = cache->table_width * cache->page_size;
+    const int few = cache->dtype == SV_E4M3 && slots <= 2048 ? 64 : 32;
     CUtensorMap kmap, vmap;
-    const bool wide = !cluster && rows > 32 && cache->page_size >= 8 &&
+    const bool wide = !cluster && rows > few && cache->page_size >= 8 &&
                       cache_map(&kmap, cache->k, cache) && cache_map(&vmap, cache->v, cache);
     const int tile = wide ? (rows <= 128 ? 128 : 256) : rows <= 16 ? 16 : 32;
     const int unit = wide ? kTcUnit : kUnit;
@@ -2643,7 +2649,8 @@ sv_status spec_kv_attention(const sv_kv_cache* cache, const void* q, const sv_st
     a.ctas = fit < most ? fit : most;
     const AttentionWs l = attention_ws(B, cache->heads, rows, cache->dim);
     a.mts = mts;
-    a.ends = (int2*)ws;
+    a.started = (int*)ws;
+    a.ended = a.started + kMaxCtas;
     a.part_o = (float*)((char*)ws + l.part_o);
     a.part_ml = (float2*)((char*)ws + l.part_ml);
     // Pieces per item, if all sequences were alike: with many, the warps of a CTA share a row.
@@ -2673,7 +2680,7 @@ sv_status spec_kv_attention(const sv_kv_cache* cache, const void* q, const sv_st
         cfg.blockDim = dim3(128);
         cfg.dynamicSmemBytes = 0;
         const int parts = wide ? tile / 32 * (cache->dim <= 64 ? 16 : 32) : tile;
-        cfg.gridDim = dim3(B * cache->heads * mts, warps == 4 ? parts : parts / 4);
+        cfg.gridDim = dim3(a.ctas, warps == 4 ? parts : parts / 4);
         return cudaLaunchKernelEx(&cfg, join, a, tile, warps);
     };
     const cudaError_t e = wide ? with_wide(dtype, cache->dtype, cache->dim, rows, launch)
