@@ -70,7 +70,7 @@ extern "C" {
 typedef struct {
     void* k;                /* DEVICE */
     void* v;                /* DEVICE */
-    const int32_t* table;   /* DEVICE [B, table_width]: the pages of each sequence */
+    const int32_t* table;   /* DEVICE [B, table_width]: the pages of each sequence; may be NULL if B is 0 */
     const float* k_scale;   /* DEVICE [heads], SV_E4M3 only (NULL otherwise):   */
     const float* v_scale;   /* an entry stands for its stored value times this; */
                             /* spec_kv_commit does not look at them             */

@@ -2429,8 +2429,8 @@ static AttentionWs attention_ws(int B, int heads, int rows, int dim) {
 }
 
 // scales: the call needs the scales of a float8 cache.
-static sv_status check_cache(const sv_kv_cache* c, bool scales, Cache* out) {
-    if (!c || !c->k || !c->v || !c->table) return SV_ERR_INVALID_ARG;
+static sv_status check_cache(const sv_kv_cache* c, bool scales, int B, Cache* out) {
+    if (!c || !c->k || !c->v || (B > 0 && !c->table)) return SV_ERR_INVALID_ARG;
     if (!aligned16(c->k) || !aligned16(c->v) || !aligned16(c->table)) return SV_ERR_INVALID_ARG;
     if (c->dtype != SV_BF16 && c->dtype != SV_F16 && c->dtype != SV_E4M3) return SV_ERR_INVALID_ARG;
     const bool scaled = c->dtype == SV_E4M3;
@@ -2537,7 +2537,7 @@ sv_status spec_kv_append(const sv_kv_cache* cache, const sv_rope* rope, const vo
                          const int32_t* num_new, const int32_t* tree_parents, int B, int N,
                          int q_heads, void* q_out, uint32_t* status, cudaStream_t stream) {
     AppendArgs a = {};
-    sv_status st = check_cache(cache, true, &a.c);
+    sv_status st = check_cache(cache, true, B, &a.c);
     if (st != SV_OK) return st;
     if (!q) q_heads = cache->heads;
     st = check_tokens(cache, dtype, kv_len, num_new, tree_parents, status, B, N, q_heads);
@@ -2602,7 +2602,7 @@ sv_status spec_kv_attention(const sv_kv_cache* cache, const void* q, const sv_st
                             void* out, void* ws, size_t ws_bytes, uint32_t* status,
                             cudaStream_t stream) {
     AttentionArgs a = {};
-    sv_status st = check_cache(cache, true, &a.c);
+    sv_status st = check_cache(cache, true, B, &a.c);
     if (st != SV_OK) return st;
     st = check_tokens(cache, dtype, kv_len, num_new, tree_parents, status, B, N, q_heads);
     if (st != SV_OK) return st;
@@ -2698,7 +2698,7 @@ sv_status spec_kv_commit(const sv_kv_cache* cache, int layers, int64_t layer_str
                          const int32_t* num_accepted, int B, int N, int32_t* kv_len_out,
                          uint32_t* status, cudaStream_t stream) {
     CommitArgs a = {};
-    sv_status st = check_cache(cache, false, &a.c);
+    sv_status st = check_cache(cache, false, B, &a.c);
     if (st != SV_OK) return st;
     if (layers < 1 || B < 0 || N < 1) return SV_ERR_INVALID_ARG;
     const int e = elem_bytes(cache->dtype);

@@ -98,7 +98,7 @@ def test_append_argument_errors(kv):
         assert call(**bad) == code, bad
     assert kv.load().spec_kv_append(None, None, P, ctypes.byref(st), P, P, ctypes.byref(st), 0, P,
                                     None, None, 2, 3, 4, P, None, None) == 1
-    assert call(B=0) == 0  # launches nothing
+    assert call(B=0) == 0 and call(B=0, cache=cache_struct(kv, table=None)) == 0  # no launch
 
 
 def test_attention_argument_errors(kv):
@@ -124,7 +124,7 @@ def test_attention_argument_errors(kv):
                       (dict(status=P + 4), 1), (dict(parents=P + 4), 1),
                       (dict(qs=Strides(64, 64, 4)), 1)):
         assert call(**bad) == code, bad
-    assert call(B=0) == 0
+    assert call(B=0) == 0 and call(B=0, cache=cache_struct(kv, table=None)) == 0
 
 
 def test_commit_argument_errors(kv):
@@ -144,7 +144,7 @@ def test_commit_argument_errors(kv):
                       (dict(B=-1), 1), (dict(N=0), 1), (dict(N=66), 3), (dict(nodes=P + 4), 1), (dict(acc=P + 4), 1),
                       (dict(out=P + 4), 1), (dict(status=P + 4), 1)):
         assert call(**bad) == code, bad
-    assert call(B=0) == 0
+    assert call(B=0) == 0 and call(B=0, cache=cache_struct(kv, table=None)) == 0
 
 
 def test_logits_calls_refuse_the_cache_types(kv):
