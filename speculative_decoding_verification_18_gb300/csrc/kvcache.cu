@@ -209,9 +209,10 @@ __global__ void __launch_bounds__(kAppendThreads, 2) kv_append_kernel(const Appe
     }
     const int j1 = min(n, j0 + a.run);
     if (j0 >= j1) return;
-    if (tid < j1 - j0) {
-        s_place[tid] = slot_offset(c, b, len + j0 + tid);
-        if (s_place[tid] < 0) mark(a.status, b, SV_DEV_BAD_PAGE);
+    // (a block of one or two short heads has fewer threads than its run has tokens)
+    for (int i = tid; i < j1 - j0; i += threads) {
+        s_place[i] = slot_offset(c, b, len + j0 + i);
+        if (s_place[i] < 0) mark(a.status, b, SV_DEV_BAD_PAGE);
     }
     if (a.parents) {
         int bad = 0;

@@ -1,0 +1,119 @@
+"""Cache calls over many tokens and many planes on the GPU: there a CTA of append takes several
+tokens in turn and a CTA of commit several layers' keys and values.  Compared on the device with
+float64 (append) or bit by bit (commit)."""
+import pytest
+import torch
+
+import kv_plain
+from kv_plain import E4M3
+from parity import Guarded
+from test_kv_gpu import BF, HF, built, kv, tree  # noqa: F401 (fixtures)
+
+pytestmark = pytest.mark.gpu
+
+
+def sms():
+    return torch.cuda.get_device_properties(0).multi_processor_count
+
+
+def depths(parents, B, N):
+    """[B, N] depth of each node on the CPU."""
+    if parents is None:
+        return torch.arange(N).expand(B, N)
+    d = torch.zeros(B, N, dtype=torch.long)
+    for j in range(1, N):
+        d[:, j] = d.gather(1, parents[:, j:j + 1].long())[:, 0] + 1
+    return d
+
+
+def entries_at(pool, place):
+    """pool[page, slot] for an index pair, float8 by its bytes."""
+    return pool[place] if pool.element_size() > 1 else \
+        pool.view(torch.uint8)[place].view(pool.dtype)
+
+
+# Tokens per CTA: those of all sequences over six per SM, four at most.
+@pytest.mark.parametrize("run", [2, 3, 4])
+@pytest.mark.parametrize("heads,group,dim,rot,dtype,cache,form,kw", [
+    (1, 0, 16, 0, BF, BF, "chain", {}),              # two threads per CTA
+    (1, 0, 16, 16, HF, HF, "tree", {}),
+    (1, 1, 16, 0, BF, E4M3, "tree", {}),             # three
+    (1, 1, 16, 16, BF, BF, "chain", dict(in_place=True)),
+    (1, 2, 16, 16, BF, BF, "tree", {}),              # four
+    (2, 4, 64, 64, BF, BF, "tree", {}),
+    (2, 4, 64, 20, HF, E4M3, "tree", dict(interleaved=True)),
+    (8, 16, 128, 128, BF, BF, "tree", dict(in_place=True)),  # more heads than one pass takes
+    (8, 16, 128, 64, HF, HF, "chain", dict(interleaved=True)),
+    (3, 5, 80, 40, BF, E4M3, "star", {}),
+])
+def test_append_runs_of_tokens(kv, run, heads, group, dim, rot, dtype, cache, form, kw):
+    g = torch.Generator().manual_seed(run * 100 + heads)
+    N = 65 if run > 2 else 33
+    B = (6 * sms() * run + N - 1) // N
+    page, hq = 16, heads * group
+    lens = torch.randint(0, 50, (B,), generator=g).to(torch.int32)
+    # ragged, with counts of 0, of N, and of every remainder by the run's length
+    counts = torch.tensor([N if b % 5 == 0 else (b * 7) % (N + 1) for b in range(B)],
+                          dtype=torch.int32)
+    parents = None if form == "chain" else torch.stack([tree(N, form, g) for _ in range(B)])
+    width = (50 + N + page - 1) // page
+    pages = B * width
+    table = torch.randperm(pages, generator=g).to(torch.int32).view(B, width).cuda()
+    rand = lambda *s: torch.randn(*s, generator=g).cuda()
+    gd = Guarded()
+    pools = [gd.empty((pages, page, heads, dim), torch.uint8 if cache == E4M3 else dtype)
+             for _ in range(2)]
+    for p in pools:
+        p.view(torch.uint8).fill_(0x31)
+    pools = [p.view(cache) for p in pools]
+    scales = [None, None]
+    if cache == E4M3:
+        scales = [torch.rand(heads, generator=g).cuda() * 0.02 + 0.01 for _ in range(2)]
+    before = [p.view(torch.uint8).clone() for p in pools]
+    c = kv.PagedCache(*pools, table, *scales)
+    q = rand(B, N, hq, dim).to(dtype) if group else None
+    k, v = rand(B, N, heads, dim).to(dtype), rand(B, N, heads, dim).to(dtype)
+    out = gd.empty((B, N, hq, dim), dtype, fill=7.0) if group else None
+    if kw.get("in_place"):
+        out.copy_(q)
+    held = None if out is None else out.clone()
+    interleaved = kw.get("interleaved", False)
+    rope = kv.Rope(rot, interleaved=interleaved) if rot else None
+    status = gd.empty((B,), torch.int32, fill=0)
+    kv.spec_kv_append(c, k, v, lens.cuda(), q=out if kw.get("in_place") else q, q_out=out,
+                      rope=rope, parents=None if parents is None else parents.cuda(),
+                      num_new=counts.cuda(), status=status)
+    gd.check()
+    assert not bool(status.any())
+
+    live = (torch.arange(N) < counts[:, None]).cuda()
+    pos = (lens[:, None] + depths(parents, B, N)).cuda()[:, :, None, None].double()
+    rate = kv_plain.rates(rot, 10000.0).cuda()
+
+    def turned(x):
+        x = x.double()
+        i = torch.arange(rot // 2, device="cuda")
+        one, two = (2 * i, 2 * i + 1) if interleaved else (i, i + rot // 2)
+        y, slack = x.clone(), torch.zeros_like(x)
+        a, b, co, si = x[..., one], x[..., two], torch.cos(pos * rate), torch.sin(pos * rate)
+        y[..., one], y[..., two] = a * co - b * si, b * co + a * si
+        slack[..., one] = slack[..., two] = a.abs() + b.abs()
+        return y, slack
+
+    if group:
+        y, slack = turned(q)
+        assert bool(((out.double() - y).abs() <= kv_plain.stored_bound(y, slack, dtype))[live].all())
+        assert torch.equal(out[~live], held[~live])
+    slot = (lens[:, None] + torch.arange(N)).long().cuda()
+    place = table.long().gather(1, slot // page)[live], (slot % page)[live]
+    for pool, was, x, scale, turn in zip(pools, before, (k, v), scales, (True, False)):
+        y, slack = turned(x) if turn else (x.double(), torch.zeros_like(x, dtype=torch.float64))
+        y, slack = y[live], slack[live]
+        got, one = entries_at(pool, place).double(), None
+        if cache == E4M3:
+            one = scale.double()[:, None]
+            got, y = got * one, y.clamp(-448 * one, 448 * one)
+        assert bool(((got - y).abs() <= kv_plain.stored_bound(y, slack, cache, one)).all())
+        now = pool.view(torch.uint8).clone()
+        now[place], was[place] = 0, 0
+        assert torch.equal(now, was)  # nothing else was written
