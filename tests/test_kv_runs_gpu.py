@@ -117,3 +117,72 @@ def test_append_runs_of_tokens(kv, run, heads, group, dim, rot, dtype, cache, fo
         now = pool.view(torch.uint8).clone()
         now[place], was[place] = 0, 0
         assert torch.equal(now, was)  # nothing else was written
+
+
+# Planes (a layer's keys or values) per CTA: those of all sequences over eight CTAs per SM.
+@pytest.mark.parametrize("cache,heads,dim,order", [
+    (BF, 8, 128, "slot"),     # 128 columns of 16 bytes: a plane fills the block
+    (BF, 9, 128, "head"),     # 144: two blocks, the second mostly empty
+    (E4M3, 16, 128, "slot"),
+    (HF, 2, 64, "head"),      # 16: eight planes side by side
+    (E4M3, 1, 16, "slot"),    # one
+    (BF, 3, 80, "slot"),      # 30: four planes, eight threads left over
+])
+@pytest.mark.parametrize("N,few", [(65, False), (9, True), (2, True)])
+def test_commit_runs_of_planes(kv, cache, heads, dim, order, N, few):
+    """Every CTA takes more planes than it has side by side, with 0 to N - 1 moves in each."""
+    g = torch.Generator().manual_seed(N + heads)
+    size = 1 if cache == E4M3 else 2
+    units = heads * dim * size // 16
+    side = max(1, 128 // units)
+    layers = 24
+    blocks = (units + 127) // 128
+    B = 8 * sms() * (2 * side + 1) // (2 * layers * blocks) + 1  # more than two turns per CTA
+    if 2 * side + 1 > 2 * layers:
+        layers, B = 140, 8 * sms() * 270 // 280 + 1
+    page, span = 8, 40
+    width = (span + N + page) // page
+    # all pages but those of the committed slots are a sequence's own
+    pages = B * width
+    lens = torch.randint(0, span, (B,), generator=g).to(torch.int32)
+    table = torch.randperm(pages, generator=g).view(B, width).to(torch.int32).cuda()
+    nodes = torch.full((B, N), -1, dtype=torch.int32)
+    acc = torch.zeros(B, dtype=torch.int32)
+    for b in range(B):
+        most = 1 + (b % 3 if few else N - 1)
+        n = int(torch.randint(0, min(N, most + 1), (1,), generator=g))
+        pick = torch.randperm(N - 1, generator=g)[:n].sort().values + 1
+        if b % 4 == 0:  # the first ones stay where they are
+            pick[:n // 2] = torch.arange(1, n // 2 + 1)
+            pick = pick.unique()
+        acc[b] = len(pick)
+        nodes[b, :len(pick)] = pick.to(torch.int32)
+    bits = torch.uint8 if size == 1 else torch.int16
+    inner = (page, heads, dim) if order == "slot" else (heads, page, dim)
+    gd, want = Guarded(), []
+    pools = [gd.empty((layers, pages) + inner, bits) for _ in range(2)]
+    dg = torch.Generator(device="cuda").manual_seed(7)
+    look = (lambda x: x) if order == "slot" else (lambda x: x.transpose(2, 3))
+    to = torch.arange(1, N + 1).expand(B, N)
+    moved = (torch.arange(N) < acc[:, None])
+
+    def place(node):
+        slot = (lens[:, None] + node.long()).cuda()
+        m = moved.cuda()
+        return table.long().gather(1, (slot // page).clamp(0, width - 1))[m], (slot % page)[m]
+
+    src, dst = place(nodes.clamp(min=0)), place(to)
+    for p in pools:
+        p.random_(0, 120, generator=dg)
+        x = look(p.clone())
+        x[:, dst[0], dst[1]] = x[:, src[0], src[1]]
+        want.append(x)
+    c = kv.PagedCache(look(pools[0].view(cache)), look(pools[1].view(cache)), table)
+    out = gd.empty((B,), torch.int32, fill=-7)
+    status = gd.empty((B,), torch.int32, fill=0)
+    kv.spec_kv_commit(c, lens.cuda(), acc.cuda(), out, nodes.cuda(), status=status)
+    gd.check()
+    assert not bool(status.any())
+    assert torch.equal(out.cpu(), lens + acc + 1)
+    for p, w in zip(pools, want):
+        assert torch.equal(look(p), w)
