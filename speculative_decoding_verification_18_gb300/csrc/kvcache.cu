@@ -1143,6 +1143,8 @@ constexpr int kTcThreads = 512;
 constexpr int kTcUnit = 128;  // slots
 constexpr int kTcMaxCtas = 152;
 
+constexpr int kBadFlags = 16;  // a power of two
+
 template <int DP, int ROWS, bool F8> struct Tc {
     static constexpr int kTile = 128 * DP * 2;          // bytes of 128 keys, values or queries
     static constexpr int kQ = ROWS / 128 * kTile;
@@ -1156,6 +1158,11 @@ template <int DP, int ROWS, bool F8> struct Tc {
     static constexpr int kRawFit = (224 * 1024 - kQ - (kK + kV) * kTile) / (2 * kRaw);
     static constexpr int kRaws = !F8 ? 0 : kRawFit > 4 ? 4 : kRawFit;  // of each
     static constexpr int kSmem = kQ + (kK + kV) * kTile + 2 * kRaws * kRaw;
+    // A piece's bad page is flagged before the loads wait for a stage and looked at when its rows
+    // are written.  With a tile per piece the loads of piece P have then met the products of piece
+    // P - kRaws - kK - 1 (float8) or the scores of P - kK - 1, whose rows, or those of the piece
+    // before, may still wait to be written: flags of so many pieces and one more are alive.
+    static_assert(kK + kRaws + 3 <= kBadFlags, "flags of bad pages would be written over");
 };
 
 struct TcBars {
@@ -1344,7 +1351,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     __shared__ TcBars bars;
     __shared__ long long s_scan[kTcThreads / 32];
     __shared__ Start s_start;
-    __shared__ int s_gave_up, s_bad_piece[8], s_par[kMaxN];
+    __shared__ int s_gave_up, s_bad_piece[kBadFlags], s_par[kMaxN];
     __shared__ uint64_t s_anc[kMaxN];
     __shared__ uint32_t s_tmem, s_wild[6][4];
     __shared__ float2 s_ml[128];
@@ -1382,7 +1389,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         s_gave_up = 0;
     }
-    if (tid < 8) s_bad_piece[tid] = -1;
+    if (tid < kBadFlags) s_bad_piece[tid] = -1;
     if (w == 12) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;"
                      ::"r"(saddr(&s_tmem)), "r"(512) : "memory");
@@ -1518,7 +1525,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 if (w < 10) {
                     const bool want = lane < boxes && s < total;
                     const bool good = want && (unsigned)page < (unsigned)c.num_pages;
-                    if (want && !good) s_bad_piece[pieces & 7] = pieces;
+                    if (want && !good) s_bad_piece[pieces % kBadFlags] = pieces;
                     const int pg = page;
                     page = page_of(t + 1);
                     ok = ok &&
@@ -1601,7 +1608,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                     const long long s = (long long)t * kTcUnit + ((long long)lane << shift);
                     const bool want = lane < boxes && s < total;
                     const bool good = want && (unsigned)page < (unsigned)c.num_pages;
-                    if (want && !good) s_bad_piece[pieces & 7] = pieces;
+                    if (want && !good) s_bad_piece[pieces % kBadFlags] = pieces;
                     const int pg = page, slot = (int)(s & ((1 << c.page_shift) - 1));
                     page = page_of(t + 1);
                     const uint32_t bytes =
@@ -1975,7 +1982,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             if (ok && done > 0) ok = warp_wait(&bars.pv_done[st], (pv + done - 1) & 1, gave_up);
             pv += done;
             tc_after();
-            bool nan_piece = nan_rows || s_bad_piece[pieces & 7] == pieces || !ok;
+            bool nan_piece = nan_rows || s_bad_piece[pieces % kBadFlags] == pieces || !ok;
             if (nan_piece && !nan_rows && ok && tid == 0) mark(a.status, p.b, SV_DEV_BAD_PAGE);
             if (!ok && tid == 0) mark(a.status, p.b, SV_DEV_TIMEOUT);
             const bool whole = p.t0 == 0 && p.t1 == sh.tiles;

@@ -1,0 +1,48 @@
+"""Attention with many query rows per key head on the GPU, over tables that keep the calls with
+the form that multiplies in tensor memory: more than 64 rows per key head and room for more slots
+than the calls of few items take."""
+import pytest
+import torch
+
+import kv_plain
+from kv_plain import E4M3
+from test_kv_gpu import BF, HF, Round, built, kv  # noqa: F401 (fixtures)
+
+pytestmark = pytest.mark.gpu
+
+
+def part(r, rows):
+    """The sequences `rows` of a round, for the plain form."""
+    return (r.q[rows], r.k, r.v, r.table[rows], r.lens[rows], r.counts[rows],
+            None if r.parents is None else r.parents[rows], r.scale, r.k_scale, r.v_scale)
+
+
+@pytest.mark.parametrize("dtype,cache,dim", [(BF, E4M3, 64), (HF, E4M3, 16), (HF, HF, 64),
+                                             (BF, BF, 128), (BF, E4M3, 128)])
+@pytest.mark.parametrize("heads,bad", [(8, "pairs"), (16, "one"), (8, "all"), (5, "pairs")])
+def test_bad_pages_of_neighbours(kv, dtype, cache, dim, heads, bad):
+    """Many sequences of one tile each, so that the loads run as many pieces ahead as they can, and
+    bad pages eight pieces apart and closer: each bad sequence is all NaN and says so, the others
+    have the bits that they have without them."""
+    N, group = 9, 8
+    B = 3200 // heads  # 21 pieces per CTA
+    g = torch.Generator().manual_seed(heads)
+    lens = torch.randint(0, 100, (B,), generator=g).tolist()
+    r = Round(lens, N, "tree", heads=heads, group=group, dim=dim, dtype=dtype, cache=cache,
+              page=16, seed=heads + dim, far=True)
+    clean, status = r.attend(kv)
+    assert status == [0] * B
+    some = torch.arange(0, B, B // 6)
+    kv_plain.check_attention(clean[some], *part(r, some))
+    hit = {"pairs": [b for b in range(B) if b % 6 in (1, 2)], "one": list(range(3, B, 8)),
+           "all": list(range(B))}[bad]
+    for b in hit:
+        r.table[b, 0 if b % 2 else (lens[b] + N - 1) // 16] = -1 if b % 3 else r.k.shape[0]
+    out, status = r.attend(kv)
+    is_bad = torch.zeros(B, dtype=torch.bool)
+    is_bad[hit] = True
+    assert [s != 0 for s in status] == is_bad.tolist()
+    assert set(status) <= {0, kv.SV_DEV_BAD_PAGE}
+    assert bool(torch.isnan(out[is_bad].float()).all())
+    # by their bits: among so many float8 entries a few are too large for the type, and NaN
+    assert torch.equal(out[~is_bad].view(torch.int16), clean[~is_bad].view(torch.int16))
