@@ -363,7 +363,10 @@ __device__ __forceinline__ Share share_of(const AttentionArgs& a, int b, int row
     Share s;
     s.n = new_tokens(a.kv_len, a.num_new, b, a.N, a.c, &s.len);
     s.bad = s.n < 0;
-    if (s.bad) s.n = a.N;  // one unit per item: its rows become NaN
+    if (s.bad) {  // one unit per item: its rows become NaN, all N where the count itself is bad
+        s.n = a.num_new ? a.num_new[b] : a.N;
+        if (s.n < 0 || s.n > a.N) s.n = a.N;
+    }
     s.tiles = s.bad ? 1 : (int)(((long long)s.len + s.n + unit - 1) / unit);
     s.mts = (s.n * a.group + rows - 1) / rows;
     s.last = s.n * a.group - (s.mts - 1) * rows > 128 ? 2 : 1;
@@ -433,7 +436,12 @@ __device__ __forceinline__ Walk start_walk(const AttentionArgs& a, int rows, int
     const int per = (a.B + THREADS - 1) / THREADS;
     const int b0 = min(a.B, tid * per), b1 = min(a.B, b0 + per);
     long long sum = 0;
-    for (int b = b0; b < b1; ++b) sum += share_of(a, b, rows, unit).units(a.c.heads, full);
+    for (int b = b0; b < b1; ++b) {
+        const Share s = share_of(a, b, rows, unit);
+        sum += s.units(a.c.heads, full);
+        // (here: a sequence without tokens has no piece that would say so)
+        if (s.bad && blockIdx.x == 0) mark(a.status, b, SV_DEV_BAD_LENGTH);
+    }
     long long inc = sum;
     for (int k = 1; k < 32; k <<= 1) {
         const long long y = __shfl_up_sync(~0u, inc, k);
@@ -500,8 +508,10 @@ __device__ __forceinline__ bool item_piece(const AttentionArgs& a, int rows, int
     p->h = item / mts % a.c.heads;
     p->b = item / mts / a.c.heads;
     *sh = share_of(a, p->b, rows, unit);
-    if (p->mt >= sh->mts) return false;
     const int rank = cluster_rank();
+    if (sh->bad && p->mt == 0 && rank == 0 && threadIdx.x == 0)
+        mark(a.status, p->b, SV_DEV_BAD_LENGTH);
+    if (p->mt >= sh->mts) return false;
     p->t0 = (int)((long long)sh->tiles * rank / kCluster);
     p->t1 = (int)((long long)sh->tiles * (rank + 1) / kCluster);
     p->rows = min(rows, sh->n * a.group - p->mt * rows);
@@ -657,7 +667,6 @@ __global__ void __launch_bounds__(kSplitThreads * WM, 2) kv_split_kernel(const A
         const int len = sh.len, total = len + sh.n, rows = piece.rows;
         if (!CLUSTER && tid == 0) tell_ends(a, piece, sh.tiles);
         bool bad = sh.bad;
-        if (bad && tid == 0) mark(a.status, b, SV_DEV_BAD_LENGTH);
 
         const char* kb = c.k + h * c.head_stride;
         const char* vb = c.v + h * c.head_stride;
@@ -1790,7 +1799,6 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             T* out = (T*)a.out +
                      (((long long)p.b * a.N + j) * a.q_heads + p.h * a.group + g) * c.dim;
             if (sh.bad) {
-                if (tid == 0) mark(a.status, p.b, SV_DEV_BAD_LENGTH);
                 if (live && (two || st == 0))
                     for (int d = 0; d < c.dim; ++d) out[d] = Conv<T>::from(NAN);
                 __syncwarp();

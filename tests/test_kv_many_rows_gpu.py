@@ -46,3 +46,29 @@ def test_bad_pages_of_neighbours(kv, dtype, cache, dim, heads, bad):
     assert bool(torch.isnan(out[is_bad].float()).all())
     # by their bits: among so many float8 entries a few are too large for the type, and NaN
     assert torch.equal(out[~is_bad].view(torch.int16), clean[~is_bad].view(torch.int16))
+
+
+@pytest.mark.parametrize("N,group,far", [(6, 2, False), (6, 2, True), (6, 5, True), (16, 6, True),
+                                         (33, 8, True)])
+def test_bad_lengths_leave_rows_behind_the_counts(kv, N, group, far):
+    """A bad length makes NaN of the tokens that the sequence has; only a bad count makes NaN of
+    all N.  The bit is set for a sequence without tokens too."""
+    counts = [N, 3, 0, N - 1, 1, 0, 2, -1, N + 1, 3]
+    r = Round([40, 50, 60, 70, 80, 33, 20, 90, 5, 60], N, "tree", counts=[max(0, min(N, n))
+                                                                          for n in counts],
+              heads=2, group=group, dim=64, seed=9, extra=0, far=far)
+    clean = r.lens.clone()
+    width = r.table.shape[1] * r.page
+    r.counts = torch.tensor(counts, dtype=torch.int32)
+    r.lens[1], r.lens[2] = -1, -2           # three tokens, none
+    r.lens[3], r.lens[5] = width - N + 2, width + 1
+    r.lens[4] = width                       # one token, the first behind the table
+    out, status = r.attend(kv)
+    L = kv.SV_DEV_BAD_LENGTH
+    assert status == [0, L, L, L, L, L, 0, L, L, 0]
+    for b, n in ((1, 3), (2, 0), (3, N - 1), (4, 1), (5, 0), (7, N), (8, N)):
+        assert bool(torch.isnan(out[b, :n].float()).all()), b
+        assert bool((out[b, n:] == 7.0).all()), b
+    r.lens = clean
+    good = torch.tensor([0, 6, 9])
+    kv_plain.check_attention(out[good], *part(r, good), torch.full_like(out[good], 7.0))
