@@ -119,15 +119,13 @@ template <typename CT, int V> __device__ __forceinline__ void round_to(void* p, 
 
 // ---------------------------------------------------------------- sequences
 
-// Tokens of sequence b, or -1 for a bad length.
-__device__ __forceinline__ int new_tokens(const int32_t* kv_len, const int32_t* num_new, int b,
-                                          int N, const Cache& c, int* len) {
-    const int n = num_new ? num_new[b] : N;
-    const int l = kv_len[b];
-    *len = l;
+// Whether sequence b's length and number of tokens are good.
+__device__ __forceinline__ bool tokens_of(const int32_t* kv_len, const int32_t* num_new, int b,
+                                          int N, const Cache& c, int* len, int* n) {
+    *n = num_new ? num_new[b] : N;
+    *len = kv_len[b];
     const long long cap = (long long)c.table_width << c.page_shift;
-    if (n < 0 || n > N || l < 0 || (long long)l + n > cap) return -1;
-    return n;
+    return *n >= 0 && *n <= N && *len >= 0 && (long long)*len + *n <= cap;
 }
 
 __device__ __forceinline__ void mark(uint32_t* status, int b, uint32_t bits) {
@@ -201,9 +199,8 @@ __global__ void __launch_bounds__(kAppendThreads, 2) kv_append_kernel(const Appe
     Heads now, next;
     load(now, j0, threadIdx.y);
 
-    int len;
-    const int n = new_tokens(a.kv_len, a.num_new, b, a.N, c, &len);
-    if (n < 0) {
+    int len, n;
+    if (!tokens_of(a.kv_len, a.num_new, b, a.N, c, &len, &n)) {
         if (j0 == 0 && tid == 0) mark(a.status, b, SV_DEV_BAD_LENGTH);
         return;
     }
@@ -361,12 +358,9 @@ __device__ __forceinline__ constexpr int full_weight(int rows) { return rows > 1
 
 __device__ __forceinline__ Share share_of(const AttentionArgs& a, int b, int rows, int unit) {
     Share s;
-    s.n = new_tokens(a.kv_len, a.num_new, b, a.N, a.c, &s.len);
-    s.bad = s.n < 0;
-    if (s.bad) {  // one unit per item: its rows become NaN, all N where the count itself is bad
-        s.n = a.num_new ? a.num_new[b] : a.N;
-        if (s.n < 0 || s.n > a.N) s.n = a.N;
-    }
+    s.bad = !tokens_of(a.kv_len, a.num_new, b, a.N, a.c, &s.len, &s.n);
+    // one unit per item of a bad one: its rows become NaN, all N where the count itself is bad
+    if (s.n < 0 || s.n > a.N) s.n = a.N;
     s.tiles = s.bad ? 1 : (int)(((long long)s.len + s.n + unit - 1) / unit);
     s.mts = (s.n * a.group + rows - 1) / rows;
     s.last = s.n * a.group - (s.mts - 1) * rows > 128 ? 2 : 1;
