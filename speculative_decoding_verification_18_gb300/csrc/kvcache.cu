@@ -739,11 +739,14 @@ __global__ void __launch_bounds__(kSplitThreads * WM, 2) kv_split_kernel(const A
         }
 
         // Queries as the A operand: thread (row lane / 4, + 8; elements by lane % 4), with the
-        // sign of the scale, so that the largest product is the largest exponent.
+        // sign of the scales, so that the largest product is the largest exponent.
         uint32_t qa[KS][4];
-        float mul[2];  // from a product to the exponent (base 2); never 0, for 0 * -inf is NaN
-        const float unit = fabsf(a.scale) * 1.4426950408889634f * (kF8 ? c.k_scale[h] : 1.0f);
-        const uint32_t sign = a.scale < 0.0f ? 0x80008000u : 0u;
+        float mul[2];  // from a product to the exponent (base 2)
+        const float ks_h = kF8 ? c.k_scale[h] : 1.0f;
+        const float unit = fabsf(a.scale) * 1.4426950408889634f * fabsf(ks_h);
+        const uint32_t sign = (a.scale < 0.0f) != (ks_h < 0.0f) ? 0x80008000u : 0u;
+        // never 0, for 0 * -inf is NaN; a scale that is NaN stays so
+        auto not_zero = [](float x) { return x < 1e-37f ? 1e-37f : x; };
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
             const int row = wm * 16 + half * 8 + (lane >> 2), R = mt * ROWS + row;
@@ -768,7 +771,7 @@ __global__ void __launch_bounds__(kSplitThreads * WM, 2) kv_split_kernel(const A
                                 fmaxf(fabsf(f1.x), fabsf(f1.y)));
                 }
             }
-            mul[half] = fmaxf(unit, 1e-37f);
+            mul[half] = not_zero(unit);
             if constexpr (!kFit) {
                 top = fmaxf(top, __shfl_xor_sync(~0u, top, 1));
                 top = fmaxf(top, __shfl_xor_sync(~0u, top, 2));
@@ -777,7 +780,7 @@ __global__ void __launch_bounds__(kSplitThreads * WM, 2) kv_split_kernel(const A
                 int e = top > 0.0f && top < INFINITY ? ilogbf(top) - 8 : 0;
                 e = max(-100, min(100, e));
                 const float down = exp2f((float)-e);
-                mul[half] = fmaxf(unit * exp2f((float)e), 1e-37f);
+                mul[half] = not_zero(unit * exp2f((float)e));
 #pragma unroll
                 for (int ks = 0; ks < KS; ++ks)
 #pragma unroll
@@ -1703,8 +1706,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         if (w == 12 && elect_one()) {
             const uint32_t pv = product<M>(c.dim, true);  // the elements that heads have
             constexpr uint32_t kPanel = DP > 64 ? 16384 : 1024;  // one panel: not used
-            // scores times the sign of the scale: the largest is then the one to look for
-            const uint32_t qk = product<M>(128, false) | (a.scale < 0.0f ? 1u << 13 : 0u);
+            // scores times the sign of the scales: the largest is then the one to look for
+            constexpr uint32_t kNegate = 1u << 13;
+            uint32_t qk = product<M>(128, false);
             const uint64_t qd = operand(sq, 16384), kd = operand(sk, 16384);
             const uint64_t vd = operand(sv, kPanel);
             constexpr int kStep = L::kTile >> 4;  // a tile further in a descriptor
@@ -1715,6 +1719,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 if (walk.sh.bad) continue;
                 const bool two = p.rows > 128;
                 const int nt = p.t1 - p.t0, jobs = two ? 2 * nt : nt;
+                const bool negate = (a.scale < 0.0f) != (kF8 && c.k_scale[p.h] < 0.0f);
+                qk = negate ? qk | kNegate : qk & ~kNegate;
                 ok = bar_wait(&bars.q_full, pieces & 1, gave_up);
                 // Job i belongs to stream i & 1.  Its scores take the place of the weights of job
                 // i - 2, whose product comes before them; products of one thread run in order.
@@ -1828,7 +1834,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             const uint64_t anc = anc_of == p.b ? s_anc[j] : 0;
             // from a score to an exponent of two; the products carry the sign
             const float unit0 =
-                fabsf(a.scale) * 1.4426950408889634f * (kF8 ? c.k_scale[p.h] : 1.0f);
+                fabsf(a.scale) * 1.4426950408889634f * (kF8 ? fabsf(c.k_scale[p.h]) : 1.0f);
             float unit = unit0;
             const bool busy = (two ? st * 128 : 0) + (w & 3) * 32 < p.rows;  // rows in this warp
             float l = 0.0f, ref = -INFINITY;

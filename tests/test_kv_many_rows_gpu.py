@@ -72,3 +72,34 @@ def test_bad_lengths_leave_rows_behind_the_counts(kv, N, group, far):
     r.lens = clean
     good = torch.tensor([0, 6, 9])
     kv_plain.check_attention(out[good], *part(r, good), torch.full_like(out[good], 7.0))
+
+
+FORMS = [(1, 4, False), (1, 4, True), (3, 8, True), (9, 8, False), (16, 8, True), (33, 7, True)]
+
+
+@pytest.mark.parametrize("N,group,far", FORMS)
+@pytest.mark.parametrize("dtype", [BF, HF])
+@pytest.mark.parametrize("scale", [0.125, -0.125])
+def test_negative_scales_of_entries(kv, N, group, far, dtype, scale):
+    """An entry stands for its stored value times the head's scale, whatever the sign."""
+    r = Round([300, 5, 40], N, "tree", heads=3, group=group, dim=64, dtype=dtype, cache=E4M3,
+              seed=N, far=far, spread=3.0)
+    r.k_scale[0] *= -1
+    r.v_scale[1] *= -1
+    r.k_scale[2] *= -1
+    r.v_scale[2] *= -1
+    r.scale = scale
+    out, status = r.attend(kv)
+    assert status == [0] * 3
+    r.check(out)
+
+
+@pytest.mark.parametrize("N,group,far", FORMS)
+def test_a_scale_that_is_not_a_number_shows(kv, N, group, far):
+    r = Round([300, 5], N, "tree", heads=2, group=group, dim=64, cache=E4M3, seed=N, far=far)
+    r.k_scale[1] = float("nan")
+    out, _ = r.attend(kv)
+    assert bool(torch.isnan(out[:, :, group:].float()).all())
+    one = torch.arange(group)
+    kv_plain.check_attention(out[:, :, one], r.q[:, :, one], r.k[:, :, :1], r.v[:, :, :1], r.table,
+                             r.lens, r.counts, r.parents, r.scale, r.k_scale[:1], r.v_scale[:1])
