@@ -570,6 +570,13 @@ __device__ __forceinline__ void widen(uint32_t& low, uint32_t& high, uint32_t w)
         "cvt.rn.f16x2.e4m3x2 %1, h; }" : "=r"(low), "=r"(high) : "r"(w));
 }
 
+// The power of two that a query row of bfloat16 is divided by to fit halves, top its largest
+// element: at most 119 (2^127), at least -126, so that 2^-e and 2^e are floats.  It is multiplied
+// back before the key scale, which may be as small as the row is large.
+__device__ __forceinline__ int row_power(float top) {
+    return top > 0.0f && top < INFINITY ? max(-126, ilogbf(top) - 8) : 0;
+}
+
 // Layout of a warp's stage: 16 keys, then 16 values, rows of DP elements whose 16-byte chunks
 // are exchanged so that neither ldmatrix (8 rows, one chunk) nor the 16-byte loads of float8
 // keys (two rows, four chunks at a time) meet in a bank.
@@ -777,10 +784,10 @@ __global__ void __launch_bounds__(kSplitThreads * WM, 2) kv_split_kernel(const A
                 top = fmaxf(top, __shfl_xor_sync(~0u, top, 2));
                 // the row's largest element becomes 2^8 .. 2^9: what then falls below the smallest
                 // half is 2^-33 of it
-                int e = top > 0.0f && top < INFINITY ? ilogbf(top) - 8 : 0;
-                e = max(-100, min(100, e));
+                const int e = row_power(top);
                 const float down = exp2f((float)-e);
-                mul[half] = not_zero(unit * exp2f((float)e));
+                mul[half] = not_zero(fabsf(a.scale) * 1.4426950408889634f * exp2f((float)e) *
+                                     fabsf(ks_h));
 #pragma unroll
                 for (int ks = 0; ks < KS; ++ks)
 #pragma unroll
@@ -1681,8 +1688,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                             for (int e = 0; e < 8; ++e) top = fmaxf(top, fabsf(f[e]));
                         }
                         for (int k = 4; k; k >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, k));
-                        int e2 = top > 0.0f && top < INFINITY ? ilogbf(top) - 8 : 0;
-                        e2 = max(-100, min(100, e2));
+                        const int e2 = row_power(top);
                         const float down = exp2f((float)-e2);
                         if ((lane & 7) == 0) s_exp[pieces & 1][row] = (int8_t)e2;
 #pragma unroll
@@ -1833,9 +1839,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             const bool nan_rows = tree_bad && anc_of == p.b;
             const uint64_t anc = anc_of == p.b ? s_anc[j] : 0;
             // from a score to an exponent of two; the products carry the sign
-            const float unit0 =
-                fabsf(a.scale) * 1.4426950408889634f * (kF8 ? fabsf(c.k_scale[p.h]) : 1.0f);
-            float unit = unit0;
+            const float unit0 = fabsf(a.scale) * 1.4426950408889634f;
+            const float ks_h = kF8 ? fabsf(c.k_scale[p.h]) : 1.0f;
+            float unit = unit0 * ks_h;
             const bool busy = (two ? st * 128 : 0) + (w & 3) * 32 < p.rows;  // rows in this warp
             float l = 0.0f, ref = -INFINITY;
             int done = 0;  // jobs of this stream
@@ -1856,7 +1862,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 s_phase ^= 1;
                 if (!ok) break;
                 tc_after();
-                if (!kFit && done == 0) unit = unit0 * exp2f((float)s_exp[pieces & 1][row]);
+                if (!kFit && done == 0)
+                    unit = unit0 * exp2f((float)s_exp[pieces & 1][row]) * ks_h;
                 if (!busy) {  // rows that nothing comes of: any weights will do
                     tc_before();
                     bar_arrive(&bars.p_full[st][0]);

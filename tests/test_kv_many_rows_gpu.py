@@ -103,3 +103,17 @@ def test_a_scale_that_is_not_a_number_shows(kv, N, group, far):
     one = torch.arange(group)
     kv_plain.check_attention(out[:, :, one], r.q[:, :, one], r.k[:, :, :1], r.v[:, :, :1], r.table,
                              r.lens, r.counts, r.parents, r.scale, r.k_scale[:1], r.v_scale[:1])
+
+
+@pytest.mark.parametrize("N,group,far", FORMS)
+@pytest.mark.parametrize("power", [126, 112, 90, -60, -100, -120])
+def test_queries_of_any_size_over_float8(kv, N, group, far, power):
+    """bfloat16 queries are scaled by a power of two per row on the way to halves, which can hold
+    no others: rows of 2^126 and of 2^-100, with scales that bring the scores back to a few."""
+    r = Round([300, 5], N, "tree", heads=2, group=group, dim=64, cache=E4M3, seed=N, far=far)
+    r.q = (r.q.clamp(-1.9, 1.9).double() * 2.0 ** power).to(BF)
+    r.k_scale *= 2.0 ** (-power // 2)
+    r.scale *= 2.0 ** (-power - -power // 2)
+    out, status = r.attend(kv)
+    assert status == [0] * 2 and not bool(torch.isnan(out.float()).any())
+    r.check(out)
