@@ -97,24 +97,42 @@ template <typename T, int V> __device__ __forceinline__ void widen_to(float* f, 
         if (V > 1) f[i + 1] = x.y;
     }
 }
-// V floats rounded to CT and written: 2 V or (float8: to nearest, saturating) V bytes.
-template <typename CT, int V> __device__ __forceinline__ void round_to(void* p, const float* f) {
-    if constexpr (sizeof(CT) == 2) {
-        Words<V> r;
+// V floats rounded to a 16-bit type and written.
+template <typename T, int V> __device__ __forceinline__ void round_to(void* p, const float* f) {
+    Words<V> r;
 #pragma unroll
-        for (int i = 0; i < V; i += 2) r.w[i / 2] = pair<CT>(f[i], V > 1 ? f[i + 1] : 0.0f);
-        put<V>(p, r);
-    } else {
-        uint32_t w[V > 4 ? 2 : 1] = {};
+    for (int i = 0; i < V; i += 2) r.w[i / 2] = pair<T>(f[i], V > 1 ? f[i + 1] : 0.0f);
+    put<V>(p, r);
+}
+__device__ __forceinline__ uint32_t two_e4m3(float x, float y) {
+    return __nv_cvt_float2_to_fp8x2(make_float2(x, y), __NV_SATFINITE, __NV_E4M3);
+}
+// V entries x / scale rounded to float8.  The product with the scale's reciprocal is off by less
+// than 2^-22 of itself, and that tells only next to the middle between two float8 values: where the
+// ends of an interval of 2^-21 to both sides round alike, that is the entry; the quotients are
+// taken where some do not (one element in 2^16), or where the reciprocal is no full float.  (Trees
+// of 16 nodes, 64 sequences: 8.2 us, with nothing but quotients 10.2 us.)
+template <int V>
+__device__ __forceinline__ void put_quotients(void* p, const float* x, float scale) {
+    const float inverse = __fdiv_rn(1.0f, scale), size = fabsf(inverse);
+    bool near = !(size >= 1e-37f && size <= 3e38f);
+    uint32_t w[V > 4 ? 2 : 1] = {};
 #pragma unroll
-        for (int i = 0; i < V; i += 2)
-            w[i / 4] |= (uint32_t)__nv_cvt_float2_to_fp8x2(
-                            make_float2(f[i], V > 1 ? f[i + 1] : 0.0f), __NV_SATFINITE, __NV_E4M3)
-                        << (i % 4 * 8);
-        if constexpr (V == 8) *reinterpret_cast<uint2*>(p) = make_uint2(w[0], w[1]);
-        else if constexpr (V == 4) *reinterpret_cast<uint32_t*>(p) = w[0];
-        else *reinterpret_cast<uint8_t*>(p) = (uint8_t)w[0];
+    for (int i = 0; i < V; i += 2) {
+        const float u = x[i] * inverse, v = V > 1 ? x[i + 1] * inverse : 0.0f;
+        const uint32_t lo = two_e4m3(u * (1.0f - 0x1p-21f), v * (1.0f - 0x1p-21f));
+        near |= lo != two_e4m3(u * (1.0f + 0x1p-21f), v * (1.0f + 0x1p-21f));
+        w[i / 4] |= lo << (i % 4 * 8);
     }
+    if (near) {
+        w[0] = w[V > 4 ? 1 : 0] = 0;
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+            w[i / 4] |= (two_e4m3(__fdiv_rn(x[i], scale), 0.0f) & 0xff) << (i % 4 * 8);
+    }
+    if constexpr (V == 8) *reinterpret_cast<uint2*>(p) = make_uint2(w[0], w[1]);
+    else if constexpr (V == 4) *reinterpret_cast<uint32_t*>(p) = w[0];
+    else *reinterpret_cast<uint8_t*>(p) = (uint8_t)w[0];
 }
 
 // ---------------------------------------------------------------- sequences
@@ -277,20 +295,13 @@ __global__ void __launch_bounds__(kAppendThreads, 2) kv_append_kernel(const Appe
             } else {
                 CT* dst = (CT*)((is_v ? c.v : c.k) + place + ch * c.head_stride);
                 if constexpr (sizeof(CT) == 1) {
-                    // times the reciprocal, which is off by half a step more than the quotient;
-                    // the quotient itself where there is no finite one
                     const float scale = (is_v ? c.v_scale : c.k_scale)[ch];
-                    const float inverse = __fdiv_rn(1.0f, scale);
-                    if (fabsf(inverse) <= 3.0e38f) {
-#pragma unroll
-                        for (int k = 0; k < 2 * V; ++k) r[k] *= inverse;
-                    } else {
-#pragma unroll
-                        for (int k = 0; k < 2 * V; ++k) r[k] = __fdiv_rn(r[k], scale);
-                    }
+                    put_quotients<V>(dst + e0, r, scale);
+                    put_quotients<V>(dst + e1, r + V, scale);
+                } else {
+                    round_to<CT, V>(dst + e0, r);
+                    round_to<CT, V>(dst + e1, r + V);
                 }
-                round_to<CT, V>(dst + e0, r);
-                round_to<CT, V>(dst + e1, r + V);
             }
         }
     };

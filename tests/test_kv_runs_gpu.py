@@ -186,3 +186,29 @@ def test_commit_runs_of_planes(kv, cache, heads, dim, order, N, few):
     assert torch.equal(out.cpu(), lens + acc + 1)
     for p, w in zip(pools, want):
         assert torch.equal(look(p), w)
+
+
+@pytest.mark.parametrize("dtype", [BF, HF])
+def test_append_float8_is_the_quotient_rounded(kv, dtype):
+    """Entries are the quotient by the head's scale, rounded to nearest even, in every bit: among
+    them quotients half way between two float8 values, where the product with the scale's rounded
+    reciprocal lies on the other side."""
+    ties = torch.tensor([t * 2.0 ** e for t in range(17, 32, 2) for e in range(-6, 5)])
+    odd = torch.arange(3, 128, 2).float()
+    heads, D = len(odd), 128
+    g = torch.Generator().manual_seed(3)
+    x = torch.randn(1, 60, heads, D, generator=g)
+    x[0, :, :, :len(ties)] = ties * odd[:, None]  # exact in the type for the smaller scales
+    x[0, 1::2] *= -1
+    x = x.to(dtype)
+    N = x.shape[1]
+    lens = torch.tensor([5], dtype=torch.int32)
+    k, v = (torch.zeros(5, 16, heads, D, dtype=torch.uint8, device="cuda").view(E4M3)
+            for _ in range(2))
+    table = torch.arange(5, dtype=torch.int32).view(1, 5).cuda()
+    c = kv.PagedCache(k, v, table, odd.cuda(), (odd / 3).cuda())
+    kv.spec_kv_append(c, x.cuda(), x.cuda(), lens.cuda())
+    for pool, scale in ((k, odd), (v, odd / 3)):
+        got = pool.view(torch.uint8).view(-1, heads, D)[5:5 + N].cpu()
+        want = (x[0].float() / scale[:, None]).clamp(-448, 448).to(E4M3).view(torch.uint8)
+        assert torch.equal(got, want), int((got != want).sum())
