@@ -1218,26 +1218,30 @@ __device__ __forceinline__ void tma_page(uint32_t dst, const CUtensorMap* map, i
         "[%0], [%1, {%2, %3, %4, %5}], [%6];"
         ::"r"(dst), "l"(map), "r"(x), "r"(h), "r"(s), "r"(p), "r"(saddr(bar)) : "memory");
 }
-constexpr uint64_t kGiveUp = 2000000000;  // two seconds
-__device__ __forceinline__ uint64_t nanoseconds() {
-    uint64_t now;
-    asm volatile("mov.u64 %0, %globaltimer;" : "=l"(now));
+constexpr uint32_t kGiveUp = 2000000000;  // two seconds
+constexpr uint32_t kGap = 100000000;      // of them at most so much between two looks at the clock
+__device__ __forceinline__ uint32_t nanoseconds() {
+    uint32_t now;
+    asm volatile("mov.u32 %0, %globaltimer_lo;" : "=r"(now));
     return now;
 }
 // Waits for a phase of a barrier, two seconds at most, and no longer once another wait has given
-// up; false when it gave up.
+// up; false when it gave up.  A longer gap between two looks at the clock, as when the whole CTA was
+// put aside for another process, counts as a tenth of a second: what was waited for then still has
+// time to come.
 __device__ __forceinline__ bool bar_wait(uint64_t* bar, uint32_t parity, volatile int* gave_up) {
     const uint32_t at = saddr(bar);
-    uint64_t since = 0;
+    uint32_t last = 0, waited = 0;
     for (int i = 1;; ++i) {
         uint32_t done;
         asm volatile("{ .reg .pred p; mbarrier.try_wait.parity.shared.b64 p, [%1], %2; "
                      "selp.u32 %0, 1, 0, p; }" : "=r"(done) : "r"(at), "r"(parity) : "memory");
         if (done) return true;
         if (i & 31) continue;
-        const uint64_t now = nanoseconds();
-        if (!since) since = now;
-        if (*gave_up || now - since > kGiveUp) break;
+        const uint32_t now = nanoseconds();
+        if (i > 32) waited += min(now - last, kGap);
+        last = now;
+        if (*gave_up || waited > kGiveUp) break;
     }
     *gave_up = 1;
     return false;
@@ -2008,9 +2012,6 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             if (ok && done > 0) ok = warp_wait(&bars.pv_done[st], (pv + done - 1) & 1, gave_up);
             pv += done;
             tc_after();
-            bool nan_piece = nan_rows || s_bad_piece[pieces % kBadFlags] == pieces || !ok;
-            if (nan_piece && !nan_rows && ok && tid == 0) mark(a.status, p.b, SV_DEV_BAD_PAGE);
-            if (!ok && tid == 0) mark(a.status, p.b, SV_DEV_TIMEOUT);
             const bool whole = p.t0 == 0 && p.t1 == sh.tiles;
             float f0 = 1.0f, f1 = 0.0f;  // shares of the two streams where they are joined
             if (!two) {
@@ -2027,8 +2028,14 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                     ref = top;
                 }
             }
+            // Whatever wait of the CTA gave up (the other stream's, a load's), the rows may be made
+            // of anything: its flag was set before what came here.
+            const bool late = !ok || *gave_up;
+            const bool bad_page = s_bad_piece[pieces % kBadFlags] == pieces;
+            if (late && r == 0) mark(a.status, p.b, SV_DEV_TIMEOUT);
+            if (bad_page && !nan_rows && tid == 0) mark(a.status, p.b, SV_DEV_BAD_PAGE);
             if (two || st == 0) {
-                if (nan_piece) l = NAN;
+                if (nan_rows || bad_page || late) l = NAN;
                 const long long part = 2 * (long long)blockIdx.x + (p.t0 == 0 ? 1 : 0);
                 const float inv = (kF8 ? c.v_scale[p.h] : 1.0f) / l;
 #pragma unroll 1
@@ -2076,7 +2083,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         }
     }
     if (*gave_up) {  // loads that nobody waited for land within a millisecond
-        const uint64_t since = nanoseconds();
+        const uint32_t since = nanoseconds();
         while (nanoseconds() - since < 1000000) __nanosleep(1000);
     }
     tc_before();
