@@ -2396,48 +2396,56 @@ static bool cache_map(CUtensorMap* map, void* base, const sv_kv_cache* c) {
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// Shared memory of every attention kernel, once per device.
-static cudaError_t attention_setup() {
-    cudaError_t e = cudaSuccess;
-    for (int i = 0; i < 16 && e == cudaSuccess; ++i) {
+// Shared memory of the many-row kernels.  *can: false where a compiler gave them other registers
+// than their roles share out (256 threads of 184, 256 of 72: those of a launch with 128 each; with
+// fewer the larger share would be waited for).
+static bool wide_setup(bool* can) {
+    bool ok = true;
+    *can = true;
+    for (int i = 0; i < 16 && ok; ++i) {
         const sv_dtype t = i & 1 ? SV_F16 : SV_BF16;
-        e = with_wide(t, i & 2 ? SV_E4M3 : t, i & 4 ? 128 : 64, i & 8 ? 256 : 128,
-                      [](auto k, auto, int smem) {
-            // the roles' shares (256 threads of 184, 256 of 72) are those of a launch with 128
-            // each: with fewer the larger share would be waited for
+        ok = with_wide(t, i & 2 ? SV_E4M3 : t, i & 4 ? 128 : 64, i & 8 ? 256 : 128,
+                       [&](auto k, auto, int smem) {
             cudaFuncAttributes f;
-            cudaError_t r = cudaFuncGetAttributes(&f, k);
-            if (r == cudaSuccess && f.numRegs != 128) r = cudaErrorInvalidConfiguration;
-            return r != cudaSuccess ? r
-                                    : cudaFuncSetAttribute(
-                                          k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+            if (cudaFuncGetAttributes(&f, k) != cudaSuccess) return false;
+            *can = *can && f.numRegs == 128;
+            return cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) ==
+                   cudaSuccess;
         });
     }
+    return ok;
+}
+// The same of the others.
+static bool split_setup() {
+    auto set = [](auto k, auto, int smem) {
+        return cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) ==
+               cudaSuccess;
+    };
+    bool ok = true;
     for (sv_dtype t : {SV_BF16, SV_F16})
-        for (bool f8 : {false, true})
+        for (sv_dtype ct : {t, SV_E4M3})
             for (int dim : {64, 128})
                 for (int rows : {16, 32})
-                    if (e == cudaSuccess) {
-                        auto set = [](auto k, auto, int smem) {
-                            return cudaFuncSetAttribute(
-                                k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-                        };
-                        const sv_dtype ct = f8 ? SV_E4M3 : t;
-                        e = with_split<false>(t, ct, dim, rows, set);
-                        if (e == cudaSuccess) e = with_split<true>(t, ct, dim, rows, set);
-                    }
-    return e;
+                    ok = ok && with_split<false>(t, ct, dim, rows, set) &&
+                         with_split<true>(t, ct, dim, rows, set);
+    return ok;
 }
 
-// The current device's SM count, if it is one that these kernels run on.
-static sv_status device_ok(int* sms) {
+// The current device's SM count, if it is one that these kernels run on.  wide (attention): whether
+// the many-row kernels can be launched; the split kernel takes any number of rows.
+static sv_status device_ok(int* sms, bool* wide = nullptr) {
+    struct Known {
+        int sms;        // 0 unknown, -1 another device
+        int attention;  // 0 unknown, 1 without the many-row kernels, 2 with them
+    };
     static std::mutex mu;
-    static int known[64];  // 0 unknown, -1 another device, else the SM count
+    static Known known[64];
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) return SV_ERR_CUDA;
     if (dev < 0 || dev >= 64) return SV_ERR_UNSUPPORTED;
     std::lock_guard<std::mutex> lk(mu);
-    if (!known[dev]) {
+    Known& k = known[dev];
+    if (!k.sms) {
         int major = 0, minor = 0;
         if (cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev) != cudaSuccess ||
             cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev) != cudaSuccess)
@@ -2446,11 +2454,17 @@ static sv_status device_ok(int* sms) {
         if (major == 10 && minor == 3 &&
             cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
             return SV_ERR_CUDA;
-        if (n > 0 && attention_setup() != cudaSuccess) return SV_ERR_CUDA;
-        known[dev] = n;
+        k.sms = n;
     }
-    if (known[dev] < 0) return SV_ERR_UNSUPPORTED;
-    *sms = known[dev];
+    if (k.sms < 0) return SV_ERR_UNSUPPORTED;
+    *sms = k.sms;
+    if (!wide) return SV_OK;
+    if (!k.attention) {
+        bool can;
+        if (!split_setup() || !wide_setup(&can)) return SV_ERR_CUDA;
+        k.attention = can ? 2 : 1;
+    }
+    *wide = k.attention == 2;
     return SV_OK;
 }
 
@@ -2656,7 +2670,8 @@ sv_status spec_kv_attention(const sv_kv_cache* cache, const void* q, const sv_st
         return SV_ERR_WORKSPACE;
     if (B == 0) return SV_OK;
     int sms;
-    if ((st = device_ok(&sms)) != SV_OK) return st;
+    bool wide;
+    if ((st = device_ok(&sms, &wide)) != SV_OK) return st;
     a.q = (const char*)q;
     a.out = (char*)out;
     a.qb = q_strides->batch, a.qt = q_strides->token, a.qh = q_strides->head;
@@ -2681,8 +2696,8 @@ sv_status spec_kv_attention(const sv_kv_cache* cache, const void* q, const sv_st
     const int slots = cache->table_width * cache->page_size;
     const int few = cache->dtype == SV_E4M3 && slots <= 2048 ? 64 : 32;
     CUtensorMap kmap, vmap;
-    const bool wide = !cluster && rows > few && cache->page_size >= 8 &&
-                      cache_map(&kmap, cache->k, cache) && cache_map(&vmap, cache->v, cache);
+    wide = wide && !cluster && rows > few && cache->page_size >= 8 &&
+           cache_map(&kmap, cache->k, cache) && cache_map(&vmap, cache->v, cache);
     const int tile = wide ? (rows <= 128 ? 128 : 256) : rows <= 16 ? 16 : 32;
     const int unit = wide ? kTcUnit : kUnit;
     const int mts = (rows + tile - 1) / tile;

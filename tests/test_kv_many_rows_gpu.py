@@ -117,3 +117,17 @@ def test_queries_of_any_size_over_float8(kv, N, group, far, power):
     out, status = r.attend(kv)
     assert status == [0] * 2 and not bool(torch.isnan(out.float()).any())
     r.check(out)
+
+
+@pytest.mark.parametrize("dtype,cache", [(BF, BF), (HF, HF), (BF, E4M3), (HF, E4M3)])
+@pytest.mark.parametrize("dim,page", [(64, 4), (128, 1), (80, 2)])
+@pytest.mark.parametrize("N,group", [(9, 8), (65, 3), (33, 16)])
+def test_many_rows_over_the_smallest_pages(kv, dtype, cache, dim, page, N, group):
+    """Pages of fewer slots than the swizzle's eight: the form for few rows takes them, in row
+    tiles of 32, as it takes every call where the other one cannot be launched."""
+    counts = [N, 0, N - 2, 1]
+    r = Round([70, 3, 500, 0], N, "tree", counts=counts, heads=1, group=group, dim=dim,
+              dtype=dtype, cache=cache, page=page, seed=N + dim, far=True)
+    out, status = r.attend(kv)
+    assert status == [0] * 4
+    kv_plain.check_attention(out, *part(r, torch.arange(4)), torch.full_like(out, 7.0))
