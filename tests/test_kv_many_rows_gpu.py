@@ -5,6 +5,7 @@ import pytest
 import torch
 
 import kv_plain
+import test_kv_gpu
 from kv_plain import E4M3
 from test_kv_gpu import BF, HF, Round, built, kv  # noqa: F401 (fixtures)
 
@@ -131,3 +132,145 @@ def test_many_rows_over_the_smallest_pages(kv, dtype, cache, dim, page, N, group
     out, status = r.attend(kv)
     assert status == [0] * 4
     kv_plain.check_attention(out, *part(r, torch.arange(4)), torch.full_like(out, 7.0))
+
+
+# dtype, cache, N, group: row tiles of 128 (one, and a part), and of 256 with a short last one
+WIDE = [(BF, BF, 16, 8), (HF, HF, 9, 4), (BF, E4M3, 9, 8), (HF, E4M3, 16, 8), (BF, BF, 33, 8),
+        (HF, HF, 65, 8), (BF, E4M3, 65, 8), (HF, E4M3, 20, 13)]
+
+
+@pytest.mark.parametrize("dtype,cache,N,group", WIDE)
+@pytest.mark.parametrize("scale", [0.0, -0.3, -0.125, 1e-30, 0.9])
+def test_scales(kv, dtype, cache, N, group, scale):
+    r = Round([300, 70, 0], N, "tree", heads=2, group=group, dim=64, dtype=dtype, cache=cache,
+              seed=4, far=True)
+    r.scale = scale
+    out, status = r.attend(kv)
+    assert status == [0] * 3
+    r.check(out)
+
+
+@pytest.mark.parametrize("dtype,cache,N,group", WIDE)
+@pytest.mark.parametrize("dim", [16, 32, 48, 80, 96, 112])
+@pytest.mark.parametrize("order", ["slot", "head"])
+def test_elements_and_orders(kv, dtype, cache, N, group, dim, order):
+    r = Round([150, 0, 127], N, "tree", counts=[N, N - 1, 9], heads=3, group=group, dim=dim,
+              dtype=dtype, cache=cache, order=order, page=8, seed=dim, far=True)
+    out, status = r.attend(kv)
+    assert status == [0] * 3
+    kv_plain.check_attention(out, *part(r, torch.arange(3)), torch.full_like(out, 7.0))
+
+
+@pytest.mark.parametrize("dtype,cache,N,group", WIDE)
+@pytest.mark.parametrize("page", [8, 64, 128, 256, 2048])
+def test_pages_and_borders(kv, dtype, cache, N, group, page):
+    """Lengths that end on, before and behind borders of pages, of tiles of 128 slots and of words
+    of the masks, and new tokens that begin there."""
+    lens = [0, 1, 63, 64, 95, 127 - N, 127, 128, 129, 255 - N, 255, 256, 257]
+    r = Round(lens, N, "tree", heads=1, group=group, dim=64, dtype=dtype, cache=cache, page=page,
+              seed=page, far=True)
+    out, status = r.attend(kv)
+    assert status == [0] * len(lens)
+    r.check(out)
+
+
+@pytest.mark.parametrize("dtype,cache,N,group", WIDE)
+def test_repeats_bit_for_bit(kv, dtype, cache, N, group):
+    r = Round([3000, 10, 777, 129], N, "tree", heads=2, group=group, dim=128, dtype=dtype,
+              cache=cache, seed=11, far=True)
+    first, _ = r.attend(kv)
+    for _ in range(3):
+        assert torch.equal(r.attend(kv)[0], first)
+
+
+@pytest.mark.parametrize("dtype,cache,N,group", WIDE)
+def test_rows_that_overflow_are_nan_and_stay_alone(kv, dtype, cache, N, group):
+    r = Round([300, 30], N, "tree", heads=1, group=group, dim=64, dtype=dtype, cache=cache, seed=2,
+              far=True)
+    hit = [(0, 1, 0, float("inf")), (0, N - 1, group - 1, float("-inf")), (1, 3, 2, float("nan"))]
+    for b, j, h, x in hit:
+        r.q[b, j, h] = x
+    out, _ = r.attend(kv)
+    for b, j, h, _ in hit:
+        assert bool(torch.isnan(out[b, j, h].float()).all())
+        r.q[b, j, h] = 0
+    want, bound, _ = kv_plain.attention(*part(r, torch.arange(2)))
+    err = (out.double() - want).abs()
+    for b, j, h, _ in hit:
+        err[b, j, h] = 0
+    assert bool((err <= bound).all())
+
+
+@pytest.mark.parametrize("N,group", [(16, 8), (33, 8)])
+def test_lowest_and_large_scores(kv, N, group):
+    """As for few rows: scores of +-60000 that differ by thousands."""
+    r = Round([200, 64, 300], N, "tree", heads=1, group=group, dim=16, spread=1.0, seed=8, far=True)
+    for b in range(3):
+        for i, (p, s) in enumerate(kv_plain.slots(r.table[b], r.page, int(r.lens[b]))):
+            if i % 3 == 0:
+                r.k[p, s] = 3000.0 * r.k[p, s]
+    r.q[0] = 40.0 * r.q[0]
+    out, status = r.attend(kv)
+    assert status == [0] * 3 and bool(torch.isfinite(out.float()).all())
+    want, bound, _ = kv_plain.attention(*part(r, torch.arange(3)))
+    err, tell = (out.double() - want).abs(), bound < 0.5
+    assert float(tell.double().mean()) > 0.2 and bool((err <= bound)[tell].all())
+
+
+@pytest.mark.parametrize("dtype,cache,N,group", WIDE)
+def test_bad_trees(kv, dtype, cache, N, group):
+    lens = [40, 300, 60, 70]
+    counts = [N, N, N, 3]
+    r = Round(lens, N, "tree", counts=counts, heads=2, group=group, dim=64, dtype=dtype,
+              cache=cache, seed=9, far=True)
+    r.parents[0, 2], r.parents[1, N - 1], r.parents[3, 4] = 2, -1, 77  # the last one is not read
+    out, status = r.attend(kv)
+    assert status == [0x40, 0x40, 0, 0]
+    assert bool(torch.isnan(out[:2].float()).all())
+    r.parents[3, 4] = 0
+    good = torch.tensor([2, 3])
+    kv_plain.check_attention(out[good], *part(r, good), torch.full_like(out[good], 7.0))
+
+
+@pytest.mark.parametrize("dtype,cache,N,group", WIDE)
+def test_strided_queries_and_far_pages(kv, dtype, cache, N, group):
+    """Queries are a slice of a wider projection, and pages lie more than 2^32 bytes into the cache
+    (by way of the tensor map here)."""
+    page, heads, dim = 64, 2, 128
+    r = Round([200, 64], N, "tree", heads=heads, group=group, dim=dim, dtype=dtype, cache=cache,
+              page=page, seed=4, extra=0, far=True)
+    each = page * heads * dim * (1 if cache == E4M3 else 2)
+    pages = (5 << 30) // each
+    k, v = (torch.empty(pages * each, dtype=torch.uint8, device="cuda").view(cache)
+            .view(pages, page, heads, dim) for _ in range(2))
+    raw = lambda x: x.view(torch.uint8)
+    table = r.table.clone()
+    held = (200 + N + page - 1) // page
+    for b in range(2):
+        for i in range(held):
+            table[b, i] = pages - 1 - (b * held + i)
+            raw(k)[int(table[b, i])] = raw(r.k)[int(r.table[b, i])].cuda()
+            raw(v)[int(table[b, i])] = raw(r.v)[int(r.table[b, i])].cuda()
+    d = lambda x: None if x is None else x.cuda()
+    c = kv.PagedCache(k, v, table.cuda(), d(r.k_scale), d(r.v_scale))
+    hq = heads * group
+    wide = torch.zeros(2, N, hq + 2 * heads, dim, dtype=dtype, device="cuda")
+    wide[:, :, heads:heads + hq] = r.q.cuda()
+    out = torch.full_like(r.q, 7.0, device="cuda")
+    kv.spec_kv_attention(c, wide[:, :, heads:heads + hq], r.lens.cuda(), out,
+                         kv.attention_workspace(c, 2, N, hq), r.scale, parents=r.parents.cuda())
+    r.check(out.cpu())
+
+
+@pytest.mark.parametrize("capture", [False, True])
+def test_whole_rounds_over_roomy_tables(kv, capture, monkeypatch):
+    """The rounds of append, attention, tree verify and commit with 36 rows per key head, over a
+    table with room for 9700 slots, which takes them off the form of few items."""
+    made = kv.PagedCache
+
+    def roomy(k, v, table):
+        more = torch.full((table.shape[0], 600), -1, dtype=torch.int32, device=table.device)
+        return made(k, v, torch.cat([table, more], dim=1))
+
+    monkeypatch.setattr(kv, "PagedCache", roomy)
+    test_kv_gpu.test_whole_rounds(kv, capture)

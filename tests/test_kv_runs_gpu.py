@@ -102,7 +102,8 @@ def test_append_runs_of_tokens(kv, run, heads, group, dim, rot, dtype, cache, fo
 
     if group:
         y, slack = turned(q)
-        assert bool(((out.double() - y).abs() <= kv_plain.stored_bound(y, slack, dtype))[live].all())
+        off = (out.double() - y).abs()
+        assert bool((off <= kv_plain.stored_bound(y, slack, dtype))[live].all())
         assert torch.equal(out[~live], held[~live])
     slot = (lens[:, None] + torch.arange(N)).long().cuda()
     place = table.long().gather(1, slot // page)[live], (slot % page)[live]
