@@ -879,7 +879,7 @@ __global__ void __launch_bounds__(kSplitThreads * WM, 2) kv_split_kernel(const A
                     }
                 }
             }
-            const bool fresh = slot0 + 16 > len;  // new tokens or the end are among the 16
+            const bool fresh = slot0 > len - 16;  // new tokens or the end are among the 16
             if (fresh) {
 #pragma unroll
                 for (int half = 0; half < 2; ++half) {

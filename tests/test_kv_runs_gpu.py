@@ -213,3 +213,35 @@ def test_append_float8_is_the_quotient_rounded(kv, dtype):
         got = pool.view(torch.uint8).view(-1, heads, D)[5:5 + N].cpu()
         want = (x[0].float() / scale[:, None]).clamp(-448, 448).to(E4M3).view(torch.uint8)
         assert torch.equal(got, want), int((got != want).sum())
+
+
+@pytest.mark.parametrize("N,group", [(1, 4), (4, 4), (4, 8), (9, 8)])
+def test_attention_up_to_the_last_slot(kv, N, group):
+    """A table of 2^31 - 8 slots, filled to the last one: 2^28 - 1 pages of eight, all but the new
+    tokens' the same.  With queries of zero all weights are equal: committed values are zero, a
+    new token's is 2^31 times its number, so that each row is the sum of the numbers it sees."""
+    page, dim, width = 8, 16, (1 << 28) - 1
+    slots = width * page
+    own = (N + page - 1) // page + 1
+    table = torch.zeros(1, width, dtype=torch.int32, device="cuda")
+    table[0, width - own:] = torch.arange(1, own + 1, dtype=torch.int32, device="cuda")
+    k = torch.zeros(own + 1, page, 1, dim, dtype=BF, device="cuda")
+    v = torch.zeros_like(k)
+    numbers = torch.arange(1, N + 1, device="cuda") % 5
+    v.view(-1, dim)[(own + 1) * page - N:] = (numbers.double() * 2.0 ** 31).to(BF)[:, None]
+    g = torch.Generator().manual_seed(N)
+    parents = tree(N, "tree", g)
+    lens = torch.tensor([slots - N], dtype=torch.int32, device="cuda")
+    c = kv.PagedCache(k, v, table)
+    q = torch.zeros(1, N, group, dim, dtype=BF, device="cuda")
+    out, status = torch.full_like(q, 7.0), torch.zeros_like(lens)
+    kv.spec_kv_attention(c, q, lens, out, kv.attention_workspace(c, 1, N, group), 1.0,
+                         parents=parents.view(1, N).cuda(), status=status)
+    assert status.tolist() == [0], status.tolist()
+    up = kv_plain.paths(parents, N)
+    seen = torch.tensor([len(p) for p in up]).double()  # of them and of the committed slots
+    want = torch.tensor([sum(int(numbers[i]) for i in p) for p in up]).double()
+    want = want * 2.0 ** 31 / (slots - N + seen)
+    # whole numbers: the sums are exact, but for those of the pieces' counts (2^-24 per piece)
+    off = (out.cpu().double() - want[None, :, None, None]).abs()
+    assert bool((off <= (kv_plain.U[BF] + 305 * 2.0 ** -24) * want[None, :, None, None]).all())
