@@ -1225,13 +1225,19 @@ __device__ __forceinline__ uint32_t nanoseconds() {
     asm volatile("mov.u32 %0, %globaltimer_lo;" : "=r"(now));
     return now;
 }
-// Waits for a phase of a barrier, two seconds at most, and no longer once another wait has given
-// up; false when it gave up.  A longer gap between two looks at the clock, as when the whole CTA was
-// put aside for another process, counts as a tenth of a second: what was waited for then still has
-// time to come.
-__device__ __forceinline__ bool bar_wait(uint64_t* bar, uint32_t parity, volatile int* gave_up) {
+// What the waits of a CTA look at: whether one has given up, and how many products were issued.
+struct Watch {
+    int gave_up, issued;
+};
+// Waits for a phase of a barrier until two seconds have gone by without a product, or until another
+// wait has given up; false when it gave up.  (Some wait for the end of a piece, which can take
+// longer than any limit: a range of a context of 2^31 slots has 330000 tiles.)  A longer gap
+// between two looks at the clock, as when the whole CTA was put aside for another process, counts
+// as a tenth of a second: what was waited for then still has time to come.
+__device__ __forceinline__ bool bar_wait(uint64_t* bar, uint32_t parity, volatile Watch* watch) {
     const uint32_t at = saddr(bar);
     uint32_t last = 0, waited = 0;
+    int issued = -1;
     for (int i = 1;; ++i) {
         uint32_t done;
         asm volatile("{ .reg .pred p; mbarrier.try_wait.parity.shared.b64 p, [%1], %2; "
@@ -1239,16 +1245,18 @@ __device__ __forceinline__ bool bar_wait(uint64_t* bar, uint32_t parity, volatil
         if (done) return true;
         if (i & 31) continue;
         const uint32_t now = nanoseconds();
-        if (i > 32) waited += min(now - last, kGap);
+        const int so_far = watch->issued;
+        waited = so_far == issued ? waited + min(now - last, kGap) : 0;
+        issued = so_far;
         last = now;
-        if (*gave_up || waited > kGiveUp) break;
+        if (watch->gave_up || waited > kGiveUp) break;
     }
-    *gave_up = 1;
+    watch->gave_up = 1;
     return false;
 }
 // The same for a whole warp, with one answer.
-__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* gave_up) {
-    return __all_sync(~0u, bar_wait(bar, parity, gave_up));
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile Watch* watch) {
+    return __all_sync(~0u, bar_wait(bar, parity, watch));
 }
 __device__ __forceinline__ void named_sync(int id, int threads) {
     asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
@@ -1379,7 +1387,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     __shared__ TcBars bars;
     __shared__ long long s_scan[kTcThreads / 32];
     __shared__ Start s_start;
-    __shared__ int s_gave_up, s_bad_piece[kBadFlags], s_par[kMaxN];
+    __shared__ Watch s_watch;
+    __shared__ int s_bad_piece[kBadFlags], s_par[kMaxN];
     __shared__ uint64_t s_anc[kMaxN];
     __shared__ uint32_t s_tmem, s_wild[6][4];
     __shared__ float2 s_ml[128];
@@ -1415,7 +1424,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             bar_init(&bars.pv_done[i], 1);
         }
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-        s_gave_up = 0;
+        s_watch = Watch{0, 0};
     }
     if (tid < kBadFlags) s_bad_piece[tid] = -1;
     if (w == 12) {
@@ -1430,7 +1439,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     Walk walk = start_walk<kTcThreads>(a, ROWS, kTcUnit, s_scan, &s_start);
     tc_after();
     const uint32_t tmem = s_tmem;
-    volatile int* gave_up = &s_gave_up;
+    volatile Watch* watch = &s_watch;
     Piece p;
 
     if (kF8 && w >= 8 && w < 12) {
@@ -1448,9 +1457,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 #pragma unroll 1
                 for (int kv = 0; kv < 2; ++kv) {
                     const bool tail = kv && (long long)(t + 1) * kTcUnit > len + 1;
-                    ok = ok && warp_wait(&bars.r_full[kv][rs], r_phase, gave_up);
+                    ok = ok && warp_wait(&bars.r_full[kv][rs], r_phase, watch);
                     ok = ok &&
-                         warp_wait(kv ? &bars.v_empty[ds] : &bars.k_empty[ds], again, gave_up);
+                         warp_wait(kv ? &bars.v_empty[ds] : &bars.k_empty[ds], again, watch);
                     if (tail) {
                         named_sync(2, 128);
                         if (lt < 4) s_wild[ds][lt] = 0;
@@ -1557,7 +1566,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                     const int pg = page;
                     page = page_of(t + 1);
                     ok = ok &&
-                         warp_wait(vals ? &bars.v_empty[st] : &bars.k_empty[st], again, gave_up);
+                         warp_wait(vals ? &bars.v_empty[st] : &bars.k_empty[st], again, watch);
                     const uint32_t n = __popc(__ballot_sync(~0u, good));
                     if (ok) {
                         if (lane == 0) bar_expect(full, n * bytes);
@@ -1575,7 +1584,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                     // A masked entry may hold anything, but 0 times NaN is NaN: what lies behind
                     // the last token is zeroed here, and so are new tokens' values that are not
                     // finite; those are added row by row.
-                    ok = ok && warp_wait(&bars.v_land, landed, gave_up);
+                    ok = ok && warp_wait(&bars.v_land, landed, watch);
                     landed ^= 1;
                     if (lt < 4) s_wild[st][lt] = 0;
                     named_sync(2, 96);
@@ -1642,7 +1651,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                     const uint32_t bytes =
                         __popc(__ballot_sync(~0u, good)) * ((uint32_t)DP << shift);
                     for (int kv = 0; ok && kv < 2; ++kv) {
-                        ok = warp_wait(&bars.r_empty[kv][rs], again, gave_up);
+                        ok = warp_wait(&bars.r_empty[kv][rs], again, watch);
                         if (!ok) break;
                         if (lane == 0) bar_expect(&bars.r_full[kv][rs], bytes);
                         __syncwarp();
@@ -1663,7 +1672,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             bool ok = true;
             while (ok && walk.next(a, ROWS, kTcUnit, &p)) {
                 if (walk.sh.bad) continue;
-                ok = warp_wait(&bars.q_empty, (pieces & 1) ^ 1, gave_up);
+                ok = warp_wait(&bars.q_empty, (pieces & 1) ^ 1, watch);
                 auto query = [&](int row) {
                     const int R = p.mt * ROWS + (row < p.rows ? row : 0);
                     const int j = R / a.group, g = R - j * a.group;
@@ -1735,6 +1744,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             constexpr int kStep = L::kTile >> 4;  // a tile further in a descriptor
             int ks = 0, vs = 0;  // stages and parities of the next tiles of keys and of values
             uint32_t k_phase = 0, v_phase = 0, pieces = 0, p_phase = 0;
+            int issued = 0;
             bool ok = true;
             while (ok && walk.next(a, ROWS, kTcUnit, &p)) {
                 if (walk.sh.bad) continue;
@@ -1742,14 +1752,14 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 const int nt = p.t1 - p.t0, jobs = two ? 2 * nt : nt;
                 const bool negate = (a.scale < 0.0f) != (kF8 && c.k_scale[p.h] < 0.0f);
                 qk = negate ? qk | kNegate : qk & ~kNegate;
-                ok = bar_wait(&bars.q_full, pieces & 1, gave_up);
+                ok = bar_wait(&bars.q_full, pieces & 1, watch);
                 // Job i belongs to stream i & 1.  Its scores take the place of the weights of job
                 // i - 2, whose product comes before them; products of one thread run in order.
                 // Each stream's product and next scores are issued together, so that the streams
                 // take turns.
                 auto scores = [&](int i) {
                     const int st = i & 1;
-                    if (!two || st == 0) ok = ok && bar_wait(&bars.k_full[ks], k_phase, gave_up);
+                    if (!two || st == 0) ok = ok && bar_wait(&bars.k_full[ks], k_phase, watch);
                     if (!ok) return;
                     const uint64_t qa = qd + (two ? st * kStep : 0), ka = kd + ks * kStep;
 #pragma unroll
@@ -1770,12 +1780,12 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 if (ok && jobs > 1) scores(1);
                 for (int i = 0; ok && i < jobs; ++i) {
                     const int st = i & 1;
-                    if (!two || st == 0) ok = bar_wait(&bars.v_full[vs], v_phase, gave_up);
+                    if (!two || st == 0) ok = bar_wait(&bars.v_full[vs], v_phase, watch);
                     const uint64_t va = vd + vs * kStep;
                     const uint32_t pd = tmem + st * 128, od = tmem + 256 + st * DP;
 #pragma unroll
                     for (int half = 0; half < 2; ++half) {
-                        ok = ok && bar_wait(&bars.p_full[st][half], p_phase >> st & 1, gave_up);
+                        ok = ok && bar_wait(&bars.p_full[st][half], p_phase >> st & 1, watch);
                         if (!ok) break;
                         tc_after();
 #pragma unroll
@@ -1785,6 +1795,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                     p_phase ^= 1u << st;
                     if (!ok) break;
                     tc_commit(&bars.pv_done[st]);
+                    watch->issued = ++issued;
                     if (!two || st == 1) {
                         tc_commit(&bars.v_empty[vs]);
                         if (++vs == SV) vs = 0, v_phase ^= 1;
@@ -1794,9 +1805,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 ++pieces;
             }
             if (!ok) {  // products in flight end before the tensor memory goes back
-                volatile int none = 0;
+                volatile Watch alone = {0, 0};
                 tc_commit(&bars.drain);
-                bar_wait(&bars.drain, 0, &none);
+                bar_wait(&bars.drain, 0, &alone);
             }
         }
         __syncwarp();
@@ -1861,7 +1872,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             float l = 0.0f, ref = -INFINITY;
             int done = 0;  // jobs of this stream
             // the outputs of the piece before have been read; this one's start at zero
-            ok = ok && warp_wait(&bars.epi_done, (pieces & 1) ^ 1, gave_up);
+            ok = ok && warp_wait(&bars.epi_done, (pieces & 1) ^ 1, watch);
             tc_after();
             {
                 float zero[32];
@@ -1873,7 +1884,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             }
             for (int i = st; ok && i < jobs; i += 2, ++done) {
                 const int t = p.t0 + (two ? i >> 1 : i);
-                ok = warp_wait(&bars.s_full[st], s_phase, gave_up);
+                ok = warp_wait(&bars.s_full[st], s_phase, watch);
                 s_phase ^= 1;
                 if (!ok) break;
                 tc_after();
@@ -1924,7 +1935,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                     if (grow) ref = mx;
                     l *= f;
                     if (done > 0) {
-                        ok = warp_wait(&bars.pv_done[st], (pv + done - 1) & 1, gave_up);
+                        ok = warp_wait(&bars.pv_done[st], (pv + done - 1) & 1, watch);
                         waited = true;
                         tc_after();
 #pragma unroll 1
@@ -1943,12 +1954,12 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 if (tail) {
                     const long long tile = tiles + (two ? i >> 1 : i);
                     const int vs = (int)(tile % SV);
-                    ok = ok && warp_wait(&bars.v_full[vs], (uint32_t)(tile / SV & 1), gave_up);
+                    ok = ok && warp_wait(&bars.v_full[vs], (uint32_t)(tile / SV & 1), watch);
 #pragma unroll 1
                     for (int sl = 0; ok && sl < 128; ++sl) {
                         if (!(s_wild[vs][sl >> 5] >> (sl & 31) & 1)) continue;
                         if (done > 0 && !waited) {
-                            ok = warp_wait(&bars.pv_done[st], (pv + done - 1) & 1, gave_up);
+                            ok = warp_wait(&bars.pv_done[st], (pv + done - 1) & 1, watch);
                             waited = true;
                             tc_after();
                         }
@@ -2009,7 +2020,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
             }
             // the stream's last product
-            if (ok && done > 0) ok = warp_wait(&bars.pv_done[st], (pv + done - 1) & 1, gave_up);
+            if (ok && done > 0) ok = warp_wait(&bars.pv_done[st], (pv + done - 1) & 1, watch);
             pv += done;
             tc_after();
             const bool whole = p.t0 == 0 && p.t1 == sh.tiles;
@@ -2030,7 +2041,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             }
             // Whatever wait of the CTA gave up (the other stream's, a load's), the rows may be made
             // of anything: its flag was set before what came here.
-            const bool late = !ok || *gave_up;
+            const bool late = !ok || watch->gave_up;
             const bool bad_page = s_bad_piece[pieces % kBadFlags] == pieces;
             if (late && r == 0) mark(a.status, p.b, SV_DEV_TIMEOUT);
             if (bad_page && !nan_rows && tid == 0) mark(a.status, p.b, SV_DEV_BAD_PAGE);
@@ -2082,7 +2093,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             ++pieces;
         }
     }
-    if (*gave_up) {  // loads that nobody waited for land within a millisecond
+    if (watch->gave_up) {  // loads that nobody waited for land within a millisecond
         const uint32_t since = nanoseconds();
         while (nanoseconds() - since < 1000000) __nanosleep(1000);
     }

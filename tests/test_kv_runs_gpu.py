@@ -215,8 +215,9 @@ def test_append_float8_is_the_quotient_rounded(kv, dtype):
         assert torch.equal(got, want), int((got != want).sum())
 
 
-@pytest.mark.parametrize("N,group", [(1, 4), (4, 4), (4, 8), (9, 8)])
-def test_attention_up_to_the_last_slot(kv, N, group):
+@pytest.mark.parametrize("cache,N,group", [(BF, 1, 4), (BF, 4, 4), (BF, 4, 8), (BF, 9, 8),
+                                           (BF, 33, 8), (E4M3, 4, 8), (E4M3, 33, 8)])
+def test_attention_up_to_the_last_slot(kv, cache, N, group):
     """A table of 2^31 - 8 slots, filled to the last one: 2^28 - 1 pages of eight, all but the new
     tokens' the same.  With queries of zero all weights are equal: committed values are zero, a
     new token's is 2^31 times its number, so that each row is the sum of the numbers it sees."""
@@ -225,14 +226,15 @@ def test_attention_up_to_the_last_slot(kv, N, group):
     own = (N + page - 1) // page + 1
     table = torch.zeros(1, width, dtype=torch.int32, device="cuda")
     table[0, width - own:] = torch.arange(1, own + 1, dtype=torch.int32, device="cuda")
-    k = torch.zeros(own + 1, page, 1, dim, dtype=BF, device="cuda")
-    v = torch.zeros_like(k)
+    k, v = (torch.zeros(own + 1, page, 1, dim, dtype=BF, device="cuda") for _ in range(2))
     numbers = torch.arange(1, N + 1, device="cuda") % 5
-    v.view(-1, dim)[(own + 1) * page - N:] = (numbers.double() * 2.0 ** 31).to(BF)[:, None]
+    one = 1.0 if cache == E4M3 else 2.0 ** 31  # float8: the scale has it
+    v.view(-1, dim)[(own + 1) * page - N:] = (numbers.double() * one).to(BF)[:, None]
+    scales = [torch.ones(1, device="cuda"), torch.full((1,), 2.0 ** 31, device="cuda")]
     g = torch.Generator().manual_seed(N)
     parents = tree(N, "tree", g)
     lens = torch.tensor([slots - N], dtype=torch.int32, device="cuda")
-    c = kv.PagedCache(k, v, table)
+    c = kv.PagedCache(k.to(cache), v.to(cache), table, *(scales if cache == E4M3 else []))
     q = torch.zeros(1, N, group, dim, dtype=BF, device="cuda")
     out, status = torch.full_like(q, 7.0), torch.zeros_like(lens)
     kv.spec_kv_attention(c, q, lens, out, kv.attention_workspace(c, 1, N, group), 1.0,
