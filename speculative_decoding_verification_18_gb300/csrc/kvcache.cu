@@ -1427,13 +1427,14 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         s_watch = Watch{0, 0};
     }
     if (tid < kBadFlags) s_bad_piece[tid] = -1;
+    cudaGridDependencySynchronize();
+    cudaTriggerProgrammaticLaunchCompletion();
+    // (not before: a kernel that is still to end may have its own tensor memory to ask for)
     if (w == 12) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;"
                      ::"r"(saddr(&s_tmem)), "r"(512) : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
     }
-    cudaGridDependencySynchronize();
-    cudaTriggerProgrammaticLaunchCompletion();
 
     tc_before();
     Walk walk = start_walk<kTcThreads>(a, ROWS, kTcUnit, s_scan, &s_start);
@@ -2105,8 +2106,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 }
 
 // Adds up the pieces of the items that more than one range holds, at most one per range that
-// starts one: sum over pieces of 2^(m - max) (o, l), then o / l.  A CTA of four warps per four rows of an item (a warp each), or
-// per row (the warps share its pieces) where the host expects many pieces per item.
+// starts one: sum over pieces of 2^(m - max) (o, l), then o / l.  A CTA of four warps per four
+// rows of an item (a warp each), or per row (the warps share its pieces) where the host expects
+// many pieces per item.
 template <typename T, int DP>
 __global__ void __launch_bounds__(128) kv_join_kernel(const AttentionArgs a, int rows, int warps) {
     __shared__ float4 s_o[4][DP / 4];

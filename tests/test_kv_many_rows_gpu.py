@@ -274,3 +274,17 @@ def test_whole_rounds_over_roomy_tables(kv, capture, monkeypatch):
 
     monkeypatch.setattr(kv, "PagedCache", roomy)
     test_kv_gpu.test_whole_rounds(kv, capture)
+
+
+@pytest.mark.parametrize("dtype,cache", [(BF, BF), (HF, E4M3)])
+@pytest.mark.parametrize("N,heads,group", [(65, 1, 128), (2, 1, 1024), (1, 1024, 1), (3, 128, 8),
+                                           (17, 2, 8), (32, 1, 4)])
+@pytest.mark.parametrize("far", [False, True])
+def test_many_query_heads(kv, dtype, cache, N, heads, group, far):
+    """From one key head for 1024 query heads to as many of both: 33 row tiles of 256, tiles with
+    their second half nearly empty, and 1024 items per sequence."""
+    r = Round([130, 5], N, "tree", counts=[N, max(1, N - 1)], heads=heads, group=group, dim=16,
+              dtype=dtype, cache=cache, seed=N, far=far)
+    out, status = r.attend(kv)
+    assert status == [0] * 2
+    kv_plain.check_attention(out, *part(r, torch.arange(2)), torch.full_like(out, 7.0))
