@@ -70,10 +70,12 @@ extern "C" {
 typedef struct {
     void* k;                /* DEVICE */
     void* v;                /* DEVICE */
-    const int32_t* table;   /* DEVICE [B, table_width]: the pages of each sequence; may be NULL if B is 0 */
+    const int32_t* table;   /* DEVICE [B, table_width]: the pages of each sequence; */
+                            /* may be NULL if B is 0                            */
     const float* k_scale;   /* DEVICE [heads], SV_E4M3 only (NULL otherwise):   */
-    const float* v_scale;   /* an entry stands for its stored value times this; */
-                            /* spec_kv_commit does not look at them             */
+    const float* v_scale;   /* an entry stands for its stored value times this, */
+                            /* of either sign; spec_kv_commit does not look at  */
+                            /* them                                             */
     int64_t page_stride, slot_stride, head_stride;
     int num_pages, page_size, table_width;
     int heads, dim;
@@ -138,10 +140,34 @@ size_t spec_kv_attention_workspace_size(int B, int N, int q_heads, int heads, in
  *        has the same type, or SV_E4M3.
  *   out  [B, N, q_heads, dim] contiguous (written), the type of q; it must not
  *        overlap q.
- * Entries that a node does not attend to take no part, whatever they hold.  The
- * sums are fp32.  Workspace as for the other calls (no initialisation; calls that
- * share one must not overlap).  Every row of a sequence with a bad length, tree or page is
- * NaN (its first num_new rows; all N when num_new itself is bad). */
+ * Entries that a node does not attend to take no part, whatever they hold.
+ * Workspace as for the other calls (no initialisation; calls that share one must
+ * not overlap).  Every row of a sequence with a bad length, tree or page, or of a
+ * wait that gave up (SV_DEV_TIMEOUT), is NaN (its first num_new rows; all N when
+ * num_new itself is bad).
+ *
+ * Arithmetic.  Scores, maxima and sums are fp32; the products are the tensor
+ * cores', of 16-bit operands with fp32 sums.
+ *  - The weights are multiplied as two 16-bit halves (hi + lo), which leaves
+ *    nothing of their rounding, with at most 32 query rows (N * q_heads / heads)
+ *    per key head, unless the cache is SV_E4M3 and q SV_BF16.  There, and with
+ *    more rows, they are rounded once to 16 bits: that of q's type, fp16 over
+ *    SV_E4M3.
+ *  - In fp16, weights below 2^-25 of the largest so far are missing in the output
+ *    but not in the sum that it is divided by.
+ *  - The tensor cores' sums cut off, rather than round, what lies below about
+ *    2^-24 of the running sum, so that many faint slots beside one that holds most
+ *    of the weight lose part of theirs, in every type: up to 0.2 % of the result
+ *    with 131072 of them, up to 0.8 % with 524288 (measured, 264 rows per key
+ *    head; a quarter of it with few rows).
+ *  - SV_BF16 queries over an SV_E4M3 cache become halves, after a power of two per
+ *    row has been taken out: exact down to 2^-25 of the row's largest element, and
+ *    zero below 2^-34 of it.
+ *
+ * The form is chosen from the sizes and types alone, the longest context being
+ * what the table has room for (table_width * page_size): one with no more room
+ * than its batch needs may be faster (one token over 700 slots: 5.7 us where there
+ * is room for at most 8192, 9.1 us beyond). */
 sv_status spec_kv_attention(const sv_kv_cache* cache, const void* q, const sv_strides* q_strides,
                             sv_dtype dtype, const int32_t* kv_len, const int32_t* num_new,
                             const int32_t* tree_parents, float scale, int B, int N, int q_heads,

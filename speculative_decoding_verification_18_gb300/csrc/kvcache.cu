@@ -617,10 +617,11 @@ __device__ __forceinline__ bool sees(uint64_t anc, int i) { return i == 0 || (an
 // may take two products: P = hi + lo, two 16-bit halves, so that rounding the weights costs
 // nothing next to rounding the result.  float8 caches become halves on the way into the registers
 // (exact), with a power of two taken out of each query row so that a bfloat16 query fits a half
-// too; their weights are single halves, four bits finer than a bfloat16 result.  Bound by memory
-// up to 16 rows (64 sequences of 4000-8000 slots, one token, 32 query and 8 key heads of 128:
-// 245 us, 6.5 TB/s; the same over float8, 96 sequences: 211 us, 5.6 TB/s), by conversions and
-// fixed latencies over float8 with 32 (96 sequences, 24 rows: 352 us, 3.5 TB/s).
+// too; their weights are single halves then, three bits finer than a bfloat16 result (fewer below
+// 2^-14 of the reference).  Bound by memory up to 16 rows (64 sequences of 4000-8000 slots, one
+// token, 32 query and 8 key heads of 128: 246 us, 6.4 TB/s; the same over float8, 96 sequences of
+// 4100-8200 slots: 223 us, 5.5 TB/s), by conversions and fixed latencies over float8 with 32 (96
+// sequences, 24 rows: 353 us, 3.5 TB/s).
 template <typename CT, int DP, int WM> struct Split {
     using St = Stage<CT, DP>;
     static constexpr int kRows = WM * 16, kPitch = DP + 8;  // floats: rows eight banks apart
@@ -1157,11 +1158,11 @@ __global__ void __launch_bounds__(kSplitThreads * WM, 2) kv_split_kernel(const A
 // pipe, so that one is multiplied while the other is exponentiated: two tiles of 128 rows over
 // the same slots, or, when the rows fit one tile, every other 128 slots of it (joined at the
 // end).  Work is cut into ranges and joined as for the split kernel, in units of 128 slots.
-// Measured: 32 trees of 16 nodes, 128 rows per key head, 6000-12000 slots: 229 us, 5.4 TB/s (the
+// Measured: 32 trees of 16 nodes, 128 rows per key head, 6000-12000 slots: 228 us, 5.5 TB/s (the
 // chain scores - weights - product of a stream, 5000 cycles, hides all but a fifth of the memory's
-// time); 8 trees of 65 nodes over 16000-33000 slots: 500 us, 873 TFLOP/s (the products: 128 x 128
+// time); 8 trees of 65 nodes over 16000-33000 slots: 503 us, 867 TFLOP/s (the products: 128 x 128
 // of two shared-memory operands takes all of that memory's bandwidth, 780 cycles where the tensor
-// pipe alone would need 512).
+// pipe alone would need 512); the same over float8: 264 us, 2.4 TB/s, and 643 us (making halves).
 
 constexpr int kTcThreads = 512;
 constexpr int kTcUnit = 128;  // slots
@@ -2246,9 +2247,10 @@ constexpr int kCommitResident = 8;  // CTAs per SM
 // thread owns one 16-byte column of the entries; for each plane it moves the column of all nodes
 // in order, eight moves at a time (of several planes, where one has fewer): the sources of a batch
 // are read before any of its targets is written, and since a_i >= i increases, no target is the
-// source of a later batch.  Bound by memory (or, for a few rows, by the chain node - page -
-// entry): every moved entry is read once and written once (256 trees of 65 nodes, 16 float8
-// layers: 34 us, 4.8 TB/s; one layer of one tree 3.1 us).
+// source of a later batch.  Bound by the latency of reads of scattered entries (a thread waits for
+// its eight; a third of the warps that fit are there, DRAM 36 % busy on half the sequences), for a
+// few rows by the chain node - page - entry: every moved entry is read once and written once (256
+// trees of 65 nodes, 16 float8 layers: 33 us, 4.8 TB/s; one layer of one tree 3.1 us).
 __global__ void __launch_bounds__(kCommitThreads, kCommitResident)
     kv_commit_kernel(const CommitArgs a) {
     __shared__ long long s_src[kMaxN], s_dst[kMaxN];
@@ -2704,8 +2706,8 @@ sv_status spec_kv_attention(const sv_kv_cache* cache, const void* q, const sv_st
     const bool cluster =
         small_call(B, cache->heads, rows, cache->table_width * cache->page_size, sms);
     // Float8 over short contexts stays with mma.sync up to 64 rows: pieces of one or two units, and
-    // no halves to make (100 sequences of 64 rows over at most 128 slots 38 against 62 us, 2048
-    // slots 135 against 146, 4096 slots 215 against 200).
+    // no halves to make (100 sequences, 8 key heads of 128, 64 rows each over at most 128 slots 70
+    // against 118 us, 2000 slots 235 against 252, 3000 slots 313 against 295).
     const int slots = cache->table_width * cache->page_size;
     const int few = cache->dtype == SV_E4M3 && slots <= 2048 ? 64 : 32;
     CUtensorMap kmap, vmap;
