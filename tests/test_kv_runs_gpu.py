@@ -7,7 +7,7 @@ import torch
 import kv_plain
 from kv_plain import E4M3
 from parity import Guarded
-from test_kv_gpu import BF, HF, built, kv, tree  # noqa: F401 (fixtures)
+from test_kv_gpu import BF, HF, Round, built, kv, tree  # noqa: F401 (fixtures)
 
 pytestmark = pytest.mark.gpu
 
@@ -247,3 +247,95 @@ def test_attention_up_to_the_last_slot(kv, cache, N, group):
     # whole numbers: the sums are exact, but for those of the pieces' counts (2^-24 per piece)
     off = (out.cpu().double() - want[None, :, None, None]).abs()
     assert bool((off <= (kv_plain.U[BF] + 305 * 2.0 ** -24) * want[None, :, None, None]).all())
+
+
+@pytest.mark.parametrize("cache,group", [(BF, 1), (BF, 64), (E4M3, 1), (E4M3, 80)])
+def test_the_largest_batch(kv, cache, group):
+    """65535 sequences of one token and nothing cached: each attends to itself alone, so that the
+    result is its own value; then the chain of none is committed.  Every seventh has no token."""
+    B, page, dim = 65535, 4, 16
+    g = torch.Generator(device="cuda").manual_seed(1)
+    rand = lambda *s: torch.randn(*s, generator=g, device="cuda").to(BF)
+    gd = Guarded()
+    k, v = (gd.empty((B, page, 1, dim), torch.uint8 if cache == E4M3 else BF).view(cache)
+            for _ in range(2))
+    for p in (k, v):
+        p.view(torch.uint8).fill_(0x7f)  # NaN, or (bfloat16) large
+    table = torch.randperm(B, generator=g, device="cuda").to(torch.int32).view(B, 1)
+    table = torch.cat([table, torch.full((B, 2048), -1, dtype=torch.int32, device="cuda")], 1)
+    ones = [torch.ones(1, device="cuda")] * 2 if cache == E4M3 else []
+    c = kv.PagedCache(k, v, table, *ones)
+    lens = torch.zeros(B, dtype=torch.int32, device="cuda")
+    counts = (torch.arange(B, device="cuda") % 7 != 3).to(torch.int32)
+    kn, vn = rand(B, 1, 1, dim), rand(B, 1, 1, dim)
+    q, out = rand(B, 1, group, dim), gd.empty((B, 1, group, dim), BF, fill=7.0)
+    status = gd.empty((B,), torch.int32, fill=0)
+    kv.spec_kv_append(c, kn, vn, lens, num_new=counts, status=status)
+    kv.spec_kv_attention(c, q, lens, out, kv.attention_workspace(c, B, 1, group), 0.25,
+                         num_new=counts, status=status)
+    new = gd.empty((B,), torch.int32, fill=-7)
+    kv.spec_kv_commit(c, lens, counts - 1, new, status=status)
+    gd.check()
+    assert not bool(status.any())
+    live = counts.bool()
+    own = vn.to(cache).to(BF) if cache == E4M3 else vn
+    assert torch.equal(out[live], own.expand(-1, -1, group, -1)[live])
+    assert bool((out[~live] == 7.0).all()) and torch.equal(new, counts)
+    for pool, x in ((k, kn), (v, vn)):
+        got = pool.view(torch.uint8)[table[:, 0].long(), 0]
+        assert torch.equal(got[live], x.view(B, 1, dim).to(cache).view(torch.uint8)[live])
+        assert bool((got[~live] == 0x7f).all())
+        assert bool((pool.view(torch.uint8)[:, 1:] == 0x7f).all())
+
+
+@pytest.mark.parametrize("dtype,cache", [(BF, BF), (HF, E4M3)])
+@pytest.mark.parametrize("N,group", [(3, 4), (9, 9), (33, 8)])
+def test_keys_and_values_side_by_side(kv, dtype, cache, N, group):
+    """Caches that are slices of one pool [layers, pages, 2, heads, page, dim], with a gap behind
+    each entry: append, attention and commit of a layer of three, the others untouched."""
+    r = Round([200, 7, 64], N, "tree", counts=[N, 2, N], heads=2, group=group, dim=48, dtype=dtype,
+              cache=cache, page=16, seed=N, far=N > 3)
+    heads, page, dim, pages = 2, 16, 48, r.k.shape[0]
+    raw = lambda x: x.view(torch.uint8)
+    size = 1 if cache == E4M3 else 2
+    pool = torch.full((3, pages, 2, heads, page, (dim + 16) * size), 0x31, dtype=torch.uint8,
+                      device="cuda")
+    k, v = (pool.view(cache)[:, :, i, :, :, :dim].transpose(2, 3) for i in range(2))
+    put = lambda x, y: raw(x).copy_(raw(y).cuda())
+    put(pool.view(cache)[1, :, 0, :, :, :dim].transpose(1, 2), r.k)
+    put(pool.view(cache)[1, :, 1, :, :, :dim].transpose(1, 2), r.v)
+    scales = [] if r.k_scale is None else [x.cuda().expand(3, heads).contiguous()
+                                           for x in (r.k_scale, r.v_scale)]
+    c = kv.PagedCache(k, v, r.table.cuda(), *scales)
+    lens, counts, parents = r.lens.cuda(), r.counts.cuda(), r.parents.cuda()
+    # the new tokens' entries once more, from the cache (float8: off by a step where 16 bits are)
+    kn = torch.zeros(3, N, heads, dim, dtype=dtype)
+    vn = torch.zeros_like(kn)
+    for b in range(3):
+        for j in range(int(r.counts[b])):
+            s = int(r.lens[b]) + j
+            at = int(r.table[b, s // page]), s % page
+            for new, old, sc in ((kn, r.k, r.k_scale), (vn, r.v, r.v_scale)):
+                x = old[at].float()
+                new[b, j] = (x if sc is None else x * sc[:, None]).to(dtype)
+    status = torch.zeros(3, dtype=torch.int32, device="cuda")
+    kv.spec_kv_append(c, kn.cuda(), vn.cuda(), lens, num_new=counts, parents=parents, layer=1,
+                      status=status)
+    out = torch.full_like(r.q, 7.0, device="cuda")
+    kv.spec_kv_attention(c, r.q.cuda(), lens, out, kv.attention_workspace(c, 3, N, heads * group),
+                         r.scale, parents=parents, num_new=counts, layer=1, status=status)
+    now_k, now_v = (raw(x[1]).cpu().contiguous().view(cache) for x in (k, v))
+    kv_plain.check_attention(out.cpu(), r.q, now_k, now_v, r.table, r.lens, r.counts, r.parents,
+                             r.scale, r.k_scale, r.v_scale, torch.full_like(r.q, 7.0))
+    if cache != E4M3:
+        assert torch.equal(raw(now_k), raw(r.k)) and torch.equal(raw(now_v), raw(r.v))
+    before = pool.clone()
+    nodes = torch.full((3, N), -1, dtype=torch.int32)
+    nodes[0, 0], nodes[2, 0] = N - 1, 1
+    acc = torch.tensor([1, 0, 1], dtype=torch.int32)
+    new = torch.zeros(3, dtype=torch.int32, device="cuda")
+    kv.spec_kv_commit(c, lens, acc.cuda(), new, nodes.cuda(), status=status)
+    assert status.tolist() == [0] * 3 and torch.equal(new.cpu(), r.lens + acc + 1)
+    (sp, ss), (dp, ds) = (kv_plain.slots(r.table[0], page, 200 + i + 1)[-1] for i in (N - 1, 1))
+    before[:, dp, :, :, ds, :dim * size] = before[:, sp, :, :, ss, :dim * size]
+    assert torch.equal(pool, before)
