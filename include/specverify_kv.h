@@ -174,6 +174,22 @@ sv_status spec_kv_attention(const sv_kv_cache* cache, const void* q, const sv_st
                             void* out, void* ws, size_t ws_bytes, uint32_t* status,
                             cudaStream_t stream);
 
+/* spec_kv_attention through a sliding window: what layers with a window compute, and what a drafter
+ * does that looks at a part of the target's cache only.  A node at position p (kv_len + its depth)
+ * attends to the entries that spec_kv_attention lets it see and whose position is below `sinks` or
+ * above p - window: its own and the window - 1 positions before it, and the first `sinks` of the
+ * sequence.  (A committed entry's position is its slot.)  window >= 1 and sinks >= 0, of any size;
+ * a window of kv_len + N or more hides nothing.
+ * Slots from `sinks` to kv_len - window are looked at by no node: their table entries are not read,
+ * so that pages which lie wholly among them may have been given back.  All other arguments,
+ * results, errors and the arithmetic are those of spec_kv_attention, and so is the workspace. */
+sv_status spec_kv_attention_window(const sv_kv_cache* cache, const void* q,
+                                   const sv_strides* q_strides, sv_dtype dtype,
+                                   const int32_t* kv_len, const int32_t* num_new,
+                                   const int32_t* tree_parents, float scale, int window, int sinks,
+                                   int B, int N, int q_heads, void* out, void* ws, size_t ws_bytes,
+                                   uint32_t* status, cudaStream_t stream);
+
 /* After verification: moves the accepted nodes' entries of `layers` layers
  * (layer i's keys and values at k and v + i*layer_stride elements; layer_stride
  * a multiple of 16 bytes, ignored for one layer) to the slots behind the root's

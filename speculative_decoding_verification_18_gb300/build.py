@@ -16,8 +16,10 @@ UNITS = {
     "specverify": [os.path.join(CSRC, "specverify.cu"), os.path.join(CSRC, "ff.cuh"),
                    os.path.join(INCLUDE, "specverify.h"),
                    os.path.join(INCLUDE, "specverify_debug.h")],
-    "kvcache": [os.path.join(CSRC, "kvcache.cu"), os.path.join(INCLUDE, "specverify.h"),
-                os.path.join(INCLUDE, "specverify_kv.h")],
+    "kvcache": [os.path.join(CSRC, "kvcache.cu"), os.path.join(CSRC, "kvattention.cuh"),
+                os.path.join(INCLUDE, "specverify.h"), os.path.join(INCLUDE, "specverify_kv.h")],
+    "kvwindow": [os.path.join(CSRC, "kvwindow.cu"), os.path.join(CSRC, "kvattention.cuh"),
+                 os.path.join(INCLUDE, "specverify.h"), os.path.join(INCLUDE, "specverify_kv.h")],
 }
 LIB = os.path.join(HERE, "libspecverify.so")
 #: The binding of the cache calls: an extension module of this interpreter and its torch.

@@ -11,6 +11,7 @@
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
 
+#include <climits>
 #include <exception>
 #include <string>
 
@@ -20,6 +21,7 @@ namespace {
 
 decltype(&spec_kv_append) g_append;
 decltype(&spec_kv_attention) g_attention;
+decltype(&spec_kv_attention_window) g_window;
 decltype(&spec_kv_commit) g_commit;
 
 struct Refused {
@@ -183,9 +185,20 @@ PyObject* append(PyObject*, PyObject* const* a, Py_ssize_t n) {
     });
 }
 
-// (cache, rows of the table, device, q, kv_len, out, ws, scale, parents, num_new, status, stream)
-PyObject* attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
-    return guarded(n, 12, [&] {
+int number(PyObject* o, const char* name) {
+    const long long x = PyLong_AsLongLong(o);
+    if (PyErr_Occurred()) {
+        PyErr_Clear();
+        type(std::string(name) + " must be a whole number");
+    }
+    if (x < INT_MIN || x > INT_MAX) value(std::string(name) + " is too large");
+    return (int)x;
+}
+
+// (cache, rows of the table, device, q, kv_len, out, ws, scale, parents, num_new, status, stream),
+// and with a window: its length and the number of first slots
+PyObject* attend(PyObject* const* a, Py_ssize_t n, bool windowed) {
+    return guarded(n, windowed ? 14 : 12, [&] {
         const sv_kv_cache* c = cache_of(a[0]);
         const at::Tensor& q = tensor(a[3], "q");
         if (q.dim() != 4) value("q must be [B, N, q_heads, dim]");
@@ -204,6 +217,8 @@ PyObject* attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
         void* ws = vector(a[6], "ws", {w.numel()}, at::kByte, at::kByte);
         const double scale = PyFloat_AsDouble(a[7]);
         if (PyErr_Occurred()) return SV_OK;
+        const int window = windowed ? number(a[12], "window") : 0;
+        const int sinks = windowed ? number(a[13], "sinks") : 0;
         const void* par = ints(a[8], "parents", {B, N});
         const void* num = ints(a[9], "num_new", {B});
         void* st = vector(a[10], "status", {B}, at::kInt, at::kUInt32);
@@ -216,10 +231,19 @@ PyObject* attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
         add(d, a[9], "num_new");
         add(d, a[10], "status");
         d.check((int)PyLong_AsLong(a[2]));
+        if (windowed)
+            return g_window(c, qp, &qs, t, (const int32_t*)lens, (const int32_t*)num,
+                            (const int32_t*)par, (float)scale, window, sinks, (int)B, (int)N,
+                            (int)hq, out, ws, (size_t)w.numel(), (uint32_t*)st,
+                            stream_of(a[11]));
         return g_attention(c, qp, &qs, t, (const int32_t*)lens, (const int32_t*)num,
                            (const int32_t*)par, (float)scale, (int)B, (int)N, (int)hq, out, ws,
                            (size_t)w.numel(), (uint32_t*)st, stream_of(a[11]));
     });
+}
+PyObject* attention(PyObject*, PyObject* const* a, Py_ssize_t n) { return attend(a, n, false); }
+PyObject* attention_window(PyObject*, PyObject* const* a, Py_ssize_t n) {
+    return attend(a, n, true);
 }
 
 // (cache, rows of the table, device, layers, layer stride, kv_len, num_accepted, kv_len_out,
@@ -258,13 +282,14 @@ PyObject* commit(PyObject*, PyObject* const* a, Py_ssize_t n) {
 
 // The library's entry points, as kvcache.py has loaded them.
 PyObject* bind(PyObject*, PyObject* const* a, Py_ssize_t n) {
-    if (n != 3) {
-        PyErr_SetString(PyExc_TypeError, "three entry points");
+    if (n != 4) {
+        PyErr_SetString(PyExc_TypeError, "four entry points");
         return nullptr;
     }
     g_append = reinterpret_cast<decltype(g_append)>(PyLong_AsVoidPtr(a[0]));
     g_attention = reinterpret_cast<decltype(g_attention)>(PyLong_AsVoidPtr(a[1]));
     g_commit = reinterpret_cast<decltype(g_commit)>(PyLong_AsVoidPtr(a[2]));
+    g_window = reinterpret_cast<decltype(g_window)>(PyLong_AsVoidPtr(a[3]));
     if (PyErr_Occurred()) return nullptr;
     Py_RETURN_NONE;
 }
@@ -273,6 +298,7 @@ PyMethodDef g_methods[] = {
     {"bind", reinterpret_cast<PyCFunction>(bind), METH_FASTCALL, nullptr},
     {"append", reinterpret_cast<PyCFunction>(append), METH_FASTCALL, nullptr},
     {"attention", reinterpret_cast<PyCFunction>(attention), METH_FASTCALL, nullptr},
+    {"attention_window", reinterpret_cast<PyCFunction>(attention_window), METH_FASTCALL, nullptr},
     {"commit", reinterpret_cast<PyCFunction>(commit), METH_FASTCALL, nullptr},
     {nullptr, nullptr, 0, nullptr}};
 PyModuleDef g_module = {PyModuleDef_HEAD_INIT, "_kvbind", nullptr, -1, g_methods,

@@ -1,5 +1,6 @@
 """Thin binding of the paged key-value cache calls (include/specverify_kv.h):
-``spec_kv_append``, ``spec_kv_attention`` and ``spec_kv_commit``.
+``spec_kv_append``, ``spec_kv_attention``, ``spec_kv_attention_window`` and
+``spec_kv_commit``.
 
 Like specverify.py it only marshals arguments: torch CUDA tensors on the current
 device, launches on the current torch stream unless ``stream`` is given, no CPU
@@ -30,7 +31,7 @@ SV_F16, SV_E4M3 = 2, 3
 SV_DEV_BAD_PAGE, SV_DEV_BAD_LENGTH, SV_DEV_TIMEOUT = 0x80, 0x100, 0x200
 
 EXPORTS = ("spec_kv_rope_turns", "spec_kv_append", "spec_kv_attention_workspace_size",
-           "spec_kv_attention", "spec_kv_commit")
+           "spec_kv_attention", "spec_kv_attention_window", "spec_kv_commit")
 
 _TYPES = {torch.bfloat16: sv.SV_BF16, torch.float16: SV_F16, torch.float8_e4m3fn: SV_E4M3}
 
@@ -72,7 +73,7 @@ def load():
     loader.exec_module(bind)
     address = lambda f: ctypes.cast(f, P).value
     bind.bind(address(lib.spec_kv_append), address(lib.spec_kv_attention),
-              address(lib.spec_kv_commit))
+              address(lib.spec_kv_commit), address(lib.spec_kv_attention_window))
     _lib, _bind = lib, bind
     return lib
 
@@ -211,6 +212,17 @@ def spec_kv_attention(cache, q, kv_len, out, ws, scale, parents=None, num_new=No
                          parents, num_new, status, None if stream is None else sv._stream(stream))
     if st:
         sv._check(st, "spec_kv_attention")
+
+
+def spec_kv_attention_window(cache, q, kv_len, out, ws, scale, window, sinks=0, parents=None,
+                             num_new=None, status=None, layer=0, stream=None):
+    """spec_kv_attention where a node at position p sees the positions above p - window and the
+    first `sinks` only; pages that no node of a sequence sees may be missing from its table."""
+    st = _bind.attention_window(cache.layer(layer), cache._rows, cache._device, q, kv_len, out, ws,
+                                scale, parents, num_new, status,
+                                None if stream is None else sv._stream(stream), window, sinks)
+    if st:
+        sv._check(st, "spec_kv_attention_window")
 
 
 def spec_kv_commit(cache, kv_len, num_accepted, kv_len_out, out_nodes=None, status=None,
