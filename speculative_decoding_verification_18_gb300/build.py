@@ -1,5 +1,6 @@
-"""Build ``libspecverify.so`` in-tree with nvcc for sm_103a, and the binding of its cache calls
-(``_kvbind.so``) with g++, all translation units in parallel."""
+"""Build ``libspecverify.so`` in-tree with nvcc for sm_103a, and the bindings of its cache calls
+(``_kvbind.so``) and of its log probabilities (``_lpbind.so``) with g++, all translation units in
+parallel."""
 from __future__ import annotations
 
 import importlib.util
@@ -20,12 +21,17 @@ UNITS = {
                 os.path.join(INCLUDE, "specverify.h"), os.path.join(INCLUDE, "specverify_kv.h")],
     "kvwindow": [os.path.join(CSRC, "kvwindow.cu"), os.path.join(CSRC, "kvattention.cuh"),
                  os.path.join(INCLUDE, "specverify.h"), os.path.join(INCLUDE, "specverify_kv.h")],
+    "logprobs": [os.path.join(CSRC, "logprobs.cu"), os.path.join(INCLUDE, "specverify.h"),
+                 os.path.join(INCLUDE, "specverify_logprobs.h")],
 }
 LIB = os.path.join(HERE, "libspecverify.so")
-#: The binding of the cache calls: an extension module of this interpreter and its torch.
-BIND = os.path.join(HERE, "_kvbind.so")
-BIND_FILES = [os.path.join(CSRC, "kvbind.cpp"), os.path.join(INCLUDE, "specverify.h"),
-              os.path.join(INCLUDE, "specverify_kv.h")]
+#: The bindings, extension modules of this interpreter and its torch, with the files of each.
+BINDINGS = {
+    os.path.join(HERE, f"_{name}.so"): [os.path.join(CSRC, name + ".cpp"),
+                                        os.path.join(CSRC, "bind.h"),
+                                        os.path.join(INCLUDE, "specverify.h"),
+                                        os.path.join(INCLUDE, header)]
+    for name, header in (("kvbind", "specverify_kv.h"), ("lpbind", "specverify_logprobs.h"))}
 ARCH = "-gencode=arch=compute_103a,code=sm_103a"
 
 
@@ -35,32 +41,34 @@ def nvcc() -> str:
     return path if os.path.exists(path) else "nvcc"
 
 
-def bind_command(out: str) -> list[str]:
+def bind_command(source: str, out: str) -> list[str]:
     torch = importlib.util.find_spec("torch").submodule_search_locations[0]
     cuda = os.path.dirname(os.path.dirname(nvcc()))
     include = [sysconfig.get_paths()["include"], INCLUDE, os.path.join(torch, "include"),
                os.path.join(torch, "include", "torch", "csrc", "api", "include"),
                os.path.join(cuda, "include")]
     return (["g++", "-O2", "-std=c++17", "-shared", "-fPIC", "-w"] + [f"-I{p}" for p in include]
-            + ["-o", out, BIND_FILES[0], "-L" + os.path.join(torch, "lib"), "-ltorch_python",
+            + ["-o", out, source, "-L" + os.path.join(torch, "lib"), "-ltorch_python",
                "-ltorch_cpu", "-lc10", "-lc10_cuda"])
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
-    """Compile the CUDA library and the cache calls' binding unless they are newer
-    than every source; of the library's units only those older than their files."""
+    """Compile the CUDA library and the bindings unless they are newer than every
+    source; of the library's units only those older than their files."""
     newer = lambda out, files: not force and os.path.exists(out) and (
         os.path.getmtime(out) >= max(os.path.getmtime(f) for f in files))
     lib_done = newer(LIB, [f for files in UNITS.values() for f in files])
-    if lib_done and newer(BIND, BIND_FILES):
+    if lib_done and all(newer(*b) for b in BINDINGS.items()):
         return LIB
     folder = os.path.join(HERE, "_build")
     os.makedirs(folder, exist_ok=True)
     running = []
-    if not newer(BIND, BIND_FILES):
-        tmp = BIND + f".tmp{os.getpid()}"
-        cmd = bind_command(tmp)
-        running.append((cmd, subprocess.Popen(cmd), tmp, BIND))
+    for bind, files in BINDINGS.items():
+        if newer(bind, files):
+            continue
+        tmp = bind + f".tmp{os.getpid()}"
+        cmd = bind_command(files[0], tmp)
+        running.append((cmd, subprocess.Popen(cmd), tmp, bind))
     for name, files in UNITS.items():
         obj = os.path.join(folder, name + ".o")
         if lib_done or newer(obj, files):
