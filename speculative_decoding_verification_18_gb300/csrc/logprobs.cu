@@ -87,6 +87,12 @@ template <> struct Elt<__nv_bfloat16> {
             f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
         }
     }
+    // (NaN only where all are)
+    static __device__ __forceinline__ float largest(const uint4& v) {
+        auto two = [](uint32_t w) { return reinterpret_cast<const __nv_bfloat162&>(w); };
+        const __nv_bfloat162 m = __hmax2(__hmax2(two(v.x), two(v.y)), __hmax2(two(v.z), two(v.w)));
+        return fmaxf(__low2float(m), __high2float(m));
+    }
     static __device__ __forceinline__ uint4 pack(const float* f) {
         uint32_t w[4];
 #pragma unroll
@@ -105,6 +111,10 @@ template <> struct Elt<float> {
     static __device__ __forceinline__ void unpack(const uint4& v, float* f) {
         f[0] = __uint_as_float(v.x), f[1] = __uint_as_float(v.y);
         f[2] = __uint_as_float(v.z), f[3] = __uint_as_float(v.w);
+    }
+    static __device__ __forceinline__ float largest(const uint4& v) {
+        return fmaxf(fmaxf(__uint_as_float(v.x), __uint_as_float(v.y)),
+                     fmaxf(__uint_as_float(v.z), __uint_as_float(v.w)));
     }
     static __device__ __forceinline__ uint4 pack(const float* f) {
         return make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]),
@@ -180,7 +190,7 @@ struct Args {
     const void* logits;
     long long stride;
     const int32_t* tokens;
-    float T, c;  // c: log2(e) / T
+    float T, c, c_low;  // c + c_low: log2(e) / T
     int V, given, top;
     float* logprobs;
     float* normalizer;
@@ -190,6 +200,31 @@ struct Args {
     uint32_t* status;
 };
 
+// Two fp32 operations in one instruction.
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+    float2 d;
+    asm("{ .reg .b64 a, b, c; mov.b64 a, {%2, %3}; mov.b64 b, {%4, %5}; mov.b64 c, {%6, %7}; "
+        "fma.rn.f32x2 a, a, b, c; mov.b64 {%0, %1}, a; }"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+    return d;
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+    float2 d;
+    asm("{ .reg .b64 a, b; mov.b64 a, {%2, %3}; mov.b64 b, {%4, %5}; "
+        "mul.rn.f32x2 a, a, b; mov.b64 {%0, %1}, a; }"
+        : "=f"(d.x), "=f"(d.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return d;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+    float2 d;
+    asm("{ .reg .b64 a, b; mov.b64 a, {%2, %3}; mov.b64 b, {%4, %5}; "
+        "add.rn.f32x2 a, a, b; mov.b64 {%0, %1}, a; }"
+        : "=f"(d.x), "=f"(d.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return d;
+}
+__device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
+
 // A cluster of CTAs per row, each with an equal run of its vectors, read once with the running
 // maximum and sums of a softmax; joined through distributed shared memory.
 //
@@ -198,7 +233,7 @@ struct Args {
 // these are in the vectors of the threads whose own maximum reaches it, about as many again.  Only
 // those threads' vectors are read a second time (by their warp, from L2), the elements that reach
 // the bound are put in order by counting, and rank 0 joins the lists of the cluster's CTAs.
-template <typename T>
+template <typename T, bool ENTROPY, bool TOP>
 __global__ void __launch_bounds__(kThreads, 4) lp_kernel(const Args a) {
     using E = Elt<T>;
     constexpr int VW = E::kVec;
@@ -214,45 +249,63 @@ __global__ void __launch_bounds__(kThreads, 4) lp_kernel(const Args a) {
     const Row<T> row((const T*)a.logits + r * a.stride, a.V);
     const int i0 = (int)((long long)row.vectors * rank / G);
     const int i1 = (int)((long long)row.vectors * (rank + 1) / G);
-    const bool known = token >= 0 && token < a.V;
-    const float given = rank == 0 && known ? E::get(row.row + token) : 0.0f;
+    const uint4 none = make_uint4(E::kLowest, E::kLowest, E::kLowest, E::kLowest);
 
     Stats st = {-INFINITY, 0.0f, 0.0f};
     int best = i0 + tid;  // the vector that holds this thread's first maximum
+    uint4 v[kBatch];
+#pragma unroll
+    for (int q = 0; q < kBatch; ++q) {
+        const int k = i0 + tid + q * kThreads;
+        v[q] = k < i1 ? row.load(k) : none;
+    }
+    const bool known = token >= 0 && token < a.V;
+    const float given = rank == 0 && known ? E::get(row.row + token) : 0.0f;
     for (int i = i0 + tid; i < i1; i += kThreads * kBatch) {
-        uint4 v[kBatch];
+        uint4 next[kBatch];
 #pragma unroll
         for (int q = 0; q < kBatch; ++q) {
-            const int k = i + q * kThreads;
-            v[q] = k < i1 ? row.load(k)
-                          : make_uint4(E::kLowest, E::kLowest, E::kLowest, E::kLowest);
+            const int k = i + (kBatch + q) * kThreads;
+            next[q] = k < i1 ? row.load(k) : none;
         }
-        float x[kBatch][VW], top[kBatch];
+        float top[kBatch];
 #pragma unroll
-        for (int q = 0; q < kBatch; ++q) {
-            E::unpack(v[q], x[q]);
-            top[q] = x[q][0];
-#pragma unroll
-            for (int e = 1; e < VW; ++e) top[q] = fmaxf(top[q], x[q][e]);
-        }
+        for (int q = 0; q < kBatch; ++q) top[q] = E::largest(v[q]);
         float most = top[0];
 #pragma unroll
         for (int q = 1; q < kBatch; ++q) most = fmaxf(most, top[q]);
         if (most > st.m) {
+            if (TOP) {
 #pragma unroll
-            for (int q = kBatch - 1; q >= 0; --q)
-                if (top[q] == most) best = i + q * kThreads;
+                for (int q = kBatch - 1; q >= 0; --q)
+                    if (top[q] == most) best = i + q * kThreads;
+            }
             add(st, Stats{most, 0.0f, 0.0f}, a.c);
         }
-        const float ref = st.m == -INFINITY ? 0.0f : st.m;
+        const float2 less = both(st.m == -INFINITY ? 0.0f : -st.m);
+        float2 s = make_float2(0.0f, 0.0f), u = s;
 #pragma unroll
-        for (int q = 0; q < kBatch; ++q)
+        for (int q = 0; q < kBatch; ++q) {
+            float x[VW];
+            E::unpack(v[q], x);
 #pragma unroll
-            for (int e = 0; e < VW; ++e) {
-                const float d = x[q][e] - ref, p = ex2(d * a.c);
-                st.s += p;
-                st.u = fmaf(p, fmaxf(d, -FLT_MAX), st.u);  // (0 times -inf is NaN)
+            for (int e = 0; e < VW; e += 2) {
+                float2 d = add2(make_float2(x[e], x[e + 1]), less);
+                float2 p = fma2(d, both(a.c_low), mul2(d, both(a.c)));
+                p.x = ex2(p.x);
+                p.y = ex2(p.y);
+                s = add2(s, p);
+                if (ENTROPY) {  // (0 times -inf is NaN)
+                    d.x = fmaxf(d.x, -FLT_MAX);
+                    d.y = fmaxf(d.y, -FLT_MAX);
+                    u = fma2(p, d, u);
+                }
             }
+        }
+        st.s += s.x + s.y;
+        st.u += u.x + u.y;
+#pragma unroll
+        for (int q = 0; q < kBatch; ++q) v[q] = next[q];
     }
     const float mine = st.m;
 #pragma unroll
@@ -265,7 +318,7 @@ __global__ void __launch_bounds__(kThreads, 4) lp_kernel(const Args a) {
     }
     if (lane == 0) s_warp[w] = st;
     uint64_t key = 0;
-    if (a.top) {
+    if (TOP) {
         // (the last place of the vector: nothing that equals the maximum is left out)
         if (i0 + tid < i1) key = key_of(mine, min(best * VW + VW - 1 - row.skew, a.V - 1));
         const uint64_t other = __shfl_xor_sync(~0u, key, 1);
@@ -279,7 +332,7 @@ __global__ void __launch_bounds__(kThreads, 4) lp_kernel(const Args a) {
         for (int k = 1; k < kWarps; ++k) add(t, s_warp[k], a.c);
         s_stats = t;
     }
-    if (a.top) {
+    if (TOP) {
         if (tid < kPairs) {
             const uint64_t p = s_pair[tid];
             int above = 0;
@@ -361,13 +414,13 @@ __global__ void __launch_bounds__(kThreads, 4) lp_kernel(const Args a) {
         if (a.status && bits && (tid == 0 || token != -1)) atomicOr(a.status + r, bits);
         if (tid == 0 && a.normalizer)
             reinterpret_cast<float2*>(a.normalizer)[r] = make_float2(m, log_s);
-        if (tid == 0 && a.entropy) a.entropy[r] = log_s - __fdiv_rn(t.u, t.s * a.T);
+        if (ENTROPY && tid == 0) a.entropy[r] = log_s - __fdiv_rn(t.u, t.s * a.T);
         const long long out = (long long)r * a.top;
-        for (int i = (bad ? 0 : a.V) + tid; i < a.top; i += kThreads) {
+        for (int i = (bad ? 0 : a.V) + tid; TOP && i < a.top; i += kThreads) {
             a.top_tokens[out + i] = -1;
             a.top_logprobs[out + i] = bad ? NAN : -INFINITY;
         }
-        if (a.top && !bad) {
+        if (TOP && !bad) {
             // the lists side by side; an element's place is its place in its own list and how
             // many of each other one are above it
             const int all = G * a.top;
@@ -409,15 +462,36 @@ struct GradArgs {
     const float* entropy;
     const float* grad_logprobs;
     const float* grad_entropy;
-    float T;
+    float T, c, c_low;  // c + c_low: log2(e) / T
     int V, given, parts;
     uint32_t* status;
 };
 
-// A part of a row per CTA: each logit read once, its gradient written once; then the places of
-// given tokens again, with their own share (their logits are read before anything is written, so
-// that the gradient may take the logits' place).
-template <typename T>
+constexpr int kGradBatches = 2;  // of kBatch vectors per thread: a CTA's part of a row
+
+// Elements o .. o + kVec - 1 of two vectors side by side.
+template <typename T> __device__ __forceinline__ uint4 shifted(const uint4& a, const uint4& b, int o) {
+    constexpr int kPer = 4 / sizeof(T);  // elements per word
+    uint32_t w[5];
+    switch (o / kPer) {
+        case 0: w[0] = a.x, w[1] = a.y, w[2] = a.z, w[3] = a.w, w[4] = b.x; break;
+        case 1: w[0] = a.y, w[1] = a.z, w[2] = a.w, w[3] = b.x, w[4] = b.y; break;
+        case 2: w[0] = a.z, w[1] = a.w, w[2] = b.x, w[3] = b.y, w[4] = b.z; break;
+        default: w[0] = a.w, w[1] = b.x, w[2] = b.y, w[3] = b.z, w[4] = b.w; break;
+    }
+    if (kPer == 2 && o % 2) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) w[k] = __funnelshift_r(w[k], w[k + 1], 16);
+    }
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// A part of a row per CTA: each logit read once, its gradient written once, in vectors of the
+// gradient's row (where the logits lie at another place of a 16-byte word: two of theirs, shifted
+// together: SHIFT).  With x = (l - m) / T in base 2 and less ln S, p = 2^x, a gradient is p (A + B x): A
+// and B are the row's.  Then the places of given tokens again, with their own share (their logits
+// are read before anything is written, so that the gradient may take the logits' place).
+template <typename T, bool ENTROPY, bool SHIFT>
 __global__ void __launch_bounds__(kThreads, 4) lp_grad_kernel(const GradArgs a) {
     using E = Elt<T>;
     constexpr int VW = E::kVec;
@@ -426,78 +500,107 @@ __global__ void __launch_bounds__(kThreads, 4) lp_grad_kernel(const GradArgs a) 
     const int tid = threadIdx.x, r = blockIdx.x / a.parts, part = blockIdx.x % a.parts;
     int token = -1;
     if (tid < a.given) token = a.tokens[(long long)r * a.given + tid];
-    const bool live = __syncthreads_or(token != -1);
-    const bool bad_token = __syncthreads_or(token < -1 || token >= a.V);
-    const Row<T> from((const T*)a.logits + r * a.stride, a.V);
     T* const out = (T*)a.grad + r * a.grad_stride;
-    const Row<T> to(out, a.V);
-    const int i0 = (int)((long long)to.vectors * part / a.parts);
-    const int i1 = (int)((long long)to.vectors * (part + 1) / a.parts);
-    const bool same = from.skew == to.skew;
-
-    float m = 0.0f, log_s = 0.0f, H = 0.0f, gh = 0.0f, sum = 0.0f, own = 0.0f;
-    bool bad = false;
-    if (live) {
-        const float2 z = reinterpret_cast<const float2*>(a.normalizer)[r];
-        m = z.x, log_s = z.y;
-        if (a.grad_entropy) H = a.entropy[r], gh = a.grad_entropy[r];
-        bad = !(fabsf(m) < INFINITY && fabsf(log_s) < INFINITY);
-        if (tid < a.given) {
-            s_token[tid] = token;
-            s_g[tid] = token != -1 ? a.grad_logprobs[(long long)r * a.given + tid] : 0.0f;
+    const Row<T> from((const T*)a.logits + r * a.stride, a.V), to(out, a.V);
+    const int i0 = part * kThreads * kBatch * kGradBatches;
+    const int i1 = min(to.vectors, i0 + kThreads * kBatch * kGradBatches);
+    const bool live = __syncthreads_or(token != -1);
+    uint4* const to16 = reinterpret_cast<uint4*>(out - to.skew);
+    if (!live) {
+        for (int i = i0 + tid; i < i1; i += kThreads) {
+            if (to.whole(i)) {
+                to16[i] = make_uint4(0, 0, 0, 0);
+            } else {
+                for (int e = 0; e < VW; ++e) {
+                    const int v = i * VW + e - to.skew;
+                    if (v >= 0 && v < a.V) out[v] = E::from(0.0f);
+                }
+            }
         }
-        if (part == 0 && tid == 0 && a.status && (bad || bad_token))
-            atomicOr(a.status + r, (bad ? SV_DEV_BAD_ROW : 0) | (bad_token ? SV_DEV_BAD_TOKEN : 0));
-        bad |= bad_token;
+        return;
     }
-    // (of given tokens: this thread's place is in this part, and none before it is the same)
-    const int at = token < 0 || bad ? -1 : (token + to.skew) / VW;
-    bool mine = at >= i0 && at < i1;
-    if (mine) own = E::get(from.row + token);
-    __syncthreads();
-    if (live)
-        for (int k = 0; k < a.given; ++k) sum += s_g[k];
-    auto grad = [&](float l) -> float {
-        if (!live) return 0.0f;
-        if (bad) return NAN;
-        const float lp = __fdiv_rn(l - m, a.T) - log_s;
-        const float p = ex2(lp * 1.4426950408889634f);
-        return -p * (sum + gh * (max_nan(lp, -1e4f) + H));
+    const int off = SHIFT ? from.skew - to.skew : 0, by = off < 0 ? off + VW : off;  // shift of a vector
+    const int back = off < 0 ? 1 : 0;
+    // Vectors that lie wholly in the row, as what they are made of does; the others, two at each
+    // end at most, go element by element.
+    auto fast = [&](int i) {
+        return to.whole(i) &&
+               (off == 0 || (from.whole(i - back) && i - back >= 0 && from.whole(i - back + 1)));
     };
-    for (int i = i0 + tid; i < i1; i += kThreads) {
-        float x[VW];
-        const bool whole = to.whole(i);
-        if (same && whole) {
-            E::unpack(ld_own16(from.at(i)), x);
-        } else {
+    auto load = [&](int i) -> uint4 {
+        if (i >= i1 || !fast(i)) return make_uint4(0, 0, 0, 0);
+        if (off == 0) return ld_own16(from.at(i));
+        return shifted<T>(ld_own16(from.at(i - back)), ld_own16(from.at(i - back + 1)), by);
+    };
+    uint4 x[kBatch];
 #pragma unroll
-            for (int e = 0; e < VW; ++e) {
-                const int v = i * VW + e - to.skew;
-                x[e] = v >= 0 && v < a.V ? E::get(from.row + v) : 0.0f;
-            }
+    for (int q = 0; q < kBatch; ++q) x[q] = load(i0 + tid + q * kThreads);
+
+    const float2 z = reinterpret_cast<const float2*>(a.normalizer)[r];
+    const float m = z.x, log_s = z.y;
+    float H = 0.0f, gh = 0.0f;
+    if (ENTROPY) H = a.entropy[r], gh = a.grad_entropy[r];
+    bool bad = !(fabsf(m) < INFINITY && fabsf(log_s) < INFINITY);
+    if (tid < a.given) {
+        s_token[tid] = token;
+        s_g[tid] = token != -1 ? a.grad_logprobs[(long long)r * a.given + tid] : 0.0f;
+    }
+    // (of given tokens: this thread's place is in this part)
+    const int at = token < 0 || token >= a.V ? -1 : (token + to.skew) / VW;
+    bool mine = at >= i0 && at < i1;
+    const float own = mine ? E::get(from.row + token) : 0.0f;
+    const bool bad_token = __syncthreads_or(token < -1 || token >= a.V);
+    if (part == 0 && tid == 0 && a.status && (bad || bad_token))
+        atomicOr(a.status + r, (bad ? SV_DEV_BAD_ROW : 0) | (bad_token ? SV_DEV_BAD_TOKEN : 0));
+    bad |= bad_token;
+    float sum = 0.0f;
+    for (int k = 0; k < a.given; ++k) sum += s_g[k];
+    const float base = log_s * 1.4426950408889634f;
+    const float A = bad ? NAN : -__fdiv_rn(ENTROPY ? fmaf(gh, H, sum) : sum, a.T);
+    const float B = ENTROPY ? -__fdiv_rn(gh * 0.6931471805599453f, a.T) : 0.0f;
+    auto grad = [&](float l) -> float {
+        const float d = l - m;
+        // (the low half of the factor where the gradient has the bits to show it)
+        const float y = fmaf(d, a.c, sizeof(T) == 4 ? fmaf(d, a.c_low, -base) : -base);
+        const float p = ex2(y);
+        return p * (ENTROPY ? fmaf(B, max_nan(y, -1e4f), A) : A);
+    };
+    for (int n = 0;; ++n) {
+        const int i = i0 + n * kThreads * kBatch + tid;
+        uint4 next[kBatch];
+        if (n + 1 < kGradBatches) {
+#pragma unroll
+            for (int q = 0; q < kBatch; ++q) next[q] = load(i + (kBatch + q) * kThreads);
         }
 #pragma unroll
-        for (int e = 0; e < VW; ++e) x[e] = __fdiv_rn(grad(x[e]), a.T);
-        if (whole) {
-            const uint4 y = E::pack(x);
-            *(reinterpret_cast<uint4*>(out - to.skew) + i) = y;
-        } else {
+        for (int q = 0; q < kBatch; ++q) {
+            const int k = i + q * kThreads;
+            if (k >= i1 || !fast(k)) continue;
+            float f[VW];
+            E::unpack(x[q], f);
 #pragma unroll
-            for (int e = 0; e < VW; ++e) {
-                const int v = i * VW + e - to.skew;
-                if (v >= 0 && v < a.V) out[v] = E::from(x[e]);
-            }
+            for (int e = 0; e < VW; ++e) f[e] = grad(f[e]);
+            to16[k] = E::pack(f);
         }
+        if (n + 1 == kGradBatches) break;
+#pragma unroll
+        for (int q = 0; q < kBatch; ++q) x[q] = next[q];
+    }
+    if (tid < 4 * VW) {
+        const int n = tid / VW, i = n < 2 ? n : to.vectors - 4 + n;
+        const int v = i * VW + tid % VW - to.skew;
+        if (i >= i0 && i < i1 && (n < 2 || i > 1) && !fast(i) && v >= 0 && v < a.V)
+            out[v] = E::from(grad(E::get(from.row + v)));
     }
     __syncthreads();
-    if (mine) {
+    if (mine && !bad) {
         float g = 0.0f;
         for (int k = 0; k < a.given; ++k) {
             if (s_token[k] != token) continue;
-            if (k < tid) mine = false;
+            if (k < tid) mine = false;  // an equal one before it writes
             g += s_g[k];
         }
-        if (mine) out[token] = E::from(__fdiv_rn(grad(own) + g, a.T));
+        if (mine) out[token] = E::from(grad(own) + __fdiv_rn(g, a.T));
     }
 }
 
@@ -540,9 +643,13 @@ static sv_status check_rows(const void* logits, sv_dtype dtype, int64_t stride,
     return SV_OK;
 }
 
-// log2(e) / T, a float for the smallest T too (0 times infinity is NaN).
-static float base2(float T) {
-    return (float)std::fmin(1.4426950408889634 / T, (double)FLT_MAX);
+// log2(e) / T as a sum of two floats, the second positive, so that it may be multiplied with
+// -infinity too; for the smallest T the largest float (0 times infinity is NaN).
+static void base2(float T, float* high, float* low) {
+    const double c = std::fmin(1.4426950408889634 / T, (double)FLT_MAX);
+    *high = (float)c;
+    while (!((double)*high < c)) *high = std::nextafterf(*high, 0.0f);
+    *low = std::fmax((float)(c - *high), std::nextafterf(0.0f, 1.0f));
 }
 
 template <typename K, typename A>
@@ -593,13 +700,21 @@ sv_status spec_logprobs(const void* logits, sv_dtype dtype, int64_t row_stride,
     if (rows == 0) return SV_OK;
     int sms;
     if ((st = device_ok(&sms)) != SV_OK) return st;
-    const Args a = {logits, row_stride, tokens, T, base2(T), V, given, top, logprobs, normalizer,
-                    entropy, top_tokens, top_logprobs, status};
+    Args a = {logits, row_stride, tokens, T, 0.0f, 0.0f, V, given, top, logprobs, normalizer,
+              entropy, top_tokens, top_logprobs, status};
+    base2(T, &a.c, &a.c_low);
     int G = 1;
     while (G < kMaxCluster && (long long)rows * G < 4 * sms && V / G >= 16384) G *= 2;
     const long long ctas = (long long)rows * G;
-    return dtype == SV_BF16 ? launch(lp_kernel<__nv_bfloat16>, ctas, G, stream, a)
-                            : launch(lp_kernel<float>, ctas, G, stream, a);
+    auto typed = [&](auto t) {
+        using E = decltype(t);
+        if (entropy)
+            return top ? launch(lp_kernel<E, true, true>, ctas, G, stream, a)
+                       : launch(lp_kernel<E, true, false>, ctas, G, stream, a);
+        return top ? launch(lp_kernel<E, false, true>, ctas, G, stream, a)
+                   : launch(lp_kernel<E, false, false>, ctas, G, stream, a);
+    };
+    return dtype == SV_BF16 ? typed(__nv_bfloat16()) : typed(0.0f);
 }
 
 sv_status spec_logprobs_grad(const void* logits, sv_dtype dtype, int64_t row_stride,
@@ -622,13 +737,24 @@ sv_status spec_logprobs_grad(const void* logits, sv_dtype dtype, int64_t row_str
     if (rows == 0) return SV_OK;
     int sms;
     if ((st = device_ok(&sms)) != SV_OK) return st;
-    const int part = kThreads * 64;  // elements
-    const GradArgs a = {logits, grad_logits, row_stride, grad_stride, tokens, normalizer, entropy,
-                        grad_logprobs, grad_entropy, T, V, given, (V + part - 1) / part, status};
+    // (of vectors; a row may begin inside of one)
+    const int width = dtype == SV_BF16 ? 8 : 4, part = kThreads * kBatch * kGradBatches;
+    GradArgs a = {logits, grad_logits, row_stride, grad_stride, tokens, normalizer, entropy,
+                  grad_logprobs, grad_entropy, T, 0.0f, 0.0f, V, given,
+                  ((V + width - 1 + width - 1) / width + part - 1) / part, status};
+    base2(T, &a.c, &a.c_low);
     const long long ctas = (long long)rows * a.parts;
     if (ctas >= (1ll << 31)) return SV_ERR_UNSUPPORTED;
-    return dtype == SV_BF16 ? launch(lp_grad_kernel<__nv_bfloat16>, ctas, 1, stream, a)
-                            : launch(lp_grad_kernel<float>, ctas, 1, stream, a);
+    const bool shift = rows > 1 && (row_stride - grad_stride) % width != 0;
+    auto typed = [&](auto t) {
+        using E = decltype(t);
+        if (grad_entropy)
+            return shift ? launch(lp_grad_kernel<E, true, true>, ctas, 1, stream, a)
+                         : launch(lp_grad_kernel<E, true, false>, ctas, 1, stream, a);
+        return shift ? launch(lp_grad_kernel<E, false, true>, ctas, 1, stream, a)
+                     : launch(lp_grad_kernel<E, false, false>, ctas, 1, stream, a);
+    };
+    return dtype == SV_BF16 ? typed(__nv_bfloat16()) : typed(0.0f);
 }
 
 }  // extern "C"
