@@ -518,8 +518,8 @@ __device__ __forceinline__ int low_of(const AttentionArgs& a, const Share& sh, i
 }
 // Whether a row with these ancestors and this window looks at slot s of the sequence's.
 template <bool WINDOW>
-__device__ __forceinline__ bool looks(const AttentionArgs& a, const Share& sh, uint64_t anc, int low,
-                                      int s) {
+__device__ __forceinline__ bool looks(const AttentionArgs& a, const Share& sh, uint64_t anc,
+                                      int low, int s) {
     const int i = s - sh.len;
     if (WINDOW && i <= 0) return s < a.sinks || s >= low;
     return i < sh.n && (i <= 0 || sees(anc, i));
@@ -808,7 +808,8 @@ __global__ void __launch_bounds__(kSplitThreads * WM, 2) kv_split_kernel(const A
 #pragma unroll
                 for (int half = 0; half < 2; ++half) {
                     const int R = mt * ROWS + wm * 16 + half * 8 + (lane >> 2);
-                    const int j = min(R / a.group, sh.n - 1), low = low_of(a, sh, s_deep[WINDOW ? j : 0]);
+                    const int j = min(R / a.group, sh.n - 1);
+                    const int low = low_of(a, sh, s_deep[WINDOW ? j : 0]);
                     const uint64_t anc = s_anc[j];
 #pragma unroll
                     for (int k = 0; k < 4; ++k)

@@ -13,13 +13,12 @@
 
 namespace svlp {
 
-constexpr int kThreads = 256;
-constexpr int kWarps = kThreads / 32;
-constexpr int kBatch = 4;        // 16-byte vectors of a thread in flight
+constexpr int kThreads = 256;    // of the gradient's CTAs
+constexpr int kBatch = 4;        // 16-byte vectors of a thread in flight there
 constexpr int kMaxV = 1 << 21;
 constexpr int kMaxGiven = SV_LOGPROBS_MAX_GIVEN;
 constexpr int kMaxTop = SV_LOGPROBS_MAX_TOP;
-constexpr int kPairs = kThreads / 2;
+constexpr int kGroups = 128;     // of threads, whose largest elements make the alternatives' bound
 constexpr int kCandidates = 1024;
 constexpr int kMaxCluster = 8;
 
@@ -47,6 +46,18 @@ __device__ __forceinline__ uint4 ld_own16(const uint4* p) {
     asm volatile("ld.global.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
                  : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p) : "memory");
     return v;
+}
+// A 64-bit word of shared memory, and two of them from a 16-byte boundary.
+__device__ __forceinline__ uint64_t lds64(uint32_t at) {
+    uint64_t x;
+    asm volatile("ld.shared.u64 %0, [%1];" : "=l"(x) : "r"(at) : "memory");
+    return x;
+}
+__device__ __forceinline__ void lds64x2(uint64_t* x, uint32_t at) {
+    asm volatile("ld.shared.v2.u64 {%0, %1}, [%2];" : "=l"(x[0]), "=l"(x[1]) : "r"(at) : "memory");
+}
+__device__ __forceinline__ void sts64(uint32_t at, uint64_t x) {
+    asm volatile("st.shared.u64 [%0], %1;" ::"r"(at), "l"(x) : "memory");
 }
 __device__ __forceinline__ int cluster_rank() {
     int r;
@@ -226,66 +237,92 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
 __device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
 
 // A cluster of CTAs per row, each with an equal run of its vectors, read once with the running
-// maximum and sums of a softmax; joined through distributed shared memory.
+// maximum and sums of a softmax; joined through distributed shared memory.  A thread's vectors come
+// through a ring of its own in shared memory (asynchronous 16-byte copies), so that many are on
+// their way whatever the registers hold, and the CTAs of an SM hide each other's beginnings and
+// ends.
 //
-// Alternatives.  Each thread knows its largest element and the vector that it is in.  Of the
-// maxima of pairs of threads the top-th is a bound: as many elements are at or above it, and
-// these are in the vectors of the threads whose own maximum reaches it, about as many again.  Only
-// those threads' vectors are read a second time (by their warp, from L2), the elements that reach
-// the bound are put in order by counting, and rank 0 joins the lists of the cluster's CTAs.
+// Alternatives.  Each thread knows its largest element, the batch of vectors that it is in and the
+// largest element of its others.  Of the largest elements of 128 groups of threads the top-th is a
+// bound: as many elements are at or above it, and these are in the batches of the threads whose
+// own maximum reaches it, about as many again.  Those threads look into their batch again, and
+// where another of theirs reaches the bound too, their warp goes through all of them.  The elements
+// that reach the bound are put in order by counting, and rank 0 joins the lists of the cluster's
+// CTAs.
+//
+// Measured: 4096 rows of 128256 in bf16 without entropy and alternatives 157 us, 6.7 TB/s (memory);
+// with the entropy 167 us, with it and 20 alternatives 205 us (instructions: the second product per
+// element, and a warp's turn of many small steps at the end of each row).  Stages of two vectors
+// instead of four, five CTAs per SM: 162, 178 and 220 us; 128 threads: 160, 164 and 211 us, but 32
+// instead of 24 us for nine rows of 256000 with five alternatives by one CTA each.
+constexpr int kLpThreads = 256, kLpWarps = kLpThreads / 32;
+constexpr int kLpBatch = 4;      // vectors of a thread per stage
+constexpr int kLpStages = 3;
+constexpr int kLpResident = 4;   // CTAs per SM
+constexpr int kLpRing = kLpStages * kLpBatch * kLpThreads * 16;  // bytes
+
 template <typename T, bool ENTROPY, bool TOP>
-__global__ void __launch_bounds__(kThreads, 4) lp_kernel(const Args a) {
+__global__ void __launch_bounds__(kLpThreads, kLpResident) lp_kernel(const Args a) {
     using E = Elt<T>;
-    constexpr int VW = E::kVec;
-    __shared__ Stats s_warp[kWarps], s_stats;
-    __shared__ uint64_t s_pair[kPairs], s_top[kMaxTop], s_bound, s_cand[kCandidates];
+    constexpr int VW = E::kVec, B = kLpBatch, S = kLpStages;
+    extern __shared__ __align__(16) uint64_t s_mem[];  // the ring; then candidates
+    __shared__ __align__(16) uint64_t s_group[kGroups];
+    __shared__ uint64_t s_top[kMaxTop], s_bound;
+    __shared__ Stats s_warp[kLpWarps], s_stats;
     __shared__ int s_count;
+    static_assert(kLpRing >= kCandidates * 8 && 32 % B == 0, "candidates in the ring");
     const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
-    const int G = cluster_size(), rank = cluster_rank(), r = blockIdx.x / G;
+    const int G = cluster_size(), rank = cluster_rank();
+    const int r = blockIdx.x / G;
 
     int token = -1;
     if (tid < a.given) token = a.tokens[(long long)r * a.given + tid];
     if (!__syncthreads_or(token != -1)) return;  // (the whole cluster)
     const Row<T> row((const T*)a.logits + r * a.stride, a.V);
-    const int i0 = (int)((long long)row.vectors * rank / G);
-    const int i1 = (int)((long long)row.vectors * (rank + 1) / G);
-    const uint4 none = make_uint4(E::kLowest, E::kLowest, E::kLowest, E::kLowest);
-
-    Stats st = {-INFINITY, 0.0f, 0.0f};
-    int best = i0 + tid;  // the vector that holds this thread's first maximum
-    uint4 v[kBatch];
+    // whole vectors here; the two that the row may share with others by a thread each
+    const int w0 = row.skew != 0, w1 = (a.V + row.skew) / VW, whole = max(w1 - w0, 0);
+    const int i0 = w0 + (int)((long long)whole * rank / G);
+    const int i1 = w0 + (int)((long long)whole * (rank + 1) / G);
+    const uint32_t cand = (uint32_t)__cvta_generic_to_shared(s_mem), ring = cand + tid * 16;
+    const uint32_t group = (uint32_t)__cvta_generic_to_shared(s_group);
+    auto issue = [&](int n, int slot) {
 #pragma unroll
-    for (int q = 0; q < kBatch; ++q) {
-        const int k = i0 + tid + q * kThreads;
-        v[q] = k < i1 ? row.load(k) : none;
-    }
+        for (int q = 0; q < B; ++q) {
+            const int k = i0 + tid + (n * B + q) * kLpThreads;
+            if (k < i1)
+                asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(
+                    ring + (slot * B + q) * kLpThreads * 16), "l"(row.at(k)) : "memory");
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+#pragma unroll
+    for (int n = 0; n < S - 1; ++n) issue(n, n);
     const bool known = token >= 0 && token < a.V;
     const float given = rank == 0 && known ? E::get(row.row + token) : 0.0f;
-    for (int i = i0 + tid; i < i1; i += kThreads * kBatch) {
-        uint4 next[kBatch];
+
+    // The warp's reference and this thread's sums; its largest element, the batch of vectors that
+    // holds it first, and the largest element of its other batches.
+    Stats st = {-INFINITY, 0.0f, 0.0f};
+    float mine = -INFINITY, next = -INFINITY;
+    int best = 0;
+    auto take = [&](const uint4 (&v)[B], int n) {
+        float most = E::largest(v[0]);
 #pragma unroll
-        for (int q = 0; q < kBatch; ++q) {
-            const int k = i + (kBatch + q) * kThreads;
-            next[q] = k < i1 ? row.load(k) : none;
+        for (int q = 1; q < B; ++q) most = fmaxf(most, E::largest(v[q]));
+        if (TOP) {
+            best = most > mine ? n : best;
+            next = fmaxf(next, fminf(most, mine));
+            mine = fmaxf(mine, most);
         }
-        float top[kBatch];
+        if (__any_sync(~0u, most > st.m)) {  // all lanes follow the largest of theirs
 #pragma unroll
-        for (int q = 0; q < kBatch; ++q) top[q] = E::largest(v[q]);
-        float most = top[0];
-#pragma unroll
-        for (int q = 1; q < kBatch; ++q) most = fmaxf(most, top[q]);
-        if (most > st.m) {
-            if (TOP) {
-#pragma unroll
-                for (int q = kBatch - 1; q >= 0; --q)
-                    if (top[q] == most) best = i + q * kThreads;
-            }
+            for (int k = 16; k; k >>= 1) most = fmaxf(most, __shfl_xor_sync(~0u, most, k));
             add(st, Stats{most, 0.0f, 0.0f}, a.c);
         }
         const float2 less = both(st.m == -INFINITY ? 0.0f : -st.m);
         float2 s = make_float2(0.0f, 0.0f), u = s;
 #pragma unroll
-        for (int q = 0; q < kBatch; ++q) {
+        for (int q = 0; q < B; ++q) {
             float x[VW];
             E::unpack(v[q], x);
 #pragma unroll
@@ -304,103 +341,173 @@ __global__ void __launch_bounds__(kThreads, 4) lp_kernel(const Args a) {
         }
         st.s += s.x + s.y;
         st.u += u.x + u.y;
+    };
+    const uint4 none = make_uint4(E::kLowest, E::kLowest, E::kLowest, E::kLowest);
+    const int stages = (i1 - i0 + B * kLpThreads - 1) / (B * kLpThreads);
+    // (the shared vectors: the first thread's batch before its others, the last one's behind)
+    const bool head = rank == 0 && w0 == 1;
+    const bool tail = rank == G - 1 && row.vectors > max(w0, w1);
+    if (head && w == 0) {
+        uint4 v[B];
 #pragma unroll
-        for (int q = 0; q < kBatch; ++q) v[q] = next[q];
+        for (int q = 0; q < B; ++q) v[q] = none;
+        if (tid == 0) v[0] = row.load(0);
+        take(v, -1);
     }
-    const float mine = st.m;
+    int slot = 0;
+    for (int n = 0; n < stages; ++n) {
+        asm volatile("cp.async.wait_group %0;" ::"n"(S - 2) : "memory");
+        uint4 v[B];
+#pragma unroll
+        for (int q = 0; q < B; ++q) {
+            v[q] = none;
+            if (i0 + tid + (n * B + q) * kLpThreads < i1)
+                asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
+                             : "=r"(v[q].x), "=r"(v[q].y), "=r"(v[q].z), "=r"(v[q].w)
+                             : "r"(ring + (slot * B + q) * kLpThreads * 16) : "memory");
+        }
+        // (into the place of the stage before this one)
+        issue(n + S - 1, slot == 0 ? S - 1 : slot - 1);
+        slot = slot == S - 1 ? 0 : slot + 1;
+        take(v, n);
+    }
+    asm volatile("cp.async.wait_all;" ::: "memory");
+    if (tail && w == kLpWarps - 1) {
+        uint4 v[B];
+#pragma unroll
+        for (int q = 0; q < B; ++q) v[q] = none;
+        if (tid == kLpThreads - 1) v[0] = row.load(row.vectors - 1);
+        take(v, stages);
+    }
 #pragma unroll
     for (int k = 16; k; k >>= 1) {
-        Stats o;
-        o.m = __shfl_xor_sync(~0u, st.m, k);
-        o.s = __shfl_xor_sync(~0u, st.s, k);
-        o.u = __shfl_xor_sync(~0u, st.u, k);
-        add(st, o, a.c);
+        st.s += __shfl_xor_sync(~0u, st.s, k);
+        if (ENTROPY) st.u += __shfl_xor_sync(~0u, st.u, k);
     }
     if (lane == 0) s_warp[w] = st;
-    uint64_t key = 0;
+    // The first and the last vector of batch n of thread t.
+    auto first_of = [&](int t, int n) {
+        return n < 0 ? 0 : n == stages ? row.vectors - 1 : i0 + t + n * B * kLpThreads;
+    };
+    bool some = false;  // whether this thread has had elements of the row
+    // Threads per group: few groups are quicker to put in order, and bring few elements more than
+    // are wanted (24 of 64 groups: about 30).
+    const int share = a.top <= 24 ? 2 * kLpThreads / kGroups : kLpThreads / kGroups;
     if (TOP) {
-        // (the last place of the vector: nothing that equals the maximum is left out)
-        if (i0 + tid < i1) key = key_of(mine, min(best * VW + VW - 1 - row.skew, a.V - 1));
-        const uint64_t other = __shfl_xor_sync(~0u, key, 1);
-        if (!(tid & 1)) s_pair[tid >> 1] = key > other ? key : other;
+        some = i0 + tid < i1 || (head && tid == 0) || (tail && tid == kLpThreads - 1);
+        if (mine == -INFINITY) best = head && tid == 0 ? -1 : i0 + tid < i1 ? 0 : stages;
+        // As many elements as there are groups are at or above their largest elements' keys, of
+        // which the last place of the batch is known only.
+        const int end = first_of(tid, best) + (best < 0 || best == stages ? 0 : B - 1) * kLpThreads;
+        uint64_t largest = some ? key_of(mine, min(min(end, row.vectors) * VW + VW - 1 - row.skew,
+                                                   a.V - 1)) : 0;
+        for (int k = 1; k < share; k *= 2) {
+            const uint64_t o = __shfl_xor_sync(~0u, largest, k);
+            largest = o > largest ? o : largest;
+        }
+        if (tid % share == 0) s_group[tid / share] = largest;
         if (tid < kMaxTop) s_top[tid] = 0;
         if (tid == 0) s_bound = 0, s_count = 0;
     }
     __syncthreads();
-    if (tid == kThreads - 1) {
-        Stats t = s_warp[0];
-        for (int k = 1; k < kWarps; ++k) add(t, s_warp[k], a.c);
-        s_stats = t;
+    if (w == kLpWarps - 1) {
+        Stats t = s_warp[lane % kLpWarps];
+#pragma unroll
+        for (int k = kLpWarps / 2; k; k >>= 1) {
+            Stats o;
+            o.m = __shfl_xor_sync(~0u, t.m, k);
+            o.s = __shfl_xor_sync(~0u, t.s, k);
+            o.u = __shfl_xor_sync(~0u, t.u, k);
+            add(t, o, a.c);
+        }
+        if (lane == 0) s_stats = t;
     }
     if (TOP) {
-        if (tid < kPairs) {
-            const uint64_t p = s_pair[tid];
-            int above = 0;
+        // a group's place among all: counted by its threads, a share of the groups each
+        const int part = kLpThreads / share / share / 2;
+        const uint64_t p = lds64(group + tid / share * 8);
+        int places = 0;  // how many are above, and (from bit 16 on) how many are not below
 #pragma unroll 8
-            for (int k = 0; k < kPairs; ++k) above += s_pair[k] > p;
-            if (p && above == a.top - 1) s_bound = p;
-        }
-        __syncthreads();
-        const uint64_t bound = s_bound;
-        // Vectors of the threads whose maximum reaches the bound.
-        const int per = (i1 - i0 + kThreads - 1) / kThreads;
-        for (uint32_t reach = __ballot_sync(~0u, key && key >= bound); reach; reach &= reach - 1) {
-            const int t = (w << 5) + __ffs(reach) - 1;
-            for (int j = lane; j < per; j += 32) {
-                const int i = i0 + t + j * kThreads;
-                if (i >= i1) continue;
-                float x[VW];
-                E::unpack(row.load(i), x);
+        for (int k = 0; k < part; ++k) {
+            uint64_t o[2];
+            lds64x2(o, group + (tid % share * part + k) * 16);
 #pragma unroll
-                for (int e = 0; e < VW; ++e) {
-                    const int at = i * VW + e - row.skew;
-                    if (at < 0 || at >= a.V) continue;
-                    const uint64_t k = key_of(x[e], at);
-                    if (k < bound) continue;
-                    const int n = atomicAdd(&s_count, 1);
-                    if (n < kCandidates) s_cand[n] = k;
+            for (int e = 0; e < 2; ++e) places += (o[e] > p ? 1 : 0) + (o[e] >= p ? 1 << 16 : 0);
+        }
+        for (int k = 1; k < share; k *= 2) places += __shfl_xor_sync(~0u, places, k);
+        // (equal keys: of threads whose batches end with the row)
+        if (p && (places & 0xffff) < a.top && places >> 16 >= a.top) s_bound = p;
+        // What nothing has to be looked for below; the elements that reach it; where they are more
+        // than there is room for (many that are equal, or large ones that lie together), the top-th
+        // of those that found room is the next, higher bound.
+        const uint64_t highest =
+            some ? key_of(mine, max(first_of(tid, best) * VW - row.skew, 0)) : 0;
+        for (;;) {
+            __syncthreads();
+            const uint64_t bound = s_bound;
+            auto look = [&](float x, int at) {
+                const uint64_t k = key_of(x, at);
+                if (k < bound) return;
+                const int n = atomicAdd(&s_count, 1);
+                if (n < kCandidates) sts64(cand + n * 8, k);
+            };
+            const bool reaches = some && highest >= bound;
+            const bool more = reaches && ordered(next) >= (uint32_t)(bound >> 32);
+            // a lane per element of the batches that have to be looked into
+#pragma unroll 1
+            for (uint32_t few = __ballot_sync(~0u, reaches && !more); few; few &= few - 1) {
+                const int t = __ffs(few) - 1, n = __shfl_sync(~0u, best, t);
+                const bool one = n < 0 || n == stages;
+#pragma unroll
+                for (int e = lane; e < B * VW; e += 32) {
+                    const int i = first_of(w * 32 + t, n) + e / VW * kLpThreads;
+                    const int at = i * VW + e % VW - row.skew;
+                    if (at >= 0 && at < a.V && (one ? e < VW : i < i1))
+                        look(E::get(row.row + at), at);
                 }
             }
-        }
-        __syncthreads();
-        const int n = s_count;
-        if (n <= kCandidates) {
-            for (int i = tid; i < n; i += kThreads) {
-                const uint64_t k = s_cand[i];
-                int above = 0;
-                for (int j = 0; j < n; ++j) above += s_cand[j] > k;
-                if (above < a.top) s_top[above] = k;
-            }
-        } else {
-            // Large elements that lie together, many more than are wanted: the whole run again for
-            // each of them.
-            uint64_t last = ~0ull;
-            for (int out = 0; out < a.top; ++out) {
-                uint64_t most = 0;
-                for (int i = i0 + tid; i < i1; i += kThreads) {
+            // and of those threads' vectors that have more than one
+#pragma unroll 1
+            for (uint32_t all = __ballot_sync(~0u, more); all; all &= all - 1) {
+                const int t = w * 32 + __ffs(all) - 1;
+                const int edge = head && t == 0                ? 0
+                                 : tail && t == kLpThreads - 1 ? row.vectors - 1
+                                                               : -1;
+                if (edge >= 0 && lane < VW) {
+                    const int at = edge * VW + lane - row.skew;
+                    if (at >= 0 && at < a.V) look(E::get(row.row + at), at);
+                }
+#pragma unroll 1
+                for (int i = i0 + t + lane * kLpThreads; i < i1; i += 32 * kLpThreads) {
                     float x[VW];
-                    E::unpack(row.load(i), x);
+                    E::unpack(ld_stream16(row.at(i)), x);
 #pragma unroll
-                    for (int e = 0; e < VW; ++e) {
-                        const int at = i * VW + e - row.skew;
-                        const uint64_t k = at < 0 || at >= a.V ? 0 : key_of(x[e], at);
-                        if (k < last && k > most) most = k;
-                    }
+                    for (int e = 0; e < VW; ++e) look(x[e], i * VW + e - row.skew);
                 }
-                for (int k = 16; k; k >>= 1) {
-                    const uint64_t o = __shfl_xor_sync(~0u, most, k);
-                    most = o > most ? o : most;
-                }
-                if (lane == 0) s_pair[w] = most;
-                __syncthreads();
-                for (int k = 0; k < kWarps; ++k) most = s_pair[k] > most ? s_pair[k] : most;
-                if (tid == 0) s_top[out] = most;
-                last = most;
-                __syncthreads();
             }
+            __syncthreads();
+            const int n = s_count, here = min(n, kCandidates);
+            // eight threads count for each
+            const int sub = tid % 8;
+            for (int i0 = 0; i0 < here; i0 += kLpThreads / 8) {
+                const int i = i0 + tid / 8;
+                const uint64_t k = i < here ? lds64(cand + i * 8) : 0;
+                int before = 0;
+#pragma unroll 4
+                for (int j = sub; j < here; j += 8) before += lds64(cand + j * 8) > k;
+#pragma unroll
+                for (int x = 1; x < 8; x *= 2) before += __shfl_xor_sync(~0u, before, x);
+                if (sub || i >= here) continue;
+                if (n <= kCandidates && before < a.top) s_top[before] = k;
+                if (n > kCandidates && before == a.top - 1) s_bound = k;
+            }
+            if (n <= kCandidates) break;
+            __syncthreads();
+            if (tid == 0) s_count = 0;
         }
     }
-    cluster_sync();
+    if (G > 1) cluster_sync();
+    else __syncthreads();
     if (rank == 0) {
         Stats t = s_stats;
         for (int k = 1; k < G; ++k) add(t, *cluster_at(&s_stats, k), a.c);
@@ -416,39 +523,45 @@ __global__ void __launch_bounds__(kThreads, 4) lp_kernel(const Args a) {
             reinterpret_cast<float2*>(a.normalizer)[r] = make_float2(m, log_s);
         if (ENTROPY && tid == 0) a.entropy[r] = log_s - __fdiv_rn(t.u, t.s * a.T);
         const long long out = (long long)r * a.top;
-        for (int i = (bad ? 0 : a.V) + tid; TOP && i < a.top; i += kThreads) {
+        for (int i = (bad ? 0 : a.V) + tid; TOP && i < a.top; i += kLpThreads) {
             a.top_tokens[out + i] = -1;
             a.top_logprobs[out + i] = bad ? NAN : -INFINITY;
         }
         if (TOP && !bad) {
-            // the lists side by side; an element's place is its place in its own list and how
-            // many of each other one are above it
-            const int all = G * a.top;
-            for (int i = tid; i < all; i += kThreads)
-                s_cand[i] = *cluster_at(&s_top[i % a.top], i / a.top);
-            __syncthreads();
-            for (int i = tid; i < all; i += kThreads) {
-                const uint64_t k = s_cand[i];
-                const int list = i / a.top;
-                int above = i % a.top;
-                for (int q = 0; q < G; ++q) {
-                    if (q == list) continue;
-                    int lo = 0, hi = a.top;  // how many of list q are above
-                    while (lo < hi) {
-                        const int mid = (lo + hi) / 2;
-                        if (s_cand[q * a.top + mid] > k) lo = mid + 1;
-                        else hi = mid;
-                    }
-                    above += lo;
-                }
-                if (!k || above >= a.top) continue;
-                a.top_tokens[out + above] = place_of(k);
-                a.top_logprobs[out + above] =
+            auto tell = [&](int place, uint64_t k) {
+                a.top_tokens[out + place] = place_of(k);
+                a.top_logprobs[out + place] =
                     __fdiv_rn(from_ordered((uint32_t)(k >> 32)) - m, a.T) - log_s;
+            };
+            if (G == 1) {
+                if (tid < min(a.top, a.V)) tell(tid, s_top[tid]);
+            } else {
+                // the lists side by side; an element's place is its place in its own list and how
+                // many of each other one are above it
+                const int all = G * a.top;
+                for (int i = tid; i < all; i += kLpThreads)
+                    sts64(cand + i * 8, *cluster_at(&s_top[i % a.top], i / a.top));
+                __syncthreads();
+                for (int i = tid; i < all; i += kLpThreads) {
+                    const uint64_t k = lds64(cand + i * 8);
+                    const int list = i / a.top;
+                    int before = i % a.top;
+                    for (int q = 0; q < G; ++q) {
+                        if (q == list) continue;
+                        int lo = 0, hi = a.top;  // how many of list q are above
+                        while (lo < hi) {
+                            const int mid = (lo + hi) / 2;
+                            if (lds64(cand + (q * a.top + mid) * 8) > k) lo = mid + 1;
+                            else hi = mid;
+                        }
+                        before += lo;
+                    }
+                    if (k && before < a.top) tell(before, k);
+                }
             }
         }
     }
-    cluster_sync();  // nobody leaves while its share is being read
+    if (G > 1) cluster_sync();  // nobody leaves while its share is being read
 }
 
 // ---------------------------------------------------------------- gradient
@@ -470,7 +583,8 @@ struct GradArgs {
 constexpr int kGradBatches = 2;  // of kBatch vectors per thread: a CTA's part of a row
 
 // Elements o .. o + kVec - 1 of two vectors side by side.
-template <typename T> __device__ __forceinline__ uint4 shifted(const uint4& a, const uint4& b, int o) {
+template <typename T>
+__device__ __forceinline__ uint4 shifted(const uint4& a, const uint4& b, int o) {
     constexpr int kPer = 4 / sizeof(T);  // elements per word
     uint32_t w[5];
     switch (o / kPer) {
@@ -488,8 +602,8 @@ template <typename T> __device__ __forceinline__ uint4 shifted(const uint4& a, c
 
 // A part of a row per CTA: each logit read once, its gradient written once, in vectors of the
 // gradient's row (where the logits lie at another place of a 16-byte word: two of theirs, shifted
-// together: SHIFT).  With x = (l - m) / T in base 2 and less ln S, p = 2^x, a gradient is p (A + B x): A
-// and B are the row's.  Then the places of given tokens again, with their own share (their logits
+// together: SHIFT).  With x = (l - m) / T in base 2 and less ln S, p = 2^x, a gradient is
+// p (A + B x): A and B are the row's.  Then the places of given tokens again, with their own share (their logits
 // are read before anything is written, so that the gradient may take the logits' place).
 template <typename T, bool ENTROPY, bool SHIFT>
 __global__ void __launch_bounds__(kThreads, 4) lp_grad_kernel(const GradArgs a) {
@@ -519,7 +633,8 @@ __global__ void __launch_bounds__(kThreads, 4) lp_grad_kernel(const GradArgs a) 
         }
         return;
     }
-    const int off = SHIFT ? from.skew - to.skew : 0, by = off < 0 ? off + VW : off;  // shift of a vector
+    // how much further into a vector the logits' elements lie, and in which of two vectors
+    const int off = SHIFT ? from.skew - to.skew : 0, by = off < 0 ? off + VW : off;
     const int back = off < 0 ? 1 : 0;
     // Vectors that lie wholly in the row, as what they are made of does; the others, two at each
     // end at most, go element by element.
@@ -608,6 +723,16 @@ __global__ void __launch_bounds__(kThreads, 4) lp_grad_kernel(const GradArgs a) 
 
 static bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
 
+// The ring of lp_kernel is more than a kernel gets unasked.
+template <typename T> static bool lp_setup() {
+    bool ok = true;
+    for (auto k : {lp_kernel<T, false, false>, lp_kernel<T, false, true>, lp_kernel<T, true, false>,
+                   lp_kernel<T, true, true>})
+        ok = ok && cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, kLpRing) ==
+                       cudaSuccess;
+    return ok;
+}
+
 static sv_status device_ok(int* sms) {
     static std::mutex mu;
     static int known[64];  // 0 unknown, -1 another device
@@ -623,6 +748,7 @@ static sv_status device_ok(int* sms) {
         if (major == 10 && minor == 3 &&
             cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
             return SV_ERR_CUDA;
+        if (n > 0 && !(lp_setup<__nv_bfloat16>() && lp_setup<float>())) return SV_ERR_CUDA;
         known[dev] = n;
     }
     if (known[dev] < 0) return SV_ERR_UNSUPPORTED;
@@ -653,14 +779,16 @@ static void base2(float T, float* high, float* low) {
 }
 
 template <typename K, typename A>
-static sv_status launch(K kernel, long long ctas, int cluster, cudaStream_t stream, const A& a) {
+static sv_status launch(K kernel, int threads, int smem, long long ctas, int cluster,
+                        cudaStream_t stream, const A& a) {
     cudaLaunchAttribute attr;
     attr.id = cudaLaunchAttributeClusterDimension;
     attr.val.clusterDim.x = cluster;
     attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)ctas);
-    cfg.blockDim = dim3(kThreads);
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
     cfg.attrs = &attr;
     cfg.numAttrs = cluster > 1 ? 1 : 0;
@@ -703,16 +831,23 @@ sv_status spec_logprobs(const void* logits, sv_dtype dtype, int64_t row_stride,
     Args a = {logits, row_stride, tokens, T, 0.0f, 0.0f, V, given, top, logprobs, normalizer,
               entropy, top_tokens, top_logprobs, status};
     base2(T, &a.c, &a.c_low);
+    // A cluster per row while its CTAs have SMs of their own and runs worth a CTA's beginning and
+    // end (9 rows of 256000, 5 alternatives: G = 1 20.4 us, 2 16.5, 4 14.5, 8 14.2; 40 of 128256:
+    // 16.6, 16.0, 16.6, 18.5; 5 of 32000: 8.5, 10.4).  More rows: a CTA each (300 of 65537: 20.7 us,
+    // two each 24.8; 1024 of 32000: 26.9 and 45.1), but two each where all would be resident at
+    // once and the rows that hold tokens met on some SMs by chance (576 of 151936, half of them
+    // without tokens: 41 and 32 us; all with tokens: 45 and 55).
     int G = 1;
-    while (G < kMaxCluster && (long long)rows * G < 4 * sms && V / G >= 16384) G *= 2;
+    while (G < kMaxCluster && 2ll * rows * G <= sms && V / G >= 49152) G *= 2;
+    if (rows > 2 * sms && rows < kLpResident * sms && V >= 65536) G = 2;
     const long long ctas = (long long)rows * G;
     auto typed = [&](auto t) {
         using E = decltype(t);
         if (entropy)
-            return top ? launch(lp_kernel<E, true, true>, ctas, G, stream, a)
-                       : launch(lp_kernel<E, true, false>, ctas, G, stream, a);
-        return top ? launch(lp_kernel<E, false, true>, ctas, G, stream, a)
-                   : launch(lp_kernel<E, false, false>, ctas, G, stream, a);
+            return top ? launch(lp_kernel<E, true, true>, kLpThreads, kLpRing, ctas, G, stream, a)
+                       : launch(lp_kernel<E, true, false>, kLpThreads, kLpRing, ctas, G, stream, a);
+        return top ? launch(lp_kernel<E, false, true>, kLpThreads, kLpRing, ctas, G, stream, a)
+                   : launch(lp_kernel<E, false, false>, kLpThreads, kLpRing, ctas, G, stream, a);
     };
     return dtype == SV_BF16 ? typed(__nv_bfloat16()) : typed(0.0f);
 }
@@ -749,10 +884,10 @@ sv_status spec_logprobs_grad(const void* logits, sv_dtype dtype, int64_t row_str
     auto typed = [&](auto t) {
         using E = decltype(t);
         if (grad_entropy)
-            return shift ? launch(lp_grad_kernel<E, true, true>, ctas, 1, stream, a)
-                         : launch(lp_grad_kernel<E, true, false>, ctas, 1, stream, a);
-        return shift ? launch(lp_grad_kernel<E, false, true>, ctas, 1, stream, a)
-                     : launch(lp_grad_kernel<E, false, false>, ctas, 1, stream, a);
+            return shift ? launch(lp_grad_kernel<E, true, true>, kThreads, 0, ctas, 1, stream, a)
+                         : launch(lp_grad_kernel<E, true, false>, kThreads, 0, ctas, 1, stream, a);
+        return shift ? launch(lp_grad_kernel<E, false, true>, kThreads, 0, ctas, 1, stream, a)
+                     : launch(lp_grad_kernel<E, false, false>, kThreads, 0, ctas, 1, stream, a);
     };
     return dtype == SV_BF16 ? typed(__nv_bfloat16()) : typed(0.0f);
 }
