@@ -251,8 +251,13 @@ __device__ __forceinline__ bool in_view(const AttentionArgs& a, const Share& sh,
     if (WINDOW && s >= a.sinks && s + slots <= sh.view.low) return false;
     return s < sh.len + sh.n;
 }
+// Whether some nodes of a sequence look at slot s and others do not, of those that are in view.
+template <bool WINDOW>
+__device__ __forceinline__ bool differs(const AttentionArgs& a, const Share& sh, long long s) {
+    return s > sh.len || (WINDOW && s >= a.sinks && s < sh.len + sh.n - a.window);
+}
 // The lowest n bits (none below 0, all from 32 on).
-__device__ __forceinline__ uint32_t bits_below(long long n) {
+__device__ __forceinline__ uint32_t bits_below(int n) {
     return n <= 0 ? 0u : n >= 32 ? ~0u : (1u << n) - 1;
 }
 // Whether some node of a sequence looks at slot s.
@@ -1116,8 +1121,8 @@ template <int DP, int ROWS, bool F8> struct Tc {
 };
 
 struct TcBars {
-    uint64_t q_full, q_empty, epi_done, drain, v_land;
-    uint64_t k_full[6], k_empty[6], v_full[6], v_empty[6];
+    uint64_t q_full, q_empty, epi_done, drain;
+    uint64_t k_full[6], k_empty[6], v_full[6], v_empty[6], v_land[6];
     uint64_t s_full[2], p_full[2][2], pv_done[2];  // weights: a barrier per half of the slots
     uint64_t r_full[2][4], r_empty[2][4];  // float8 keys, values as they came
 };
@@ -1331,7 +1336,6 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         bar_init(&bars.q_empty, 1);
         bar_init(&bars.drain, 1);
         bar_init(&bars.epi_done, 256);
-        bar_init(&bars.v_land, 1);
         constexpr int kFill = kF8 ? 128 : 1;
         for (int i = 0; i < SK; ++i) {
             bar_init(&bars.k_full[i], kFill);
@@ -1340,6 +1344,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         for (int i = 0; i < SV; ++i) {
             bar_init(&bars.v_full[i], kFill);
             bar_init(&bars.v_empty[i], 1);
+            bar_init(&bars.v_land[i], 1);
         }
         for (int i = 0; i < 2 * L::kRaws; ++i) {
             bar_init(&bars.r_full[i & 1][i >> 1], 1);
@@ -1381,7 +1386,6 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         bool ok = true;
         while (walk.template next<WINDOW>(a, ROWS, kTcUnit, &p)) {
             if (walk.sh.bad) continue;
-            const int len = walk.sh.len;
             for (int t = p.t0; t < p.t1; ++t) {
                 const long long slot0 = (long long)walk.sh.tile<WINDOW>(t) * kTcUnit;
                 const bool edge = mixed<WINDOW>(a, walk.sh, slot0, kTcUnit);
@@ -1439,15 +1443,16 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                             const long long slot = slot0 + r;
                             const bool take = in_view<WINDOW>(a, walk.sh, slot, 1);
                             bool wild = false;
+                            if (!take) v[0] = v[1] = v[2] = v[3] = 0;
+                            if (take && differs<WINDOW>(a, walk.sh, slot)) {
 #pragma unroll
-                            for (int k = 0; k < 4; ++k) {
-                                if (!take) v[k] = 0;
+                                for (int k = 0; k < 4; ++k)
 #pragma unroll
-                                for (int e = 0; e < 32; e += 8)
-                                    if ((WINDOW || slot > len) && (v[k] >> e & 0x7f) == 0x7f) {
-                                        wild = true;
-                                        v[k] &= ~(0xffu << e);
-                                    }
+                                    for (int e = 0; e < 32; e += 8)
+                                        if ((v[k] >> e & 0x7f) == 0x7f) {
+                                            wild = true;
+                                            v[k] &= ~(0xffu << e);
+                                        }
                             }
                             if (wild) atomicOr(&s_wild[ds][r >> 5], 1u << (r & 31));
                             write(i, v);
@@ -1464,37 +1469,40 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     } else if (!kF8 && w >= 8 && w < 12) {
         // ------------------------------------------------ loads: a warp keys, a warp values
         asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
-        const bool vals = w > 8;  // warps 10 and 11 only help to look values through
-        const int lt = tid - 288, stages = vals ? SV : SK;
-        const CUtensorMap* const map = vals ? &vmap : &kmap;
-        // A page is one box per panel (its first 128 slots where it is larger): this lane's page
-        // of a tile.
-        const int shift = min(c.page_shift, 7), boxes = kTcUnit >> shift;
-        const uint32_t bytes = (128u << shift) * (DP / 64);  // per page
+        const bool vals = w > 8;
+        const int stages = vals ? SV : SK;
         int pieces = 0, st = 0;
-        uint32_t again = 1, landed = 0;  // parities: the stage's last release; tails landed
         bool ok = true;  // once a wait gave up: no more copies, the barriers among the warps stay
-        while (walk.template next<WINDOW>(a, ROWS, kTcUnit, &p)) {
-            if (walk.sh.bad) continue;
-            const int len = walk.sh.len;
-            const int32_t* table = c.table + (long long)p.b * c.table_width;
-            auto page_of = [&](int t) -> int {
-                const long long s = (long long)walk.sh.tile<WINDOW>(t) * kTcUnit +
-                                    ((long long)lane << shift);
-                return w < 10 && lane < boxes && t < p.t1 &&
-                               in_view<WINDOW>(a, walk.sh, s, 1 << shift)
-                           ? __ldg(table + (s >> c.page_shift)) : -1;
-            };
-            int page = page_of(p.t0);
-            for (int t = p.t0; t < p.t1; ++t) {
-                const long long slot0 = (long long)walk.sh.tile<WINDOW>(t) * kTcUnit;
-                const long long s = slot0 + ((long long)lane << shift);
-                const uint32_t dst = (vals ? sv : sk) + st * L::kTile;
-                const bool tail = vals && mixed<WINDOW>(a, walk.sh, slot0, kTcUnit);
-                uint64_t* const full = tail   ? &bars.v_land
-                                       : vals ? &bars.v_full[st]
-                                              : &bars.k_full[st];
-                if (w < 10) {
+        if (w < 10) {
+            const CUtensorMap* const map = vals ? &vmap : &kmap;
+            // A page is one box per panel (its first 128 slots where it is larger): this lane's page
+            // of a tile.
+            const int shift = min(c.page_shift, 7), boxes = kTcUnit >> shift;
+            const uint32_t bytes = (128u << shift) * (DP / 64);  // per page
+            uint32_t again = 1;  // parity of the stage's last release
+            while (walk.template next<WINDOW>(a, ROWS, kTcUnit, &p)) {
+                if (walk.sh.bad) continue;
+                const int32_t* table = c.table + (long long)p.b * c.table_width;
+                auto first_of = [&](int t) {  // slot of this lane's box
+                    return (long long)walk.sh.tile<WINDOW>(t) * kTcUnit +
+                           ((long long)lane << shift);
+                };
+                auto page_of = [&](int t) -> int {
+                    const long long s = first_of(t);
+                    return lane < boxes && t < p.t1 &&
+                                   in_view<WINDOW>(a, walk.sh, s, 1 << shift)
+                               ? __ldg(table + (s >> c.page_shift)) : -1;
+                };
+                int page = page_of(p.t0);
+                for (int t = p.t0; t < p.t1; ++t) {
+                    const long long slot0 = (long long)walk.sh.tile<WINDOW>(t) * kTcUnit;
+                    const long long s = first_of(t);
+                    const uint32_t dst = (vals ? sv : sk) + st * L::kTile;
+                    // values whose rows have to be looked through first land there
+                    uint64_t* const full =
+                        !vals                                             ? &bars.k_full[st]
+                        : mixed<WINDOW>(a, walk.sh, slot0, kTcUnit) ? &bars.v_land[st]
+                                                                          : &bars.v_full[st];
                     const bool want = lane < boxes && in_view<WINDOW>(a, walk.sh, s, 1 << shift);
                     const bool good = want && (unsigned)page < (unsigned)c.num_pages;
                     if (want && !good) s_bad_piece[pieces % kBadFlags] = pieces;
@@ -1514,49 +1522,61 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                                          slot, pg, full);
                         }
                     }
+                    if (++st == stages) st = 0, again ^= 1;
                 }
-                if (tail) {
-                    // A masked entry may hold anything, but 0 times NaN is NaN: what lies behind
-                    // the last token (or between the first slots and the window) is zeroed here,
-                    // and so are values that are not finite and only some rows look at; those are
-                    // added row by row.
-                    ok = ok && warp_wait(&bars.v_land, landed, watch);
-                    landed ^= 1;
-                    if (lt < 4) s_wild[st][lt] = 0;
-                    named_sync(2, 96);
-#pragma unroll 1
-                    for (int r = lt; r < 128; r += 96) {  // a row per thread
-                        const long long slot = slot0 + r;
-                        if (!WINDOW && slot <= len) continue;
-                        constexpr uint32_t e = std::is_same<T, __half>::value ? 0x7c00u : 0x7f80u;
-                        const bool take = in_view<WINDOW>(a, walk.sh, slot, 1);
-                        bool f = !take;
-#pragma unroll 4
-                        for (int k = 0; k < CH; ++k) {
-                            uint32_t v[4];
-                            asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
-                                         : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3])
-                                         : "r"(dst + (k >> 3) * 16384 + r * 128 +
-                                               (((k & 7) ^ (r & 7)) << 4)) : "memory");
-#pragma unroll
-                            for (int q = 0; q < 4; ++q)
-                                f |= (v[q] & e) == e || (v[q] >> 16 & e) == e;
-                        }
-                        if (!f) continue;
-                        if (take) atomicOr(&s_wild[st][r >> 5], 1u << (r & 31));
-#pragma unroll 4
-                        for (int k = 0; k < CH; ++k)
-                            asm volatile("st.shared.v4.b32 [%0], {%1,%1,%1,%1};" ::"r"(
-                                dst + (k >> 3) * 16384 + r * 128 + (((k & 7) ^ (r & 7)) << 4)),
-                                "r"(0) : "memory");
-                    }
-                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-                    named_sync(2, 96);
-                    if (lt == 0) bar_arrive(&bars.v_full[st]);
-                }
-                if (++st == stages) st = 0, again ^= 1;
+                ++pieces;
             }
-            ++pieces;
+        } else {
+            // A masked entry may hold anything, but 0 times NaN is NaN: what nobody looks at (behind
+            // the last token, between the first slots and the window) is zeroed here, and so are
+            // values that are not finite and only some rows look at; those are added row by row.
+            // Two warps, so that the loads go on meanwhile.
+            const int lt = tid - 320;
+            uint32_t landed = 0;  // parities: tiles that have landed in each stage
+            while (walk.template next<WINDOW>(a, ROWS, kTcUnit, &p)) {
+                if (walk.sh.bad) continue;
+                for (int t = p.t0; t < p.t1; ++t) {
+                    const long long slot0 = (long long)walk.sh.tile<WINDOW>(t) * kTcUnit;
+                    if (mixed<WINDOW>(a, walk.sh, slot0, kTcUnit)) {
+                        const uint32_t dst = sv + st * L::kTile;
+                        ok = ok && warp_wait(&bars.v_land[st], landed >> st & 1, watch);
+                        landed ^= 1u << st;
+                        if (lt < 4) s_wild[st][lt] = 0;
+                        named_sync(2, 64);
+#pragma unroll 1
+                        for (int r = lt; r < 128; r += 64) {  // a row per thread
+                            const long long slot = slot0 + r;
+                            const bool take = in_view<WINDOW>(a, walk.sh, slot, 1);
+                            if (take && !differs<WINDOW>(a, walk.sh, slot)) continue;
+                            constexpr uint32_t e =
+                                std::is_same<T, __half>::value ? 0x7c00u : 0x7f80u;
+                            bool f = !take;
+#pragma unroll 4
+                            for (int k = 0; k < CH && take; ++k) {
+                                uint32_t v[4];
+                                asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
+                                             : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3])
+                                             : "r"(dst + (k >> 3) * 16384 + r * 128 +
+                                                   (((k & 7) ^ (r & 7)) << 4)) : "memory");
+#pragma unroll
+                                for (int q = 0; q < 4; ++q)
+                                    f |= (v[q] & e) == e || (v[q] >> 16 & e) == e;
+                            }
+                            if (!f) continue;
+                            if (take) atomicOr(&s_wild[st][r >> 5], 1u << (r & 31));
+#pragma unroll 4
+                            for (int k = 0; k < CH; ++k)
+                                asm volatile("st.shared.v4.b32 [%0], {%1,%1,%1,%1};" ::"r"(
+                                    dst + (k >> 3) * 16384 + r * 128 + (((k & 7) ^ (r & 7)) << 4)),
+                                    "r"(0) : "memory");
+                        }
+                        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                        named_sync(2, 64);
+                        if (lt == 0) bar_arrive(&bars.v_full[st]);
+                    }
+                    if (++st == SV) st = 0;
+                }
+            }
         }
     } else if (w >= 12) {
         // ------------------------------------------------ products
@@ -1847,9 +1867,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                                              : ~0u;
                         if (WINDOW) {  // up to the root: the first slots and the window
                             const int s0 = t * kTcUnit + 32 * k;
-                            const uint32_t old = bits_below(len + 1ll - s0);
-                            see[k] &= ~old | bits_below((long long)a.sinks - s0) |
-                                      ~bits_below((long long)low - s0);
+                            see[k] &= ~bits_below(len + 1 - s0) | bits_below(a.sinks - s0) |
+                                      ~bits_below(max(low, 0) - s0);
                         }
                     }
                 }
@@ -1900,8 +1919,13 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                     const int vs = (int)(tile % SV);
                     ok = ok && warp_wait(&bars.v_full[vs], (uint32_t)(tile / SV & 1), watch);
 #pragma unroll 1
-                    for (int sl = 0; ok && sl < 128; ++sl) {
-                        if (!(s_wild[vs][sl >> 5] >> (sl & 31) & 1)) continue;
+                    for (int sl = -1; ok;) {
+                        uint32_t left = 0;  // the next bit that is set
+#pragma unroll 1
+                        for (++sl; sl < 128; sl = (sl | 31) + 1)
+                            if ((left = s_wild[vs][sl >> 5] >> (sl & 31)) != 0) break;
+                        if (left == 0) break;
+                        sl += __ffs(left) - 1;
                         if (done > 0 && !waited) {
                             ok = warp_wait(&bars.pv_done[st], (pv + done - 1) & 1, watch);
                             waited = true;
