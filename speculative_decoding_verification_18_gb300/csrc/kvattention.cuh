@@ -1078,6 +1078,511 @@ __global__ void __launch_bounds__(kSplitThreads * WM, 2) kv_split_kernel(const A
     }
 }
 
+// Slots of a window as rows: what kv_slots_kernel keeps in shared memory.
+template <typename CT, int DP, int NQ> struct Slots {
+    using St = Stage<CT, DP>;
+    static constexpr int kRows = NQ * 8, kPitch = DP + 4;  // floats: rows in pairs eight banks apart
+    static constexpr int kRing = 4 * St::kStages * St::kBytes;
+    static constexpr int kMerge = 4 * kRows * kPitch * 4 + 4 * kRows * 8;
+    static constexpr int kBody = kRing > kMerge ? kRing : kMerge;
+    static constexpr int kSmem = kBody + (NQ < 4 ? 0 : kRows * DP * 2);  // + queries
+};
+// An 8 x 8 matrix of 16-bit values, a row per four lanes, transposed.
+__device__ __forceinline__ uint32_t turned(uint32_t x) {
+    uint32_t y;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+    return y;
+}
+
+// The same for windows: slots are the rows of the products and query rows their columns, eight to a
+// tile, so that a warp turns its keys and values into operands once for all query rows, whatever
+// their number up to 32, and rows past the last fill at most seven columns.  Scores come with slots in
+// the place of rows; the weights are transposed in registers on the way into the second product.  A
+// warp walks its own 16 slots of every unit, with its own ring of stages, and no lane asks the others
+// for a maximum unless a product has outgrown the reference.
+template <typename T, typename CT, int DP, int NQ>
+__global__ void __launch_bounds__(kSplitThreads, 2) kv_slots_kernel(const AttentionArgs a) {
+    constexpr bool WINDOW = true;
+    constexpr bool kF8 = sizeof(CT) == 1;
+    using M = typename std::conditional<kF8, __half, T>::type;  // type of the products
+    constexpr bool kFit = !kF8 || std::is_same<T, __half>::value;  // queries are of it already
+    constexpr bool kLo = kFit;
+    using St = Stage<CT, DP>;
+    using L = Slots<CT, DP, NQ>;
+    constexpr int S = St::kStages, KS = DP / 16, MT = DP / 16, ROWS = L::kRows;
+    constexpr int THREADS = kSplitThreads;
+    extern __shared__ __align__(128) char smem[];
+    __shared__ long long s_scan[THREADS / 32];
+    __shared__ Start s_start;
+    __shared__ uint8_t s_par[kMaxN];
+    __shared__ uint64_t s_anc[kMaxN];
+    __shared__ uint8_t s_deep[WINDOW ? kMaxN : 1];
+    const int tid = threadIdx.x, lane = tid & 31, t4 = lane & 3, g8 = lane >> 2, w = tid >> 5;
+    const Cache& c = a.c;
+
+    cudaGridDependencySynchronize();
+    cudaTriggerProgrammaticLaunchCompletion();
+
+    Walk walk = start_walk<THREADS, WINDOW>(a, ROWS, kUnit, s_scan, &s_start);
+    const Share& sh = walk.sh;
+    const uint32_t base = (uint32_t)__cvta_generic_to_shared(smem);
+    const uint32_t ring = base + w * S * St::kBytes;
+    const uint32_t queries = base + L::kBody + lane * 16;
+    int anc_of = -1;  // the sequence whose ancestors s_anc holds
+    // Queries stay in registers where there is room beside the outputs.
+    constexpr bool kHeld = NQ < 4;
+    // Element of a head that this thread's row g8 (e = 1: g8 + 8) of tile k of 16 is.
+    auto element = [&](int k, int e) {
+        return kF8 ? (k >> 1) * 32 + e * 16 + 2 * g8 + (k & 1) : k * 16 + e * 8 + g8;
+    };
+
+    Piece piece;
+    while (walk.template next<WINDOW>(a, ROWS, kUnit, &piece)) {
+        const int b = piece.b, h = piece.h, mt = piece.mt, t0 = piece.t0, t1 = piece.t1;
+        const int len = sh.len, total = len + sh.n, rows = piece.rows;
+        if (tid == 0) tell_ends(a, piece, sh.tiles);
+        bool bad = sh.bad;
+
+        const char* kb = c.k + h * c.head_stride;
+        const char* vb = c.v + h * c.head_stride;
+        const int32_t* table = c.table + (long long)b * c.table_width;
+        const int my = w * 16 + (lane & 15);  // the slot of a unit whose page this lane looks up
+        const int dch = c.dim * (int)sizeof(CT) / 16;
+        bool bad_page = false;
+        auto page_of = [&](int t) -> int {
+            const int s = sh.tile<WINDOW>(t) * kUnit + my;
+            return t < t1 && wanted<WINDOW>(a, sh, s) ? __ldg(table + (s >> c.page_shift)) : -1;
+        };
+        auto issue = [&](int t, int stage, int page) {
+            const int s = sh.tile<WINDOW>(t) * kUnit + my;
+            long long off = -1;
+            if (t < t1 && wanted<WINDOW>(a, sh, s)) {
+                if ((unsigned)page < (unsigned)c.num_pages)
+                    off = page * c.page_stride + (s & ((1 << c.page_shift) - 1)) * c.slot_stride;
+                else
+                    bad_page = true;
+            }
+            if (t < t1) {
+                const uint32_t dst = ring + stage * St::kBytes;
+                constexpr int kRows = 32 / St::kChunks;  // rows per instruction
+                constexpr int kMine = 16 / kRows;
+#pragma unroll
+                for (int i = 0; i < kMine; ++i) {
+                    const int row = i * kRows + lane / St::kChunks;
+                    const int ch = lane % St::kChunks;
+                    const long long f = __shfl_sync(~0u, off, row);
+                    const bool take = f >= 0 && ch < dch;
+                    const long long at = take ? f + ch * 16 : 0;
+                    cp_async16(dst + St::at(row, ch), kb + at, take);
+                    cp_async16(dst + 16 * St::kPitch + St::at(row, ch), vb + at, take);
+                }
+            }
+            asm volatile("cp.async.commit_group;" ::: "memory");
+        };
+        int page = -1;
+        if (!bad) {
+            int first[S - 1];
+#pragma unroll
+            for (int i = 0; i < S - 1; ++i) first[i] = page_of(t0 + i);
+            page = page_of(t0 + S - 1);
+#pragma unroll
+            for (int i = 0; i < S - 1; ++i) issue(t0 + i, i, first[i]);
+        }
+
+        // With the first slots on their way: the ancestors of every node, where this piece reaches
+        // the new tokens (with a window: in any case).
+        if (!bad && (WINDOW || (long long)t1 * kUnit > len) && anc_of != b) {
+            __syncthreads();
+            int f = 0;
+            if (a.parents)
+                for (int i = tid; i < sh.n; i += THREADS) {
+                    const int p = a.parents[(long long)b * a.N + i];
+                    s_par[i] = (uint8_t)p;
+                    f |= i > 0 && (p < 0 || p >= i);
+                }
+            f = __syncthreads_or(f);
+            if (tid < sh.n && !f)
+                s_anc[tid] = ancestors_of<WINDOW>(a, sh, a.parents ? s_par : nullptr, tid,
+                                                  &s_deep[WINDOW ? tid : 0]);
+            __syncthreads();
+            if (f) {
+                bad = true;
+                if (tid == 0) mark(a.status, b, SV_DEV_BAD_TREE);
+                anc_of = -1;
+            } else {
+                anc_of = b;
+            }
+        }
+
+        // Queries as the B operand: thread (row of eight lane / 4, elements by lane % 4), with the
+        // sign of the scales, so that the largest product is the largest exponent.
+        uint32_t qb[kHeld ? NQ : 1][KS][2];
+        float mul[NQ][2];  // from a product to the exponent (base 2), of this thread's columns
+        const float ks_h = kF8 ? c.k_scale[h] : 1.0f;
+        const float unit = fabsf(a.scale) * 1.4426950408889634f * fabsf(ks_h);
+        const uint32_t sign = (a.scale < 0.0f) != (ks_h < 0.0f) ? 0x80008000u : 0u;
+        // never 0, for 0 * -inf is NaN; a scale that is NaN stays so
+        auto not_zero = [](float x) { return x < 1e-37f ? 1e-37f : x; };
+#pragma unroll
+        for (int nt = 0; nt < NQ; ++nt) {
+            const int row = nt * 8 + g8, R = mt * ROWS + row;
+            const int j = R / a.group, g = R - j * a.group;
+            const bool live = row < rows && !bad;
+            const T* q = (const T*)a.q + (live ? b * a.qb + j * a.qt +
+                                                     (long long)(h * a.group + g) * a.qh : 0);
+            uint32_t (&y)[KS][2] = qb[kHeld ? nt : 0];
+            float top = 0.0f;
+#pragma unroll
+            for (int ks = 0; ks < KS; ++ks) {
+                // float8: 16 consecutive elements of a block of 64 per thread, 4 per step
+                const int e0 = kF8 ? (ks >> 2) * 64 + t4 * 16 + (ks & 3) * 4 : ks * 16 + t4 * 2;
+                const int e1 = kF8 ? e0 + 2 : e0 + 8;
+                const bool in = live && (kF8 ? e0 : ks * 16) < c.dim;
+                y[ks][0] = in ? __ldg((const uint32_t*)(q + e0)) ^ sign : 0u;
+                y[ks][1] = in ? __ldg((const uint32_t*)(q + e1)) ^ sign : 0u;
+                if constexpr (!kFit) {
+                    const float2 f0 = unpair<T>(y[ks][0]), f1 = unpair<T>(y[ks][1]);
+                    top = fmaxf(fmaxf(top, fmaxf(fabsf(f0.x), fabsf(f0.y))),
+                                fmaxf(fabsf(f1.x), fabsf(f1.y)));
+                }
+            }
+            mul[nt][0] = mul[nt][1] = not_zero(unit);
+            if constexpr (!kFit) {
+                top = fmaxf(top, __shfl_xor_sync(~0u, top, 1));
+                top = fmaxf(top, __shfl_xor_sync(~0u, top, 2));
+                // the row's largest element becomes 2^8 .. 2^9: what then falls below the smallest
+                // half is 2^-33 of it
+                const int e = row_power(top);
+                const float down = exp2f((float)-e);
+                const float m = not_zero(fabsf(a.scale) * 1.4426950408889634f * exp2f((float)e) *
+                                         fabsf(ks_h));
+#pragma unroll
+                for (int x = 0; x < 2; ++x) mul[nt][x] = __shfl_sync(~0u, m, (2 * t4 + x) * 4);
+#pragma unroll
+                for (int ks = 0; ks < KS; ++ks)
+#pragma unroll
+                    for (int x = 0; x < 2; ++x) {
+                        const float2 f = unpair<T>(y[ks][x]);
+                        y[ks][x] = pair<__half>(f.x * down, f.y * down);
+                    }
+            }
+            if constexpr (!kHeld) {  // in shared memory, as each lane will want them
+                if (w == nt % 4)
+#pragma unroll
+                    for (int ks = 0; ks < KS; ks += 2)
+                        asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(
+                                         queries + (nt * (KS / 2) + ks / 2) * 512),
+                                     "r"(y[ks][0]), "r"(y[ks][1]), "r"(y[ks + 1][0]),
+                                     "r"(y[ks + 1][1]) : "memory");
+            }
+        }
+        if (!kHeld) __syncthreads();
+        // Queries of steps ks and ks + 1.
+        auto query = [&](int nt, int ks, uint32_t (&f)[4]) {
+            if constexpr (kHeld)
+                f[0] = qb[nt][ks][0], f[1] = qb[nt][ks][1], f[2] = qb[nt][ks + 1][0],
+                f[3] = qb[nt][ks + 1][1];
+            else
+                asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
+                             : "=r"(f[0]), "=r"(f[1]), "=r"(f[2]), "=r"(f[3])
+                             : "r"(queries + (nt * (KS / 2) + ks / 2) * 512) : "memory");
+        };
+
+        // Outputs, elements by rows: thread (elements g8 and g8 + 8 of 16, rows 2 t4 and 2 t4 + 1 of
+        // eight); the rows' sums over this thread's slots and references.
+        float o[MT][NQ][4], l[NQ][2], mr[NQ][2];
+#pragma unroll
+        for (int nt = 0; nt < NQ; ++nt) {
+            l[nt][0] = l[nt][1] = 0.0f;
+            mr[nt][0] = mr[nt][1] = -INFINITY;
+#pragma unroll
+            for (int k = 0; k < MT; ++k)
+                o[k][nt][0] = o[k][nt][1] = o[k][nt][2] = o[k][nt][3] = 0.0f;
+        }
+        auto node_of = [&](int nt, int x) {  // of this thread's row
+            return min((mt * ROWS + nt * 8 + 2 * t4 + x) / a.group, sh.n - 1);
+        };
+
+        int stage = 0;
+        for (int t = t0; t < t1 && !bad; ++t) {
+            asm volatile("cp.async.wait_group %0;" ::"n"(S - 2) : "memory");
+            __syncwarp();
+            issue(t + S - 1, stage == 0 ? S - 1 : stage - 1, page);
+            page = page_of(t + S);
+            const uint32_t kt = ring + stage * St::kBytes, vt = kt + 16 * St::kPitch;
+            stage = stage == S - 1 ? 0 : stage + 1;
+            const int slot0 = sh.tile<WINDOW>(t) * kUnit + w * 16;
+            if (slot0 >= total) continue;
+            if (slot0 >= a.sinks && slot0 + 16 <= sh.view.low) continue;
+
+            // Scores: 16 slots by NQ tiles of eight rows.
+            float s[NQ][4];
+#pragma unroll
+            for (int nt = 0; nt < NQ; ++nt) s[nt][0] = s[nt][1] = s[nt][2] = s[nt][3] = 0.0f;
+            if constexpr (!kF8) {
+#pragma unroll
+                for (int ks = 0; ks < KS; ks += 2) {
+                    uint32_t f[2][4], q[4];
+                    const int row = lane & 15, ch = lane >> 4;
+                    ldsm4(f[0], kt + St::at(row, ks * 2 + ch));
+                    ldsm4(f[1], kt + St::at(row, ks * 2 + 2 + ch));
+#pragma unroll
+                    for (int nt = 0; nt < NQ; ++nt) {
+                        query(nt, ks, q);
+                        mma<M>(s[nt], f[0], q[0], q[1]);
+                        mma<M>(s[nt], f[1], q[2], q[3]);
+                    }
+                }
+            } else {
+#pragma unroll
+                for (int kb4 = 0; kb4 < DP / 64; ++kb4) {
+                    uint32_t f[2][4];
+#pragma unroll
+                    for (int x = 0; x < 2; ++x)
+                        asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
+                                     : "=r"(f[x][0]), "=r"(f[x][1]), "=r"(f[x][2]), "=r"(f[x][3])
+                                     : "r"(kt + St::at(x * 8 + g8, kb4 * 4 + t4)) : "memory");
+#pragma unroll
+                    for (int k = 0; k < 4; k += 2) {
+                        uint32_t y[2][4];
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) {
+                            widen(y[i][0], y[i][2], f[0][k + i]);
+                            widen(y[i][1], y[i][3], f[1][k + i]);
+                        }
+#pragma unroll
+                        for (int nt = 0; nt < NQ; ++nt) {
+                            uint32_t q[4];
+                            query(nt, kb4 * 4 + k, q);
+                            mma<M>(s[nt], y[0], q[0], q[1]);
+                            mma<M>(s[nt], y[1], q[2], q[3]);
+                        }
+                    }
+                }
+            }
+            // new tokens, the end or the window's beginning are among the 16
+            const bool fresh = mixed<WINDOW>(a, sh, slot0, 16);
+            if (fresh) {
+#pragma unroll
+                for (int nt = 0; nt < NQ; ++nt)
+#pragma unroll
+                    for (int x = 0; x < 2; ++x) {
+                        const int j = node_of(nt, x), low = low_of(a, sh, s_deep[j]);
+                        const uint64_t anc = s_anc[j];
+#pragma unroll
+                        for (int k = 0; k < 2; ++k)
+                            if (!looks<WINDOW>(a, sh, anc, low, slot0 + g8 + 8 * k))
+                                s[nt][2 * k + x] = -INFINITY;
+                    }
+            }
+            // The reference of a row follows its maximum only when that has grown by 2^8: weights
+            // stay below 2^8, the output is rarely rescaled, and no lane asks the others before
+            // one of them has seen a product so large.
+            bool grows = false;
+#pragma unroll
+            for (int nt = 0; nt < NQ; ++nt)
+#pragma unroll
+                for (int x = 0; x < 2; ++x)
+                    grows |= fmaxf(s[nt][x], s[nt][2 + x]) * mul[nt][x] > mr[nt][x] + 8.0f;
+            if (__any_sync(~0u, grows)) {
+#pragma unroll
+                for (int nt = 0; nt < NQ; ++nt)
+#pragma unroll
+                    for (int x = 0; x < 2; ++x) {
+                        float m = fmaxf(s[nt][x], s[nt][2 + x]);
+#pragma unroll
+                        for (int k = 4; k < 32; k *= 2) m = fmaxf(m, __shfl_xor_sync(~0u, m, k));
+                        m *= mul[nt][x];
+                        if (!(m > mr[nt][x] + 8.0f)) continue;
+                        const float f = ex2(mr[nt][x] - m);
+                        mr[nt][x] = m;
+                        l[nt][x] *= f;
+#pragma unroll
+                        for (int k = 0; k < MT; ++k) {
+                            o[k][nt][x] *= f;
+                            o[k][nt][2 + x] *= f;
+                        }
+                    }
+            }
+#pragma unroll
+            for (int nt = 0; nt < NQ; ++nt)
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                    const float ref = mr[nt][x] == -INFINITY ? 0.0f : mr[nt][x];
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) {
+                        float& p = s[nt][2 * k + x];
+                        p = ex2(fmaf(p, mul[nt][x], -ref));
+                        l[nt][x] += p;
+                    }
+                }
+            if (fresh) {
+                // A masked entry may hold anything, but 0 times NaN is NaN: values that are not
+                // finite are taken out of the product and added for the rows that see them.
+                bool f = false;
+                const int row = lane >> 1;
+                if (slot0 + row < total) {
+                    for (int ch = (lane & 1); ch < dch; ch += 2) {
+                        uint32_t v[4];
+                        asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
+                                     : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3])
+                                     : "r"(vt + St::at(row, ch)) : "memory");
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            if constexpr (kF8) {
+                                for (int i = 0; i < 32; i += 8) f |= (v[k] >> i & 0x7f) == 0x7f;
+                            } else {
+                                constexpr uint32_t e = std::is_same<T, __half>::value ? 0x7c00u
+                                                                                      : 0x7f80u;
+                                f |= (v[k] & e) == e || (v[k] >> 16 & e) == e;
+                            }
+                        }
+                    }
+                }
+                const uint32_t wild = __ballot_sync(~0u, f);
+                for (int rw = 0; wild != 0 && rw < 16; ++rw) {
+                    if (!(wild >> (2 * rw) & 3)) continue;
+#pragma unroll
+                    for (int nt = 0; nt < NQ; ++nt)
+#pragma unroll
+                        for (int x = 0; x < 2; ++x) {
+                            const float p = __shfl_sync(~0u, rw < 8 ? s[nt][x] : s[nt][2 + x],
+                                                        (rw & 7) * 4 + t4);
+                            const int j = node_of(nt, x);
+                            if (!looks<WINDOW>(a, sh, s_anc[j], low_of(a, sh, s_deep[j]),
+                                               slot0 + rw))
+                                continue;
+#pragma unroll
+                            for (int k = 0; k < MT; ++k)
+#pragma unroll
+                                for (int e = 0; e < 2; ++e) {
+                                    const int by = element(k, e) * (int)sizeof(CT);
+                                    const CT* v = reinterpret_cast<const CT*>(
+                                        smem + (vt + St::at(rw, by >> 4) + (by & 15) - base));
+                                    o[k][nt][2 * e + x] += p * Conv<CT>::to(*v);
+                                }
+                        }
+                    __syncwarp();
+                    for (int ch = lane; ch < St::kChunks; ch += 32)
+                        asm volatile("st.shared.v4.b32 [%0], {%1,%1,%1,%1};" ::"r"(
+                                         vt + St::at(rw, ch)), "r"(0) : "memory");
+                    __syncwarp();
+                }
+            }
+            // Weights as the B operand: slots and rows change places.
+            uint32_t ph[NQ][2], pl[NQ][2];
+#pragma unroll
+            for (int nt = 0; nt < NQ; ++nt)
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    const float u = s[nt][2 * k], v = s[nt][2 * k + 1];
+                    if constexpr (kLo) {
+                        const uint32_t y = cut<M>(u, v);
+                        const float2 f = unpair<M>(y);
+                        ph[nt][k] = turned(y);
+                        pl[nt][k] = turned(pair<M>(u - f.x, v - f.y));
+                    } else {
+                        ph[nt][k] = turned(pair<M>(u, v));
+                    }
+                }
+            if constexpr (!kF8) {
+#pragma unroll
+                for (int k = 0; k < MT; ++k) {
+                    uint32_t f[4];
+                    ldsm4t(f, vt + St::at((lane & 7) + (lane >> 4) * 8, k * 2 + (lane >> 3 & 1)));
+#pragma unroll
+                    for (int nt = 0; nt < NQ; ++nt) {
+                        mma<M>(o[k][nt], f, ph[nt][0], ph[nt][1]);
+                        mma<M>(o[k][nt], f, pl[nt][0], pl[nt][1]);
+                    }
+                }
+            } else {
+                // a word: elements 2i and 2i + 1 of two slots; the even elements of 32 make one
+                // tile of 16, the odd ones the next
+#pragma unroll
+                for (int k = 0; k < MT; k += 2) {
+                    uint32_t f[4], even[4], odd[4];
+                    ldsm4t(f, vt + St::at((lane & 7) + (lane >> 4) * 8, k + (lane >> 3 & 1)));
+#pragma unroll
+                    for (int x = 0; x < 4; ++x) widen(even[x], odd[x], __byte_perm(f[x], 0, 0x3120));
+#pragma unroll
+                    for (int nt = 0; nt < NQ; ++nt) {
+                        mma<M>(o[k][nt], even, ph[nt][0], ph[nt][1]);
+                        mma<M>(o[k + 1][nt], odd, ph[nt][0], ph[nt][1]);
+                        if constexpr (kLo) {
+                            mma<M>(o[k][nt], even, pl[nt][0], pl[nt][1]);
+                            mma<M>(o[k + 1][nt], odd, pl[nt][0], pl[nt][1]);
+                        }
+                    }
+                }
+            }
+        }
+        asm volatile("cp.async.wait_all;" ::: "memory");
+        bad_page = __syncthreads_or(bad_page);
+        if (bad_page) {
+            if (tid == 0) mark(a.status, b, SV_DEV_BAD_PAGE);
+            bad = true;
+        }
+
+        // Join the four groups.
+        float* so = reinterpret_cast<float*>(smem);
+        constexpr int kP = L::kPitch;
+        float2* sml = reinterpret_cast<float2*>(so + 4 * ROWS * kP);
+#pragma unroll
+        for (int nt = 0; nt < NQ; ++nt)
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+                const int row = nt * 8 + 2 * t4 + x;
+                float sum = l[nt][x];
+#pragma unroll
+                for (int k = 4; k < 32; k *= 2) sum += __shfl_xor_sync(~0u, sum, k);
+                if (g8 == 0) sml[w * ROWS + row] = make_float2(mr[nt][x], sum);
+                float* dst = so + (w * ROWS + row) * kP;
+#pragma unroll
+                for (int k = 0; k < MT; ++k)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) dst[element(k, e)] = o[k][nt][2 * e + x];
+            }
+        __syncthreads();
+        const bool whole = t0 == 0 && t1 == sh.tiles;
+        const long long part = 2 * blockIdx.x + (t0 == 0 ? 1 : 0);
+        const float vs = kF8 ? c.v_scale[h] : 1.0f;
+        for (int i = tid; i < rows * (DP / 4); i += THREADS) {
+            const int row = i / (DP / 4), d = i % (DP / 4) * 4;
+            float2 ml[4];
+            float top = -INFINITY;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                ml[k] = sml[k * ROWS + row];
+                top = fmaxf(top, ml[k].x);
+            }
+            const float ref = top == -INFINITY ? 0.0f : top;
+            float sum = 0.0f;
+            float4 y = make_float4(0, 0, 0, 0);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const float f = ex2(ml[k].x - ref);
+                const float4 v = *reinterpret_cast<const float4*>(so + (k * ROWS + row) * kP + d);
+                sum += ml[k].y * f;
+                y.x += v.x * f, y.y += v.y * f, y.z += v.z * f, y.w += v.w * f;
+            }
+            if (bad) sum = NAN;
+            if (!whole) {
+                *reinterpret_cast<float4*>(a.part_o + (part * ROWS + row) * DP + d) = y;
+                if (d == 0) a.part_ml[part * ROWS + row] = make_float2(top, sum);
+            } else if (d < c.dim) {
+                const int R = mt * ROWS + row, j = R / a.group, g = R - j * a.group;
+                const float f = vs / sum;
+                T* dst = (T*)a.out +
+                         (((long long)b * a.N + j) * a.q_heads + h * a.group + g) * c.dim + d;
+                *reinterpret_cast<uint2*>(dst) =
+                    make_uint2(pair<T>(y.x * f, y.y * f), pair<T>(y.z * f, y.w * f));
+            }
+        }
+        __syncthreads();
+    }
+}
+
 // ---------------------------------------------------------------- many rows: tcgen05
 //
 // With more query rows per key head than mma.sync keeps up with, the products run on tcgen05.mma:
@@ -2217,6 +2722,37 @@ static auto with_split(sv_dtype dtype, sv_dtype cache, int dim, int rows, F f) {
     return cache == SV_E4M3 ? sized(__half(), __nv_fp8_e4m3()) : sized(__half(), __half());
 }
 
+// The same for windows: tiles of eight rows of a key head, four of them per CTA at most.
+template <typename F>
+static auto with_slots(sv_dtype dtype, sv_dtype cache, int dim, int rows, F f) {
+    auto tiled = [&](auto t, auto ct, auto dp, auto nq) {
+        using T = decltype(t);
+        using CT = decltype(ct);
+        constexpr int DP = decltype(dp)::value, NQ = decltype(nq)::value;
+        return f(kv_slots_kernel<T, CT, DP, NQ>, kv_join_kernel<T, DP, true>,
+                 Slots<CT, DP, NQ>::kSmem);
+    };
+    auto sized = [&](auto t, auto ct, auto dp) {
+        return rows <= 8    ? tiled(t, ct, dp, std::integral_constant<int, 1>())
+               : rows <= 16 ? tiled(t, ct, dp, std::integral_constant<int, 2>())
+               : rows <= 24 ? tiled(t, ct, dp, std::integral_constant<int, 3>())
+                            : tiled(t, ct, dp, std::integral_constant<int, 4>());
+    };
+    auto typed = [&](auto t, auto ct) {
+        return dim <= 64 ? sized(t, ct, std::integral_constant<int, 64>())
+                         : sized(t, ct, std::integral_constant<int, 128>());
+    };
+    if (dtype == SV_BF16)
+        return cache == SV_E4M3 ? typed(__nv_bfloat16(), __nv_fp8_e4m3())
+                                : typed(__nv_bfloat16(), __nv_bfloat16());
+    return cache == SV_E4M3 ? typed(__half(), __nv_fp8_e4m3()) : typed(__half(), __half());
+}
+// Rows of a row tile of the forms that cut units into ranges, with few rows.
+template <bool WINDOW> static int few_rows_tile(int rows) {
+    if (WINDOW) return rows <= 8 ? 8 : rows <= 16 ? 16 : rows <= 24 ? 24 : 32;
+    return rows <= 16 ? 16 : 32;
+}
+
 // The same for the wide kernel: tiles of 128 rows, or of two times 128.
 template <bool WINDOW, typename F>
 static auto with_wide(sv_dtype dtype, sv_dtype cache, int dim, int rows, F f) {
@@ -2319,9 +2855,11 @@ template <bool WINDOW> static bool split_setup() {
     for (sv_dtype t : {SV_BF16, SV_F16})
         for (sv_dtype ct : {t, SV_E4M3})
             for (int dim : {64, 128})
-                for (int rows : {16, 32})
-                    ok = ok && with_split<false, WINDOW>(t, ct, dim, rows, set) &&
-                         with_split<true, WINDOW>(t, ct, dim, rows, set);
+                for (int rows : {8, 16, 24, 32}) {
+                    ok = ok && with_split<true, WINDOW>(t, ct, dim, rows, set);
+                    if constexpr (WINDOW) ok = ok && with_slots(t, ct, dim, rows, set);
+                    else ok = ok && with_split<false, WINDOW>(t, ct, dim, rows, set);
+                }
     return ok;
 }
 
@@ -2483,7 +3021,9 @@ static sv_status attend(const sv_kv_cache* cache, const void* q, const sv_stride
     CUtensorMap kmap, vmap;
     wide = wide && !cluster && rows > few && cache->page_size >= 8 &&
            cache_map(&kmap, cache->k, cache) && cache_map(&vmap, cache->v, cache);
-    const int tile = wide ? (rows <= 128 ? 128 : 256) : rows <= 16 ? 16 : 32;
+    const int tile = wide      ? (rows <= 128 ? 128 : 256)
+                     : cluster ? few_rows_tile<false>(rows)
+                               : few_rows_tile<WINDOW>(rows);
     const int unit = wide ? kTcUnit : kUnit;
     const int mts = (rows + tile - 1) / tile;
     if ((long double)B * cache->heads * mts *
@@ -2509,7 +3049,9 @@ static sv_status attend(const sv_kv_cache* cache, const void* q, const sv_stride
     auto launch = [&](auto kernel, auto join, int smem) {
         cudaLaunchConfig_t cfg = {};
         cfg.gridDim = dim3(cluster ? B * cache->heads * mts * kCluster : a.ctas);
-        cfg.blockDim = dim3(wide ? kTcThreads : kSplitThreads * tile / 16);
+        cfg.blockDim = dim3(wide                 ? kTcThreads
+                            : WINDOW && !cluster ? kSplitThreads
+                                                 : kSplitThreads * tile / 16);
         cfg.dynamicSmemBytes = smem;
         cfg.stream = stream;
         cfg.attrs = attrs;
@@ -2528,9 +3070,15 @@ static sv_status attend(const sv_kv_cache* cache, const void* q, const sv_stride
         cfg.gridDim = dim3(a.ctas, warps == 4 ? parts : parts / 4);
         return cudaLaunchKernelEx(&cfg, join, a, tile, warps);
     };
-    const cudaError_t e = wide ? with_wide<WINDOW>(dtype, cache->dtype, cache->dim, rows, launch)
-                    : cluster ? with_split<true, WINDOW>(dtype, cache->dtype, cache->dim, rows, launch)
-                              : with_split<false, WINDOW>(dtype, cache->dtype, cache->dim, rows, launch);
+    cudaError_t e;
+    if (wide)
+        e = with_wide<WINDOW>(dtype, cache->dtype, cache->dim, rows, launch);
+    else if (cluster)
+        e = with_split<true, WINDOW>(dtype, cache->dtype, cache->dim, rows, launch);
+    else if constexpr (WINDOW)
+        e = with_slots(dtype, cache->dtype, cache->dim, rows, launch);
+    else
+        e = with_split<false, WINDOW>(dtype, cache->dtype, cache->dim, rows, launch);
     return e == cudaSuccess ? SV_OK : SV_ERR_CUDA;
 }
 
