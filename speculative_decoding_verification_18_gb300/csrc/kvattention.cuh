@@ -140,12 +140,15 @@ __device__ __forceinline__ void put_quotients(void* p, const float* x, float sca
 // ---------------------------------------------------------------- sequences
 
 // Whether sequence b's length and number of tokens are good.
+__device__ __forceinline__ bool tokens_good(int len, int n, int N, const Cache& c) {
+    const long long cap = (long long)c.table_width << c.page_shift;
+    return n >= 0 && n <= N && len >= 0 && (long long)len + n <= cap;
+}
 __device__ __forceinline__ bool tokens_of(const int32_t* kv_len, const int32_t* num_new, int b,
                                           int N, const Cache& c, int* len, int* n) {
     *n = num_new ? num_new[b] : N;
     *len = kv_len[b];
-    const long long cap = (long long)c.table_width << c.page_shift;
-    return *n >= 0 && *n <= N && *len >= 0 && (long long)*len + *n <= cap;
+    return tokens_good(*len, *n, N, c);
 }
 
 __device__ __forceinline__ void mark(uint32_t* status, int b, uint32_t bits) {
@@ -196,7 +199,7 @@ struct AttentionArgs {
 
 constexpr int kUnit = 64;          // slots of a unit: 16 per warp
 constexpr int kSplitThreads = 128;
-constexpr int kMaxCtas = 304;      // two per SM
+constexpr int kMaxCtas = 456;      // three per SM
 
 // The slots that some node of a sequence looks at through the window, beside the new ones: the
 // first `sinks`, and those from `low` on (the window of the root, which lies furthest back).  The
@@ -224,9 +227,12 @@ struct Share {
 __device__ __forceinline__ constexpr int full_weight(int rows) { return rows > 128 ? 2 : 1; }
 
 template <bool WINDOW>
-__device__ __forceinline__ Share share_of(const AttentionArgs& a, int b, int rows, int unit) {
+__device__ __forceinline__ Share share_from(const AttentionArgs& a, int len, int n, int rows,
+                                            int unit) {
     Share s;
-    s.bad = !tokens_of(a.kv_len, a.num_new, b, a.N, a.c, &s.len, &s.n);
+    s.len = len;
+    s.n = n;
+    s.bad = !tokens_good(len, n, a.N, a.c);
     // one unit per item of a bad one: its rows become NaN, all N where the count itself is bad
     if (s.n < 0 || s.n > a.N) s.n = a.N;
     s.tiles = s.bad ? 1 : (int)(((long long)s.len + s.n + unit - 1) / unit);
@@ -243,6 +249,11 @@ __device__ __forceinline__ Share share_of(const AttentionArgs& a, int b, int row
     s.mts = (s.n * a.group + rows - 1) / rows;
     s.last = s.n * a.group - (s.mts - 1) * rows > 128 ? 2 : 1;
     return s;
+}
+template <bool WINDOW>
+__device__ __forceinline__ Share share_of(const AttentionArgs& a, int b, int rows, int unit) {
+    const int n = a.num_new ? a.num_new[b] : a.N;
+    return share_from<WINDOW>(a, a.kv_len[b], n, rows, unit);
 }
 // Whether some node of a sequence looks at one of `slots` slots from s on.
 template <bool WINDOW>
@@ -273,6 +284,10 @@ __device__ __forceinline__ int ranges_of(long long W, int ctas, int full) {
 }
 // Range c of P equal ranges of W units starts at floor(c W / P).
 __device__ __forceinline__ long long range_start(long long W, int P, int c) {
+    if (W < (1ll << 31)) {  // (divisions of 64 bits take a CTA's beginning half a microsecond each)
+        const uint32_t w = (uint32_t)W, q = w / P;
+        return (long long)q * c + (w - q * P) * (uint32_t)c / P;
+    }
     return W / P * c + W % P * c / P;
 }
 
@@ -312,7 +327,7 @@ struct Walk {
 };
 struct Start {
     long long at;
-    int b;
+    int b, len, n;  // the sequence, its length and count
 };
 
 // Says where the pieces of an item are, for the join.
@@ -331,8 +346,11 @@ __device__ __forceinline__ Walk start_walk(const AttentionArgs& a, int rows, int
     const int per = (a.B + THREADS - 1) / THREADS;
     const int b0 = min(a.B, tid * per), b1 = min(a.B, b0 + per);
     long long sum = 0;
+    int len = 0, n = 0;  // of the last one: where each thread has one, they are not read again
     for (int b = b0; b < b1; ++b) {
-        const Share s = share_of<WINDOW>(a, b, rows, unit);
+        n = a.num_new ? a.num_new[b] : a.N;
+        len = a.kv_len[b];
+        const Share s = share_from<WINDOW>(a, len, n, rows, unit);
         sum += s.units(a.c.heads, full);
         // (here: a sequence without tokens has no piece that would say so)
         if (s.bad && blockIdx.x == 0) mark(a.status, b, SV_DEV_BAD_LENGTH);
@@ -357,8 +375,13 @@ __device__ __forceinline__ Walk start_walk(const AttentionArgs& a, int rows, int
     if (here) {
         long long at = before;
         for (int b = b0; b < b1; ++b) {
-            const long long u = share_of<WINDOW>(a, b, rows, unit).units(a.c.heads, full);
-            if (x >= at && x < at + u) *s_start = Start{at, b};
+            if (per > 1) {
+                n = a.num_new ? a.num_new[b] : a.N;
+                len = a.kv_len[b];
+            }
+            const long long u =
+                per > 1 ? share_from<WINDOW>(a, len, n, rows, unit).units(a.c.heads, full) : sum;
+            if (x >= at && x < at + u) *s_start = Start{at, b, len, n};
             at += u;
         }
     }
@@ -367,11 +390,14 @@ __device__ __forceinline__ Walk start_walk(const AttentionArgs& a, int rows, int
     if (some) {
         k.left = range_start(W, P, blockIdx.x + 1) - x;
         k.b = s_start->b;
-        k.sh = share_of<WINDOW>(a, k.b, rows, unit);
+        k.sh = share_from<WINDOW>(a, s_start->len, s_start->n, rows, unit);
         const long long r = x - s_start->at, head = k.sh.units(1, full);
         const long long tile = (long long)k.sh.tiles * full;  // weight of an item but the last
-        const int h = (int)(r / head);
-        const int mt = (int)min((r - h * head) / tile, (long long)k.sh.mts - 1);
+        const bool small = W < (1ll << 31);
+        const int h = small ? (int)((uint32_t)r / (uint32_t)head) : (int)(r / head);
+        const long long in = r - h * head;
+        const int mt = (int)min(small ? (long long)((uint32_t)in / (uint32_t)tile) : in / tile,
+                                (long long)k.sh.mts - 1);
         k.item = h * k.sh.mts + mt;
         k.at = r - h * head - mt * tile;
     }
@@ -767,7 +793,7 @@ __global__ void __launch_bounds__(kSplitThreads * WM, 2) kv_split_kernel(const A
             stage = stage == S - 1 ? 0 : stage + 1;
             const int slot0 = sh.tile<WINDOW>(t) * kUnit + w * 16;
             if (slot0 >= total) continue;
-            if (WINDOW && slot0 >= a.sinks && slot0 + 16 <= sh.view.low) continue;
+            if (WINDOW && slot0 >= a.sinks && slot0 <= sh.view.low - 16) continue;
 
             // Scores: 16 slots = two tiles of 8 columns.
             float s[2][4];
@@ -1078,14 +1104,23 @@ __global__ void __launch_bounds__(kSplitThreads * WM, 2) kv_split_kernel(const A
     }
 }
 
+// CTAs per SM of kv_slots_kernel, for nq tiles of rows and elements of `bytes` bytes.
+__host__ __device__ constexpr int slots_resident(int nq, int dp, int bytes) {
+    return nq == 4 ? 2 : 3;
+}
 // Slots of a window as rows: what kv_slots_kernel keeps in shared memory.
 template <typename CT, int DP, int NQ> struct Slots {
     using St = Stage<CT, DP>;
+    // CTAs per SM, and stages that fit beside the others'
+    static constexpr int kResident = slots_resident(NQ, DP, (int)sizeof(CT));
+    static constexpr int kFit = (kResident == 3 ? 65536 : 98304) / (4 * St::kBytes);
+    static constexpr int kStages = kFit > 6 ? 6 : kFit;
     static constexpr int kRows = NQ * 8, kPitch = DP + 4;  // floats: rows in pairs eight banks apart
-    static constexpr int kRing = 4 * St::kStages * St::kBytes;
+    static constexpr int kRing = 4 * kStages * St::kBytes;
     static constexpr int kMerge = 4 * kRows * kPitch * 4 + 4 * kRows * 8;
     static constexpr int kBody = kRing > kMerge ? kRing : kMerge;
-    static constexpr int kSmem = kBody + (NQ < 4 ? 0 : kRows * DP * 2);  // + queries
+    static constexpr bool kHeld = NQ < 2;  // queries in registers, else in shared memory
+    static constexpr int kSmem = kBody + (kHeld ? 0 : kRows * DP * 2);
 };
 // An 8 x 8 matrix of 16-bit values, a row per four lanes, transposed.
 __device__ __forceinline__ uint32_t turned(uint32_t x) {
@@ -1101,7 +1136,8 @@ __device__ __forceinline__ uint32_t turned(uint32_t x) {
 // warp walks its own 16 slots of every unit, with its own ring of stages, and no lane asks the others
 // for a maximum unless a product has outgrown the reference.
 template <typename T, typename CT, int DP, int NQ>
-__global__ void __launch_bounds__(kSplitThreads, 2) kv_slots_kernel(const AttentionArgs a) {
+__global__ void __launch_bounds__(kSplitThreads, Slots<CT, DP, NQ>::kResident)
+    kv_slots_kernel(const AttentionArgs a) {
     constexpr bool WINDOW = true;
     constexpr bool kF8 = sizeof(CT) == 1;
     using M = typename std::conditional<kF8, __half, T>::type;  // type of the products
@@ -1109,14 +1145,16 @@ __global__ void __launch_bounds__(kSplitThreads, 2) kv_slots_kernel(const Attent
     constexpr bool kLo = kFit;
     using St = Stage<CT, DP>;
     using L = Slots<CT, DP, NQ>;
-    constexpr int S = St::kStages, KS = DP / 16, MT = DP / 16, ROWS = L::kRows;
+    constexpr bool kHeld = L::kHeld;
+    constexpr int S = L::kStages, KS = DP / 16, MT = DP / 16, ROWS = L::kRows;
     constexpr int THREADS = kSplitThreads;
     extern __shared__ __align__(128) char smem[];
     __shared__ long long s_scan[THREADS / 32];
     __shared__ Start s_start;
     __shared__ uint8_t s_par[kMaxN];
     __shared__ uint64_t s_anc[kMaxN];
-    __shared__ uint8_t s_deep[WINDOW ? kMaxN : 1];
+    __shared__ uint8_t s_deep[kMaxN];
+    __shared__ float s_mul[L::kRows];
     const int tid = threadIdx.x, lane = tid & 31, t4 = lane & 3, g8 = lane >> 2, w = tid >> 5;
     const Cache& c = a.c;
 
@@ -1129,8 +1167,6 @@ __global__ void __launch_bounds__(kSplitThreads, 2) kv_slots_kernel(const Attent
     const uint32_t ring = base + w * S * St::kBytes;
     const uint32_t queries = base + L::kBody + lane * 16;
     int anc_of = -1;  // the sequence whose ancestors s_anc holds
-    // Queries stay in registers where there is room beside the outputs.
-    constexpr bool kHeld = NQ < 4;
     // Element of a head that this thread's row g8 (e = 1: g8 + 8) of tile k of 16 is.
     auto element = [&](int k, int e) {
         return kF8 ? (k >> 1) * 32 + e * 16 + 2 * g8 + (k & 1) : k * 16 + e * 8 + g8;
@@ -1143,6 +1179,25 @@ __global__ void __launch_bounds__(kSplitThreads, 2) kv_slots_kernel(const Attent
         if (tid == 0) tell_ends(a, piece, sh.tiles);
         bool bad = sh.bad;
 
+        // Queries, asked for before anything else: this thread's words of eight rows (a warp's own
+        // eight where they are shared).
+        uint32_t qb[KS][2];
+        {
+            const int row = (kHeld ? 0 : w * 8) + g8, R = mt * ROWS + row;
+            const int j = R / a.group, g = R - j * a.group;
+            const bool live = row < rows && !bad;
+            const T* q = (const T*)a.q + (live ? b * a.qb + j * a.qt +
+                                                     (long long)(h * a.group + g) * a.qh : 0);
+#pragma unroll
+            for (int ks = 0; ks < KS; ++ks) {
+                // float8: 16 consecutive elements of a block of 64 per thread, 4 per step
+                const int e0 = kF8 ? (ks >> 2) * 64 + t4 * 16 + (ks & 3) * 4 : ks * 16 + t4 * 2;
+                const int e1 = kF8 ? e0 + 2 : e0 + 8;
+                const bool in = live && (kF8 ? e0 : ks * 16) < c.dim;
+                qb[ks][0] = in ? __ldg((const uint32_t*)(q + e0)) : 0u;
+                qb[ks][1] = in ? __ldg((const uint32_t*)(q + e1)) : 0u;
+            }
+        }
         const char* kb = c.k + h * c.head_stride;
         const char* vb = c.v + h * c.head_stride;
         const int32_t* table = c.table + (long long)b * c.table_width;
@@ -1216,7 +1271,6 @@ __global__ void __launch_bounds__(kSplitThreads, 2) kv_slots_kernel(const Attent
 
         // Queries as the B operand: thread (row of eight lane / 4, elements by lane % 4), with the
         // sign of the scales, so that the largest product is the largest exponent.
-        uint32_t qb[kHeld ? NQ : 1][KS][2];
         float mul[NQ][2];  // from a product to the exponent (base 2), of this thread's columns
         const float ks_h = kF8 ? c.k_scale[h] : 1.0f;
         const float unit = fabsf(a.scale) * 1.4426950408889634f * fabsf(ks_h);
@@ -1224,29 +1278,19 @@ __global__ void __launch_bounds__(kSplitThreads, 2) kv_slots_kernel(const Attent
         // never 0, for 0 * -inf is NaN; a scale that is NaN stays so
         auto not_zero = [](float x) { return x < 1e-37f ? 1e-37f : x; };
 #pragma unroll
-        for (int nt = 0; nt < NQ; ++nt) {
-            const int row = nt * 8 + g8, R = mt * ROWS + row;
-            const int j = R / a.group, g = R - j * a.group;
-            const bool live = row < rows && !bad;
-            const T* q = (const T*)a.q + (live ? b * a.qb + j * a.qt +
-                                                     (long long)(h * a.group + g) * a.qh : 0);
-            uint32_t (&y)[KS][2] = qb[kHeld ? nt : 0];
+        for (int nt = 0; nt < NQ; ++nt) mul[nt][0] = mul[nt][1] = not_zero(unit);
+        {
             float top = 0.0f;
 #pragma unroll
-            for (int ks = 0; ks < KS; ++ks) {
-                // float8: 16 consecutive elements of a block of 64 per thread, 4 per step
-                const int e0 = kF8 ? (ks >> 2) * 64 + t4 * 16 + (ks & 3) * 4 : ks * 16 + t4 * 2;
-                const int e1 = kF8 ? e0 + 2 : e0 + 8;
-                const bool in = live && (kF8 ? e0 : ks * 16) < c.dim;
-                y[ks][0] = in ? __ldg((const uint32_t*)(q + e0)) ^ sign : 0u;
-                y[ks][1] = in ? __ldg((const uint32_t*)(q + e1)) ^ sign : 0u;
-                if constexpr (!kFit) {
-                    const float2 f0 = unpair<T>(y[ks][0]), f1 = unpair<T>(y[ks][1]);
-                    top = fmaxf(fmaxf(top, fmaxf(fabsf(f0.x), fabsf(f0.y))),
-                                fmaxf(fabsf(f1.x), fabsf(f1.y)));
+            for (int ks = 0; ks < KS; ++ks)
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                    qb[ks][x] ^= sign;
+                    if constexpr (!kFit) {
+                        const float2 f = unpair<T>(qb[ks][x]);
+                        top = fmaxf(top, fmaxf(fabsf(f.x), fabsf(f.y)));
+                    }
                 }
-            }
-            mul[nt][0] = mul[nt][1] = not_zero(unit);
             if constexpr (!kFit) {
                 top = fmaxf(top, __shfl_xor_sync(~0u, top, 1));
                 top = fmaxf(top, __shfl_xor_sync(~0u, top, 2));
@@ -1256,32 +1300,42 @@ __global__ void __launch_bounds__(kSplitThreads, 2) kv_slots_kernel(const Attent
                 const float down = exp2f((float)-e);
                 const float m = not_zero(fabsf(a.scale) * 1.4426950408889634f * exp2f((float)e) *
                                          fabsf(ks_h));
+                if (kHeld) {
 #pragma unroll
-                for (int x = 0; x < 2; ++x) mul[nt][x] = __shfl_sync(~0u, m, (2 * t4 + x) * 4);
+                    for (int x = 0; x < 2; ++x)
+                        mul[0][x] = __shfl_sync(~0u, m, (2 * t4 + x) * 4);
+                } else if (w < NQ && t4 == 0) {
+                    s_mul[w * 8 + g8] = m;
+                }
 #pragma unroll
                 for (int ks = 0; ks < KS; ++ks)
 #pragma unroll
                     for (int x = 0; x < 2; ++x) {
-                        const float2 f = unpair<T>(y[ks][x]);
-                        y[ks][x] = pair<__half>(f.x * down, f.y * down);
+                        const float2 f = unpair<T>(qb[ks][x]);
+                        qb[ks][x] = pair<__half>(f.x * down, f.y * down);
                     }
             }
-            if constexpr (!kHeld) {  // in shared memory, as each lane will want them
-                if (w == nt % 4)
+        }
+        if constexpr (!kHeld) {  // in shared memory, as each lane will want them
+            if (w < NQ)
 #pragma unroll
-                    for (int ks = 0; ks < KS; ks += 2)
-                        asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(
-                                         queries + (nt * (KS / 2) + ks / 2) * 512),
-                                     "r"(y[ks][0]), "r"(y[ks][1]), "r"(y[ks + 1][0]),
-                                     "r"(y[ks + 1][1]) : "memory");
+                for (int ks = 0; ks < KS; ks += 2)
+                    asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(
+                                     queries + (w * (KS / 2) + ks / 2) * 512),
+                                 "r"(qb[ks][0]), "r"(qb[ks][1]), "r"(qb[ks + 1][0]),
+                                 "r"(qb[ks + 1][1]) : "memory");
+            __syncthreads();
+            if constexpr (!kFit) {
+#pragma unroll
+                for (int nt = 0; nt < NQ; ++nt)
+#pragma unroll
+                    for (int x = 0; x < 2; ++x) mul[nt][x] = s_mul[nt * 8 + 2 * t4 + x];
             }
         }
-        if (!kHeld) __syncthreads();
         // Queries of steps ks and ks + 1.
         auto query = [&](int nt, int ks, uint32_t (&f)[4]) {
             if constexpr (kHeld)
-                f[0] = qb[nt][ks][0], f[1] = qb[nt][ks][1], f[2] = qb[nt][ks + 1][0],
-                f[3] = qb[nt][ks + 1][1];
+                f[0] = qb[ks][0], f[1] = qb[ks][1], f[2] = qb[ks + 1][0], f[3] = qb[ks + 1][1];
             else
                 asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
                              : "=r"(f[0]), "=r"(f[1]), "=r"(f[2]), "=r"(f[3])
@@ -1313,7 +1367,7 @@ __global__ void __launch_bounds__(kSplitThreads, 2) kv_slots_kernel(const Attent
             stage = stage == S - 1 ? 0 : stage + 1;
             const int slot0 = sh.tile<WINDOW>(t) * kUnit + w * 16;
             if (slot0 >= total) continue;
-            if (slot0 >= a.sinks && slot0 + 16 <= sh.view.low) continue;
+            if (slot0 >= a.sinks && slot0 <= sh.view.low - 16) continue;
 
             // Scores: 16 slots by NQ tiles of eight rows.
             float s[NQ][4];
@@ -1361,7 +1415,8 @@ __global__ void __launch_bounds__(kSplitThreads, 2) kv_slots_kernel(const Attent
                 }
             }
             // new tokens, the end or the window's beginning are among the 16
-            const bool fresh = mixed<WINDOW>(a, sh, slot0, 16);
+            const bool fresh =
+                slot0 > len - 15 || (slot0 < total - a.window && slot0 > a.sinks - 16);
             if (fresh) {
 #pragma unroll
                 for (int nt = 0; nt < NQ; ++nt)
@@ -1819,6 +1874,11 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     constexpr bool kFit = !kF8 || std::is_same<T, __half>::value;  // queries are of it already
     using L = Tc<DP, ROWS, kF8>;
     constexpr int SK = L::kK, SV = L::kV, CH = DP / 8;
+    // Registers of the roles, of a launch with 128 each: 256 threads of either kind.  With a window
+    // (more to keep about what a row sees) 184 and 72 leave a score in eight to local memory: trees
+    // of 16 nodes 128 us, of 65 345; 192 and 64: 125 and 331; 200 and 56: 121 and 334; 208 and 48:
+    // 123 and 341.
+    constexpr int kManyRegs = WINDOW ? 200 : 184, kFewRegs = 256 - kManyRegs;
     extern __shared__ __align__(1024) char smem_tc[];  // the swizzle counts from 1024
     __shared__ TcBars bars;
     __shared__ long long s_scan[kTcThreads / 32];
@@ -1883,7 +1943,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 
     if (kF8 && w >= 8 && w < 12) {
         // ------------------------------------------------ float8: bytes into halves
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kFewRegs));
         constexpr int kCh = DP / 16, R = L::kRaws > 0 ? L::kRaws : 1;  // 16-byte chunks of a row
         const int lt = tid - 256;
         int rs = 0, ds = 0;  // stages of bytes, of halves (keys and values have as many)
@@ -1973,7 +2033,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         }
     } else if (!kF8 && w >= 8 && w < 12) {
         // ------------------------------------------------ loads: a warp keys, a warp values
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kFewRegs));
         const bool vals = w > 8;
         const int stages = vals ? SV : SK;
         int pieces = 0, st = 0;
@@ -2085,7 +2145,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         }
     } else if (w >= 12) {
         // ------------------------------------------------ products
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kFewRegs));
         if (kF8 && w == 15) {
             // float8: bytes of keys and values, a box per page
             const int shift = min(c.page_shift, 7), boxes = kTcUnit >> shift;
@@ -2279,7 +2339,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         __syncwarp();
     } else {
         // ------------------------------------------------ weights: a row per thread
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 184;");
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kManyRegs));
         const int st = w >> 2, r = tid & 127;
         const uint32_t mine = tmem + ((uint32_t)(w & 3) * 32 << 16);
         const uint32_t sc = mine + st * 128, oc = mine + 256 + st * DP;
@@ -2330,7 +2390,10 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             // from a score to an exponent of two; the products carry the sign
             const float unit0 = fabsf(a.scale) * 1.4426950408889634f;
             const float ks_h = kF8 ? fabsf(c.k_scale[p.h]) : 1.0f;
-            float unit = unit0 * ks_h;
+            // (with a window never 0, so that a score of -inf, which no row looks at, is a weight of
+            // 0 by itself; a scale that is NaN stays so)
+            auto not_zero = [](float x) { return WINDOW && x < 1e-37f ? 1e-37f : x; };
+            float unit = not_zero(unit0 * ks_h);
             const bool busy = (two ? st * 128 : 0) + (w & 3) * 32 < p.rows;  // rows in this warp
             float l = 0.0f, ref = -INFINITY;
             int done = 0;  // jobs of this stream
@@ -2352,7 +2415,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 if (!ok) break;
                 tc_after();
                 if (!kFit && done == 0)
-                    unit = unit0 * exp2f((float)s_exp[pieces & 1][row]) * ks_h;
+                    unit = not_zero(unit0 * exp2f((float)s_exp[pieces & 1][row]) * ks_h);
                 if (!busy) {  // rows that nothing comes of: any weights will do
                     tc_before();
                     bar_arrive(&bars.p_full[st][0]);
@@ -2476,7 +2539,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                                         make_float2(unit, unit), make_float2(-less, -less));
                         v.x = ex2(v.x);
                         v.y = ex2(v.y);
-                        if (tail) {
+                        if (!WINDOW && tail) {
                             if (!(see[k] >> (2 * e) & 1)) v.x = 0.0f;
                             if (!(see[k] >> (2 * e + 1) & 1)) v.y = 0.0f;
                         }
@@ -2827,8 +2890,8 @@ static bool cache_map(CUtensorMap* map, void* base, const sv_kv_cache* c) {
 }
 
 // Shared memory of the many-row kernels.  *can: false where a compiler gave them other registers
-// than their roles share out (256 threads of 184, 256 of 72: those of a launch with 128 each; with
-// fewer the larger share would be waited for).
+// than their roles share out (256 threads each of two numbers whose sum is 256: those of a launch
+// with 128 each; with fewer the larger share would be waited for).
 template <bool WINDOW> static bool wide_setup(bool* can) {
     bool ok = true;
     *can = true;
@@ -3030,7 +3093,11 @@ static sv_status attend(const sv_kv_cache* cache, const void* q, const sv_stride
             ((double)cache->table_width * cache->page_size / unit + 1) >= (long double)(1ll << 50))
         return SV_ERR_UNSUPPORTED;
     if ((long long)B * cache->heads * mts >= (1ll << 31)) return SV_ERR_UNSUPPORTED;  // grid size
-    const int most = wide ? kTcMaxCtas : kMaxCtas, fit = wide ? sms : 2 * sms;
+    const int resident = WINDOW && !wide && !cluster
+                             ? slots_resident(tile / 8, cache->dim <= 64 ? 64 : 128,
+                                              elem_bytes(cache->dtype))
+                             : 2;
+    const int most = wide ? kTcMaxCtas : kMaxCtas, fit = wide ? sms : resident * sms;
     a.ctas = fit < most ? fit : most;
     const AttentionWs l = attention_ws(B, cache->heads, rows, cache->dim);
     a.mts = mts;
