@@ -275,6 +275,9 @@ __global__ void __launch_bounds__(kLpThreads, kLpResident) lp_kernel(const Args 
     const int G = cluster_size(), rank = cluster_rank();
     const int r = blockIdx.x / G;
 
+    // (launched while the kernel before ends; nothing is read before it has)
+    cudaGridDependencySynchronize();
+    cudaTriggerProgrammaticLaunchCompletion();
     int token = -1;
     if (tid < a.given) token = a.tokens[(long long)r * a.given + tid];
     if (!__syncthreads_or(token != -1)) return;  // (the whole cluster)
@@ -612,6 +615,8 @@ __global__ void __launch_bounds__(kThreads, 4) lp_grad_kernel(const GradArgs a) 
     __shared__ int s_token[kMaxGiven];
     __shared__ float s_g[kMaxGiven];
     const int tid = threadIdx.x, r = blockIdx.x / a.parts, part = blockIdx.x % a.parts;
+    cudaGridDependencySynchronize();
+    cudaTriggerProgrammaticLaunchCompletion();
     int token = -1;
     if (tid < a.given) token = a.tokens[(long long)r * a.given + tid];
     T* const out = (T*)a.grad + r * a.grad_stride;
@@ -781,17 +786,19 @@ static void base2(float T, float* high, float* low) {
 template <typename K, typename A>
 static sv_status launch(K kernel, int threads, int smem, long long ctas, int cluster,
                         cudaStream_t stream, const A& a) {
-    cudaLaunchAttribute attr;
-    attr.id = cudaLaunchAttributeClusterDimension;
-    attr.val.clusterDim.x = cluster;
-    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+    cudaLaunchAttribute attrs[2];
+    attrs[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attrs[0].val.programmaticStreamSerializationAllowed = 1;
+    attrs[1].id = cudaLaunchAttributeClusterDimension;
+    attrs[1].val.clusterDim.x = cluster;
+    attrs[1].val.clusterDim.y = attrs[1].val.clusterDim.z = 1;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)ctas);
     cfg.blockDim = dim3(threads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
-    cfg.attrs = &attr;
-    cfg.numAttrs = cluster > 1 ? 1 : 0;
+    cfg.attrs = attrs;
+    cfg.numAttrs = cluster > 1 ? 2 : 1;
     return cudaLaunchKernelEx(&cfg, kernel, a) == cudaSuccess ? SV_OK : SV_ERR_CUDA;
 }
 
