@@ -121,6 +121,14 @@ def test_batches(lp, dtype, R, V):
     Told(lp, rows, tokens, 0.8, 20).check(rows, tokens, 0.8, 20)
 
 
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_the_largest_vocabulary(lp, dtype):
+    V, g = 1 << 21, torch.Generator().manual_seed(2)
+    rows, tokens = zipf(2, V, g, dtype), some_tokens(2, V, 64, g)
+    Told(lp, rows, tokens, 1.0, 64).check(rows, tokens, 1.0, 64)
+    gradient_case(lp, rows, tokens, 1.0, True, V, V)
+
+
 @pytest.mark.parametrize("optional", [dict(entropy=False), dict(normalizer=False),
                                       dict(entropy=False, normalizer=False, status=False)])
 def test_outputs_that_nobody_wants(lp, optional):

@@ -85,10 +85,11 @@ def good(r, kv):
 @pytest.mark.parametrize("dtype,cache", TYPES)
 @pytest.mark.parametrize("dim", [16, 64, 80, 128])
 @pytest.mark.parametrize("order", ["slot", "head"])
-@pytest.mark.parametrize("N,group", [(3, 2), (5, 5), (6, 8), (20, 8)])
+@pytest.mark.parametrize("N,group", [(3, 2), (3, 5), (4, 6), (5, 5), (6, 8), (20, 8)])
 def test_types_and_heads(kv, dtype, cache, dim, order, N, group):
-    good(Windowed([37, 0, 230, 64], N, 50, 3, "tree", heads=3, group=group, dim=dim, dtype=dtype,
-                  cache=cache, order=order, seed=dim + N), kv)
+    """(Three heads: a cluster per item; ten: ranges.)"""
+    good(Windowed([37, 0, 230, 64], N, 50, 3, "tree", heads=3 if order == "slot" else 10,
+                  group=group, dim=dim, dtype=dtype, cache=cache, order=order, seed=dim + N), kv)
 
 
 @pytest.mark.parametrize("window", [1, 3, 16, 64, 65, 129, ALL])
@@ -104,10 +105,11 @@ def test_windows_and_first_slots(kv, window, sinks, N, form, heads, group):
 
 @pytest.mark.parametrize("page", [1, 4, 16, 64, 256])
 @pytest.mark.parametrize("window,sinks", [(1, 0), (33, 4), (100, 20)])
-@pytest.mark.parametrize("N,group", [(1, 3), (6, 3), (12, 8)])
-def test_lengths_around_borders(kv, page, window, sinks, N, group):
+@pytest.mark.parametrize("N,heads,group", [(1, 1, 3), (1, 3, 3), (6, 1, 3), (6, 3, 3), (12, 1, 8)])
+def test_lengths_around_borders(kv, page, window, sinks, N, heads, group):
     lens = [0, 1, 15, 16, 17, 32, 33, 63, 64, 65, 127, 128, 129, 191, 255, 256, 257, 300]
-    good(Windowed(lens, N, window, sinks, heads=1, group=group, dim=64, page=page, seed=page), kv)
+    good(Windowed(lens, N, window, sinks, heads=heads, group=group, dim=64, page=page, seed=page),
+         kv)
 
 
 @pytest.mark.parametrize("dtype,cache", TYPES)
@@ -146,20 +148,36 @@ def test_a_window_that_hides_nothing(kv, N, group, form, dtype, cache):
     assert torch.equal(out, full)
 
 
+@pytest.mark.parametrize("window,sinks", [(2 ** 31 - 1, 0), (1, 2 ** 31 - 1),
+                                          (2 ** 31 - 1, 2 ** 31 - 1)])
+@pytest.mark.parametrize("N,heads,group", [(3, 1, 4), (3, 20, 4), (9, 10, 8)])
+def test_the_largest_windows(kv, window, sinks, N, heads, group):
+    good(Windowed([200, 0, 31], N, window, sinks, "tree", heads=heads, group=group, dim=64), kv)
+
+
+@pytest.mark.parametrize("N,group", [(1, 4), (6, 4), (16, 8), (65, 4)])
+def test_the_same_bits_each_time(kv, N, group):
+    r = Windowed([900, 300, 0], N, 500, 20, "tree", heads=14, group=group, dim=64, seed=N)
+    first, _ = r.attend(kv)
+    for _ in range(4):
+        assert torch.equal(r.attend(kv)[0], first)
+
+
 @pytest.mark.parametrize("dtype,cache", TYPES)
 @pytest.mark.parametrize("N,group,form", [(6, 2, "chain"), (7, 4, "tree"), (16, 8, "tree"),
                                           (40, 8, "chain")])
-def test_hidden_places_may_hold_anything(kv, dtype, cache, N, group, form):
+@pytest.mark.parametrize("heads", [2, 10])
+def test_hidden_places_may_hold_anything(kv, heads, dtype, cache, N, group, form):
     """The first slot of the root's window is out of its descendants' reach: NaN or an infinity
     there reaches the root's row only; behind a first slot it would reach all."""
-    r = Windowed([270, 133, 160, 500], N, 40, 3, form, heads=2, group=group, dim=64, dtype=dtype,
-                 cache=cache, seed=5)
+    r = Windowed([270, 133, 160, 500], N, 40, 3, form, heads=heads, group=group, dim=64,
+                 dtype=dtype, cache=cache, seed=5)
     want, bound, _ = r.plain()
     for b, bad in enumerate((math.nan, math.inf, -math.inf, math.nan)):
         s = int(r.lens[b]) - 39
         at = int(r.table[b, s // r.page]), s % r.page
         for pool in (r.k, r.v):
-            pool[at] = torch.full((2, 64), bad if cache != E4M3 else math.nan).to(cache)
+            pool[at] = torch.full((heads, 64), bad if cache != E4M3 else math.nan).to(cache)
     out, status = r.attend(kv)
     assert status == [0] * 4
     assert bool(torch.isnan(out[:, 0].float()).any(dim=-1).all())
@@ -167,11 +185,12 @@ def test_hidden_places_may_hold_anything(kv, dtype, cache, N, group, form):
     assert bool((err <= bound[:, 1:]).all())
 
 
+@pytest.mark.parametrize("heads", [1, 20])
 @pytest.mark.parametrize("N,group", [(5, 2), (16, 8)])
-def test_new_tokens_out_of_reach(kv, N, group):
+def test_new_tokens_out_of_reach(kv, heads, N, group):
     """A window shorter than the chain: a new token that is not finite is seen by those behind it
     that its window still reaches."""
-    r = Windowed([100, 0], N, 3, 0, heads=1, group=group, dim=64, seed=6)
+    r = Windowed([100, 0], N, 3, 0, heads=heads, group=group, dim=64, seed=6)
     want, bound, _ = r.plain()
     for b in range(2):
         s = int(r.lens[b]) + 1
@@ -182,11 +201,12 @@ def test_new_tokens_out_of_reach(kv, N, group):
     assert bool((err <= bound)[:, 0].all()) and bool((err <= bound)[:, 4:].all())
 
 
+@pytest.mark.parametrize("heads", [2, 6])
 @pytest.mark.parametrize("N,group", [(6, 3), (20, 8)])
-def test_bad_data(kv, N, group):
+def test_bad_data(kv, heads, N, group):
     """Bad lengths, counts, trees and pages: NaN rows and the bit, the others untouched by it."""
     r = Windowed([240, 250, 260, 270, 280, 233, 220, 290], N, 30, 4, "tree",
-                 counts=[N, N, N, N, N, N, 3, N], heads=2, group=group, dim=64, seed=9)
+                 counts=[N, N, N, N, N, N, 3, N], heads=heads, group=group, dim=64, seed=9)
     want, bound, _ = r.plain()
     width = r.table.shape[1] * r.page
     r.lens[0] = -1
@@ -205,9 +225,10 @@ def test_bad_data(kv, N, group):
     assert bool((out[6, 3:] == 7.0).all())
 
 
+@pytest.mark.parametrize("heads", [1, 20])
 @pytest.mark.parametrize("N,group", [(1, 4), (16, 8)])
-def test_bad_page_where_the_window_begins(kv, N, group):
-    r = Windowed([1000, 1000], N, 100, 4, heads=1, group=group, dim=64, seed=1)
+def test_bad_page_where_the_window_begins(kv, heads, N, group):
+    r = Windowed([1000, 1000], N, 100, 4, heads=heads, group=group, dim=64, seed=1)
     want, bound, _ = r.plain()
     r.table[0, 901 // r.page] = -1
     out, status = r.attend(kv)
@@ -216,11 +237,12 @@ def test_bad_page_where_the_window_begins(kv, N, group):
     assert bool(((out[1].double() - want[1]).abs() <= bound[1]).all())
 
 
+@pytest.mark.parametrize("heads", [1, 40])
 @pytest.mark.parametrize("N,group,dtype,cache", [(1, 4, BF, BF), (9, 8, BF, BF), (9, 8, HF, E4M3),
                                                  (3, 8, BF, E4M3)])
-def test_positions_up_to_the_last_slot(kv, N, group, dtype, cache):
+def test_positions_up_to_the_last_slot(kv, heads, N, group, dtype, cache):
     """Positions just below 2^31, of which a window and four first slots are held."""
-    page, W, S, heads, dim = 128, 300, 4, 1, 64
+    page, W, S, dim = 128, 300, 4, 64
     width = (1 << 31) // page - 1
     n = width * page - N
     g = torch.Generator().manual_seed(N)
