@@ -61,7 +61,7 @@ extern "C" {
 
 #define SV_DEV_BAD_PAGE 0x80u
 #define SV_DEV_BAD_LENGTH 0x100u
-#define SV_DEV_TIMEOUT 0x200u /* spec_kv_attention: a bounded wait inside the kernel gave up */
+#define SV_DEV_TIMEOUT 0x200u /* attention: a bounded wait inside the kernel gave up */
 
 /* One layer of a paged cache.  Entry (page p, slot s, head h) starts at element
  * p*page_stride + s*slot_stride + h*head_stride of k and of v, its dim elements
@@ -182,7 +182,9 @@ sv_status spec_kv_attention(const sv_kv_cache* cache, const void* q, const sv_st
  * a window of kv_len + N or more hides nothing.
  * Slots from `sinks` to kv_len - window are looked at by no node: their table entries are not read,
  * so that pages which lie wholly among them may have been given back.  All other arguments,
- * results, errors and the arithmetic are those of spec_kv_attention, and so is the workspace. */
+ * results, errors and the arithmetic are those of spec_kv_attention, and so is the workspace (sums
+ * may be taken in another order).  The form is chosen from the sizes and types alone, the longest
+ * context being the window and the sinks, or what the table has room for where that is less. */
 sv_status spec_kv_attention_window(const sv_kv_cache* cache, const void* q,
                                    const sv_strides* q_strides, sv_dtype dtype,
                                    const int32_t* kv_len, const int32_t* num_new,

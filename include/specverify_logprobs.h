@@ -59,7 +59,10 @@ size_t spec_logprobs_workspace_size(int rows, int V, sv_dtype dtype, int given, 
  *   top_logprobs  [rows, top] fp32 (written): their ln p; -inf behind V of them.
  * A bad row gets NaN everywhere (top_tokens -1), a bad token NaN at its own place.
  * Workspace as for the verify calls (no initialisation; calls that share one must
- * not overlap). */
+ * not overlap).
+ * Accuracy: the exponential is off by 2^-21 at most and the sums by the fp32
+ * additions of a thread's share; ln p and H are off by about 1e-6 for rows of 2^18
+ * tokens.  Alternatives are told apart by their exact values. */
 sv_status spec_logprobs(const void* logits, sv_dtype dtype, int64_t row_stride,
                         const int32_t* tokens, float T, int rows, int V, int given, int top,
                         float* logprobs, float* normalizer, float* entropy, int32_t* top_tokens,

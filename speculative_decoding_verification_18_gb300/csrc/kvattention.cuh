@@ -1244,21 +1244,18 @@ __global__ void __launch_bounds__(kSplitThreads, Slots<CT, DP, NQ>::kResident)
             for (int i = 0; i < S - 1; ++i) issue(t0 + i, i, first[i]);
         }
 
-        // With the first slots on their way: the ancestors of every node, where this piece reaches
-        // the new tokens (with a window: in any case).
-        if (!bad && (WINDOW || (long long)t1 * kUnit > len) && anc_of != b) {
+        // With the first slots on their way: the ancestors of every node of a tree.
+        if (!bad && a.parents && anc_of != b) {
             __syncthreads();
             int f = 0;
-            if (a.parents)
-                for (int i = tid; i < sh.n; i += THREADS) {
-                    const int p = a.parents[(long long)b * a.N + i];
-                    s_par[i] = (uint8_t)p;
-                    f |= i > 0 && (p < 0 || p >= i);
-                }
+            for (int i = tid; i < sh.n; i += THREADS) {
+                const int p = a.parents[(long long)b * a.N + i];
+                s_par[i] = (uint8_t)p;
+                f |= i > 0 && (p < 0 || p >= i);
+            }
             f = __syncthreads_or(f);
             if (tid < sh.n && !f)
-                s_anc[tid] = ancestors_of<WINDOW>(a, sh, a.parents ? s_par : nullptr, tid,
-                                                  &s_deep[WINDOW ? tid : 0]);
+                s_anc[tid] = ancestors_of<WINDOW>(a, sh, s_par, tid, &s_deep[tid]);
             __syncthreads();
             if (f) {
                 bad = true;
@@ -1357,6 +1354,13 @@ __global__ void __launch_bounds__(kSplitThreads, Slots<CT, DP, NQ>::kResident)
             return min((mt * ROWS + nt * 8 + 2 * t4 + x) / a.group, sh.n - 1);
         };
 
+        // Whether node j looks at slot s.  (In a chain slots are positions for new tokens too.)
+        auto at_slot = [&](int j, int s) {
+            if (!a.parents)
+                return s <= len + j && (s < a.sinks || s >= low_of(a, sh, j));
+            return looks<WINDOW>(a, sh, s_anc[j], low_of(a, sh, s_deep[j]), s);
+        };
+
         int stage = 0;
         for (int t = t0; t < t1 && !bad; ++t) {
             asm volatile("cp.async.wait_group %0;" ::"n"(S - 2) : "memory");
@@ -1422,12 +1426,10 @@ __global__ void __launch_bounds__(kSplitThreads, Slots<CT, DP, NQ>::kResident)
                 for (int nt = 0; nt < NQ; ++nt)
 #pragma unroll
                     for (int x = 0; x < 2; ++x) {
-                        const int j = node_of(nt, x), low = low_of(a, sh, s_deep[j]);
-                        const uint64_t anc = s_anc[j];
+                        const int j = node_of(nt, x);
 #pragma unroll
                         for (int k = 0; k < 2; ++k)
-                            if (!looks<WINDOW>(a, sh, anc, low, slot0 + g8 + 8 * k))
-                                s[nt][2 * k + x] = -INFINITY;
+                            if (!at_slot(j, slot0 + g8 + 8 * k)) s[nt][2 * k + x] = -INFINITY;
                     }
             }
             // The reference of a row follows its maximum only when that has grown by 2^8: weights
@@ -1503,10 +1505,7 @@ __global__ void __launch_bounds__(kSplitThreads, Slots<CT, DP, NQ>::kResident)
                         for (int x = 0; x < 2; ++x) {
                             const float p = __shfl_sync(~0u, rw < 8 ? s[nt][x] : s[nt][2 + x],
                                                         (rw & 7) * 4 + t4);
-                            const int j = node_of(nt, x);
-                            if (!looks<WINDOW>(a, sh, s_anc[j], low_of(a, sh, s_deep[j]),
-                                               slot0 + rw))
-                                continue;
+                            if (!at_slot(node_of(nt, x), slot0 + rw)) continue;
 #pragma unroll
                             for (int k = 0; k < MT; ++k)
 #pragma unroll
