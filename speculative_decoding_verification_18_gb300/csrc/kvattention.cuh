@@ -211,25 +211,31 @@ struct View {
 
 // One sequence's share of the work, for row tiles of `rows` rows.  A unit of a tile of 256 rows
 // weighs as two where more than 128 of them are there: it takes both streams' time.
-struct Share {
+struct Count {
     int len, n, tiles, mts;
     int last;  // weight of the last row tile's units; the others weigh `full`
     bool bad;
-    View view;  // WINDOW only
     __device__ long long units(int heads, int full) const {
         return (long long)heads * tiles * (mts > 0 ? full * (mts - 1) + last : 0);
     }
+};
+// (Without a window no view is kept: 24 rows over an 8-bit cache lose 5 % to its registers.)
+template <bool WINDOW> struct Share : Count {
     // The place among the sequence's tiles of tile t of those that are looked at.
-    template <bool WINDOW> __device__ __forceinline__ int tile(int t) const {
-        return !WINDOW || t < view.first ? t : t + view.gap;
+    __device__ __forceinline__ int tile(int t) const { return t; }
+};
+template <> struct Share<true> : Count {
+    View view;
+    __device__ __forceinline__ int tile(int t) const {
+        return t < view.first ? t : t + view.gap;
     }
 };
 __device__ __forceinline__ constexpr int full_weight(int rows) { return rows > 128 ? 2 : 1; }
 
 template <bool WINDOW>
-__device__ __forceinline__ Share share_from(const AttentionArgs& a, int len, int n, int rows,
+__device__ __forceinline__ Share<WINDOW> share_from(const AttentionArgs& a, int len, int n, int rows,
                                             int unit) {
-    Share s;
+    Share<WINDOW> s;
     s.len = len;
     s.n = n;
     s.bad = !tokens_good(len, n, a.N, a.c);
@@ -251,20 +257,21 @@ __device__ __forceinline__ Share share_from(const AttentionArgs& a, int len, int
     return s;
 }
 template <bool WINDOW>
-__device__ __forceinline__ Share share_of(const AttentionArgs& a, int b, int rows, int unit) {
+__device__ __forceinline__ Share<WINDOW> share_of(const AttentionArgs& a, int b, int rows, int unit) {
     const int n = a.num_new ? a.num_new[b] : a.N;
     return share_from<WINDOW>(a, a.kv_len[b], n, rows, unit);
 }
 // Whether some node of a sequence looks at one of `slots` slots from s on.
 template <bool WINDOW>
-__device__ __forceinline__ bool in_view(const AttentionArgs& a, const Share& sh, long long s,
+__device__ __forceinline__ bool in_view(const AttentionArgs& a, const Share<WINDOW>& sh, long long s,
                                         int slots) {
-    if (WINDOW && s >= a.sinks && s + slots <= sh.view.low) return false;
+    if constexpr (WINDOW)
+        if (s >= a.sinks && s + slots <= sh.view.low) return false;
     return s < sh.len + sh.n;
 }
 // Whether some nodes of a sequence look at slot s and others do not, of those that are in view.
 template <bool WINDOW>
-__device__ __forceinline__ bool differs(const AttentionArgs& a, const Share& sh, long long s) {
+__device__ __forceinline__ bool differs(const AttentionArgs& a, const Share<WINDOW>& sh, long long s) {
     return s > sh.len || (WINDOW && s >= a.sinks && s < sh.len + sh.n - a.window);
 }
 // The lowest n bits (none below 0, all from 32 on).
@@ -273,8 +280,9 @@ __device__ __forceinline__ uint32_t bits_below(int n) {
 }
 // Whether some node of a sequence looks at slot s.
 template <bool WINDOW>
-__device__ __forceinline__ bool wanted(const AttentionArgs& a, const Share& sh, int s) {
-    if (WINDOW && s >= a.sinks && s < sh.view.low) return false;
+__device__ __forceinline__ bool wanted(const AttentionArgs& a, const Share<WINDOW>& sh, int s) {
+    if constexpr (WINDOW)
+        if (s >= a.sinks && s < sh.view.low) return false;
     return s < sh.len + sh.n;
 }
 
@@ -295,12 +303,11 @@ __device__ __forceinline__ long long range_start(long long W, int P, int c) {
 struct Piece {
     int b, h, mt, t0, t1, rows;
 };
-struct Walk {
+template <bool WINDOW> struct Walk {
     long long left;  // weight of the range still to come
     long long at;    // weight of the item before the range's part of it
     int b, item;
-    Share sh;
-    template <bool WINDOW>
+    Share<WINDOW> sh;
     __device__ __forceinline__ bool next(const AttentionArgs& a, int rows, int unit, Piece* p) {
         const int full = full_weight(rows);
         for (;;) {
@@ -340,7 +347,7 @@ __device__ __forceinline__ void tell_ends(const AttentionArgs& a, const Piece& p
 // The range of this CTA: weight of the units before each sequence (a scan over the batch), their
 // sum W, range blockIdx.x of those that W is cut into.
 template <int THREADS, bool WINDOW>
-__device__ __forceinline__ Walk start_walk(const AttentionArgs& a, int rows, int unit,
+__device__ __forceinline__ Walk<WINDOW> start_walk(const AttentionArgs& a, int rows, int unit,
                                            long long* s_scan, Start* s_start) {
     const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5, full = full_weight(rows);
     const int per = (a.B + THREADS - 1) / THREADS;
@@ -350,7 +357,7 @@ __device__ __forceinline__ Walk start_walk(const AttentionArgs& a, int rows, int
     for (int b = b0; b < b1; ++b) {
         n = a.num_new ? a.num_new[b] : a.N;
         len = a.kv_len[b];
-        const Share s = share_from<WINDOW>(a, len, n, rows, unit);
+        const Share<WINDOW> s = share_from<WINDOW>(a, len, n, rows, unit);
         sum += s.units(a.c.heads, full);
         // (here: a sequence without tokens has no piece that would say so)
         if (s.bad && blockIdx.x == 0) mark(a.status, b, SV_DEV_BAD_LENGTH);
@@ -386,7 +393,7 @@ __device__ __forceinline__ Walk start_walk(const AttentionArgs& a, int rows, int
         }
     }
     __syncthreads();
-    Walk k = {};
+    Walk<WINDOW> k = {};
     if (some) {
         k.left = range_start(W, P, blockIdx.x + 1) - x;
         k.b = s_start->b;
@@ -423,7 +430,7 @@ template <typename P> __device__ __forceinline__ const P* cluster_at(P* p, int k
 // The part of its cluster's item that this CTA takes: equal shares of the units, perhaps none.
 // False for an item that the sequence does not have (fewer tokens than the launch counts on).
 template <bool WINDOW>
-__device__ __forceinline__ bool item_piece(const AttentionArgs& a, int rows, int unit, Share* sh,
+__device__ __forceinline__ bool item_piece(const AttentionArgs& a, int rows, int unit, Share<WINDOW>* sh,
                                            Piece* p) {
     const int mts = (a.N * a.group + rows - 1) / rows, item = blockIdx.x / kCluster;
     p->mt = item % mts;
@@ -528,7 +535,7 @@ __device__ __forceinline__ bool sees(uint64_t anc, int i) { return i == 0 || (an
 // The ancestors (and itself) of node j, as bits for sees(); par: parents (NULL: a chain).  WINDOW:
 // those that its window reaches, and in *deep its depth.
 template <bool WINDOW>
-__device__ __forceinline__ uint64_t ancestors_of(const AttentionArgs& a, const Share& sh,
+__device__ __forceinline__ uint64_t ancestors_of(const AttentionArgs& a, const Share<WINDOW>& sh,
                                                  const uint8_t* par, int j, uint8_t* deep) {
     if (!WINDOW && !par) return j == 64 ? ~0ull : (1ull << j) - 1;
     uint64_t m = 0;
@@ -544,12 +551,12 @@ __device__ __forceinline__ uint64_t ancestors_of(const AttentionArgs& a, const S
 }
 // Where the window of a node of this depth begins.  Slots up to the root's are positions too, so
 // that one comparison with it and with the first slots decides them.
-__device__ __forceinline__ int low_of(const AttentionArgs& a, const Share& sh, int depth) {
+__device__ __forceinline__ int low_of(const AttentionArgs& a, const Count& sh, int depth) {
     return sh.len - a.window + 1 + depth;
 }
 // Whether a row with these ancestors and this window looks at slot s of the sequence's.
 template <bool WINDOW>
-__device__ __forceinline__ bool looks(const AttentionArgs& a, const Share& sh, uint64_t anc,
+__device__ __forceinline__ bool looks(const AttentionArgs& a, const Share<WINDOW>& sh, uint64_t anc,
                                       int low, int s) {
     const int i = s - sh.len;
     if (WINDOW && i <= 0) return s < a.sinks || s >= low;
@@ -558,7 +565,7 @@ __device__ __forceinline__ bool looks(const AttentionArgs& a, const Share& sh, u
 // Whether rows of the sequence differ in what they look at among `slots` slots from s0 on, or
 // slots there are looked at by none.
 template <bool WINDOW>
-__device__ __forceinline__ bool mixed(const AttentionArgs& a, const Share& sh, long long s0,
+__device__ __forceinline__ bool mixed(const AttentionArgs& a, const Share<WINDOW>& sh, long long s0,
                                       int slots) {
     if (s0 + slots > sh.len + 1ll) return true;
     return WINDOW && s0 < sh.len + sh.n - a.window && s0 + slots > a.sinks;
@@ -622,9 +629,9 @@ __global__ void __launch_bounds__(kSplitThreads * WM, 2) kv_split_kernel(const A
     cudaGridDependencySynchronize();
     cudaTriggerProgrammaticLaunchCompletion();
 
-    Walk walk = {};
+    Walk<WINDOW> walk = {};
     if constexpr (!CLUSTER) walk = start_walk<THREADS, WINDOW>(a, ROWS, kUnit, s_scan, &s_start);
-    const Share& sh = walk.sh;
+    const Share<WINDOW>& sh = walk.sh;
     const uint32_t base = (uint32_t)__cvta_generic_to_shared(smem);
     const uint32_t ring = base + w * S * St::kBytes;
     const uint32_t queries = base + L::kBody + wm * KS * 512 + lane * 16;
@@ -632,7 +639,7 @@ __global__ void __launch_bounds__(kSplitThreads * WM, 2) kv_split_kernel(const A
 
     Piece piece;
     while (CLUSTER ? item_piece<WINDOW>(a, ROWS, kUnit, &walk.sh, &piece)
-                   : walk.template next<WINDOW>(a, ROWS, kUnit, &piece)) {
+                   : walk.next(a, ROWS, kUnit, &piece)) {
         const int b = piece.b, h = piece.h, mt = piece.mt, t0 = piece.t0, t1 = piece.t1;
         const int len = sh.len, total = len + sh.n, rows = piece.rows;
         if (!CLUSTER && tid == 0) tell_ends(a, piece, sh.tiles);
@@ -645,11 +652,11 @@ __global__ void __launch_bounds__(kSplitThreads * WM, 2) kv_split_kernel(const A
         const int dch = c.dim * (int)sizeof(CT) / 16;
         bool bad_page = false;
         auto page_of = [&](int t) -> int {
-            const int s = sh.tile<WINDOW>(t) * kUnit + my;
+            const int s = sh.tile(t) * kUnit + my;
             return t < t1 && wanted<WINDOW>(a, sh, s) ? __ldg(table + (s >> c.page_shift)) : -1;
         };
         auto issue = [&](int t, int stage, int page) {
-            const int s = sh.tile<WINDOW>(t) * kUnit + my;
+            const int s = sh.tile(t) * kUnit + my;
             long long off = -1;
             if (t < t1 && wanted<WINDOW>(a, sh, s)) {
                 if ((unsigned)page < (unsigned)c.num_pages)
@@ -791,9 +798,10 @@ __global__ void __launch_bounds__(kSplitThreads * WM, 2) kv_split_kernel(const A
             page = page_of(t + S);
             const uint32_t kt = ring + stage * St::kBytes, vt = kt + 16 * St::kPitch;
             stage = stage == S - 1 ? 0 : stage + 1;
-            const int slot0 = sh.tile<WINDOW>(t) * kUnit + w * 16;
+            const int slot0 = sh.tile(t) * kUnit + w * 16;
             if (slot0 >= total) continue;
-            if (WINDOW && slot0 >= a.sinks && slot0 <= sh.view.low - 16) continue;
+            if constexpr (WINDOW)
+                if (slot0 >= a.sinks && slot0 <= sh.view.low - 16) continue;
 
             // Scores: 16 slots = two tiles of 8 columns.
             float s[2][4];
@@ -834,7 +842,9 @@ __global__ void __launch_bounds__(kSplitThreads * WM, 2) kv_split_kernel(const A
                 }
             }
             // new tokens, the end or the window's beginning are among the 16
-            const bool fresh = mixed<WINDOW>(a, sh, slot0, 16);
+            const bool fresh =
+                slot0 > len - 16 ||
+                (WINDOW && slot0 < total - a.window && slot0 > a.sinks - 16);
             if (fresh) {
 #pragma unroll
                 for (int half = 0; half < 2; ++half) {
@@ -1161,8 +1171,8 @@ __global__ void __launch_bounds__(kSplitThreads, Slots<CT, DP, NQ>::kResident)
     cudaGridDependencySynchronize();
     cudaTriggerProgrammaticLaunchCompletion();
 
-    Walk walk = start_walk<THREADS, WINDOW>(a, ROWS, kUnit, s_scan, &s_start);
-    const Share& sh = walk.sh;
+    Walk<WINDOW> walk = start_walk<THREADS, WINDOW>(a, ROWS, kUnit, s_scan, &s_start);
+    const Share<WINDOW>& sh = walk.sh;
     const uint32_t base = (uint32_t)__cvta_generic_to_shared(smem);
     const uint32_t ring = base + w * S * St::kBytes;
     const uint32_t queries = base + L::kBody + lane * 16;
@@ -1173,7 +1183,7 @@ __global__ void __launch_bounds__(kSplitThreads, Slots<CT, DP, NQ>::kResident)
     };
 
     Piece piece;
-    while (walk.template next<WINDOW>(a, ROWS, kUnit, &piece)) {
+    while (walk.next(a, ROWS, kUnit, &piece)) {
         const int b = piece.b, h = piece.h, mt = piece.mt, t0 = piece.t0, t1 = piece.t1;
         const int len = sh.len, total = len + sh.n, rows = piece.rows;
         if (tid == 0) tell_ends(a, piece, sh.tiles);
@@ -1205,11 +1215,11 @@ __global__ void __launch_bounds__(kSplitThreads, Slots<CT, DP, NQ>::kResident)
         const int dch = c.dim * (int)sizeof(CT) / 16;
         bool bad_page = false;
         auto page_of = [&](int t) -> int {
-            const int s = sh.tile<WINDOW>(t) * kUnit + my;
+            const int s = sh.tile(t) * kUnit + my;
             return t < t1 && wanted<WINDOW>(a, sh, s) ? __ldg(table + (s >> c.page_shift)) : -1;
         };
         auto issue = [&](int t, int stage, int page) {
-            const int s = sh.tile<WINDOW>(t) * kUnit + my;
+            const int s = sh.tile(t) * kUnit + my;
             long long off = -1;
             if (t < t1 && wanted<WINDOW>(a, sh, s)) {
                 if ((unsigned)page < (unsigned)c.num_pages)
@@ -1369,7 +1379,7 @@ __global__ void __launch_bounds__(kSplitThreads, Slots<CT, DP, NQ>::kResident)
             page = page_of(t + S);
             const uint32_t kt = ring + stage * St::kBytes, vt = kt + 16 * St::kPitch;
             stage = stage == S - 1 ? 0 : stage + 1;
-            const int slot0 = sh.tile<WINDOW>(t) * kUnit + w * 16;
+            const int slot0 = sh.tile(t) * kUnit + w * 16;
             if (slot0 >= total) continue;
             if (slot0 >= a.sinks && slot0 <= sh.view.low - 16) continue;
 
@@ -1934,7 +1944,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     }
 
     tc_before();
-    Walk walk = start_walk<kTcThreads, WINDOW>(a, ROWS, kTcUnit, s_scan, &s_start);
+    Walk<WINDOW> walk = start_walk<kTcThreads, WINDOW>(a, ROWS, kTcUnit, s_scan, &s_start);
     tc_after();
     const uint32_t tmem = s_tmem;
     volatile Watch* watch = &s_watch;
@@ -1948,10 +1958,10 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         int rs = 0, ds = 0;  // stages of bytes, of halves (keys and values have as many)
         uint32_t r_phase = 0, again = 1;
         bool ok = true;
-        while (walk.template next<WINDOW>(a, ROWS, kTcUnit, &p)) {
+        while (walk.next(a, ROWS, kTcUnit, &p)) {
             if (walk.sh.bad) continue;
             for (int t = p.t0; t < p.t1; ++t) {
-                const long long slot0 = (long long)walk.sh.tile<WINDOW>(t) * kTcUnit;
+                const long long slot0 = (long long)walk.sh.tile(t) * kTcUnit;
                 const bool edge = mixed<WINDOW>(a, walk.sh, slot0, kTcUnit);
 #pragma unroll 1
                 for (int kv = 0; kv < 2; ++kv) {
@@ -2044,11 +2054,11 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             const int shift = min(c.page_shift, 7), boxes = kTcUnit >> shift;
             const uint32_t bytes = (128u << shift) * (DP / 64);  // per page
             uint32_t again = 1;  // parity of the stage's last release
-            while (walk.template next<WINDOW>(a, ROWS, kTcUnit, &p)) {
+            while (walk.next(a, ROWS, kTcUnit, &p)) {
                 if (walk.sh.bad) continue;
                 const int32_t* table = c.table + (long long)p.b * c.table_width;
                 auto first_of = [&](int t) {  // slot of this lane's box
-                    return (long long)walk.sh.tile<WINDOW>(t) * kTcUnit +
+                    return (long long)walk.sh.tile(t) * kTcUnit +
                            ((long long)lane << shift);
                 };
                 auto page_of = [&](int t) -> int {
@@ -2059,7 +2069,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 };
                 int page = page_of(p.t0);
                 for (int t = p.t0; t < p.t1; ++t) {
-                    const long long slot0 = (long long)walk.sh.tile<WINDOW>(t) * kTcUnit;
+                    const long long slot0 = (long long)walk.sh.tile(t) * kTcUnit;
                     const long long s = first_of(t);
                     const uint32_t dst = (vals ? sv : sk) + st * L::kTile;
                     // values whose rows have to be looked through first land there
@@ -2097,10 +2107,10 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             // Two warps, so that the loads go on meanwhile.
             const int lt = tid - 320;
             uint32_t landed = 0;  // parities: tiles that have landed in each stage
-            while (walk.template next<WINDOW>(a, ROWS, kTcUnit, &p)) {
+            while (walk.next(a, ROWS, kTcUnit, &p)) {
                 if (walk.sh.bad) continue;
                 for (int t = p.t0; t < p.t1; ++t) {
-                    const long long slot0 = (long long)walk.sh.tile<WINDOW>(t) * kTcUnit;
+                    const long long slot0 = (long long)walk.sh.tile(t) * kTcUnit;
                     if (mixed<WINDOW>(a, walk.sh, slot0, kTcUnit)) {
                         const uint32_t dst = sv + st * L::kTile;
                         ok = ok && warp_wait(&bars.v_land[st], landed >> st & 1, watch);
@@ -2152,11 +2162,11 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             int pieces = 0, rs = 0;
             uint32_t again = 1;
             bool ok = true;
-            while (ok && walk.template next<WINDOW>(a, ROWS, kTcUnit, &p)) {
+            while (ok && walk.next(a, ROWS, kTcUnit, &p)) {
                 if (walk.sh.bad) continue;
                 const int32_t* table = c.table + (long long)p.b * c.table_width;
                 auto first_of = [&](int t) {  // slot of this lane's box
-                    return (long long)walk.sh.tile<WINDOW>(t) * kTcUnit +
+                    return (long long)walk.sh.tile(t) * kTcUnit +
                            ((long long)lane << shift);
                 };
                 auto page_of = [&](int t) -> int {
@@ -2195,7 +2205,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             const int lt = tid & 31 | (w - 13) << 5, dch = c.dim / 8;
             int pieces = 0;
             bool ok = true;
-            while (ok && walk.template next<WINDOW>(a, ROWS, kTcUnit, &p)) {
+            while (ok && walk.next(a, ROWS, kTcUnit, &p)) {
                 if (walk.sh.bad) continue;
                 ok = warp_wait(&bars.q_empty, (pieces & 1) ^ 1, watch);
                 auto query = [&](int row) {
@@ -2271,7 +2281,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             uint32_t k_phase = 0, v_phase = 0, pieces = 0, p_phase = 0;
             int issued = 0;
             bool ok = true;
-            while (ok && walk.template next<WINDOW>(a, ROWS, kTcUnit, &p)) {
+            while (ok && walk.next(a, ROWS, kTcUnit, &p)) {
                 if (walk.sh.bad) continue;
                 const bool two = p.rows > 128;
                 const int nt = p.t1 - p.t0, jobs = two ? 2 * nt : nt;
@@ -2346,8 +2356,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         long long tiles = 0;
         int pieces = 0, anc_of = -1;
         bool tree_bad = false, ok = true;  // a wait that gave up skips the rest, not the barriers
-        while (walk.template next<WINDOW>(a, ROWS, kTcUnit, &p)) {
-            const Share& sh = walk.sh;
+        while (walk.next(a, ROWS, kTcUnit, &p)) {
+            const Share<WINDOW>& sh = walk.sh;
             const bool two = p.rows > 128;
             const int row = two ? st * 128 + r : r, R = p.mt * ROWS + row;
             const int j = min(R / a.group, sh.n - 1), g = R - R / a.group * a.group;
@@ -2408,7 +2418,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 tc_wait_st();
             }
             for (int i = st; ok && i < jobs; i += 2, ++done) {
-                const int t = sh.tile<WINDOW>(p.t0 + (two ? i >> 1 : i));
+                const int t = sh.tile(p.t0 + (two ? i >> 1 : i));
                 ok = warp_wait(&bars.s_full[st], s_phase, watch);
                 s_phase ^= 1;
                 if (!ok) break;
@@ -2653,7 +2663,7 @@ __global__ void __launch_bounds__(128) kv_join_kernel(const AttentionArgs a, int
     if (item < 0) return;
     const int mt = item % a.mts, h = item / a.mts % c.heads, b = item / a.mts / c.heads;
     const int c0 = blockIdx.x, c1 = a.ended[item];
-    const Share sh = share_of<WINDOW>(a, b, rows, kUnit);
+    const Share<WINDOW> sh = share_of<WINDOW>(a, b, rows, kUnit);
     const int row = warps == 1 ? blockIdx.y * 4 + w : blockIdx.y;
     const int live = min(rows, sh.n * a.group - mt * rows);
     const bool mine = row < live;
@@ -2714,7 +2724,7 @@ __global__ void __launch_bounds__(128) kv_wide_join_kernel(const AttentionArgs a
     if (item < 0) return;
     const int mt = item % a.mts, h = item / a.mts % c.heads, b = item / a.mts / c.heads;
     const int c0 = blockIdx.x, c1 = a.ended[item];
-    const Share sh = share_of<WINDOW>(a, b, rows, kTcUnit);
+    const Share<WINDOW> sh = share_of<WINDOW>(a, b, rows, kTcUnit);
     const int cols = DP / 4 / (warps == 4 ? 1 : 4);  // blocks of four elements, or of sixteen
     const int row = blockIdx.y / cols * 32 + lane;
     const int d4 = warps == 4 ? blockIdx.y % cols : blockIdx.y % cols * 4 + w;
