@@ -233,7 +233,8 @@ template <> struct Share<true> : Count {
 __device__ __forceinline__ constexpr int full_weight(int rows) { return rows > 128 ? 2 : 1; }
 
 template <bool WINDOW>
-__device__ __forceinline__ Share<WINDOW> share_from(const AttentionArgs& a, int len, int n, int rows,
+__device__ __forceinline__ Share<WINDOW>
+share_from(const AttentionArgs& a, int len, int n, int rows,
                                             int unit) {
     Share<WINDOW> s;
     s.len = len;
@@ -257,21 +258,23 @@ __device__ __forceinline__ Share<WINDOW> share_from(const AttentionArgs& a, int 
     return s;
 }
 template <bool WINDOW>
-__device__ __forceinline__ Share<WINDOW> share_of(const AttentionArgs& a, int b, int rows, int unit) {
+__device__ __forceinline__ Share<WINDOW>
+share_of(const AttentionArgs& a, int b, int rows, int unit) {
     const int n = a.num_new ? a.num_new[b] : a.N;
     return share_from<WINDOW>(a, a.kv_len[b], n, rows, unit);
 }
 // Whether some node of a sequence looks at one of `slots` slots from s on.
 template <bool WINDOW>
-__device__ __forceinline__ bool in_view(const AttentionArgs& a, const Share<WINDOW>& sh, long long s,
-                                        int slots) {
+__device__ __forceinline__ bool in_view(const AttentionArgs& a, const Share<WINDOW>& sh,
+                                        long long s, int slots) {
     if constexpr (WINDOW)
         if (s >= a.sinks && s + slots <= sh.view.low) return false;
     return s < sh.len + sh.n;
 }
 // Whether some nodes of a sequence look at slot s and others do not, of those that are in view.
 template <bool WINDOW>
-__device__ __forceinline__ bool differs(const AttentionArgs& a, const Share<WINDOW>& sh, long long s) {
+__device__ __forceinline__ bool differs(const AttentionArgs& a, const Share<WINDOW>& sh,
+                                        long long s) {
     return s > sh.len || (WINDOW && s >= a.sinks && s < sh.len + sh.n - a.window);
 }
 // The lowest n bits (none below 0, all from 32 on).
@@ -430,8 +433,8 @@ template <typename P> __device__ __forceinline__ const P* cluster_at(P* p, int k
 // The part of its cluster's item that this CTA takes: equal shares of the units, perhaps none.
 // False for an item that the sequence does not have (fewer tokens than the launch counts on).
 template <bool WINDOW>
-__device__ __forceinline__ bool item_piece(const AttentionArgs& a, int rows, int unit, Share<WINDOW>* sh,
-                                           Piece* p) {
+__device__ __forceinline__ bool item_piece(const AttentionArgs& a, int rows, int unit,
+                                           Share<WINDOW>* sh, Piece* p) {
     const int mts = (a.N * a.group + rows - 1) / rows, item = blockIdx.x / kCluster;
     p->mt = item % mts;
     p->h = item / mts % a.c.heads;
@@ -1114,18 +1117,18 @@ __global__ void __launch_bounds__(kSplitThreads * WM, 2) kv_split_kernel(const A
     }
 }
 
-// CTAs per SM of kv_slots_kernel, for nq tiles of rows and elements of `bytes` bytes.
-__host__ __device__ constexpr int slots_resident(int nq, int dp, int bytes) {
-    return nq == 4 ? 2 : 3;
-}
+// CTAs per SM of kv_slots_kernel, for nq tiles of rows.  Three hide each other's beginnings and
+// ends better than two (chains of 1-6 over an 8-bit cache 78 against 80 us, decode over one 153
+// against 160); four tiles of rows take 255 registers, which three do not have.
+__host__ __device__ constexpr int slots_resident(int nq) { return nq == 4 ? 2 : 3; }
 // Slots of a window as rows: what kv_slots_kernel keeps in shared memory.
 template <typename CT, int DP, int NQ> struct Slots {
     using St = Stage<CT, DP>;
     // CTAs per SM, and stages that fit beside the others'
-    static constexpr int kResident = slots_resident(NQ, DP, (int)sizeof(CT));
+    static constexpr int kResident = slots_resident(NQ);
     static constexpr int kFit = (kResident == 3 ? 65536 : 98304) / (4 * St::kBytes);
     static constexpr int kStages = kFit > 6 ? 6 : kFit;
-    static constexpr int kRows = NQ * 8, kPitch = DP + 4;  // floats: rows in pairs eight banks apart
+    static constexpr int kRows = NQ * 8, kPitch = DP + 4;  // floats: pairs of rows 8 banks apart
     static constexpr int kRing = 4 * kStages * St::kBytes;
     static constexpr int kMerge = 4 * kRows * kPitch * 4 + 4 * kRows * 8;
     static constexpr int kBody = kRing > kMerge ? kRing : kMerge;
@@ -1141,10 +1144,15 @@ __device__ __forceinline__ uint32_t turned(uint32_t x) {
 
 // The same for windows: slots are the rows of the products and query rows their columns, eight to a
 // tile, so that a warp turns its keys and values into operands once for all query rows, whatever
-// their number up to 32, and rows past the last fill at most seven columns.  Scores come with slots in
-// the place of rows; the weights are transposed in registers on the way into the second product.  A
-// warp walks its own 16 slots of every unit, with its own ring of stages, and no lane asks the others
-// for a maximum unless a product has outgrown the reference.
+// their number up to 32, and rows past the last fill at most seven columns.  Scores come with
+// slots in the place of rows; the weights are transposed in registers on the way into the second
+// product.  A warp walks its own 16 slots of every unit, with its own ring of stages, and no lane
+// asks the others for a maximum unless a product has outgrown the reference.
+//
+// Over a 16-bit cache memory is the bound: one token behind 64 windows of 4096, 32/8 heads of 128,
+// 163 us, 6.6 TB/s.  Over an 8-bit one fixed latencies are: 24 rows, 96 windows of 1024, 75 us,
+// 2.8 TB/s (issue slots 46 % busy); a third of a CTA's time is where its pieces begin and end. 
+// The split kernel with a window took 107 us there.
 template <typename T, typename CT, int DP, int NQ>
 __global__ void __launch_bounds__(kSplitThreads, Slots<CT, DP, NQ>::kResident)
     kv_slots_kernel(const AttentionArgs a) {
@@ -1349,8 +1357,8 @@ __global__ void __launch_bounds__(kSplitThreads, Slots<CT, DP, NQ>::kResident)
                              : "r"(queries + (nt * (KS / 2) + ks / 2) * 512) : "memory");
         };
 
-        // Outputs, elements by rows: thread (elements g8 and g8 + 8 of 16, rows 2 t4 and 2 t4 + 1 of
-        // eight); the rows' sums over this thread's slots and references.
+        // Outputs, elements by rows: thread (elements g8 and g8 + 8 of 16, rows 2 t4 and 2 t4 + 1
+        // of eight); the rows' sums over this thread's slots and references.
         float o[MT][NQ][4], l[NQ][2], mr[NQ][2];
 #pragma unroll
         for (int nt = 0; nt < NQ; ++nt) {
@@ -1568,7 +1576,8 @@ __global__ void __launch_bounds__(kSplitThreads, Slots<CT, DP, NQ>::kResident)
                     uint32_t f[4], even[4], odd[4];
                     ldsm4t(f, vt + St::at((lane & 7) + (lane >> 4) * 8, k + (lane >> 3 & 1)));
 #pragma unroll
-                    for (int x = 0; x < 4; ++x) widen(even[x], odd[x], __byte_perm(f[x], 0, 0x3120));
+                    for (int x = 0; x < 4; ++x)
+                        widen(even[x], odd[x], __byte_perm(f[x], 0, 0x3120));
 #pragma unroll
                     for (int nt = 0; nt < NQ; ++nt) {
                         mma<M>(o[k][nt], even, ph[nt][0], ph[nt][1]);
@@ -1883,10 +1892,10 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     constexpr bool kFit = !kF8 || std::is_same<T, __half>::value;  // queries are of it already
     using L = Tc<DP, ROWS, kF8>;
     constexpr int SK = L::kK, SV = L::kV, CH = DP / 8;
-    // Registers of the roles, of a launch with 128 each: 256 threads of either kind.  With a window
-    // (more to keep about what a row sees) 184 and 72 leave a score in eight to local memory: trees
-    // of 16 nodes 128 us, of 65 345; 192 and 64: 125 and 331; 200 and 56: 121 and 334; 208 and 48:
-    // 123 and 341.
+    // Registers of the roles, of a launch with 128 each: 256 threads of either kind.  With a
+    // window (more to keep about what a row sees) 184 and 72 leave a score in eight to local
+    // memory: trees of 16 nodes 128 us, of 65 345; 192 and 64: 125 and 331; 200 and 56: 121 and
+    // 334 (with the later steps 114 and 302); 208 and 48: 123 and 341.
     constexpr int kManyRegs = WINDOW ? 200 : 184, kFewRegs = 256 - kManyRegs;
     extern __shared__ __align__(1024) char smem_tc[];  // the swizzle counts from 1024
     __shared__ TcBars bars;
@@ -2049,8 +2058,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         bool ok = true;  // once a wait gave up: no more copies, the barriers among the warps stay
         if (w < 10) {
             const CUtensorMap* const map = vals ? &vmap : &kmap;
-            // A page is one box per panel (its first 128 slots where it is larger): this lane's page
-            // of a tile.
+            // A page is one box per panel (its first 128 slots where it is larger): this lane's
+            // page of a tile.
             const int shift = min(c.page_shift, 7), boxes = kTcUnit >> shift;
             const uint32_t bytes = (128u << shift) * (DP / 64);  // per page
             uint32_t again = 1;  // parity of the stage's last release
@@ -2101,10 +2110,10 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 ++pieces;
             }
         } else {
-            // A masked entry may hold anything, but 0 times NaN is NaN: what nobody looks at (behind
-            // the last token, between the first slots and the window) is zeroed here, and so are
-            // values that are not finite and only some rows look at; those are added row by row.
-            // Two warps, so that the loads go on meanwhile.
+            // A masked entry may hold anything, but 0 times NaN is NaN: what nobody looks at
+            // (behind the last token, between the first slots and the window) is zeroed here, and
+            // so are values that are not finite and only some rows look at; those are added row by
+            // row. Two warps, so that the loads go on meanwhile.
             const int lt = tid - 320;
             uint32_t landed = 0;  // parities: tiles that have landed in each stage
             while (walk.next(a, ROWS, kTcUnit, &p)) {
@@ -2399,8 +2408,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             // from a score to an exponent of two; the products carry the sign
             const float unit0 = fabsf(a.scale) * 1.4426950408889634f;
             const float ks_h = kF8 ? fabsf(c.k_scale[p.h]) : 1.0f;
-            // (with a window never 0, so that a score of -inf, which no row looks at, is a weight of
-            // 0 by itself; a scale that is NaN stays so)
+            // (with a window never 0, so that a score of -inf, which no row looks at, is a weight
+            // of 0 by itself; a scale that is NaN stays so)
             auto not_zero = [](float x) { return WINDOW && x < 1e-37f ? 1e-37f : x; };
             float unit = not_zero(unit0 * ks_h);
             const bool busy = (two ? st * 128 : 0) + (w & 3) * 32 < p.rows;  // rows in this warp
@@ -2775,18 +2784,20 @@ static bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 
 // of a key head per CTA, or 32 where there are more (one CTA then reads each key once for all).
 template <bool CLUSTER, bool WINDOW, typename F>
 static auto with_split(sv_dtype dtype, sv_dtype cache, int dim, int rows, F f) {
-    auto sized = [&](auto t, auto ct) {
+    auto tiled = [&](auto t, auto ct, auto dp, auto wm) {
         using T = decltype(t);
         using CT = decltype(ct);
-        if (dim <= 64)
-            return rows <= 16 ? f(kv_split_kernel<T, CT, 64, 1, CLUSTER, WINDOW>, kv_join_kernel<T, 64, WINDOW>,
-                                  Split<CT, 64, 1>::kSmem)
-                              : f(kv_split_kernel<T, CT, 64, 2, CLUSTER, WINDOW>, kv_join_kernel<T, 64, WINDOW>,
-                                  Split<CT, 64, 2>::kSmem);
-        return rows <= 16 ? f(kv_split_kernel<T, CT, 128, 1, CLUSTER, WINDOW>, kv_join_kernel<T, 128, WINDOW>,
-                              Split<CT, 128, 1>::kSmem)
-                          : f(kv_split_kernel<T, CT, 128, 2, CLUSTER, WINDOW>, kv_join_kernel<T, 128, WINDOW>,
-                              Split<CT, 128, 2>::kSmem);
+        constexpr int DP = decltype(dp)::value, WM = decltype(wm)::value;
+        return f(kv_split_kernel<T, CT, DP, WM, CLUSTER, WINDOW>, kv_join_kernel<T, DP, WINDOW>,
+                 Split<CT, DP, WM>::kSmem);
+    };
+    auto sized = [&](auto t, auto ct) {
+        constexpr std::integral_constant<int, 1> one;
+        constexpr std::integral_constant<int, 2> two;
+        constexpr std::integral_constant<int, 64> d64;
+        constexpr std::integral_constant<int, 128> d128;
+        if (dim <= 64) return rows <= 16 ? tiled(t, ct, d64, one) : tiled(t, ct, d64, two);
+        return rows <= 16 ? tiled(t, ct, d128, one) : tiled(t, ct, d128, two);
     };
     if (dtype == SV_BF16)
         return cache == SV_E4M3 ? sized(__nv_bfloat16(), __nv_fp8_e4m3())
@@ -2828,19 +2839,19 @@ template <bool WINDOW> static int few_rows_tile(int rows) {
 // The same for the wide kernel: tiles of 128 rows, or of two times 128.
 template <bool WINDOW, typename F>
 static auto with_wide(sv_dtype dtype, sv_dtype cache, int dim, int rows, F f) {
-    auto sized = [&](auto t, auto ct) {
+    auto tiled = [&](auto t, auto ct, auto dp, auto tile) {
         using T = decltype(t);
         using CT = decltype(ct);
-        constexpr bool F8 = sizeof(CT) == 1;
-        if (dim <= 64)
-            return rows <= 128 ? f(kv_wide_kernel<T, CT, 64, 128, WINDOW>, kv_wide_join_kernel<T, 64, WINDOW>,
-                                   Tc<64, 128, F8>::kSmem)
-                               : f(kv_wide_kernel<T, CT, 64, 256, WINDOW>, kv_wide_join_kernel<T, 64, WINDOW>,
-                                   Tc<64, 256, F8>::kSmem);
-        return rows <= 128 ? f(kv_wide_kernel<T, CT, 128, 128, WINDOW>, kv_wide_join_kernel<T, 128, WINDOW>,
-                               Tc<128, 128, F8>::kSmem)
-                           : f(kv_wide_kernel<T, CT, 128, 256, WINDOW>, kv_wide_join_kernel<T, 128, WINDOW>,
-                               Tc<128, 256, F8>::kSmem);
+        constexpr int DP = decltype(dp)::value, ROWS = decltype(tile)::value;
+        return f(kv_wide_kernel<T, CT, DP, ROWS, WINDOW>, kv_wide_join_kernel<T, DP, WINDOW>,
+                 Tc<DP, ROWS, sizeof(CT) == 1>::kSmem);
+    };
+    auto sized = [&](auto t, auto ct) {
+        constexpr std::integral_constant<int, 64> d64;
+        constexpr std::integral_constant<int, 128> d128;
+        constexpr std::integral_constant<int, 256> r256;
+        if (dim <= 64) return rows <= 128 ? tiled(t, ct, d64, d128) : tiled(t, ct, d64, r256);
+        return rows <= 128 ? tiled(t, ct, d128, d128) : tiled(t, ct, d128, r256);
     };
     if (dtype == SV_BF16)
         return cache == SV_E4M3 ? sized(__nv_bfloat16(), __nv_fp8_e4m3())
@@ -3102,10 +3113,7 @@ static sv_status attend(const sv_kv_cache* cache, const void* q, const sv_stride
             ((double)cache->table_width * cache->page_size / unit + 1) >= (long double)(1ll << 50))
         return SV_ERR_UNSUPPORTED;
     if ((long long)B * cache->heads * mts >= (1ll << 31)) return SV_ERR_UNSUPPORTED;  // grid size
-    const int resident = WINDOW && !wide && !cluster
-                             ? slots_resident(tile / 8, cache->dim <= 64 ? 64 : 128,
-                                              elem_bytes(cache->dtype))
-                             : 2;
+    const int resident = WINDOW && !wide && !cluster ? slots_resident(tile / 8) : 2;
     const int most = wide ? kTcMaxCtas : kMaxCtas, fit = wide ? sms : resident * sms;
     a.ctas = fit < most ? fit : most;
     const AttentionWs l = attention_ws(B, cache->heads, rows, cache->dim);
