@@ -25,8 +25,8 @@
  *    the caller zeroes it when it wants fresh bits.
  *      SV_DEV_BAD_ROW    a NaN or +inf among the row's logits, or all are -inf;
  *      SV_DEV_BAD_TOKEN  a token below -1 or not below V.
- *  - Limits: V <= 2^21, rows < 2^27, rows * row_stride < 2^40.  rows == 0
- *    launches nothing.
+ *  - Limits: V <= 2^21, rows < 2^27, rows * row_stride < 2^40, T from 2^-100 to
+ *    2^100.  rows == 0 launches nothing.
  *  - The arithmetic is fp32, whatever the type of the logits; results repeat bit
  *    for bit.
  */

@@ -250,11 +250,15 @@ __device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
 // that reach the bound are put in order by counting, and rank 0 joins the lists of the cluster's
 // CTAs.
 //
-// Measured: 4096 rows of 128256 in bf16 without entropy and alternatives 157 us, 6.7 TB/s (memory);
-// with the entropy 167 us, with it and 20 alternatives 205 us (instructions: the second product per
-// element, and a warp's turn of many small steps at the end of each row).  Stages of two vectors
-// instead of four, five CTAs per SM: 162, 178 and 220 us; 128 threads: 160, 164 and 211 us, but 32
-// instead of 24 us for nine rows of 256000 with five alternatives by one CTA each.
+// Measured: 4096 rows of 128256 in bf16 without entropy and alternatives 156 us, 6.7 TB/s
+// (memory); 300 of 65537 in fp32 with eight alternatives 18.2 us, 576 of 151936, half of them
+// without tokens, with 20 alternatives 29.8 us, nine of 256000 with five 11.2 us (the steps behind
+// the row wait for one another: 3 us, 7 where others keep the SM busy).  Choices, measured before
+// the kernel was launched ahead of the end of the one before it: 157 us on the first of these, 167
+// with the entropy, 205 with it and 20 alternatives (instructions: the second product per element,
+// and a warp's turn of many small steps at the end of each row).  Stages of two vectors instead of
+// four, five CTAs per SM: 162, 178 and 220 us; 128 threads: 160, 164 and 211 us, but 32 instead of
+// 24 us for nine rows of 256000 with five alternatives by one CTA each.
 constexpr int kLpThreads = 256, kLpWarps = kLpThreads / 32;
 constexpr int kLpBatch = 4;      // vectors of a thread per stage
 constexpr int kLpStages = 3;
@@ -589,16 +593,14 @@ constexpr int kGradBatches = 2;  // of kBatch vectors per thread: a CTA's part o
 template <typename T>
 __device__ __forceinline__ uint4 shifted(const uint4& a, const uint4& b, int o) {
     constexpr int kPer = 4 / sizeof(T);  // elements per word
-    uint32_t w[5];
-    switch (o / kPer) {
-        case 0: w[0] = a.x, w[1] = a.y, w[2] = a.z, w[3] = a.w, w[4] = b.x; break;
-        case 1: w[0] = a.y, w[1] = a.z, w[2] = a.w, w[3] = b.x, w[4] = b.y; break;
-        case 2: w[0] = a.z, w[1] = a.w, w[2] = b.x, w[3] = b.y, w[4] = b.z; break;
-        default: w[0] = a.w, w[1] = b.x, w[2] = b.y, w[3] = b.z, w[4] = b.w; break;
-    }
-    if (kPer == 2 && o % 2) {
+    const bool two = o / kPer & 2, one = o / kPer & 1;
+    uint32_t w[6] = {two ? a.z : a.x, two ? a.w : a.y, two ? b.x : a.z,
+                     two ? b.y : a.w, two ? b.z : b.x, two ? b.w : b.y};
 #pragma unroll
-        for (int k = 0; k < 4; ++k) w[k] = __funnelshift_r(w[k], w[k + 1], 16);
+    for (int k = 0; k < 5; ++k) w[k] = one ? w[k + 1] : w[k];
+    if (kPer == 2) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) w[k] = __funnelshift_r(w[k], w[k + 1], o % 2 * 16);
     }
     return make_uint4(w[0], w[1], w[2], w[3]);
 }
@@ -606,10 +608,18 @@ __device__ __forceinline__ uint4 shifted(const uint4& a, const uint4& b, int o) 
 // A part of a row per CTA: each logit read once, its gradient written once, in vectors of the
 // gradient's row (where the logits lie at another place of a 16-byte word: two of theirs, shifted
 // together: SHIFT).  With x = (l - m) / T in base 2 and less ln S, p = 2^x, a gradient is
-// p (A + B x): A and B are the row's.  Then the places of given tokens again, with their own share (their logits
-// are read before anything is written, so that the gradient may take the logits' place).
+// p (A + B x): A and B are the row's.  Then the places of given tokens again, with their own share
+// (their logits are read before anything is written, so that the gradient may take the logits'
+// place).
+//
+// Bound by memory: 4096 rows of 128256 in bf16 310 us, 6.8 TB/s (all of them read); 1024 of 65537
+// in fp32 with the entropy and 32 tokens each 87 us, 6.2 TB/s.  Shifted, the first takes 352 us,
+// and in fp32 630 where rows that lie alike take 598: a warp's vectors lie side by side and a lane
+// has what lies behind its own from its neighbour (two loads per vector, each waited for by its
+// shift: 528 and 1095 us; from the neighbour, but with the next batch under way and thus three
+// CTAs per SM: 426 and 814; four CTAs without it 357 and 647, five 352 and 630).
 template <typename T, bool ENTROPY, bool SHIFT>
-__global__ void __launch_bounds__(kThreads, 4) lp_grad_kernel(const GradArgs a) {
+__global__ void __launch_bounds__(kThreads, SHIFT ? 5 : 4) lp_grad_kernel(const GradArgs a) {
     using E = Elt<T>;
     constexpr int VW = E::kVec;
     __shared__ int s_token[kMaxGiven];
@@ -647,14 +657,23 @@ __global__ void __launch_bounds__(kThreads, 4) lp_grad_kernel(const GradArgs a) 
         return to.whole(i) &&
                (off == 0 || (from.whole(i - back) && i - back >= 0 && from.whole(i - back + 1)));
     };
-    auto load = [&](int i) -> uint4 {
-        if (i >= i1 || !fast(i)) return make_uint4(0, 0, 0, 0);
-        if (off == 0) return ld_own16(from.at(i));
-        return shifted<T>(ld_own16(from.at(i - back)), ld_own16(from.at(i - back + 1)), by);
+    // Vector q of this thread in batch n.  Shifted ones are a warp's side by side: what lies behind
+    // a lane's is its neighbour's, and the warp's last has one vector more.
+    const int lane = tid % 32;
+    auto place = [&](int n, int q) {
+        return i0 + n * kThreads * kBatch +
+               (SHIFT ? (tid - lane) * kBatch + q * 32 + lane : q * kThreads + tid);
     };
-    uint4 x[kBatch];
+    auto load = [&](int i) {
+        if (!SHIFT) return i < i1 && fast(i) ? ld_own16(from.at(i)) : uint4();
+        const int j = i - back;  // (i may lie one behind this CTA's part)
+        return i <= i1 && j >= 0 && from.whole(j) ? ld_stream16(from.at(j)) : uint4();
+    };
+    auto behind = [&](int n) { return lane == 31 ? load(place(n, kBatch - 1) + 1) : uint4(); };
+    uint4 x[kBatch], last = {};
 #pragma unroll
-    for (int q = 0; q < kBatch; ++q) x[q] = load(i0 + tid + q * kThreads);
+    for (int q = 0; q < kBatch; ++q) x[q] = load(place(0, q));
+    if (SHIFT) last = behind(0);
 
     const float2 z = reinterpret_cast<const float2*>(a.normalizer)[r];
     const float m = z.x, log_s = z.y;
@@ -686,25 +705,34 @@ __global__ void __launch_bounds__(kThreads, 4) lp_grad_kernel(const GradArgs a) 
         return p * (ENTROPY ? fmaf(B, max_nan(y, -1e4f), A) : A);
     };
     for (int n = 0;; ++n) {
-        const int i = i0 + n * kThreads * kBatch + tid;
         uint4 next[kBatch];
-        if (n + 1 < kGradBatches) {
+        if (!SHIFT && n + 1 < kGradBatches) {
 #pragma unroll
-            for (int q = 0; q < kBatch; ++q) next[q] = load(i + (kBatch + q) * kThreads);
+            for (int q = 0; q < kBatch; ++q) next[q] = load(place(n + 1, q));
         }
 #pragma unroll
         for (int q = 0; q < kBatch; ++q) {
-            const int k = i + q * kThreads;
+            const int k = place(n, q);
+            uint4 v = x[q];
+            if (SHIFT) {
+                const uint4 y = lane ? v : q + 1 < kBatch ? x[(q + 1) % kBatch] : last;
+                const int up = (lane + 1) % 32;
+                uint4 o = {__shfl_sync(~0u, y.x, up), __shfl_sync(~0u, y.y, up),
+                           __shfl_sync(~0u, y.z, up), __shfl_sync(~0u, y.w, up)};
+                if (q + 1 == kBatch && lane == 31) o = last;
+                v = shifted<T>(v, o, by);
+            }
             if (k >= i1 || !fast(k)) continue;
             float f[VW];
-            E::unpack(x[q], f);
+            E::unpack(v, f);
 #pragma unroll
             for (int e = 0; e < VW; ++e) f[e] = grad(f[e]);
             to16[k] = E::pack(f);
         }
         if (n + 1 == kGradBatches) break;
 #pragma unroll
-        for (int q = 0; q < kBatch; ++q) x[q] = next[q];
+        for (int q = 0; q < kBatch; ++q) x[q] = SHIFT ? load(place(n + 1, q)) : next[q];
+        if (SHIFT) last = behind(n + 1);
     }
     if (tid < 4 * VW) {
         const int n = tid / VW, i = n < 2 ? n : to.vectors - 4 + n;
@@ -766,6 +794,8 @@ static sv_status check_rows(const void* logits, sv_dtype dtype, int64_t stride,
     if (dtype != SV_BF16 && dtype != SV_F32) return SV_ERR_INVALID_ARG;
     if (rows < 0 || V < 1 || given < 1 || stride < V) return SV_ERR_INVALID_ARG;
     if (!(T > 0.0f) || !std::isfinite(T)) return SV_ERR_INVALID_ARG;
+    // (so that 1 / T, T times a sum and a far element's share of one stay within fp32)
+    if (T < 0x1p-100f || T > 0x1p100f) return SV_ERR_UNSUPPORTED;
     if (V > kMaxV || given > kMaxGiven || rows >= (1 << 27) || stride >= (1ll << 40) ||
         (long double)rows * stride >= (long double)(1ll << 40))
         return SV_ERR_UNSUPPORTED;
@@ -775,9 +805,9 @@ static sv_status check_rows(const void* logits, sv_dtype dtype, int64_t stride,
 }
 
 // log2(e) / T as a sum of two floats, the second positive, so that it may be multiplied with
-// -infinity too; for the smallest T the largest float (0 times infinity is NaN).
+// -infinity too (0 times infinity is NaN).
 static void base2(float T, float* high, float* low) {
-    const double c = std::fmin(1.4426950408889634 / T, (double)FLT_MAX);
+    const double c = 1.4426950408889634 / T;
     *high = (float)c;
     while (!((double)*high < c)) *high = std::nextafterf(*high, 0.0f);
     *low = std::fmax((float)(c - *high), std::nextafterf(0.0f, 1.0f));
@@ -840,9 +870,9 @@ sv_status spec_logprobs(const void* logits, sv_dtype dtype, int64_t row_stride,
     base2(T, &a.c, &a.c_low);
     // A cluster per row while its CTAs have SMs of their own and runs worth a CTA's beginning and
     // end (9 rows of 256000, 5 alternatives: G = 1 20.4 us, 2 16.5, 4 14.5, 8 14.2; 40 of 128256:
-    // 16.6, 16.0, 16.6, 18.5; 5 of 32000: 8.5, 10.4).  More rows: a CTA each (300 of 65537: 20.7 us,
-    // two each 24.8; 1024 of 32000: 26.9 and 45.1), but two each where all would be resident at
-    // once and the rows that hold tokens met on some SMs by chance (576 of 151936, half of them
+    // 16.6, 16.0, 16.6, 18.5; 5 of 32000: 8.5, 10.4).  More rows: a CTA each (300 of 65537: 20.7
+    // us, two each 24.8; 1024 of 32000: 26.9 and 45.1), but two each where all would be resident
+    // at once and the rows that hold tokens met on some SMs by chance (576 of 151936, half of them
     // without tokens: 41 and 32 us; all with tokens: 45 and 55).
     int G = 1;
     while (G < kMaxCluster && 2ll * rows * G <= sms && V / G >= 49152) G *= 2;

@@ -156,3 +156,13 @@ def test_plain_gradient_is_autograds():
         step[v] = h
         d = (value(x + step) - value(x - step)) / (2 * h)
         assert float((d - y[:, v]).abs().max()) < 1e-8
+
+
+def test_temperatures_out_of_range(lp):
+    """Beyond 2^-100 to 2^100 a gradient's factor, or the entropy of a row whose masks are its
+    type's lowest value, would leave fp32."""
+    for T, code in ((2.0**-101, 3), (1e-45, 3), (2.0**101, 3), (3e38, 3), (2.0**-100, 0), (2.0**100, 0)):
+        assert lp.load().spec_logprobs(P, 1, 100, P, T, 0, 100, 1, 0, P, None, None, None, None, P,
+                                       256, None, None) == code
+        assert lp.load().spec_logprobs_grad(P, 1, 100, P, P, None, P, None, T, 0, 100, 1, 2 * P, 100,
+                                            None, None) == code

@@ -343,6 +343,21 @@ def test_gradient_alignments(lp, dtype, V, more, out_more):
 
 
 @pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("V", [1, 9, 24, 130, 2047, 8200, 16390])
+@pytest.mark.parametrize("more", [1, 3, 4, 5])
+def test_gradient_every_shift(lp, dtype, V, more):
+    """Logits and gradient at every pair of places of a 16-byte word, row after row; the first and
+    the last vectors of rows, of warps and of CTAs' parts."""
+    g = torch.Generator().manual_seed(V)
+    rows, tokens = zipf(17, V, g, dtype), some_tokens(17, V, 2, g, gone=0.1)
+    tokens[0] = V - 1
+    even = (V + 15) // 8 * 8
+    gradient_case(lp, rows, tokens, 1.0, True, even + more, even)
+    gradient_case(lp, rows, tokens, 1.0, False, even, even + more)
+    gradient_case(lp, rows, tokens, 1.0, True, even + more, even + 2)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
 def test_gradient_of_repeated_tokens_in_place(lp, dtype):
     """The same token many times, at part borders and row ends; the gradient over its logits."""
     V = 40001
