@@ -60,9 +60,13 @@ size_t spec_logprobs_workspace_size(int rows, int V, sv_dtype dtype, int given, 
  * A bad row gets NaN everywhere (top_tokens -1), a bad token NaN at its own place.
  * Workspace as for the verify calls (no initialisation; calls that share one must
  * not overlap).
- * Accuracy: the exponential is off by 2^-21 at most and the sums by the fp32
- * additions of a thread's share; ln p and H are off by about 1e-6 for rows of 2^18
- * tokens.  Alternatives are told apart by their exact values. */
+ * Accuracy: a weight's exponent is off by the rounding of l - m and its own, 2^-24
+ * |l - m| / T each, the exponential by 2^-21 besides, and the sums by the fp32
+ * additions of a thread's share.  Against 64 bits, in rows of 2^18 tokens like a
+ * model's, ln p is off by 3e-6 at most (2^-20 for each of two roundings where it is
+ * below -16) and H by 1.5e-6; where many nearly equal elements weigh as much as the
+ * large ones, 2e-6 and 7e-6 (rows of 2^21: 6e-6 and 2e-5).  Alternatives are told
+ * apart by their exact values. */
 sv_status spec_logprobs(const void* logits, sv_dtype dtype, int64_t row_stride,
                         const int32_t* tokens, float T, int rows, int V, int given, int top,
                         float* logprobs, float* normalizer, float* entropy, int32_t* top_tokens,

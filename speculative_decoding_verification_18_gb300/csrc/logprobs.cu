@@ -183,11 +183,13 @@ __device__ __forceinline__ int place_of(uint64_t key) {
 struct Stats {
     float m, s, u;
 };
-__device__ __forceinline__ void add(Stats& a, const Stats& b, float c) {
+__device__ __forceinline__ void add(Stats& a, const Stats& b, float c, float c_low) {
     const float m = fmaxf(a.m, b.m);
     const float da = a.m == m || a.m == -INFINITY ? 0.0f : a.m - m;
     const float db = b.m == m || b.m == -INFINITY ? 0.0f : b.m - m;
-    const float fa = ex2(da * c), fb = ex2(db * c);
+    // (the small product first, so that the exponent is rounded once; a side's factor is all of its
+    // sum's, so that the low half tells here too)
+    const float fa = ex2(fmaf(da, c, da * c_low)), fb = ex2(fmaf(db, c, db * c_low));
     // (a side so far below that nothing of it is left may have da * s = -inf)
     a.u = (fa > 0.0f ? fa * fmaf(da, a.s, a.u) : 0.0f) +
           (fb > 0.0f ? fb * fmaf(db, b.s, b.u) : 0.0f);
@@ -324,7 +326,7 @@ __global__ void __launch_bounds__(kLpThreads, kLpResident) lp_kernel(const Args 
         if (__any_sync(~0u, most > st.m)) {  // all lanes follow the largest of theirs
 #pragma unroll
             for (int k = 16; k; k >>= 1) most = fmaxf(most, __shfl_xor_sync(~0u, most, k));
-            add(st, Stats{most, 0.0f, 0.0f}, a.c);
+            add(st, Stats{most, 0.0f, 0.0f}, a.c, a.c_low);
         }
         const float2 less = both(st.m == -INFINITY ? 0.0f : -st.m);
         float2 s = make_float2(0.0f, 0.0f), u = s;
@@ -335,7 +337,7 @@ __global__ void __launch_bounds__(kLpThreads, kLpResident) lp_kernel(const Args 
 #pragma unroll
             for (int e = 0; e < VW; e += 2) {
                 float2 d = add2(make_float2(x[e], x[e + 1]), less);
-                float2 p = fma2(d, both(a.c_low), mul2(d, both(a.c)));
+                float2 p = fma2(d, both(a.c), mul2(d, both(a.c_low)));  // rounded once
                 p.x = ex2(p.x);
                 p.y = ex2(p.y);
                 s = add2(s, p);
@@ -425,7 +427,7 @@ __global__ void __launch_bounds__(kLpThreads, kLpResident) lp_kernel(const Args 
             o.m = __shfl_xor_sync(~0u, t.m, k);
             o.s = __shfl_xor_sync(~0u, t.s, k);
             o.u = __shfl_xor_sync(~0u, t.u, k);
-            add(t, o, a.c);
+            add(t, o, a.c, a.c_low);
         }
         if (lane == 0) s_stats = t;
     }
@@ -517,7 +519,7 @@ __global__ void __launch_bounds__(kLpThreads, kLpResident) lp_kernel(const Args 
     else __syncthreads();
     if (rank == 0) {
         Stats t = s_stats;
-        for (int k = 1; k < G; ++k) add(t, *cluster_at(&s_stats, k), a.c);
+        for (int k = 1; k < G; ++k) add(t, *cluster_at(&s_stats, k), a.c, a.c_low);
         const bool bad = !(t.s > 0.0f && t.s < INFINITY) || t.m == INFINITY;
         const float log_s = bad ? NAN : logf(t.s), m = bad ? NAN : t.m;
         if (tid < a.given && token != -1)
