@@ -244,13 +244,14 @@ __device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
 // their way whatever the registers hold, and the CTAs of an SM hide each other's beginnings and
 // ends.
 //
-// Alternatives.  Each thread knows its largest element, the batch of vectors that it is in and the
-// largest element of its others.  Of the largest elements of 128 groups of threads the top-th is a
-// bound: as many elements are at or above it, and these are in the batches of the threads whose
-// own maximum reaches it, about as many again.  Those threads look into their batch again, and
-// where another of theirs reaches the bound too, their warp goes through all of them.  The elements
-// that reach the bound are put in order by counting, and rank 0 joins the lists of the cluster's
-// CTAs.
+// Alternatives.  Each thread knows its largest element, the first batch of vectors that it is in
+// and the largest element of its others.  Of the largest elements of 128 groups of threads the
+// top-th is a bound: as many elements are at or above it, and these are in the batches of the
+// threads whose own maximum reaches it, about as many again.  Those threads look into their batch
+// again, and where another of theirs may reach the bound too (equal ones: by its place, which is
+// behind the first), their warp goes through all of them.  The elements that reach the bound are
+// put in order by counting, 256 at most: of more, those below the top-th of the first 256 go first.
+// Rank 0 joins the lists of the cluster's CTAs.
 //
 // Measured: 4096 rows of 128256 in bf16 without entropy and alternatives 156 us, 6.7 TB/s
 // (memory); 300 of 65537 in fp32 with eight alternatives 18.2 us, 576 of 151936, half of them
@@ -276,7 +277,7 @@ __global__ void __launch_bounds__(kLpThreads, kLpResident) lp_kernel(const Args 
     __shared__ uint64_t s_top[kMaxTop], s_bound;
     __shared__ Stats s_warp[kLpWarps], s_stats;
     __shared__ int s_count;
-    static_assert(kLpRing >= kCandidates * 8 && 32 % B == 0, "candidates in the ring");
+    static_assert(kLpRing / S >= kCandidates * 8 && S > 1, "candidates in the ring's first stage");
     const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
     const int G = cluster_size(), rank = cluster_rank();
     const int r = blockIdx.x / G;
@@ -294,14 +295,24 @@ __global__ void __launch_bounds__(kLpThreads, kLpResident) lp_kernel(const Args 
     const int i1 = w0 + (int)((long long)whole * (rank + 1) / G);
     const uint32_t cand = (uint32_t)__cvta_generic_to_shared(s_mem), ring = cand + tid * 16;
     const uint32_t group = (uint32_t)__cvta_generic_to_shared(s_group);
-    auto issue = [&](int n, int slot) {
+    // B of this thread's vectors, from k on, into a stage of the ring; vector q of a stage.
+    auto copy = [&](int k, int slot) {
 #pragma unroll
-        for (int q = 0; q < B; ++q) {
-            const int k = i0 + tid + (n * B + q) * kLpThreads;
+        for (int q = 0; q < B; ++q, k += kLpThreads) {
             if (k < i1)
                 asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(
                     ring + (slot * B + q) * kLpThreads * 16), "l"(row.at(k)) : "memory");
         }
+    };
+    auto copied = [&](int slot, int q) {
+        uint4 v;
+        asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
+                     : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                     : "r"(ring + (slot * B + q) * kLpThreads * 16) : "memory");
+        return v;
+    };
+    auto issue = [&](int n, int slot) {
+        copy(i0 + tid + n * B * kLpThreads, slot);
         asm volatile("cp.async.commit_group;" ::: "memory");
     };
 #pragma unroll
@@ -370,10 +381,7 @@ __global__ void __launch_bounds__(kLpThreads, kLpResident) lp_kernel(const Args 
 #pragma unroll
         for (int q = 0; q < B; ++q) {
             v[q] = none;
-            if (i0 + tid + (n * B + q) * kLpThreads < i1)
-                asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
-                             : "=r"(v[q].x), "=r"(v[q].y), "=r"(v[q].z), "=r"(v[q].w)
-                             : "r"(ring + (slot * B + q) * kLpThreads * 16) : "memory");
+            if (i0 + tid + (n * B + q) * kLpThreads < i1) v[q] = copied(slot, q);
         }
         // (into the place of the stage before this one)
         issue(n + S - 1, slot == 0 ? S - 1 : slot - 1);
@@ -399,12 +407,14 @@ __global__ void __launch_bounds__(kLpThreads, kLpResident) lp_kernel(const Args 
         return n < 0 ? 0 : n == stages ? row.vectors - 1 : i0 + t + n * B * kLpThreads;
     };
     bool some = false;  // whether this thread has had elements of the row
+    int lead = 0;       // its first batch
     // Threads per group: few groups are quicker to put in order, and bring few elements more than
     // are wanted (24 of 64 groups: about 30).
     const int share = a.top <= 24 ? 2 * kLpThreads / kGroups : kLpThreads / kGroups;
     if (TOP) {
         some = i0 + tid < i1 || (head && tid == 0) || (tail && tid == kLpThreads - 1);
-        if (mine == -INFINITY) best = head && tid == 0 ? -1 : i0 + tid < i1 ? 0 : stages;
+        lead = head && tid == 0 ? -1 : i0 + tid < i1 ? 0 : stages;
+        if (mine == -INFINITY) best = lead;
         // As many elements as there are groups are at or above their largest elements' keys, of
         // which the last place of the batch is known only.
         const int end = first_of(tid, best) + (best < 0 || best == stages ? 0 : B - 1) * kLpThreads;
@@ -449,8 +459,12 @@ __global__ void __launch_bounds__(kLpThreads, kLpResident) lp_kernel(const Args 
         // What nothing has to be looked for below; the elements that reach it; where they are more
         // than there is room for (many that are equal, or large ones that lie together), the top-th
         // of those that found room is the next, higher bound.
-        const uint64_t highest =
-            some ? key_of(mine, max(first_of(tid, best) * VW - row.skew, 0)) : 0;
+        auto from = [&](float x, int n) {  // the highest key that an element of batch n may have
+            return key_of(x, max(first_of(tid, n) * VW - row.skew, 0));
+        };
+        const uint64_t highest = some ? from(mine, best) : 0;
+        // of the other batches: one that has the largest element too comes behind the first
+        const uint64_t other = from(next, next == mine || best == lead ? best + 1 : lead);
         for (;;) {
             __syncthreads();
             const uint64_t bound = s_bound;
@@ -461,18 +475,39 @@ __global__ void __launch_bounds__(kLpThreads, kLpResident) lp_kernel(const Args 
                 if (n < kCandidates) sts64(cand + n * 8, k);
             };
             const bool reaches = some && highest >= bound;
-            const bool more = reaches && ordered(next) >= (uint32_t)(bound >> 32);
-            // a lane per element of the batches that have to be looked into
+            const bool more = reaches && other >= bound;
+            // Those threads' batches: up to eight of a warp's one after the other, a lane per
+            // element; more of them at once, each thread its own (a row of equal logits, where all
+            // 32 are looked into twice: 18 us instead of 74; rows like a model's have one to three,
+            // which the first way takes half a microsecond each for and the second 1.6 together).
+            uint32_t few = __ballot_sync(~0u, reaches && !more);
+            if (__popc(few) <= 8) {
 #pragma unroll 1
-            for (uint32_t few = __ballot_sync(~0u, reaches && !more); few; few &= few - 1) {
-                const int t = __ffs(few) - 1, n = __shfl_sync(~0u, best, t);
-                const bool one = n < 0 || n == stages;
+                for (; few; few &= few - 1) {
+                    const int t = __ffs(few) - 1, n = __shfl_sync(~0u, best, t);
+                    const bool one = n < 0 || n == stages;
 #pragma unroll
-                for (int e = lane; e < B * VW; e += 32) {
-                    const int i = first_of(w * 32 + t, n) + e / VW * kLpThreads;
-                    const int at = i * VW + e % VW - row.skew;
-                    if (at >= 0 && at < a.V && (one ? e < VW : i < i1))
-                        look(E::get(row.row + at), at);
+                    for (int e = lane; e < B * VW; e += 32) {
+                        const int i = first_of(w * 32 + t, n) + e / VW * kLpThreads;
+                        const int at = i * VW + e % VW - row.skew;
+                        if (at >= 0 && at < a.V && (one ? e < VW : i < i1))
+                            look(E::get(row.row + at), at);
+                    }
+                }
+            } else if (reaches && !more) {
+                const bool one = best < 0 || best == stages;
+                const int i = first_of(tid, best), end = one ? i + 1 : i1;
+                if (!one) copy(i, 1);  // (behind the candidates)
+                asm volatile("cp.async.wait_all;" ::: "memory");
+#pragma unroll 1
+                for (int q = 0; q < B && i + q * kLpThreads < end; ++q) {
+                    float x[VW];
+                    E::unpack(one ? row.load(i) : copied(1, q), x);
+#pragma unroll
+                    for (int e = 0; e < VW; ++e) {
+                        const int at = (i + q * kLpThreads) * VW + e - row.skew;
+                        if (!one || (at >= 0 && at < a.V)) look(x[e], at);
+                    }
                 }
             }
             // and of those threads' vectors that have more than one
@@ -495,20 +530,39 @@ __global__ void __launch_bounds__(kLpThreads, kLpResident) lp_kernel(const Args 
                 }
             }
             __syncthreads();
-            const int n = s_count, here = min(n, kCandidates);
-            // eight threads count for each
-            const int sub = tid % 8;
-            for (int i0 = 0; i0 < here; i0 += kLpThreads / 8) {
-                const int i = i0 + tid / 8;
-                const uint64_t k = i < here ? lds64(cand + i * 8) : 0;
-                int before = 0;
+            const int n = s_count;
+            for (int here = min(n, kCandidates);;) {
+                // The places of the candidates, or of the first 256, counted by eight threads for
+                // each; none below the top-th of these is wanted.
+                const int some = min(here, kLpThreads), sub = tid % 8;
+                for (int i0 = 0; i0 < some; i0 += kLpThreads / 8) {
+                    const int i = i0 + tid / 8;
+                    const uint64_t k = i < some ? lds64(cand + i * 8) : 0;
+                    int before = 0;
 #pragma unroll 4
-                for (int j = sub; j < here; j += 8) before += lds64(cand + j * 8) > k;
+                    for (int j = sub; j < some; j += 8) before += lds64(cand + j * 8) > k;
 #pragma unroll
-                for (int x = 1; x < 8; x *= 2) before += __shfl_xor_sync(~0u, before, x);
-                if (sub || i >= here) continue;
-                if (n <= kCandidates && before < a.top) s_top[before] = k;
-                if (n > kCandidates && before == a.top - 1) s_bound = k;
+                    for (int x = 1; x < 8; x *= 2) before += __shfl_xor_sync(~0u, before, x);
+                    if (sub || i >= some || before >= a.top) continue;
+                    s_top[before] = k;
+                    if (before == a.top - 1) s_bound = k;
+                }
+                if (here == some) break;
+                uint64_t k[kCandidates / kLpThreads];
+#pragma unroll
+                for (int q = 0; q < kCandidates / kLpThreads; ++q) {
+                    const int i = tid + q * kLpThreads;
+                    k[q] = i < here ? lds64(cand + i * 8) : 0;
+                }
+                __syncthreads();
+                const uint64_t least = s_bound;
+                if (tid == 0) s_count = 0;
+                __syncthreads();
+#pragma unroll
+                for (int q = 0; q < kCandidates / kLpThreads; ++q)
+                    if (k[q] >= least) sts64(cand + atomicAdd(&s_count, 1) * 8, k[q]);
+                __syncthreads();
+                here = s_count;
             }
             if (n <= kCandidates) break;
             __syncthreads();

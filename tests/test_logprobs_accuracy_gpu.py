@@ -63,10 +63,10 @@ SIZES = [(1 << 18, 4), (1 << 18, 64), (1 << 21, 4)]
 def test_rows_like_a_models(lp, dtype, V, R, T):
     """Of different elements, whose roundings are as good as random.  An element's sum takes 100
     additions at most, each off by 2^-25 / sqrt(3) of the sum (together 2^-23.5), and four
-    exponentials of 2^-22 at most each, in different warps: S is off by 2^-22.5, one deviation.  Four
-    of them and the rounding of ln S (below 8: 2^-22): 1e-6.  ln p: (l - m) / T and the difference
-    from ln S are below 32 and rounded by 2^-20 each: 3e-6.  H = ln S + A with A below 8 and two
-    such sums: 4 sqrt(2) 2^-22.5 of 8, and 1e-6: 9e-6; A is nearer to 4 and the two sums go
+    exponentials of 2^-22 at most each, in different warps: S is off by 2^-22.5, one deviation.
+    Four of them and the rounding of ln S (below 8: 2^-22): 1e-6.  ln p: (l - m) / T and the
+    difference from ln S are below 32 and rounded by 2^-20 each: 3e-6.  H = ln S + A with A below 8
+    and two such sums: 4 sqrt(2) 2^-22.5 of 8, and 1e-6: 9e-6; A is nearer to 4 and the two sums go
     together, as they round the same weights: 4e-6."""
     g = torch.Generator().manual_seed(V + R)
     rows, tokens = zipf(R, V, g, dtype), some_tokens(R, V, 16, g)
