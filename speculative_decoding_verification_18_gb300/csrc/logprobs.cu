@@ -254,9 +254,9 @@ __device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
 // Rank 0 joins the lists of the cluster's CTAs.
 //
 // Measured: 4096 rows of 128256 in bf16 without entropy and alternatives 156 us, 6.7 TB/s
-// (memory); 300 of 65537 in fp32 with eight alternatives 18.2 us, 576 of 151936, half of them
-// without tokens, with 20 alternatives 29.8 us, nine of 256000 with five 11.2 us (the steps behind
-// the row wait for one another: 3 us, 7 where others keep the SM busy).  Choices, measured before
+// (memory); 300 of 65537 in fp32 with eight alternatives 18.3 us, 576 of 151936 with 20 alternatives
+// 41 us (39 where half of them are without tokens), nine of 256000 with five 11.5 us (the steps
+// behind the row wait for one another: 3 us, 7 where others keep the SM busy).  Choices, measured before
 // the kernel was launched ahead of the end of the one before it: 157 us on the first of these, 167
 // with the entropy, 205 with it and 20 alternatives (instructions: the second product per element,
 // and a warp's turn of many small steps at the end of each row).  Stages of two vectors instead of
@@ -926,13 +926,12 @@ sv_status spec_logprobs(const void* logits, sv_dtype dtype, int64_t row_stride,
     base2(T, &a.c, &a.c_low);
     // A cluster per row while its CTAs have SMs of their own and runs worth a CTA's beginning and
     // end (9 rows of 256000, 5 alternatives: G = 1 20.4 us, 2 16.5, 4 14.5, 8 14.2; 40 of 128256:
-    // 16.6, 16.0, 16.6, 18.5; 5 of 32000: 8.5, 10.4).  More rows: a CTA each (300 of 65537: 20.7
-    // us, two each 24.8; 1024 of 32000: 26.9 and 45.1), but two each where all would be resident
-    // at once and the rows that hold tokens met on some SMs by chance (576 of 151936, half of them
-    // without tokens: 41 and 32 us; all with tokens: 45 and 55).
+    // 16.6, 16.0, 16.6, 18.5; 5 of 32000: 8.5, 10.4).  More rows: a CTA each.  (300 of 65537, all
+    // with tokens: 14.3 us, two each 18.4; 576: 23 and 35; 576 of 151936: 41 and 52.  Where half of
+    // them hold none, those that do meet on some SMs by chance, and two each take 30 instead of 39
+    // there, but which rows hold tokens is known on the device only.)
     int G = 1;
     while (G < kMaxCluster && 2ll * rows * G <= sms && V / G >= 49152) G *= 2;
-    if (rows > 2 * sms && rows < kLpResident * sms && V >= 65536) G = 2;
     const long long ctas = (long long)rows * G;
     auto typed = [&](auto t) {
         using E = decltype(t);
