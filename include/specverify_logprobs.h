@@ -58,8 +58,9 @@ size_t spec_logprobs_workspace_size(int rows, int V, sv_dtype dtype, int given, 
  *                 equals; -1 behind V of them.  NULL when top is 0.
  *   top_logprobs  [rows, top] fp32 (written): their ln p; -inf behind V of them.
  * A bad row gets NaN everywhere (top_tokens -1), a bad token NaN at its own place.
- * Workspace as for the verify calls (no initialisation; calls that share one must
- * not overlap).
+ * The workspace is asked for as by the verify calls (spec_logprobs_workspace_size bytes
+ * at least, 16-byte aligned) but neither read nor written: calls that overlap, and
+ * captured graphs, may share one.
  * Accuracy: a weight's exponent is off by the rounding of l - m and its own, 2^-24
  * |l - m| / T each, the exponential by 2^-21 besides, and the sums by the fp32
  * additions of a thread's share.  Against 64 bits, in rows of 2^18 tokens like a

@@ -63,7 +63,8 @@ def spec_logprobs_workspace_size(rows, V, dtype=sv.SV_BF16, given=1, top=0) -> i
 
 
 def logprobs_workspace(logits, given=1, top=0):
-    """A workspace tensor of the required size (bytes, uint8) for rows like these."""
+    """A workspace tensor of the required size (bytes, uint8) for rows like these; calls that overlap
+    may share it."""
     V = logits.shape[-1]
     n = spec_logprobs_workspace_size(logits.numel() // max(V, 1), V, sv._dtype(logits), given, top)
     if n == 0:
