@@ -233,9 +233,8 @@ template <> struct Share<true> : Count {
 __device__ __forceinline__ constexpr int full_weight(int rows) { return rows > 128 ? 2 : 1; }
 
 template <bool WINDOW>
-__device__ __forceinline__ Share<WINDOW>
-share_from(const AttentionArgs& a, int len, int n, int rows,
-                                            int unit) {
+__device__ __forceinline__ Share<WINDOW> share_from(const AttentionArgs& a, int len, int n,
+                                                    int rows, int unit) {
     Share<WINDOW> s;
     s.len = len;
     s.n = n;
@@ -1151,7 +1150,7 @@ __device__ __forceinline__ uint32_t turned(uint32_t x) {
 //
 // Over a 16-bit cache memory is the bound: one token behind 64 windows of 4096, 32/8 heads of 128,
 // 163 us, 6.6 TB/s.  Over an 8-bit one fixed latencies are: 24 rows, 96 windows of 1024, 75 us,
-// 2.8 TB/s (issue slots 46 % busy); a third of a CTA's time is where its pieces begin and end. 
+// 2.8 TB/s (issue slots 46 % busy); a third of a CTA's time is where its pieces begin and end.
 // The split kernel with a window took 107 us there.
 template <typename T, typename CT, int DP, int NQ>
 __global__ void __launch_bounds__(kSplitThreads, Slots<CT, DP, NQ>::kResident)
@@ -2869,7 +2868,11 @@ static int most_slots(const sv_kv_cache* c, int window, int sinks, int N) {
 }
 
 // Whether a call takes a cluster per item: when all its clusters are resident at once and a CTA's
-// share of the longest context that the table can hold is at most 16 units (1024 slots).
+// share of the longest context that the table can hold is at most 16 units (1024 slots).  (Behind
+// windows, against ranges and their join, 8 key heads of 128, 4 rows: one sequence 1024 slots 8.1
+// and 9.9 us, 4096 12.8 and 14.7, 8000 18.7 and 16.6, 12000 25.1 and 21.6; four sequences 9.1 and
+// 11.9, 17.7 and 22.6, 26.5 and 31.0, 35.5 and 40.3.  With 32 rows 11.6 and 16.7, 18.3 and 20.9,
+// 27.1 and 26.2, 35.8 and 28.5; 15.1 and 19.1, 26.5 and 33.4, 38.1 and 43.7, 50.9 and 54.4.)
 static bool small_call(int B, int heads, int rows, int slots, int sms) {
     const long long items = (long long)B * heads * ((rows + (rows <= 16 ? 15 : 31)) /
                                                     (rows <= 16 ? 16 : 32));
@@ -3099,8 +3102,13 @@ static sv_status attend(const sv_kv_cache* cache, const void* q, const sv_stride
     const bool cluster = small_call(B, cache->heads, rows, slots, sms);
     // Float8 over short contexts stays with mma.sync up to 64 rows: pieces of one or two units, and
     // no halves to make (100 sequences, 8 key heads of 128, 64 rows each over at most 128 slots 70
-    // against 118 us, 2000 slots 235 against 252, 3000 slots 313 against 295).
-    const int few = cache->dtype == SV_E4M3 && slots <= 2048 ? 64 : 32;
+    // against 118 us, 2000 slots 235 against 252, 3000 slots 313 against 295).  Through a window, by
+    // slots and wide, 40 rows: 64 sequences with windows of 500 slots 90 and 95 us, 1000 119 and
+    // 124, 1800 172 and 164, 3000 244 and 213; 8 sequences 26 and 28, 30 and 32, 37 and 37, 47 and
+    // 45; 192 sequences 226 and 201, 311 and 287, 470 and 394 (heads of 64: 168 and 164, 223 and
+    // 217, 336 and 292).  16-bit caches through a window: 64 sequences with windows of 128 67 and
+    // 59 us, 512 101 and 82, 2048 222 and 126; 8 sequences 22 and 23, 27 and 25, 45 and 33.
+    const int few = cache->dtype == SV_E4M3 && slots <= (WINDOW ? 1536 : 2048) ? 64 : 32;
     CUtensorMap kmap, vmap;
     wide = wide && !cluster && rows > few && cache->page_size >= 8 &&
            cache_map(&kmap, cache->k, cache) && cache_map(&vmap, cache->v, cache);
