@@ -40,10 +40,10 @@ def test_a_few_rows_per_multiprocessor(lp, dtype, V, per_sm, more, gone):
 
 @pytest.mark.parametrize("V", [65536, 100000])
 def test_fewer_rows_take_no_longer(lp, V):
-    """All of them with tokens, with and without alternatives: up to as many as are resident at
-    once."""
+    """Than as many as are resident at once, all of them with tokens.  (Not one by one: a call's
+    CTAs come while those of the one before leave, and a few rows more than two or three per SM may
+    meet four on some.)"""
     R = 4 * sms()
     x = zipf(8, V, torch.Generator().manual_seed(1), BF)[torch.arange(R) % 8].cuda()
     times = [microseconds(lp, x[:n], 20) for n in (2 * sms(), 2 * sms() + 1, 3 * sms(), R - 1, R)]
-    for fewer, more in zip(times, times[1:]):
-        assert fewer <= 1.15 * more, times
+    assert max(times[:-1]) <= 1.15 * times[-1], times
