@@ -585,7 +585,7 @@ __device__ __forceinline__ bool mixed(const AttentionArgs& a, const Share<WINDOW
 // too; their weights are single halves then, three bits finer than a bfloat16 result (fewer below
 // 2^-14 of the reference).  Bound by memory up to 16 rows (64 sequences of 4000-8000 slots, one
 // token, 32 query and 8 key heads of 128: 246 us, 6.4 TB/s; the same over float8, 96 sequences of
-// 4100-8200 slots: 223 us, 5.5 TB/s), by conversions and fixed latencies over float8 with 32 (96
+// 4100-8200 slots: 228 us, 5.3 TB/s), by conversions and fixed latencies over float8 with 32 (96
 // sequences, 24 rows: 353 us, 3.5 TB/s).
 template <typename CT, int DP, int WM> struct Split {
     using St = Stage<CT, DP>;
@@ -1665,11 +1665,11 @@ __global__ void __launch_bounds__(kSplitThreads, Slots<CT, DP, NQ>::kResident)
 // pipe, so that one is multiplied while the other is exponentiated: two tiles of 128 rows over
 // the same slots, or, when the rows fit one tile, every other 128 slots of it (joined at the
 // end).  Work is cut into ranges and joined as for the split kernel, in units of 128 slots.
-// Measured: 32 trees of 16 nodes, 128 rows per key head, 6000-12000 slots: 228 us, 5.5 TB/s (the
-// chain scores - weights - product of a stream, 5000 cycles, hides all but a fifth of the memory's
-// time); 8 trees of 65 nodes over 16000-33000 slots: 503 us, 867 TFLOP/s (the products: 128 x 128
+// Measured: 32 trees of 16 nodes, 128 rows per key head, 6000-12000 slots: 217 us, 5.7 TB/s (the
+// chain scores - weights - product of a stream, 5000 cycles, hides all but a sixth of the memory's
+// time); 8 trees of 65 nodes over 16000-33000 slots: 457 us, 954 TFLOP/s (the products: 128 x 128
 // of two shared-memory operands takes all of that memory's bandwidth, 780 cycles where the tensor
-// pipe alone would need 512); the same over float8: 264 us, 2.4 TB/s, and 643 us (making halves).
+// pipe alone would need 512); the same over float8: 260 us, 2.4 TB/s, and 622 us (making halves).
 
 constexpr int kTcThreads = 512;
 constexpr int kTcUnit = 128;  // slots
@@ -3101,13 +3101,15 @@ static sv_status attend(const sv_kv_cache* cache, const void* q, const sv_stride
     const int slots = most_slots<WINDOW>(cache, window, sinks, N);
     const bool cluster = small_call(B, cache->heads, rows, slots, sms);
     // Float8 over short contexts stays with mma.sync up to 64 rows: pieces of one or two units, and
-    // no halves to make (100 sequences, 8 key heads of 128, 64 rows each over at most 128 slots 70
-    // against 118 us, 2000 slots 235 against 252, 3000 slots 313 against 295).  Through a window, by
-    // slots and wide, 40 rows: 64 sequences with windows of 500 slots 90 and 95 us, 1000 119 and
-    // 124, 1800 172 and 164, 3000 244 and 213; 8 sequences 26 and 28, 30 and 32, 37 and 37, 47 and
-    // 45; 192 sequences 226 and 201, 311 and 287, 470 and 394 (heads of 64: 168 and 164, 223 and
-    // 217, 336 and 292).  16-bit caches through a window: 64 sequences with windows of 128 67 and
-    // 59 us, 512 101 and 82, 2048 222 and 126; 8 sequences 22 and 23, 27 and 25, 45 and 33.
+    // no halves to make (against wide, 64 rows, 8 key heads: 8 sequences, heads of 128, at most 128
+    // slots 17 and 20 us, 1000 29 and 28, 2000 35 and 35; 100 sequences 74 and 69, 156 and 145, 236
+    // and 204, heads of 64 49 and 51, 104 and 123, 155 and 174).  Through a window, by slots and
+    // wide, 40 rows: 64 sequences with windows of 500 slots 90 and 95 us, 1000 119 and 124, 1800
+    // 172 and 164, 3000 244 and 213; 8 sequences 26 and 28, 30 and 32, 37 and 37, 47 and 45; 192
+    // sequences 226 and 201, 311 and 287, 470 and 394 (heads of 64: 168 and 164, 223 and 217, 336
+    // and 292).  16-bit caches are wide: 100 sequences over 128 slots 75 and 56 us, 2000 277 and
+    // 159; through a window, 64 sequences, 128 67 and 59, 512 101 and 82, 2048 222 and 126; 8
+    // sequences 22 and 23, 27 and 25, 45 and 33.
     const int few = cache->dtype == SV_E4M3 && slots <= (WINDOW ? 1536 : 2048) ? 64 : 32;
     CUtensorMap kmap, vmap;
     wide = wide && !cluster && rows > few && cache->page_size >= 8 &&

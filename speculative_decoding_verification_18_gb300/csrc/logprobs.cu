@@ -253,15 +253,15 @@ __device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
 // put in order by counting, 256 at most: of more, those below the top-th of the first 256 go first.
 // Rank 0 joins the lists of the cluster's CTAs.
 //
-// Measured: 4096 rows of 128256 in bf16 without entropy and alternatives 156 us, 6.7 TB/s
-// (memory); 300 of 65537 in fp32 with eight alternatives 18.3 us, 576 of 151936 with 20 alternatives
-// 41 us (39 where half of them are without tokens), nine of 256000 with five 11.5 us (the steps
-// behind the row wait for one another: 3 us, 7 where others keep the SM busy).  Choices, measured before
-// the kernel was launched ahead of the end of the one before it: 157 us on the first of these, 167
-// with the entropy, 205 with it and 20 alternatives (instructions: the second product per element,
-// and a warp's turn of many small steps at the end of each row).  Stages of two vectors instead of
-// four, five CTAs per SM: 162, 178 and 220 us; 128 threads: 160, 164 and 211 us, but 32 instead of
-// 24 us for nine rows of 256000 with five alternatives by one CTA each.
+// Measured: 4096 rows of 128256 in bf16 without entropy and alternatives 156 us, 6.7 TB/s (memory);
+// 300 of 65537 in fp32 with eight alternatives 18.6 us, 576 of 151936 with 20 41 us (38.5 where
+// half of them are without tokens), nine of 256000 with five 11.4 us (the steps behind the row wait
+// for one another: 3 us, 7 where others keep the SM busy).  Choices, measured before the kernel
+// was launched ahead of the end of the one before it: 157 us on the first of these, 167 with the
+// entropy, 205 with it and 20 alternatives (instructions: the second product per element, and a
+// warp's turn of many small steps at the end of each row).  Stages of two vectors instead of four,
+// five CTAs per SM: 162, 178 and 220 us; 128 threads: 160, 164 and 211 us, but 32 instead of 24 us
+// for nine rows of 256000 with five alternatives by one CTA each.
 constexpr int kLpThreads = 256, kLpWarps = kLpThreads / 32;
 constexpr int kLpBatch = 4;      // vectors of a thread per stage
 constexpr int kLpStages = 3;
