@@ -926,7 +926,7 @@ sv_status spec_logprobs(const void* logits, sv_dtype dtype, int64_t row_stride,
     base2(T, &a.c, &a.c_low);
     // A cluster per row while its CTAs have SMs of their own and runs worth a CTA's beginning and
     // end (9 rows of 256000, 5 alternatives: G = 1 20.4 us, 2 16.5, 4 14.5, 8 14.2; 40 of 128256:
-    // 16.6, 16.0, 16.6, 18.5; 5 of 32000: 8.5, 10.4).  More rows: a CTA each.  (300 of 65537, all
+    // 16.6, 16.0, 16.6, 18.5; 5 of 32000: 8.5, 10.4).  More rows: a CTA each.  (300 of 65536, all
     // with tokens: 14.3 us, two each 18.4; 576: 23 and 35; 576 of 151936: 41 and 52.  Where half of
     // them hold none, those that do meet on some SMs by chance, and two each take 30 instead of 39
     // there, but which rows hold tokens is known on the device only.)
